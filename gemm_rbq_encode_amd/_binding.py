@@ -36,6 +36,8 @@ RBQ_EPILOGUE_SILU_MUL = 1
 RBQ_ENCODE_FORCE_SERIAL = 1
 RBQ_LAYOUT_ROWS = 0
 RBQ_LAYOUT_TILES = 1
+RBQ_Y_F16 = 0
+RBQ_Y_F32 = 1
 
 PATH_AUTO, PATH_VALU, PATH_DECODE, PATH_PREFILL, PATH_STREAM, PATH_FLAT, PATH_GROUP, PATH_SPLIT = (
     0, 1, 2, 3, 4, 5, 6, 7)
@@ -120,6 +122,22 @@ _SIGNATURES = {
     "rbq_qat_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, Shape, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_qat_checkpoint": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_qat_backward_ckpt_workspace_bytes": (ctypes.c_size_t, [Shape, ctypes.c_int32]),
+    "rbq_qat_backward_ckpt": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, Shape, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                             ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_encode_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_quantize_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_gemm_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                   ctypes.c_uint32, ctypes.c_void_p]),
+    "rbq_gemv_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_probe_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_tiles_bytes": (ctypes.c_size_t, [Shape]),
     "rbq_pack_tiles": (ctypes.c_int, [ctypes.c_void_p, Shape, ctypes.c_void_p, ctypes.c_void_p]),
@@ -460,6 +478,201 @@ def qat_backward(planes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, dY
     check(lib().rbq_qat_backward(planes.data_ptr(), scales.data_ptr(), s, X.data_ptr(), dY.data_ptr(), M,
                                  ptr(dX), ptr(dW), ptr(ds), ptr(workspace), wn, sp, _stream(planes, stream)),
           "rbq_qat_backward")
+    return dX, (dW if need_dw else None), ds
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device all given tensors (None left out) are on."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
+    return dev
+
+
+class _Launch:
+    """Context of a call for tensors on `dev`: that device is current, and so is
+    the stream the call is for, so that buffers made inside belong to it."""
+
+    def __init__(self, dev: torch.device, stream=None):
+        self._ctx = []
+        if dev.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            self._ctx.append(torch.cuda.stream(stream))
+        self._dev = dev
+
+    def __enter__(self) -> int:
+        for c in self._ctx:
+            c.__enter__()
+        return int(torch.cuda.current_stream(self._dev).cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _out(t: torch.Tensor | None, size: tuple, dtype, name: str, dev: torch.device) -> torch.Tensor:
+    """The given output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(size, dtype=dtype, device=dev)
+    _dev(t, dtype, name)
+    if tuple(t.shape) != size:
+        raise ValueError(f"{name} must be {list(size)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    return t
+
+
+def encode_f8(W: torch.Tensor, *, status: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+              scales: torch.Tensor | None = None, stream=None):
+    """rbq_encode_f8: fp32 W [out][in] -> (codes float8_e4m3fn [out][in],
+    scales float32 [ceil(out/128)][ceil(in/128)]), one scale per block of
+    128 x 128.  `status` (int32, 1 element) receives RBQ_STATUS_* bits."""
+    _dev(W, torch.float32, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be [out][in]")
+    out_f, in_f = W.shape
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(W, status)
+    with _Launch(dev, stream) as st:
+        codes = _out(codes, (out_f, in_f), torch.float8_e4m3fn, "codes", dev)
+        scales = _out(scales, (_blocks(out_f), _blocks(in_f)), torch.float32, "scales", dev)
+        check(lib().rbq_encode_f8(W.data_ptr(), out_f, in_f, codes.data_ptr(), scales.data_ptr(),
+                                  None if status is None else status.data_ptr(), st), "rbq_encode_f8")
+    return codes, scales
+
+
+def quantize_f8(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                stream=None):
+    """rbq_quantize_f8: fp16 X [M][in] -> (codes float8_e4m3fn [M][in], scales
+    float32 [ceil(in/128)][M]), one scale per token and block of 128 columns."""
+    _dev(X, torch.float16, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [M][in]")
+    M, in_f = X.shape
+    dev = X.device
+    with _Launch(dev, stream) as st:
+        codes = _out(codes, (M, in_f), torch.float8_e4m3fn, "codes", dev)
+        scales = _out(scales, (_blocks(in_f), M), torch.float32, "scales", dev)
+        check(lib().rbq_quantize_f8(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
+              "rbq_quantize_f8")
+    return codes, scales
+
+
+def _f8_layer(codes: torch.Tensor, scales: torch.Tensor):
+    _dev(codes, torch.float8_e4m3fn, "codes")
+    _dev(scales, torch.float32, "scales")
+    if codes.dim() != 2 or tuple(scales.shape) != (_blocks(codes.shape[0]), _blocks(codes.shape[1])):
+        raise ValueError("codes must be [out][in] and scales [ceil(out/128)][ceil(in/128)]")
+    return codes.shape
+
+
+def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor, *,
+            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None, stream=None):
+    """rbq_gemm_f8: Y [M][out] (float16 or float32) of the layer of encode_f8
+    and the tokens of quantize_f8."""
+    out_f, in_f = _f8_layer(codes, scales)
+    _dev(x_codes, torch.float8_e4m3fn, "x_codes")
+    _dev(x_scales, torch.float32, "x_scales")
+    if x_codes.dim() != 2 or x_codes.shape[1] != in_f:
+        raise ValueError(f"x_codes must be [M][{in_f}], got {tuple(x_codes.shape)}")
+    M = x_codes.shape[0]
+    if tuple(x_scales.shape) != (_blocks(in_f), M):
+        raise ValueError(f"x_scales must be [{_blocks(in_f)}][{M}], got {tuple(x_scales.shape)}")
+    if dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
+    dev = _one_device(codes, scales, x_codes, x_scales)
+    with _Launch(dev, stream) as st:
+        Y = _out(Y, (M, out_f), dtype, "Y", dev)
+        check(lib().rbq_gemm_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x_codes.data_ptr(),
+                                x_scales.data_ptr(), M, Y.data_ptr(),
+                                RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16, st), "rbq_gemm_f8")
+    return Y
+
+
+def gemv_f8(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, *, y: torch.Tensor | None = None,
+            stream=None):
+    """rbq_gemv_f8: y [out] of the layer of encode_f8 for one fp16 token x [in]."""
+    out_f, in_f = _f8_layer(codes, scales)
+    _dev(x, torch.float16, "x")
+    if x.numel() != in_f:
+        raise ValueError(f"x must have {in_f} elements")
+    dev = _one_device(codes, scales, x)
+    with _Launch(dev, stream) as st:
+        y = _out(y, (out_f,), torch.float16, "y", dev)
+        check(lib().rbq_gemv_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x.data_ptr(), y.data_ptr(), st),
+              "rbq_gemv_f8")
+    return y
+
+
+def qat_checkpoint(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                   stream=None):
+    """rbq_qat_checkpoint: fp16 X [M][in] -> (codes int8 [M][in], scales
+    float16 [M][ceil(in/128)]); a code stands for fp16(code * scale)."""
+    _dev(X, torch.float16, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [M][in]")
+    M, in_f = X.shape
+    dev = X.device
+    with _Launch(dev, stream) as st:
+        codes = _out(codes, (M, in_f), torch.int8, "codes", dev)
+        scales = _out(scales, (M, _blocks(in_f)), torch.float16, "scales", dev)
+        check(lib().rbq_qat_checkpoint(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
+              "rbq_qat_checkpoint")
+    return codes, scales
+
+
+def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor,
+                      dY: torch.Tensor, group_size: int = 0, *, need_dx: bool = True, need_dw: bool = True,
+                      need_dscales: bool = True, workspace: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None):
+    """rbq_qat_backward_ckpt: qat_backward with the activations given as the
+    checkpoint of qat_checkpoint; (dX [M][in], dW [out][in], dscales
+    [K][out][G]), fp32; an output not asked for is None."""
+    _dev(planes, torch.int32, "planes")
+    _dev(scales, torch.float16, "scales")
+    _dev(x_codes, torch.int8, "x_codes")
+    _dev(x_scales, torch.float16, "x_scales")
+    _dev(dY, torch.float16, "dY")
+    if planes.dim() != 3:
+        raise ValueError("planes must be [K][out][in/32]")
+    K, out_f, words = planes.shape
+    in_f = words * 32
+    s = shape(out_f, in_f, K, group_size)
+    check(lib().rbq_check_shape(s), "rbq_qat_backward_ckpt")
+    M = dY.shape[0]
+    if tuple(dY.shape) != (M, out_f) or tuple(x_codes.shape) != (M, in_f) or \
+            tuple(x_scales.shape) != (M, _blocks(in_f)):
+        raise ValueError("x_codes must be [M][in], x_scales [M][ceil(in/128)] and dY [M][out]")
+    if scales.numel() * 2 != scales_bytes(s):
+        raise ValueError("scales do not match the shape")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(planes, scales, x_codes, x_scales, dY, workspace, status)
+    ptr = (lambda t: None if t is None else t.data_ptr())
+    with _Launch(dev, stream) as st:
+        dX = torch.empty((M, in_f), dtype=torch.float32, device=dev) if need_dx else None
+        dW = torch.empty((out_f, in_f), dtype=torch.float32, device=dev) if (need_dw or need_dscales) else None
+        ds = torch.empty((K, out_f, groups_per_row(in_f, group_size)), dtype=torch.float32, device=dev) \
+            if need_dscales else None
+        need = int(lib().rbq_qat_backward_ckpt_workspace_bytes(s, M))
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wn = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        check(lib().rbq_qat_backward_ckpt(planes.data_ptr(), scales.data_ptr(), s, x_codes.data_ptr(),
+                                          x_scales.data_ptr(), dY.data_ptr(), M, ptr(dX), ptr(dW), ptr(ds),
+                                          ptr(workspace), wn, ptr(status), st), "rbq_qat_backward_ckpt")
     return dX, (dW if need_dw else None), ds
 
 

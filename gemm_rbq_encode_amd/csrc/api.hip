@@ -593,6 +593,164 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 
+// ---- linears in 8-bit floating point blocks of 128 ---------------------------
+
+static bool f8_shape_ok(int32_t out, int32_t in) { return out >= 0 && in >= 0 && in % 32 == 0; }
+
+rbq_status rbq_encode_f8(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes, float *scales,
+                         int32_t *status_dev, void *stream) {
+    if (!f8_shape_ok(out_features, in_features))
+        return RBQ_ERR_INVALID_ARG;
+    if (out_features == 0 || in_features == 0)
+        return RBQ_OK;
+    if (W == nullptr || codes == nullptr || scales == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
+        (status_dev != nullptr && !aligned(status_dev, 4)))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st = device_present();
+    if (st != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_encode_f8(W, out_features, in_features, codes, scales, status_dev,
+                                         (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, uint8_t *codes, float *scales,
+                           void *stream) {
+    if (M < 0 || !f8_shape_ok(0, in_features))
+        return RBQ_ERR_INVALID_ARG;
+    if (M == 0 || in_features == 0)
+        return RBQ_OK;
+    if (X == nullptr || codes == nullptr || scales == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st = device_present();
+    if (st != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_quantize_f8(X, M, in_features, codes, scales, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
+                       const uint8_t *x_codes, const float *x_scales, int32_t M, void *Y, uint32_t y_type,
+                       void *stream) {
+    if (M < 0 || !f8_shape_ok(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
+        return RBQ_ERR_INVALID_ARG;
+    if (M == 0 || out_features == 0)
+        return RBQ_OK;
+    if (Y == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(Y, y_type == RBQ_Y_F32 ? 4 : 2))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st;
+    hipError_t e;
+    if (in_features == 0) {  // empty sums: Y = 0
+        if ((st = device_present()) != RBQ_OK)
+            return st;
+        const size_t n = (size_t)M * (size_t)out_features;
+        e = y_type == RBQ_Y_F32 ? rbq::launch_fill_zero_f32(static_cast<float *>(Y), n, (hipStream_t)stream)
+                                : rbq::launch_fill_zero_u16(static_cast<uint16_t *>(Y), (int64_t)n,
+                                                            (hipStream_t)stream);
+        return e == hipSuccess ? RBQ_OK : hip_fail(e);
+    }
+    if (codes == nullptr || scales == nullptr || x_codes == nullptr || x_scales == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x_codes, 16) || !aligned(x_scales, 4))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    e = rbq::launch_gemm_f8(codes, scales, out_features, in_features, x_codes, x_scales, M, Y,
+                            y_type == RBQ_Y_F32, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+rbq_status rbq_gemv_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
+                       const uint16_t *x, uint16_t *y, void *stream) {
+    if (!f8_shape_ok(out_features, in_features))
+        return RBQ_ERR_INVALID_ARG;
+    if (out_features == 0)
+        return RBQ_OK;
+    if (y == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(y, 2))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st;
+    hipError_t e;
+    if (in_features == 0) {
+        if ((st = device_present()) != RBQ_OK)
+            return st;
+        e = rbq::launch_fill_zero_u16(y, out_features, (hipStream_t)stream);
+        return e == hipSuccess ? RBQ_OK : hip_fail(e);
+    }
+    if (codes == nullptr || scales == nullptr || x == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x, 16))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    e = rbq::launch_gemv_f8(codes, scales, out_features, in_features, x, y, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+// ---- 8-bit activation checkpoints --------------------------------------------
+
+rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features, int8_t *codes, uint16_t *scales,
+                              void *stream) {
+    if (M < 0 || !f8_shape_ok(0, in_features))
+        return RBQ_ERR_INVALID_ARG;
+    if (M == 0 || in_features == 0)
+        return RBQ_OK;
+    if (X == nullptr || codes == nullptr || scales == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 2))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st = device_present();
+    if (st != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_qat_checkpoint(X, M, in_features, codes, scales, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+size_t rbq_qat_backward_ckpt_workspace_bytes(rbq_shape s, int32_t M) {
+    if (rbq_check_shape(s) != RBQ_OK || M < 1)
+        return 0;
+    return rbq::qat_backward_workspace_bytes(M, s.out_features, s.in_features);
+}
+
+rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, rbq_shape s,
+                                 const int8_t *x_codes, const uint16_t *x_scales, const uint16_t *dY, int32_t M,
+                                 float *dX, float *dW, float *dscales, void *workspace, size_t ws_bytes,
+                                 int32_t *status_dev, void *stream) {
+    rbq_status st = rbq_check_shape(s);
+    if (st != RBQ_OK)
+        return st;
+    if (!rbq::qat_supports(s.num_planes))
+        return RBQ_ERR_UNSUPPORTED;
+    if (M < 0 || (dscales != nullptr && dW == nullptr) || (ws_bytes > 0 && workspace == nullptr))
+        return RBQ_ERR_INVALID_ARG;
+    const bool some = M > 0 && s.out_features > 0 && s.in_features > 0;
+    if (!some)   // an empty sum: no activations are read
+        return rbq_qat_backward(planes, scales, s, nullptr, dY, M, dX, dW, dscales, workspace, ws_bytes, status_dev,
+                                stream);
+    if (dX == nullptr && dW == nullptr)
+        return RBQ_OK;
+    if (dY == nullptr || (dW != nullptr && (x_codes == nullptr || x_scales == nullptr)) ||
+        ((dX != nullptr || dscales != nullptr) && (planes == nullptr || scales == nullptr)))
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(planes, 4) || !aligned(scales, 2) || !aligned(x_codes, 16) || !aligned(x_scales, 2) ||
+        !aligned(dY, 2) || !aligned(dX, 4) || !aligned(dW, 4) || !aligned(dscales, 4) || !aligned(workspace, 4) ||
+        (status_dev != nullptr && !aligned(status_dev, 4)))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_qat_backward_ckpt(planes, scales, s.out_features, s.in_features, s.num_planes,
+                                                 s.group_size, x_codes, x_scales, dY, M, dX, dW, dscales, workspace,
+                                                 ws_bytes, status_dev, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
 rbq_status rbq_probe_read(const void *buf, size_t bytes, uint32_t *sink, void *stream) {
     if (buf == nullptr || sink == nullptr)
         return RBQ_ERR_INVALID_ARG;

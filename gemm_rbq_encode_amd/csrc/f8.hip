@@ -1,0 +1,285 @@
+// f8.hip -- 8-bit floating point blocks of 128: the weight encoder, the token
+// quantiser and the products for one and few tokens.
+//
+// A value is code * scale with an OCP e4m3 code (4 significant bits, at most
+// 448) and one fp32 scale per block of 128 x 128 weights, or per block of 128
+// columns of one token.  For a block with A = max |v| (at least 2^-100, so
+// that 448 / A is finite and an all-zero block needs no case of its own):
+//   scale = fl32(A / 448),  code = e4m3(fl32(v * fl32(448 / A)))
+// each rounded to nearest even.  The largest entry takes code +-448; a block
+// with a NaN or infinite entry has scale NaN and codes 0.
+#include <algorithm>
+
+#include "rbq.h"
+#include "rbq_device.h"
+#include "rbq_kernels.h"
+#include "f8_device.h"
+
+namespace rbq {
+
+namespace {
+
+constexpr int FQ_THREADS = 256;
+
+// ---------------------------------------------------------------------------
+// tokens: 16 lanes hold one block (8 consecutive fp16 each, one 16-byte load),
+// so the maximum is four DPP rotations inside a row of 16 lanes and needs no
+// LDS.  A workgroup takes 16 tokens x 4 blocks; the four loads of a lane are
+// issued together.  Bound by the read of X and the write of the codes.
+constexpr int FQ_ROWS = FQ_THREADS / 16;
+constexpr int FQ_BLOCKS = 4;
+
+__global__ __launch_bounds__(FQ_THREADS) void quantize_f8_kernel(const uint16_t *__restrict__ X, int M, int in,
+                                                                 int T, int64_t units,
+                                                                 uint8_t *__restrict__ codes,
+                                                                 float *__restrict__ scales) {
+    const int li = threadIdx.x & 15;
+    const int tg = (T + FQ_BLOCKS - 1) / FQ_BLOCKS;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t m = u / tg * FQ_ROWS + (threadIdx.x >> 4);
+        const int t0 = (int)(u % tg) * FQ_BLOCKS;
+        if (m >= M)
+            continue;
+        const uint16_t *row = X + m * in;
+        uint4 v[FQ_BLOCKS];
+#pragma unroll
+        for (int b = 0; b < FQ_BLOCKS; ++b) {
+            const int64_t c = (int64_t)(t0 + b) * F8_BLOCK + 8 * li;
+            v[b] = c < in ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int b = 0; b < FQ_BLOCKS; ++b) {
+            const int64_t c = (int64_t)(t0 + b) * F8_BLOCK + 8 * li;
+            const uint32_t top = row16_max_u32(absmax8_f16(v[b]));
+            float scale, inv;
+            f8_scale_f16(top, scale, inv);
+            if (c < in)
+                *reinterpret_cast<uint2 *>(codes + m * in + c) = f8_codes8(v[b], inv);
+            if (li == 0 && t0 + b < T)
+                scales[(int64_t)(t0 + b) * M + m] = scale;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// weights: one workgroup per 128 x 128 block, held in 64 registers per thread
+// between the maximum and the codes, so W is read once.
+
+__global__ __launch_bounds__(FQ_THREADS) void encode_f8_kernel(const float *__restrict__ W, int out, int in, int T,
+                                                               uint8_t *__restrict__ codes,
+                                                               float *__restrict__ scales,
+                                                               int32_t *__restrict__ status) {
+    __shared__ uint32_t part[FQ_THREADS / RBQ_WAVE];
+    const int t = blockIdx.x % T, rb = blockIdx.x / T;
+    const int64_t c = (int64_t)t * F8_BLOCK + 4 * (threadIdx.x & 31);
+    const int64_t r0 = (int64_t)rb * F8_BLOCK + (threadIdx.x >> 5);
+    uint4 v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t r = r0 + 8 * i;
+        v[i] = r < out && c < in ? *reinterpret_cast<const uint4 *>(W + r * in + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t a = max(v[i].x & 0x7FFFFFFFu, v[i].y & 0x7FFFFFFFu);
+        const uint32_t b = max(v[i].z & 0x7FFFFFFFu, v[i].w & 0x7FFFFFFFu);
+        top = max(top, max(a, b));
+    }
+    top = wave_max_u32_dpp(top);
+    if ((threadIdx.x & (RBQ_WAVE - 1)) == 0)
+        part[threadIdx.x / RBQ_WAVE] = top;
+    __syncthreads();
+    top = max(max(part[0], part[1]), max(part[2], part[3]));
+    float scale, inv;
+    f8_scale_f32(top, scale, inv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t r = r0 + 8 * i;
+        if (r < out && c < in) {
+            int p = __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(v[i].x) * inv, __uint_as_float(v[i].y) * inv,
+                                                    0, false);
+            p = __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(v[i].z) * inv, __uint_as_float(v[i].w) * inv, p,
+                                                true);
+            *reinterpret_cast<uint32_t *>(codes + r * in + c) = inv == 0.0f ? 0u : (uint32_t)p;
+        }
+    }
+    if (threadIdx.x == 0) {
+        scales[(int64_t)rb * T + t] = scale;
+        if (status != nullptr && inv == 0.0f)
+            atomicOr(status, (int)RBQ_STATUS_NONFINITE_W);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one and few tokens: 16 rows of W on one side of the matrix instruction, 16
+// tokens on the other.  The codes are converted to fp16 (exact) after the
+// load and the sums of a block are fp32: here the read of W is what bounds,
+// and the conversions and the slower instruction hide behind it.  The four
+// sums of a lane take their two scales in four fmas per block.  The waves of
+// a workgroup split the blocks of 16 rows and add their partial sums through
+// LDS in wave order (the same order in every run).  Lane (i, g) holds bytes
+// 16g.. and 64 + 16g.. of row i of both operands: any assignment of columns
+// gives the same sum as long as both sides share it, and this one makes a
+// load 64 contiguous bytes per row.
+
+// The 32 bytes of lane group g of block t of a row; zero beyond the row.
+__device__ __forceinline__ v8i f8_fragment(const uint8_t *__restrict__ row, int t, int g, int in) {
+    const int64_t c = (int64_t)t * F8_BLOCK + 16 * g;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 lo = c < in ? *reinterpret_cast<const uint4 *>(row + c) : z;
+    const uint4 hi = c + 64 < in ? *reinterpret_cast<const uint4 *>(row + c + 64) : z;
+    return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+// The lane's four rows x NT token tiles of every wave, added in wave order by
+// the first waves, and written: token tile j of a lane is token 16 j + i.
+template <int NT, int WAVES, typename Y>
+__device__ __forceinline__ void f8_join(float *part, const v4f (&acc)[NT], int wave, int lane, int64_t r0, int out,
+                                        int64_t m0, int M, Y *__restrict__ y) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        *reinterpret_cast<v4f *>(&part[((j * WAVES + wave) * RBQ_WAVE + lane) * 4]) = acc[j];
+    __syncthreads();
+    for (int j = wave; j < NT; j += WAVES) {
+        v4f s = *reinterpret_cast<const v4f *>(&part[(j * WAVES * RBQ_WAVE + lane) * 4]);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            s += *reinterpret_cast<const v4f *>(&part[((j * WAVES + w) * RBQ_WAVE + lane) * 4]);
+        const int64_t m = m0 + 16 * j + (lane & 15);
+        const int64_t r = r0 + 4 * (lane >> 4);
+        if (m < M)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (r + v < out)
+                    y[m * out + r + v] = to_y<Y>(s[v]);
+    }
+}
+
+template <int NT, int WAVES, typename Y>
+__global__ __launch_bounds__(WAVES *RBQ_WAVE) void gemm_f8_few_kernel(
+    const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
+    const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, int64_t groups, Y *__restrict__ y) {
+    __shared__ __align__(16) float part[NT * WAVES * RBQ_WAVE * 4];
+    const int lane = threadIdx.x & (RBQ_WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
+    const int li = lane & 15, g = lane >> 4;
+    const int64_t r0 = (int64_t)blockIdx.x * 16;
+    const uint8_t *wrow = W + std::min(r0 + li, (int64_t)out - 1) * in;   // rows past the last: not written
+    const float *wsr = ws + r0 / F8_BLOCK * T;
+    for (int64_t gr = blockIdx.y; gr < groups; gr += gridDim.y) {
+        const int64_t m0 = gr * (16 * NT);
+        const uint8_t *xrow[NT];
+        int64_t mi[NT];
+        v4f acc[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            mi[j] = std::min(m0 + 16 * j + li, (int64_t)M - 1);
+            xrow[j] = X + mi[j] * in;
+            acc[j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        for (int t = wave; t < T; t += WAVES) {
+            v8h a[4], b[4];
+            f8_to_f16(f8_fragment(wrow, t, g, in), a);
+            const float sw = wsr[t];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                f8_to_f16(f8_fragment(xrow[j], t, g, in), b);
+                const float s = sw * xs[(int64_t)t * M + mi[j]];
+                acc[j] = f8_fma(f8_mma(a, b), s, acc[j]);
+            }
+        }
+        f8_join<NT, WAVES, Y>(part, acc, wave, lane, r0, out, m0, M, y);
+        __syncthreads();                     // the partial sums are read before the next group's
+    }
+}
+
+// One fp16 token, quantised by the wave that needs the block: lane l holds
+// columns 2l and 2l + 1, the maximum is a DPP reduction over the wave, and
+// the 128 codes pass through 128 bytes of LDS of the wave's own.  Only token
+// column 0 of the product is written; the other 15 repeat it.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES *RBQ_WAVE) void gemv_f8_kernel(const uint8_t *__restrict__ W,
+                                                                  const float *__restrict__ ws, int out, int in,
+                                                                  int T, const uint16_t *__restrict__ x,
+                                                                  uint16_t *__restrict__ y) {
+    __shared__ __align__(16) float part[WAVES * RBQ_WAVE * 4];
+    __shared__ __align__(16) uint16_t xq[WAVES][F8_BLOCK / 2];
+    const int lane = threadIdx.x & (RBQ_WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
+    const int li = lane & 15, g = lane >> 4;
+    const int64_t r0 = (int64_t)blockIdx.x * 16;
+    const uint8_t *wrow = W + std::min(r0 + li, (int64_t)out - 1) * in;
+    const float *wsr = ws + r0 / F8_BLOCK * T;
+    v4f acc[1] = {(v4f){0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int t = wave; t < T; t += WAVES) {
+        v8h a[4], b[4];
+        f8_to_f16(f8_fragment(wrow, t, g, in), a);
+        const float sw = wsr[t];
+        const int64_t c = (int64_t)t * F8_BLOCK + 2 * lane;
+        const uint32_t v = c < in ? *reinterpret_cast<const uint32_t *>(x + c) : 0u;
+        const uint32_t top = wave_max_u32_dpp(max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
+        float sx, inv;
+        f8_scale_f16(top, sx, inv);
+        const int p = __builtin_amdgcn_cvt_pk_fp8_f32(h2f((uint16_t)v) * inv, h2f((uint16_t)(v >> 16)) * inv, 0,
+                                                      false);
+        xq[wave][lane] = inv == 0.0f ? (uint16_t)0 : (uint16_t)p;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const uint4 lo = *reinterpret_cast<const uint4 *>(&xq[wave][8 * g]);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(&xq[wave][32 + 8 * g]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        f8_to_f16((v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w}, b);
+        acc[0] = f8_fma(f8_mma(a, b), sw * sx, acc[0]);
+    }
+    f8_join<1, WAVES, uint16_t>(part, acc, wave, lane, r0, out, 0, 1, y);
+}
+
+template <int NT, typename Y>
+hipError_t launch_few(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
+                      Y *y, hipStream_t st) {
+    constexpr int WAVES = 8;
+    const int64_t groups = ((int64_t)M + 16 * NT - 1) / (16 * NT);
+    const dim3 grid((unsigned)(((int64_t)out + 15) / 16), (unsigned)std::min<int64_t>(groups, 65535));
+    hipLaunchKernelGGL((gemm_f8_few_kernel<NT, WAVES, Y>), grid, dim3(WAVES * RBQ_WAVE), 0, st, W, ws, out, in,
+                       f8_blocks(in), X, xs, M, groups, y);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_f8(const uint16_t *X, int M, int in, uint8_t *codes, float *scales, hipStream_t st) {
+    const int T = f8_blocks(in);
+    const int64_t units = ((int64_t)M + FQ_ROWS - 1) / FQ_ROWS * ((T + FQ_BLOCKS - 1) / FQ_BLOCKS);
+    hipLaunchKernelGGL(quantize_f8_kernel, dim3((unsigned)std::min<int64_t>(units, 1 << 22)), dim3(FQ_THREADS), 0,
+                       st, X, M, in, T, units, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, float *scales, int32_t *status,
+                            hipStream_t st) {
+    const int T = f8_blocks(in);
+    hipLaunchKernelGGL(encode_f8_kernel, dim3((unsigned)T * (unsigned)f8_blocks(out)), dim3(FQ_THREADS), 0, st, W,
+                       out, in, T, codes, scales, status);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
+                          int M, void *y, int y_f32, hipStream_t st) {
+    if (y_f32)
+        return M <= 16 ? launch_few<1, float>(W, ws, out, in, X, xs, M, static_cast<float *>(y), st)
+                       : launch_few<4, float>(W, ws, out, in, X, xs, M, static_cast<float *>(y), st);
+    return M <= 16 ? launch_few<1, uint16_t>(W, ws, out, in, X, xs, M, static_cast<uint16_t *>(y), st)
+                   : launch_few<4, uint16_t>(W, ws, out, in, X, xs, M, static_cast<uint16_t *>(y), st);
+}
+
+hipError_t launch_gemv_f8(const uint8_t *W, const float *ws, int out, int in, const uint16_t *x, uint16_t *y,
+                          hipStream_t st) {
+    constexpr int WAVES = 8;
+    hipLaunchKernelGGL(gemv_f8_kernel<WAVES>, dim3((unsigned)(((int64_t)out + 15) / 16)), dim3(WAVES * RBQ_WAVE),
+                       0, st, W, ws, out, in, f8_blocks(in), x, y);
+    return hipGetLastError();
+}
+
+}  // namespace rbq

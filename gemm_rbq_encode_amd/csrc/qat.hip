@@ -391,6 +391,8 @@ hipError_t fill_zero(float *p, size_t n, hipStream_t st) {
 
 }  // namespace
 
+hipError_t launch_fill_zero_f32(float *Y, size_t n, hipStream_t st) { return fill_zero(Y, n, st); }
+
 bool qat_supports(int K) { return K >= 1 && K <= 4; }
 
 // Contraction slices of dX: enough workgroups for about two per compute
@@ -424,6 +426,19 @@ hipError_t launch_qat_encode(const float *W, int out, int in, int K, int group_s
     return hipGetLastError();
 }
 
+hipError_t launch_qat_dscales(const uint32_t *planes, int out, int in, int K, int group_size, const float *dW,
+                              float *dscales, hipStream_t st) {
+    const int G = group_size ? in / group_size : 1;
+    const dim3 grid((unsigned)(((long)out * G + QC_WAVES - 1) / QC_WAVES));
+    switch (K) {
+    case 1: hipLaunchKernelGGL(qat_dscales_kernel<1>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
+    case 2: hipLaunchKernelGGL(qat_dscales_kernel<2>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
+    case 3: hipLaunchKernelGGL(qat_dscales_kernel<3>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
+    default: hipLaunchKernelGGL(qat_dscales_kernel<4>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
+    }
+    return hipGetLastError();
+}
+
 hipError_t launch_qat_backward(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
                                int group_size, const uint16_t *X, const uint16_t *dY, int M, float *dX,
                                float *dW, float *dscales, void *workspace, size_t ws_bytes, int32_t *status,
@@ -440,18 +455,9 @@ hipError_t launch_qat_backward(const uint32_t *planes, const uint16_t *scales, i
         if (e != hipSuccess)
             return e;
     }
-    if (dscales != nullptr && out > 0 && in > 0) {
-        const int G = group_size ? in / group_size : 1;
-        const dim3 grid((unsigned)(((long)out * G + QC_WAVES - 1) / QC_WAVES));
-        switch (K) {
-        case 1: hipLaunchKernelGGL(qat_dscales_kernel<1>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
-        case 2: hipLaunchKernelGGL(qat_dscales_kernel<2>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
-        case 3: hipLaunchKernelGGL(qat_dscales_kernel<3>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
-        default: hipLaunchKernelGGL(qat_dscales_kernel<4>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
-        }
-        if ((e = hipGetLastError()) != hipSuccess)
-            return e;
-    }
+    if (dscales != nullptr && out > 0 && in > 0 &&
+        (e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st)) != hipSuccess)
+        return e;
     if (dX != nullptr && M > 0 && in > 0) {
         if (out == 0)
             return fill_zero(dX, (size_t)M * in, st);

@@ -113,6 +113,28 @@ hipError_t launch_qat_backward(const uint32_t *planes, const uint16_t *scales, i
                                float *dW, float *dscales, void *workspace, size_t ws_bytes, int32_t *status,
                                hipStream_t st);
 
+// Scale gradients from a given dW (the last step of launch_qat_backward).
+hipError_t launch_qat_dscales(const uint32_t *planes, int out, int in, int K, int group_size, const float *dW,
+                              float *dscales, hipStream_t st);
+
+// 8-bit activation checkpoints and the backward that reads them
+// (qat_ckpt.hip); out, in, M >= 1.
+hipError_t launch_qat_checkpoint(const uint16_t *X, int M, int in, int8_t *codes, uint16_t *scales,
+                                 hipStream_t st);
+hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
+                                    int group_size, const int8_t *x_codes, const uint16_t *x_scales,
+                                    const uint16_t *dY, int M, float *dX, float *dW, float *dscales,
+                                    void *workspace, size_t ws_bytes, int32_t *status, hipStream_t st);
+
+// Linears in 8-bit floating point blocks of 128 (f8.hip); out, in, M >= 1.
+hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, float *scales, int32_t *status,
+                            hipStream_t st);
+hipError_t launch_quantize_f8(const uint16_t *X, int M, int in, uint8_t *codes, float *scales, hipStream_t st);
+hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
+                          int M, void *y, int y_f32, hipStream_t st);
+hipError_t launch_gemv_f8(const uint8_t *W, const float *ws, int out, int in, const uint16_t *x, uint16_t *y,
+                          hipStream_t st);
+
 // Streaming-read probe (probe.hip): one launch reading `bytes` bytes.
 hipError_t launch_probe_read(const void *buf, size_t bytes, uint32_t *sink, hipStream_t st);
 
@@ -127,5 +149,6 @@ hipError_t launch_pack_scale_tiles(const uint16_t *scales, int K, int out, int i
 
 // Y = 0 for in_features == 0 (an empty sum).
 hipError_t launch_fill_zero_u16(uint16_t *Y, int64_t n, hipStream_t st);
+hipError_t launch_fill_zero_f32(float *Y, size_t n, hipStream_t st);
 
 }  // namespace rbq

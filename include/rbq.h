@@ -612,6 +612,127 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
                             size_t ws_bytes, int32_t *status, void *stream);
 
 /*
+ * 8-bit activation checkpoints.  Training keeps the input X of every layer
+ * for the weight gradient (RaBiT summary, section 4.2 and "RaBiT training"
+ * in section G: the shared weight takes the whole gradient); a checkpoint
+ * keeps it as int8 codes with one fp16 scale per token and block of 128
+ * columns, about half the bytes.
+ *   codes   int8 [M][in], row-major
+ *   scales  binary16 bits [M][T], T = ceil(in / 128); the last block is
+ *           shorter where in % 128 != 0
+ * For a block with A = max |x|:
+ *   s = A / 127 rounded up to binary16, at least 2^-24, at most 515.5
+ *   c = nearest integer of the exact x / s, ties to even, within -127 .. 127
+ * and a code stands for x^ = fp16(c s) (the exact product rounded once), so
+ * |x^ - x| <= s / 2 plus one binary16 rounding (maxima above 65468 lose up
+ * to 32 more).  A block with a NaN or infinite entry has scale NaN (0x7E00)
+ * and codes 0: all of its x^ are NaN.
+ *
+ * rbq_qat_checkpoint -- write the checkpoint of X.
+ *   X       device fp16 [M][in], 16-byte aligned (read only)
+ *   codes   device, 16-byte aligned, written;  scales  device, 2-byte
+ *           aligned, written.  They may not overlap X.
+ *   in_features  a multiple of 32;  M == 0 or in == 0 enqueues nothing
+ * Errors: RBQ_ERR_INVALID_ARG, RBQ_ERR_ALIGNMENT, RBQ_ERR_NO_DEVICE,
+ * RBQ_ERR_HIP.
+ */
+rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features, int8_t *codes, uint16_t *scales,
+                              void *stream);
+
+/*
+ * rbq_qat_backward_ckpt -- rbq_qat_backward from a checkpoint: the same
+ * gradients, with x^ in the place of X:
+ *   dW[r][j]       = sum_m dY[m][r] x^[m][j]          fp32 [out][in]
+ *   dscales, dX    as rbq_qat_backward (dX does not read the checkpoint)
+ * Each product of two fp16 numbers is exact and the sums are fp32, so dW
+ * carries no error beyond the checkpoint's own and the fp32 accumulation.
+ *   x_codes, x_scales  device, as rbq_qat_checkpoint wrote them; x_codes
+ *                      16-byte aligned, x_scales 2-byte aligned.  Needed with
+ *                      dW only.
+ *   dY       device fp16 [M][out], 2-byte aligned
+ *   workspace  device memory of rbq_qat_backward_ckpt_workspace_bytes(s, M)
+ *              bytes; rules as for rbq_qat_backward
+ * Other arguments, rules (any of dX, dW may be NULL; dscales needs dW) and
+ * errors as rbq_qat_backward.
+ */
+size_t rbq_qat_backward_ckpt_workspace_bytes(rbq_shape s, int32_t M);
+rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, rbq_shape s,
+                                 const int8_t *x_codes, const uint16_t *x_scales, const uint16_t *dY, int32_t M,
+                                 float *dX, float *dW, float *dscales, void *workspace, size_t ws_bytes,
+                                 int32_t *status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Linears in 8-bit floating point.
+ *
+ * The pages binarize the decoder's linears and leave others (the output
+ * head, a distillation teacher: RaBiT summary, sections 4.1 and 5) at higher
+ * precision.  These calls serve such a layer Y = X W^T at one byte a weight:
+ * OCP e4m3 codes (4 significant bits, largest value 448) with one fp32 scale
+ * per block of 128,
+ *   W   codes uint8 [out][in], scales fp32 [ceil(out/128)][T]: one per block
+ *       of 128 rows x 128 columns
+ *   X   codes uint8 [M][in],   scales fp32 [T][M]: one per token and block of
+ *       128 columns (a block's scales of all tokens side by side)
+ * with T = ceil(in / 128); blocks at the edges are smaller.  A value is its
+ * code times its scale.  in_features is a multiple of 32 throughout.
+ * The transposed layer (dX = dY W) is the product with the transposed codes
+ * and the transposed scales: blocks of 128 x 128 stay blocks (out must then
+ * be a multiple of 32).
+ *
+ * Quantisation of a block with A = max |v|, taken as at least 2^-100:
+ *   scale = fl32(A / 448),  code = e4m3(fl32(v * fl32(448 / A))),
+ * every rounding to nearest even.  A block with a NaN or infinite entry has
+ * scale NaN and codes 0.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * rbq_encode_f8 -- codes and scales of a weight.
+ *   W       device fp32 [out][in], 16-byte aligned (read only)
+ *   codes   device, 16-byte aligned, written;  scales  device, 4-byte
+ *           aligned, written
+ *   status_dev  device int32 or NULL: RBQ_STATUS_NONFINITE_W is OR-ed in
+ * out == 0 or in == 0 enqueues nothing.  Errors: RBQ_ERR_INVALID_ARG,
+ * RBQ_ERR_ALIGNMENT, RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
+ */
+rbq_status rbq_encode_f8(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes, float *scales,
+                         int32_t *status_dev, void *stream);
+
+/* rbq_quantize_f8 -- codes and scales of M tokens: X device fp16 [M][in],
+ * 16-byte aligned; otherwise as rbq_encode_f8. */
+rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, uint8_t *codes, float *scales,
+                           void *stream);
+
+/* Output types of rbq_gemm_f8. */
+#define RBQ_Y_F16 0u
+#define RBQ_Y_F32 1u
+
+/*
+ * rbq_gemm_f8 -- the product of M quantised tokens:
+ *   Y[m][r] = sum_t xs[t][m] ws[r/128][t] sum_{j in block t} x[m][j] w[r][j]
+ * over the codes' values; the products are exact, the sums fp32, each output
+ * is rounded once to its type.
+ *   codes, scales      the layer; codes 16-byte, scales 4-byte aligned
+ *   x_codes, x_scales  the tokens; x_codes 16-byte, x_scales 4-byte aligned
+ *   M       tokens, >= 0 (0 enqueues nothing)
+ *   Y       device [M][out], written: binary16 (RBQ_Y_F16, 2-byte aligned) or
+ *           fp32 (RBQ_Y_F32, 4-byte aligned)
+ * in == 0 writes Y = 0.  Errors: RBQ_ERR_INVALID_ARG (an unknown y_type among
+ * them), RBQ_ERR_ALIGNMENT, RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
+ */
+rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
+                       const uint8_t *x_codes, const float *x_scales, int32_t M, void *Y, uint32_t y_type,
+                       void *stream);
+
+/*
+ * rbq_gemv_f8 -- one decode token, fp16 in and out, in one launch:
+ * rbq_quantize_f8 of x and rbq_gemm_f8 with M = 1 (the fp32 sums are added
+ * in another order).  x device fp16 [in], 16-byte aligned; y device fp16
+ * [out], 2-byte aligned, written.  Errors as rbq_gemm_f8.
+ */
+rbq_status rbq_gemv_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
+                       const uint16_t *x, uint16_t *y, void *stream);
+
+/*
  * rbq_probe_read -- measurement aid, not a step of the method: one launch that
  * reads `bytes` bytes at `buf` from device memory with 16-byte non-temporal
  * loads and discards them, so that a GEMV launch can be compared with a plain

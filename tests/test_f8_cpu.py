@@ -1,0 +1,205 @@
+"""Host-side checks of the 8-bit block operators: the oracle (oracle/f8.py)
+against closed forms and against torch's own e4m3 and fp16 types, and the
+arguments that the C ABI and the binding refuse before anything is launched."""
+import numpy as np
+import pytest
+import torch
+
+import gemm_rbq_encode_amd as rbq
+import workloads
+from oracle import f8
+
+pytestmark = pytest.mark.cpu
+
+
+def test_e4m3_table_is_torchs():
+    t = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(f8.e4m3_table(), t)
+
+
+def test_e4m3_rounding_is_torchs():
+    rng = np.random.default_rng(1)
+    tab = f8.e4m3_table()[:0x7F]
+    mids = (tab[1:] + tab[:-1]) / 2                         # every tie
+    v = np.concatenate([tab, mids, np.nextafter(mids, 0), np.nextafter(mids, 500), rng.uniform(0, 448, 5000),
+                        2.0 ** rng.uniform(-14, 8, 5000)]).astype(np.float32)
+    v = np.concatenate([v, -v])
+    want = torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(f8.e4m3_codes(v.astype(np.float64)), want)
+
+
+def test_block_scale_and_error():
+    """The largest entry takes +-448 and every value is within half a step:
+    2^-4 of itself, or half of the format's smallest step 2^-9 of the scale
+    (plus the fp32 roundings of the two quotients and of the product)."""
+    W = workloads.gaussian_weight(130, 288, 3, outliers=True)
+    codes, scales = f8.encode(W)
+    assert scales.shape == (2, 3) and codes.shape == W.shape
+    v = f8.values(codes, scales, 128)
+    s = np.repeat(np.repeat(scales, 128, 0)[:130], 128, 1)[:, :288].astype(np.float64)
+    assert (np.abs(v - W) <= (1 + 2.0 ** -21) * np.maximum(np.abs(W) * 2.0 ** -4, s * 2.0 ** -10)
+            + np.abs(W) * 2.0 ** -21).all()
+    for i in range(2):
+        for t in range(3):
+            b = codes[128 * i:128 * i + 128, 128 * t:128 * t + 128] & 0x7F
+            assert b.max() == 0x7E
+    zero, sz = f8.encode(np.zeros((3, 32), np.float32))
+    assert not zero.any() and sz[0, 0] == np.float32(2.0 ** -100 / 448)
+    bad = W.copy()
+    bad[0, 130] = np.inf
+    c, s2 = f8.encode(bad)
+    assert np.isnan(s2[0, 1]) and not c[:128, 128:256].any() and np.isfinite(np.delete(s2.ravel(), 1)).all()
+
+
+def test_checkpoint_of_every_fp16_maximum():
+    """For every finite fp16 maximum: the scale is the smallest allowed one,
+    the value restored for it is finite and within half a step of it."""
+    A = np.arange(0x7C00, dtype=np.uint16)
+    X = np.zeros((len(A), 32), np.uint16)
+    X[:, 5] = A
+    X[:, 6] = A | 0x8000
+    X[:, 7] = A // 2
+    codes, scales = f8.checkpoint(X)
+    s = scales[:, 0].view(np.float16).astype(np.float64)
+    a = A.view(np.float16).astype(np.float64)
+    assert (s >= 2.0 ** -24).all() and (s <= 515.5).all()
+    capped = a / 127 > 515.5
+    assert (s[~capped] * 127 >= a[~capped]).all() and capped.sum() == 2   # 65472, 65504
+    x = f8.restore(codes, scales).view(np.float16).astype(np.float64)
+    v = X.view(np.float16).astype(np.float64)
+    assert np.isfinite(x).all()
+    step = np.where(capped, 64.0, s)[:, None]               # beyond the cap: 32 lost, and one rounding
+    assert (np.abs(x - v) <= step / 2 + np.abs(v) * 2.0 ** -11 + 2.0 ** -25).all()
+    tiny = a <= 127 * 2.0 ** -24
+    assert (x[tiny] == v[tiny]).all()
+
+
+def test_checkpoint_quotients_stay_off_the_borders():
+    """A quotient x / s that is no tie is at least 2^-12 from a half-integer:
+    the codes do not depend on how the quotient is computed."""
+    rng = np.random.default_rng(2)
+    s = rng.integers(1, 0x6008, 20000).astype(np.uint16).view(np.float16).astype(np.float64)
+    k = rng.integers(0, 127, 20000) + 0.5
+    near = (s * k).astype(np.float16).astype(np.float64)
+    for v in (near, np.nextafter(near.astype(np.float16), np.float16(0)).astype(np.float64)):
+        q = v / s
+        ok = (q >= 0.25) & (q <= 127)
+        d = np.abs(q - (np.floor(q) + 0.5))[ok]
+        assert ((d == 0) | (d >= 2.0 ** -12)).all()
+
+
+def test_checkpoint_of_non_finite_blocks():
+    X = workloads.gaussian_activations(3, 288, 4).copy()
+    X[1, 200] = 0x7C00
+    X[2, 0] = 0x7E01
+    codes, scales = f8.checkpoint(X)
+    x = f8.restore(codes, scales).view(np.float16)
+    assert np.isnan(x[1, 128:256]).all() and np.isnan(x[2, :128]).all()
+    assert np.isfinite(x[0]).all() and np.isfinite(x[1, :128]).all() and np.isfinite(x[1, 256:]).all()
+
+
+OK = 0x10000   # an aligned stand-in address: checks never dereference it
+
+
+def test_f8_argument_errors():
+    L, E = rbq.lib(), rbq
+    bad, al = E.RBQ_ERR_INVALID_ARG, E.RBQ_ERR_ALIGNMENT
+    assert L.rbq_encode_f8(None, 8, 64, OK, OK, None, None) == bad
+    assert L.rbq_encode_f8(OK, 8, 64, None, OK, None, None) == bad
+    assert L.rbq_encode_f8(OK, 8, 64, OK, None, None, None) == bad
+    assert L.rbq_encode_f8(OK, -1, 64, OK, OK, None, None) == bad
+    assert L.rbq_encode_f8(OK, 8, 48, OK, OK, None, None) == bad
+    assert L.rbq_encode_f8(OK, 8, -32, OK, OK, None, None) == bad
+    assert L.rbq_encode_f8(OK + 8, 8, 64, OK, OK, None, None) == al
+    assert L.rbq_encode_f8(OK, 8, 64, OK + 8, OK, None, None) == al
+    assert L.rbq_encode_f8(OK, 8, 64, OK, OK + 2, None, None) == al
+    assert L.rbq_encode_f8(OK, 8, 64, OK, OK, OK + 2, None) == al
+    assert L.rbq_encode_f8(None, 0, 64, None, None, None, None) == E.RBQ_OK
+    assert L.rbq_encode_f8(None, 8, 0, None, None, None, None) == E.RBQ_OK
+    assert L.rbq_quantize_f8(None, 2, 64, OK, OK, None) == bad
+    assert L.rbq_quantize_f8(OK, -1, 64, OK, OK, None) == bad
+    assert L.rbq_quantize_f8(OK, 2, 33, OK, OK, None) == bad
+    assert L.rbq_quantize_f8(OK + 2, 2, 64, OK, OK, None) == al
+    assert L.rbq_quantize_f8(OK, 2, 64, OK + 4, OK, None) == al
+    assert L.rbq_quantize_f8(None, 0, 64, None, None, None) == E.RBQ_OK
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 2, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, -2, OK, 0, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 40, OK, OK, 2, OK, 0, None) == bad
+    for k in (0, 1, 4, 5, 7):
+        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None]
+        a[k] = None
+        assert L.rbq_gemm_f8(*a) == bad, k
+    for k, off in ((0, 8), (1, 2), (4, 8), (5, 2), (7, 1)):
+        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None]
+        a[k] = OK + off
+        assert L.rbq_gemm_f8(*a) == al, k
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK + 2, 1, None) == al
+    assert L.rbq_gemm_f8(None, None, 8, 64, None, None, 0, None, 0, None) == E.RBQ_OK
+    assert L.rbq_gemm_f8(None, None, 0, 64, None, None, 3, None, 0, None) == E.RBQ_OK
+    for k in (0, 1, 4, 5):
+        a = [OK, OK, 8, 64, OK, OK, None]
+        a[k] = None
+        assert L.rbq_gemv_f8(*a) == bad, k
+    for k, off in ((0, 8), (1, 2), (4, 8), (5, 1)):
+        a = [OK, OK, 8, 64, OK, OK, None]
+        a[k] = OK + off
+        assert L.rbq_gemv_f8(*a) == al, k
+    assert L.rbq_gemv_f8(OK, OK, 8, 20, OK, OK, None) == bad
+    assert L.rbq_gemv_f8(None, None, 0, 64, None, None, None) == E.RBQ_OK
+
+
+def test_checkpoint_argument_errors():
+    L, E = rbq.lib(), rbq
+    bad, al = E.RBQ_ERR_INVALID_ARG, E.RBQ_ERR_ALIGNMENT
+    assert L.rbq_qat_checkpoint(None, 2, 64, OK, OK, None) == bad
+    assert L.rbq_qat_checkpoint(OK, 2, 64, None, OK, None) == bad
+    assert L.rbq_qat_checkpoint(OK, 2, 64, OK, None, None) == bad
+    assert L.rbq_qat_checkpoint(OK, 2, 63, OK, OK, None) == bad
+    assert L.rbq_qat_checkpoint(OK, -2, 64, OK, OK, None) == bad
+    assert L.rbq_qat_checkpoint(OK + 8, 2, 64, OK, OK, None) == al
+    assert L.rbq_qat_checkpoint(OK, 2, 64, OK + 8, OK, None) == al
+    assert L.rbq_qat_checkpoint(OK, 2, 64, OK, OK + 1, None) == al
+    assert L.rbq_qat_checkpoint(None, 0, 64, None, None, None) == E.RBQ_OK
+    s = rbq.shape(64, 128, 2, 0)
+    ok = [OK, OK, s, OK, OK, OK, 4, OK, OK, OK, None, 0, None, None]
+
+    def call(**change):
+        a = list(ok)
+        for k, v in change.items():
+            a[int(k[1:])] = v
+        return L.rbq_qat_backward_ckpt(*a)
+
+    assert call(_2=rbq.shape(64, 100, 2, 0)) == bad
+    assert call(_2=rbq.shape(64, 128, 5, 0)) == E.RBQ_ERR_UNSUPPORTED
+    assert call(_6=-1) == bad
+    assert call(_8=None) == bad                       # dscales without dW
+    assert call(_11=64) == bad                        # a workspace size without one
+    for k in ("_0", "_1", "_3", "_4", "_5"):
+        assert call(**{k: None}) == bad, k
+    for k, off in (("_0", 2), ("_1", 1), ("_3", 8), ("_4", 1), ("_5", 1), ("_7", 2), ("_8", 2), ("_9", 2), ("_12", 2)):
+        assert call(**{k: OK + off}) == al, k
+    assert call(_7=None, _8=None, _9=None) == E.RBQ_OK
+    assert L.rbq_qat_backward_ckpt_workspace_bytes(rbq.shape(64, 100, 2, 0), 4) == 0
+    assert L.rbq_qat_backward_ckpt_workspace_bytes(s, 0) == 0
+
+
+def test_binding_refuses_host_tensors_and_types():
+    f = torch.zeros(4, 64)
+    for call in (lambda: rbq.encode_f8(f), lambda: rbq.quantize_f8(f.half()), lambda: rbq.qat_checkpoint(f.half()),
+                 lambda: rbq.gemv_f8(f.to(torch.float8_e4m3fn), f, f.half()),
+                 lambda: rbq.gemm_f8(f.to(torch.float8_e4m3fn), f, f.to(torch.float8_e4m3fn), f)):
+        with pytest.raises(TypeError):
+            call()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="only meaningful without a GPU")
+def test_valid_calls_without_a_device():
+    L, none = rbq.lib(), rbq.RBQ_ERR_NO_DEVICE
+    assert L.rbq_encode_f8(OK, 8, 64, OK, OK, None, None) == none
+    assert L.rbq_quantize_f8(OK, 2, 64, OK, OK, None) == none
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 0, None) == none
+    assert L.rbq_gemm_f8(None, None, 8, 0, None, None, 2, OK, 1, None) == none
+    assert L.rbq_gemv_f8(OK, OK, 8, 64, OK, OK, None) == none
+    assert L.rbq_qat_checkpoint(OK, 2, 64, OK, OK, None) == none
+    s = rbq.shape(64, 128, 2, 0)
+    assert L.rbq_qat_backward_ckpt(OK, OK, s, OK, OK, OK, 4, OK, OK, OK, None, 0, None, None) == none
