@@ -267,6 +267,8 @@ hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, flo
 
 hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
                           int M, void *y, int y_f32, hipStream_t st) {
+    if (M > 64 && gemm_f8_tile_supports(out, in, M))
+        return launch_gemm_f8_tile(W, ws, out, in, X, xs, M, y, y_f32, st);
     if (y_f32)
         return M <= 16 ? launch_few<1, float>(W, ws, out, in, X, xs, M, static_cast<float *>(y), st)
                        : launch_few<4, float>(W, ws, out, in, X, xs, M, static_cast<float *>(y), st);

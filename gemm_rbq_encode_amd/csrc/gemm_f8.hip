@@ -1,0 +1,288 @@
+// gemm_f8.hip -- the many-token product of a layer in 8-bit floating point
+// blocks of 128:
+//   Y[m][r] = sum_t xs[t][m] ws[r/128][t] sum_{j in block t} x[m][j] w[r][j]
+//
+// A workgroup computes a tile of RT rows of W by CT tokens, one block of 128
+// columns per stage.  Both operands of a stage pass through LDS by direct
+// global-to-LDS loads of 16 bytes a lane, two buffers deep: the next stage is
+// requested before the current one is computed, and one barrier per stage
+// both publishes it and frees the buffer that was read.  The loads are inline
+// assembly without register results and their waits are explicit (the
+// compiler would wait for them before every LDS read).
+//
+// LDS holds rows of 128 bytes without padding (a load instruction fills 1 KB
+// in lane order); the 16-byte piece q of row r lies at position q ^ (r & 7),
+// so that the fragment reads of 8 rows of one piece hit all banks once.  The
+// swizzle is applied to the addresses that are loaded from.
+//
+// Rows and tokens past the end repeat the last one (every element of the
+// result depends on its own row and token only) and are not written.  A short
+// last block is loaded through registers, zero past the end on both sides.
+//
+// Two kinds of sums inside a block:
+//  * fp16 outputs: v_mfma_f32_16x16x128_f8f6f4, one instruction per 16 x 16
+//    x 128 products.  Measured here: of the 8 products of 8 consecutive
+//    columns the instruction keeps what is at least 2^-13 of the power of two
+//    below the largest (each of the others is cut towards zero there), and
+//    adds the groups in fp32.  A group is off by less than 7 * 2^-13 of its
+//    largest product, about a seventieth of the 2^-4 that an e4m3 operand is
+//    off itself; it buys twice the rate of the fp16 instruction.
+//  * fp32 outputs: the codes converted to fp16 (exact) in registers and
+//    v_mfma_f32_16x16x32_f16: exact products, fp32 sums.
+// Either way the block's sums are scaled by xs ws in one fp32 fma each.
+#include <algorithm>
+
+#include "rbq.h"
+#include "rbq_device.h"
+#include "rbq_kernels.h"
+#include "f8_device.h"
+
+namespace rbq {
+
+namespace {
+
+__device__ __forceinline__ uint32_t f8_lds_addr(const void *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 bytes from base + voff to LDS [m0 + 16 lane].  M0 is set here; nothing
+// else in this kernel reads it.
+__device__ __forceinline__ void f8_load_lds(const void *base, uint32_t voff, uint32_t m0) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
+}
+
+// Waves WM x WN, each TM x TN tiles of 16 x 16.
+template <int WM, int WN, int TM, int TN, typename Y>
+__global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
+    const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
+    const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, Y *__restrict__ y, int tiles_m, int total) {
+    constexpr bool HALF = sizeof(Y) == 2;
+    constexpr int WAVES = WM * WN;
+    constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
+    constexpr int STAGE = (RT + CT) * F8_BLOCK;
+    constexpr int LW = RT / 8 / WAVES, LX = CT / 8 / WAVES;      // 1 KB loads of a wave and stage
+    static_assert(LW * 8 * WAVES == RT && LX * 8 * WAVES == CT, "tile rows per wave load");
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int lane = threadIdx.x & (RBQ_WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
+    const int wr = wave % WM, wc = wave / WM;
+    const int li = lane & 15, g = lane >> 4;
+
+    // each XCD (consecutive workgroups go to consecutive XCDs) takes a run of
+    // tiles, tokens fastest: the workgroups of one L2 share rows and tokens
+    int id = blockIdx.x;
+    const int per = total >> 3;
+    if (id < per * 8)
+        id = (id & 7) * per + (id >> 3);
+    const int64_t r0 = (int64_t)(id / tiles_m) * RT, m0 = (int64_t)(id % tiles_m) * CT;
+
+    const uint8_t *wbase = W + r0 * in, *xbase = X + m0 * in;
+    const int rlast = (int)std::min<int64_t>(out - 1 - r0, RT - 1), mlast = (int)std::min<int64_t>(M - 1 - m0, CT - 1);
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);   // the piece stored at this lane's place
+    uint32_t woff[LW], xoff[LX];
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+        woff[i] = (uint32_t)std::min((wave * LW + i) * 8 + (lane >> 3), rlast) * (uint32_t)in + piece;
+#pragma unroll
+    for (int i = 0; i < LX; ++i)
+        xoff[i] = (uint32_t)std::min((wave * LX + i) * 8 + (lane >> 3), mlast) * (uint32_t)in + piece;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(f8_lds_addr(lds));
+
+    const int full = in / F8_BLOCK;
+    // request stage t: wave-uniform LDS places, W rows first
+    auto issue = [&](int t) {
+        const uint32_t at = lds0 + (uint32_t)(t & 1) * STAGE;
+        const uint8_t *wb = wbase + (int64_t)t * F8_BLOCK, *xb = xbase + (int64_t)t * F8_BLOCK;
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            f8_load_lds(wb, woff[i], at + (uint32_t)(wave * LW + i) * 1024u);
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            f8_load_lds(xb, xoff[i], at + (uint32_t)(RT * F8_BLOCK) + (uint32_t)(wave * LX + i) * 1024u);
+    };
+    // the short last block, through registers
+    auto stage_tail = [&](int t) {
+        unsigned char *at = lds + (t & 1) * STAGE;
+        const bool ok = (int)piece < in - t * F8_BLOCK;
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            *reinterpret_cast<uint4 *>(at + (wave * LW + i) * 1024 + lane * 16) =
+                ok ? *reinterpret_cast<const uint4 *>(wbase + (int64_t)t * F8_BLOCK + woff[i]) : z;
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            *reinterpret_cast<uint4 *>(at + RT * F8_BLOCK + (wave * LX + i) * 1024 + lane * 16) =
+                ok ? *reinterpret_cast<const uint4 *>(xbase + (int64_t)t * F8_BLOCK + xoff[i]) : z;
+    };
+
+    // scales of a stage: one per token tile and lane, one per wave (its rows
+    // lie in one block of 128)
+    const float *xsp = xs + m0;
+    int sidx[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        sidx[j] = std::min((wc * TN + j) * 16 + li, mlast);
+    const float *wsp = ws + std::min<int64_t>(r0 + wr * TM * 16, out - 1) / F8_BLOCK * T;
+
+    v4f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+
+    // fragment of 16 rows starting at row `row` of an operand: pieces g and
+    // g + 4 of the lane's row (the same ones on both sides)
+    const uint32_t rd_lo = (uint32_t)(li * F8_BLOCK + ((g ^ (li & 7)) * 16));
+    const uint32_t rd_hi = (uint32_t)(li * F8_BLOCK + (((g + 4) ^ (li & 7)) * 16));
+    auto fragment = [&](const unsigned char *at, int row) {
+        const uint4 lo = *reinterpret_cast<const uint4 *>(at + row * F8_BLOCK + rd_lo);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(at + row * F8_BLOCK + rd_hi);
+        return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+
+    float sx[TN], sw;
+    auto load_scales = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            sx[j] = xsp[(int64_t)t * M + sidx[j]];
+        sw = wsp[t];
+    };
+
+    auto compute = [&](int t, const float (&s)[TN]) {
+        const unsigned char *wa = lds + (t & 1) * STAGE + wr * TM * 16 * F8_BLOCK;
+        const unsigned char *xa = lds + (t & 1) * STAGE + (RT + wc * TN * 16) * F8_BLOCK;
+        if constexpr (HALF) {
+            v8i b[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                b[j] = fragment(xa, 16 * j);
+            v8i a = fragment(wa, 0);
+            v4f p[2][TN];
+            // the sums of row tile i are scaled between the products of i + 1
+#pragma unroll
+            for (int i = 0; i <= TM; ++i) {
+                v8i an = a;
+                if (i + 1 < TM)
+                    an = fragment(wa, 16 * (i + 1));
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    if (i < TM) {
+                        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                        p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[j], z, 0, 0, 0, 0, 0, 0);
+                    }
+                    if (i > 0)
+                        acc[i - 1][j] = f8_fma(p[(i - 1) & 1][j], s[j], acc[i - 1][j]);
+                }
+                a = an;
+            }
+        } else {
+            v8h b[TN][4];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                f8_to_f16(fragment(xa, 16 * j), b[j]);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                v8h a[4];
+                f8_to_f16(fragment(wa, 16 * i), a);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = f8_fma(f8_mma(a, b[j]), s[j], acc[i][j]);
+            }
+        }
+    };
+
+    if (full > 0)
+        issue(0);
+    else
+        stage_tail(0);
+    load_scales(0);
+    for (int t = 0; t < T; ++t) {
+        float s[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            s[j] = sx[j] * sw;                          // (the compiler's wait for the scales goes here)
+            asm volatile("" : "+v"(s[j]));
+        }
+        // stage t has landed, and stage t - 1 is no longer read, in every wave
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (t + 1 < T) {
+            if (t + 1 < full)
+                issue(t + 1);
+            else
+                stage_tail(t + 1);
+            load_scales(t + 1);
+        }
+        compute(t, s);
+    }
+
+    // lane (li, g) holds rows 4 g + v of the row tile and token li of the token tile
+    const bool vec = (out & 3) == 0 && ((uintptr_t)y & (4 * sizeof(Y) - 1)) == 0;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int64_t m = m0 + (wc * TN + j) * 16 + li;
+        if (m >= M)
+            continue;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int64_t r = r0 + (wr * TM + i) * 16 + 4 * g;
+            Y *p = y + m * out + r;
+            if (vec && r < out) {
+                if constexpr (HALF)
+                    *reinterpret_cast<uint2 *>(p) =
+                        make_uint2((uint32_t)f2h(acc[i][j][0]) | (uint32_t)f2h(acc[i][j][1]) << 16,
+                                   (uint32_t)f2h(acc[i][j][2]) | (uint32_t)f2h(acc[i][j][3]) << 16);
+                else
+                    *reinterpret_cast<v4f *>(p) = acc[i][j];
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (r + v < out)
+                        p[v] = to_y<Y>(acc[i][j][v]);
+            }
+        }
+    }
+}
+
+template <int WM, int WN, int TM, int TN, typename Y>
+hipError_t launch_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
+                       Y *y, hipStream_t st) {
+    constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
+    constexpr size_t LDS = 2 * (RT + CT) * F8_BLOCK;
+    auto kernel = gemm_f8_tile_kernel<WM, WN, TM, TN, Y>;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    if (e != hipSuccess)
+        return e;
+    const int64_t tiles_m = ((int64_t)M + CT - 1) / CT, total = tiles_m * (((int64_t)out + RT - 1) / RT);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(WM * WN * RBQ_WAVE), LDS, st, W, ws, out, in,
+                       f8_blocks(in), X, xs, M, y, (int)tiles_m, (int)total);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Byte offsets inside a tile are 32-bit and the tiles are numbered in 31 bits.
+bool gemm_f8_tile_supports(int out, int in, int M) {
+    return in <= (1 << 23) && ((int64_t)out / 128 + 1) * ((int64_t)M / 128 + 1) < (1 << 30);
+}
+
+// Large tiles where they fill the 256 compute units at least once, else tiles
+// of 128 x 128.  fp16 outputs, measured at 8192 rows,
+// 8192 columns, 4096 tokens (512 large tiles): 302 us against 366; at 5003
+// rows, 4128 columns, 777 tokens (80 large, 280 small tiles): 82 against 53.
+hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
+                               int M, void *y, int y_f32, hipStream_t st) {
+    const int rt = y_f32 ? 128 : 256;
+    const bool large = ((int64_t)out + rt - 1) / rt * (((int64_t)M + 255) / 256) >= (y_f32 ? 150 : 200);
+    if (y_f32) {
+        float *o = static_cast<float *>(y);
+        return large ? launch_tile<2, 4, 4, 4, float>(W, ws, out, in, X, xs, M, o, st)
+                     : launch_tile<2, 2, 4, 4, float>(W, ws, out, in, X, xs, M, o, st);
+    }
+    uint16_t *o = static_cast<uint16_t *>(y);
+    return large ? launch_tile<2, 4, 8, 4, uint16_t>(W, ws, out, in, X, xs, M, o, st)
+                 : launch_tile<2, 2, 4, 4, uint16_t>(W, ws, out, in, X, xs, M, o, st);
+}
+
+}  // namespace rbq

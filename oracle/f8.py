@@ -98,6 +98,20 @@ def gemm(codes, scales, x_codes, x_scales):
     return x @ w.T, np.abs(x) @ np.abs(w).T
 
 
+def largest_products(codes, scales, x_codes, x_scales):
+    """Sum over the groups of 8 columns of the largest |x w| of a group,
+    float64 [M][out]."""
+    w = np.abs(values(codes, scales, BLOCK))
+    x = np.abs(values(x_codes, np.ascontiguousarray(x_scales.T), 1))
+    total = np.zeros((x.shape[0], w.shape[0]))
+    for c in range(0, w.shape[1], 8):
+        top = np.zeros_like(total)
+        for j in range(c, c + 8):
+            np.maximum(top, np.outer(x[:, j], w[:, j]), out=top)
+        total += top
+    return total
+
+
 def checkpoint(X: np.ndarray):
     """fp16 bits [M][in] -> (codes int8 [M][in], scale bits uint16 [M][T])."""
     M, inf = X.shape

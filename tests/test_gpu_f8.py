@@ -8,6 +8,10 @@ each block, the joining of partial sums), each at most 2^-23 (a matrix
 instruction may cut instead of round):
   fp32:  |err| <= n 2^-23 S
   fp16:  the same, and one rounding: 2^-11 (|y| + n 2^-23 S) + 2^-25
+More than 64 tokens with fp16 outputs take the 8-bit matrix instruction, which
+cuts the products of 8 columns at 2^-13 of the power of two below the largest:
+the other 7 lose less than that each, so an output is off by up to 7 2^-13 of
+the sum of the groups' largest products more.
 """
 import numpy as np
 import pytest
@@ -52,9 +56,9 @@ def same_scales(got, want):
         np.array_equal(bits32(np.nan_to_num(got, nan=1.0)), bits32(np.nan_to_num(want, nan=1.0)))
 
 
-def tolerance(S, y, inf, half):
+def tolerance(S, y, inf, half, cut=0.0):
     n = inf + 3 * (-(-inf // 128)) + 16
-    t = n * 2.0 ** -23 * S
+    t = n * 2.0 ** -23 * S + 7 * 2.0 ** -13 * cut
     return 2.0 ** -11 * (np.abs(y) + t) + 2.0 ** -25 + t if half else t
 
 
@@ -141,7 +145,7 @@ def test_gemm_matches_the_oracle(out, M, inf, half):
     torch.cuda.synchronize()
     assert got is Y
     err = np.abs(Y.cpu().numpy().astype(np.float64) - y_ref)
-    tol = tolerance(S, y_ref, inf, half)
+    tol = tolerance(S, y_ref, inf, half, f8.largest_products(w8, ws, x8, xs) if half and M > 64 else 0.0)
     assert (err <= tol).all(), f"{(err / tol).max():.3f} of the tolerance at {np.unravel_index((err / tol).argmax(), err.shape)}"
     assert torch.equal(Y, again)                           # the same bits in every run
 
