@@ -714,9 +714,10 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
 }
 
 size_t rbq_qat_backward_ckpt_workspace_bytes(rbq_shape s, int32_t M) {
-    if (rbq_check_shape(s) != RBQ_OK || M < 1)
+    if (rbq_check_shape(s) != RBQ_OK || !rbq::qat_supports(s.num_planes) || M < 1 || s.out_features == 0 ||
+        s.in_features == 0)
         return 0;
-    return rbq::qat_backward_workspace_bytes(M, s.out_features, s.in_features);
+    return rbq::qat_backward_ckpt_workspace_bytes(M, s.out_features, s.in_features, s.num_planes, s.group_size);
 }
 
 rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, rbq_shape s,

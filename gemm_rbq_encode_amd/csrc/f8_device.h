@@ -12,6 +12,14 @@ constexpr float F8_MAX = 448.0f;
 
 inline __host__ __device__ int f8_blocks(int n) { return (n >> 7) + ((n & 127) != 0); }
 
+// Tile of workgroup `id` of `total`: consecutive workgroups go to consecutive
+// XCDs, so each of the 8 takes a run of consecutive tiles, which share
+// operands in its L2.
+__device__ __forceinline__ int xcd_run(int id, int total) {
+    const int per = total >> 3;
+    return id < per * 8 ? (id & 7) * per + (id >> 3) : id;
+}
+
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));

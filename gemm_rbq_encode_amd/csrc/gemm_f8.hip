@@ -68,12 +68,7 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
     const int wr = wave % WM, wc = wave / WM;
     const int li = lane & 15, g = lane >> 4;
 
-    // each XCD (consecutive workgroups go to consecutive XCDs) takes a run of
-    // tiles, tokens fastest: the workgroups of one L2 share rows and tokens
-    int id = blockIdx.x;
-    const int per = total >> 3;
-    if (id < per * 8)
-        id = (id & 7) * per + (id >> 3);
+    const int id = xcd_run(blockIdx.x, total);       // tokens fastest
     const int64_t r0 = (int64_t)(id / tiles_m) * RT, m0 = (int64_t)(id % tiles_m) * CT;
 
     const uint8_t *wbase = W + r0 * in, *xbase = X + m0 * in;

@@ -121,6 +121,7 @@ hipError_t launch_qat_dscales(const uint32_t *planes, int out, int in, int K, in
 // (qat_ckpt.hip); out, in, M >= 1.
 hipError_t launch_qat_checkpoint(const uint16_t *X, int M, int in, int8_t *codes, uint16_t *scales,
                                  hipStream_t st);
+size_t qat_backward_ckpt_workspace_bytes(int M, int out, int in, int K, int group_size);
 hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
                                     int group_size, const int8_t *x_codes, const uint16_t *x_scales,
                                     const uint16_t *dY, int M, float *dX, float *dW, float *dscales,
