@@ -495,26 +495,30 @@ def _one_device(*tensors) -> torch.device:
 
 class _Launch:
     """Context of a call for tensors on `dev`: that device is current, and so is
-    the stream the call is for, so that buffers made inside belong to it."""
+    the stream the call is for, so that buffers made inside belong to it.
+    Enters as the stream's handle."""
+    __slots__ = ("_dev", "_ctx")
 
     def __init__(self, dev: torch.device, stream=None):
-        self._ctx = []
-        if dev.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(dev))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            self._ctx.append(torch.cuda.stream(stream))
         self._dev = dev
+        self._ctx = None
+        if stream is not None or dev.index != torch.cuda.current_device():
+            self._ctx = [torch.cuda.device(dev)]
+            if stream is not None:
+                if not hasattr(stream, "cuda_stream"):
+                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
+                self._ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self) -> int:
-        for c in self._ctx:
-            c.__enter__()
-        return int(torch.cuda.current_stream(self._dev).cuda_stream)
+        if self._ctx is not None:
+            for c in self._ctx:
+                c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self._dev.index)   # current_stream without the object
 
     def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
+        if self._ctx is not None:
+            for c in reversed(self._ctx):
+                c.__exit__(*exc)
 
 
 def _blocks(n: int) -> int:
