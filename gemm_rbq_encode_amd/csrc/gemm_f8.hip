@@ -98,16 +98,20 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
     // the short last block, through registers
     auto stage_tail = [&](int t) {
         unsigned char *at = lds + (t & 1) * STAGE;
+        // (a piece past the end is read from the row's first bytes)
         const bool ok = (int)piece < in - t * F8_BLOCK;
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        const int64_t step = ok ? (int64_t)t * F8_BLOCK : -(int64_t)piece;
+        auto zero_past = [&](uint4 v) {
+            return ok ? v : make_uint4(0u, 0u, 0u, 0u);
+        };
 #pragma unroll
         for (int i = 0; i < LW; ++i)
             *reinterpret_cast<uint4 *>(at + (wave * LW + i) * 1024 + lane * 16) =
-                ok ? *reinterpret_cast<const uint4 *>(wbase + (int64_t)t * F8_BLOCK + woff[i]) : z;
+                zero_past(*reinterpret_cast<const uint4 *>(wbase + step + woff[i]));
 #pragma unroll
         for (int i = 0; i < LX; ++i)
             *reinterpret_cast<uint4 *>(at + RT * F8_BLOCK + (wave * LX + i) * 1024 + lane * 16) =
-                ok ? *reinterpret_cast<const uint4 *>(xbase + (int64_t)t * F8_BLOCK + xoff[i]) : z;
+                zero_past(*reinterpret_cast<const uint4 *>(xbase + step + xoff[i]));
     };
 
     // scales of a stage: one per token tile and lane, one per wave (its rows
@@ -148,28 +152,33 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
         const unsigned char *wa = lds + (t & 1) * STAGE + wr * TM * 16 * F8_BLOCK;
         const unsigned char *xa = lds + (t & 1) * STAGE + (RT + wc * TN * 16) * F8_BLOCK;
         if constexpr (HALF) {
-            v8i b[TN];
+            v8i a[3], b[TN];
+            a[0] = fragment(wa, 0);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
                 b[j] = fragment(xa, 16 * j);
-            v8i a = fragment(wa, 0);
+            a[1] = fragment(wa, 16);
             v4f p[2][TN];
-            // the sums of row tile i are scaled between the products of i + 1
+            // The sums of row tile i - 1 are scaled between the products of
+            // row tile i, and its fragment is read two tiles ahead; the
+            // scheduling barriers keep this order (left alone, each product
+            // is waited for before its fmas).
 #pragma unroll
             for (int i = 0; i <= TM; ++i) {
-                v8i an = a;
-                if (i + 1 < TM)
-                    an = fragment(wa, 16 * (i + 1));
+                if (i + 2 < TM)
+                    a[(i + 2) % 3] = fragment(wa, 16 * (i + 2));
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     if (i < TM) {
                         const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[j], z, 0, 0, 0, 0, 0, 0);
+                        p[i & 1][j] =
+                            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i % 3], b[j], z, 0, 0, 0, 0, 0, 0);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                     if (i > 0)
                         acc[i - 1][j] = f8_fma(p[(i - 1) & 1][j], s[j], acc[i - 1][j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                a = an;
             }
         } else {
             v8h b[TN][4];
