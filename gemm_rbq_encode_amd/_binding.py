@@ -135,7 +135,9 @@ _SIGNATURES = {
                                        ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_gemm_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
-                                   ctypes.c_uint32, ctypes.c_void_p]),
+                                   ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "rbq_gemm_f8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                      ctypes.c_uint32]),
     "rbq_gemv_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_probe_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
@@ -525,6 +527,12 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _nbytes(workspace: torch.Tensor) -> int:
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return workspace.numel() * workspace.element_size()
+
+
 def _out(t: torch.Tensor | None, size: tuple, dtype, name: str, dev: torch.device) -> torch.Tensor:
     """The given output tensor, checked, or a new one."""
     if t is None:
@@ -583,7 +591,8 @@ def _f8_layer(codes: torch.Tensor, scales: torch.Tensor):
 
 
 def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor, *,
-            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None, stream=None):
+            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None):
     """rbq_gemm_f8: Y [M][out] (float16 or float32) of the layer of encode_f8
     and the tokens of quantize_f8."""
     out_f, in_f = _f8_layer(codes, scales)
@@ -596,12 +605,17 @@ def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_
         raise ValueError(f"x_scales must be [{_blocks(in_f)}][{M}], got {tuple(x_scales.shape)}")
     if dtype not in (torch.float16, torch.float32):
         raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
-    dev = _one_device(codes, scales, x_codes, x_scales)
+    dev = _one_device(codes, scales, x_codes, x_scales, workspace)
+    kind = RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16
     with _Launch(dev, stream) as st:
         Y = _out(Y, (M, out_f), dtype, "Y", dev)
+        if workspace is None and M > 32:      # none is needed for fewer
+            need = int(lib().rbq_gemm_f8_workspace_bytes(out_f, in_f, M, kind))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
         check(lib().rbq_gemm_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x_codes.data_ptr(),
-                                x_scales.data_ptr(), M, Y.data_ptr(),
-                                RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16, st), "rbq_gemm_f8")
+                                x_scales.data_ptr(), M, Y.data_ptr(), kind, wp, wn, st), "rbq_gemm_f8")
     return Y
 
 
@@ -673,7 +687,7 @@ def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch
         need = int(lib().rbq_qat_backward_ckpt_workspace_bytes(s, M))
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wn = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        wn = _nbytes(workspace) if workspace is not None else 0
         check(lib().rbq_qat_backward_ckpt(planes.data_ptr(), scales.data_ptr(), s, x_codes.data_ptr(),
                                           x_scales.data_ptr(), dY.data_ptr(), M, ptr(dX), ptr(dW), ptr(ds),
                                           ptr(workspace), wn, ptr(status), st), "rbq_qat_backward_ckpt")

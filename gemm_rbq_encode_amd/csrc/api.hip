@@ -633,10 +633,18 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 
+size_t rbq_gemm_f8_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type) {
+    if (M < 1 || out_features < 1 || in_features < 32 || in_features % 32 != 0 ||
+        (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
+        return 0;
+    return rbq::gemm_f8_workspace_bytes(out_features, in_features, M, y_type == RBQ_Y_F32);
+}
+
 rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
                        const uint8_t *x_codes, const float *x_scales, int32_t M, void *Y, uint32_t y_type,
-                       void *stream) {
-    if (M < 0 || !f8_shape_ok(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
+                       void *workspace, size_t ws_bytes, void *stream) {
+    if (M < 0 || !f8_shape_ok(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32) ||
+        (ws_bytes > 0 && workspace == nullptr))
         return RBQ_ERR_INVALID_ARG;
     if (M == 0 || out_features == 0)
         return RBQ_OK;
@@ -657,12 +665,13 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
     }
     if (codes == nullptr || scales == nullptr || x_codes == nullptr || x_scales == nullptr)
         return RBQ_ERR_INVALID_ARG;
-    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x_codes, 16) || !aligned(x_scales, 4))
+    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x_codes, 16) || !aligned(x_scales, 4) ||
+        !aligned(workspace, 4))
         return RBQ_ERR_ALIGNMENT;
     if ((st = device_present()) != RBQ_OK)
         return st;
     e = rbq::launch_gemm_f8(codes, scales, out_features, in_features, x_codes, x_scales, M, Y,
-                            y_type == RBQ_Y_F32, (hipStream_t)stream);
+                            y_type == RBQ_Y_F32, workspace, ws_bytes, (hipStream_t)stream);
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 

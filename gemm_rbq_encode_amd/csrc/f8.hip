@@ -364,19 +364,16 @@ hipError_t launch_few(const uint8_t *W, const float *ws, int out, int in, const 
 // Rows per workgroup and blocks in flight.  More rows read the tokens less
 // often, fewer rows make more workgroups: 16 tokens on 4096 x 4096, 11008 x
 // 4096 and 14336 x 4096 take 7.3, 15.8 and 20.0 us with 16 rows against 8.8,
-// 16.3 and 17.7 with 32; 64 tokens on 4096 x 4096 and 11008 x 4096 take 13.7
-// and 35.8 us with 16 rows, 20.8 and 21.9 with 64.
+// 16.3 and 17.7 with 32.  More than 32 tokens come here only where the tiled
+// kernels' offsets do not reach.
 template <typename Y>
 hipError_t launch_few_tokens(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
                              int M, Y *y, hipStream_t st) {
     if (M <= 16)
         return out >= 12288 ? launch_few<2, 1, 8, 2>(W, ws, out, in, X, xs, M, y, st)
                             : launch_few<1, 1, 8, 2>(W, ws, out, in, X, xs, M, y, st);
-    if (M <= 32)
-        return out >= 12288 ? launch_few<2, 2, 8, 2>(W, ws, out, in, X, xs, M, y, st)
-                            : launch_few<1, 2, 8, 2>(W, ws, out, in, X, xs, M, y, st);
-    return out >= 8192 ? launch_few<4, 4, 4, 1>(W, ws, out, in, X, xs, M, y, st)
-                       : launch_few<1, 4, 8, 1>(W, ws, out, in, X, xs, M, y, st);
+    return out >= 12288 ? launch_few<2, 2, 8, 2>(W, ws, out, in, X, xs, M, y, st)
+                        : launch_few<1, 2, 8, 2>(W, ws, out, in, X, xs, M, y, st);
 }
 
 }  // namespace
@@ -398,9 +395,9 @@ hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, flo
 }
 
 hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                          int M, void *y, int y_f32, hipStream_t st) {
-    if (M > 64 && gemm_f8_tile_supports(out, in, M))
-        return launch_gemm_f8_tile(W, ws, out, in, X, xs, M, y, y_f32, st);
+                          int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st) {
+    if (M > F8_FEW && gemm_f8_tile_supports(out, in, M))
+        return launch_gemm_f8_tile(W, ws, out, in, X, xs, M, y, y_f32, workspace, ws_bytes, st);
     return y_f32 ? launch_few_tokens(W, ws, out, in, X, xs, M, static_cast<float *>(y), st)
                  : launch_few_tokens(W, ws, out, in, X, xs, M, static_cast<uint16_t *>(y), st);
 }

@@ -31,6 +31,7 @@
 //    v_mfma_f32_16x16x32_f16: exact products, fp32 sums.
 // Either way the block's sums are scaled by xs ws in one fp32 fma each.
 #include <algorithm>
+#include <type_traits>
 
 #include "rbq.h"
 #include "rbq_device.h"
@@ -51,27 +52,80 @@ __device__ __forceinline__ void f8_load_lds(const void *base, uint32_t voff, uin
     asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
 }
 
-// Waves WM x WN, each TM x TN tiles of 16 x 16.
-template <int WM, int WN, int TM, int TN, typename Y>
-__global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
-    const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
-    const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, Y *__restrict__ y, int tiles_m, int total) {
+// 4 bytes from base + voff to LDS [m0 + 4 lane].
+__device__ __forceinline__ void f8_load_lds4(const void *base, uint32_t voff, uint32_t m0) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
+}
+
+// All but the N youngest loads have landed, in every wave.
+template <int N>
+__device__ __forceinline__ void f8_landed() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// A wave's sums from row r0 and token m0 on: lane (li, g) holds rows 4 g + v of
+// a row tile and token li of a token tile.
+template <int TM, int TN, typename Y>
+__device__ __forceinline__ void f8_write_tile(const v4f (&acc)[TM][TN], int64_t r0, int64_t m0, int li, int g, int out,
+                                              int M, Y *__restrict__ y) {
     constexpr bool HALF = sizeof(Y) == 2;
+    const bool vec = (out & 3) == 0 && ((uintptr_t)y & (4 * sizeof(Y) - 1)) == 0;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int64_t m = m0 + j * 16 + li;
+        if (m >= M)
+            continue;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int64_t r = r0 + i * 16 + 4 * g;
+            Y *p = y + m * out + r;
+            if (vec && r < out) {
+                if constexpr (HALF)
+                    *reinterpret_cast<uint2 *>(p) =
+                        make_uint2((uint32_t)f2h(acc[i][j][0]) | (uint32_t)f2h(acc[i][j][1]) << 16,
+                                   (uint32_t)f2h(acc[i][j][2]) | (uint32_t)f2h(acc[i][j][3]) << 16);
+                else
+                    *reinterpret_cast<v4f *>(p) = acc[i][j];
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (r + v < out)
+                        p[v] = to_y<Y>(acc[i][j][v]);
+            }
+        }
+    }
+}
+
+// Tiles of RT = 16 WM TM rows by CT = 16 WN TN tokens, a ring of NB stages of
+// one block each; workgroups of slice z (of `slices`) take their share of the
+// blocks and write at y + z M out.  (At least two waves per SIMD: with more
+// registers the products are placed in accumulation registers, and every fma
+// waits for a copy.)
+template <int WM, int WN, int TM, int TN, int NB, bool EXACT, typename Y>
+__global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void gemm_f8_tile_kernel(
+    const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
+    const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, Y *__restrict__ y, int tiles_m, int tiles,
+    int slices) {
     constexpr int WAVES = WM * WN;
     constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
-    constexpr int STAGE = (RT + CT) * F8_BLOCK;
+    constexpr int SX = RT * F8_BLOCK, SS = SX + CT * F8_BLOCK, SLOT = SS + CT * 4;   // rows, tokens, scales
     constexpr int LW = RT / 8 / WAVES, LX = CT / 8 / WAVES;      // 1 KB loads of a wave and stage
-    static_assert(LW * 8 * WAVES == RT && LX * 8 * WAVES == CT, "tile rows per wave load");
+    constexpr int PER = LW + LX + 1;
+    static_assert(LW * 8 * WAVES == RT && LX * 8 * WAVES == CT && CT % 64 == 0, "tile rows per wave load");
+    static_assert(WAVES >= CT / 64 && TM * 16 <= F8_BLOCK, "scales of a stage");
+    static_assert(NB >= 2 && NB <= 4 && PER * (NB - 2) < 64, "ring depth");
     extern __shared__ __align__(16) unsigned char lds[];
     const int lane = threadIdx.x & (RBQ_WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
     const int wr = wave % WM, wc = wave / WM;
     const int li = lane & 15, g = lane >> 4;
-
-    const int id = xcd_run(blockIdx.x, total);       // tokens fastest
-    const int64_t r0 = (int64_t)(id / tiles_m) * RT, m0 = (int64_t)(id % tiles_m) * CT;
+    const int id = xcd_run(blockIdx.x, tiles * slices);          // tokens fastest, then rows, then slices
+    const int tile = id % tiles, slice = id / tiles;
+    const int64_t r0 = (int64_t)(tile / tiles_m) * RT, m0 = (int64_t)(tile % tiles_m) * CT;
+    y += (int64_t)slice * M * out;
 
     const uint8_t *wbase = W + r0 * in, *xbase = X + m0 * in;
+    const float *sbase = xs + m0;
     const int rlast = (int)std::min<int64_t>(out - 1 - r0, RT - 1), mlast = (int)std::min<int64_t>(M - 1 - m0, CT - 1);
     const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);   // the piece stored at this lane's place
     uint32_t woff[LW], xoff[LX];
@@ -81,48 +135,27 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
 #pragma unroll
     for (int i = 0; i < LX; ++i)
         xoff[i] = (uint32_t)std::min((wave * LX + i) * 8 + (lane >> 3), mlast) * (uint32_t)in + piece;
+    constexpr int SW = CT / 64;                                   // (the other waves repeat these loads)
+    const uint32_t soff = (uint32_t)std::min((wave % SW) * 64 + lane, mlast) * 4u;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(f8_lds_addr(lds));
 
+    // this slice's blocks: t0 .. t0 + n - 1 whole ones, and the short last block in the last slice
     const int full = in / F8_BLOCK;
-    // request stage t: wave-uniform LDS places, W rows first
-    auto issue = [&](int t) {
-        const uint32_t at = lds0 + (uint32_t)(t & 1) * STAGE;
-        const uint8_t *wb = wbase + (int64_t)t * F8_BLOCK, *xb = xbase + (int64_t)t * F8_BLOCK;
-#pragma unroll
-        for (int i = 0; i < LW; ++i)
-            f8_load_lds(wb, woff[i], at + (uint32_t)(wave * LW + i) * 1024u);
-#pragma unroll
-        for (int i = 0; i < LX; ++i)
-            f8_load_lds(xb, xoff[i], at + (uint32_t)(RT * F8_BLOCK) + (uint32_t)(wave * LX + i) * 1024u);
-    };
-    // the short last block, through registers
-    auto stage_tail = [&](int t) {
-        unsigned char *at = lds + (t & 1) * STAGE;
-        // (a piece past the end is read from the row's first bytes)
-        const bool ok = (int)piece < in - t * F8_BLOCK;
-        const int64_t step = ok ? (int64_t)t * F8_BLOCK : -(int64_t)piece;
-        auto zero_past = [&](uint4 v) {
-            return ok ? v : make_uint4(0u, 0u, 0u, 0u);
-        };
-#pragma unroll
-        for (int i = 0; i < LW; ++i)
-            *reinterpret_cast<uint4 *>(at + (wave * LW + i) * 1024 + lane * 16) =
-                zero_past(*reinterpret_cast<const uint4 *>(wbase + step + woff[i]));
-#pragma unroll
-        for (int i = 0; i < LX; ++i)
-            *reinterpret_cast<uint4 *>(at + RT * F8_BLOCK + (wave * LX + i) * 1024 + lane * 16) =
-                zero_past(*reinterpret_cast<const uint4 *>(xbase + step + xoff[i]));
+    const int t0 = (int)((int64_t)full * slice / slices), n = (int)((int64_t)full * (slice + 1) / slices) - t0;
+    // load q = 0 .. PER - 1 of stage i
+    auto issue = [&](int i, int q) {
+        const int64_t t = t0 + i;
+        const uint32_t at = lds0 + (uint32_t)(i % NB) * SLOT;
+        if (q < LW)
+            f8_load_lds(wbase + t * F8_BLOCK, woff[q < LW ? q : 0], at + (uint32_t)(wave * LW + q) * 1024u);
+        else if (q < LW + LX)
+            f8_load_lds(xbase + t * F8_BLOCK, xoff[q < LW + LX ? q - LW : 0],
+                        at + (uint32_t)SX + (uint32_t)(wave * LX + q - LW) * 1024u);
+        else
+            f8_load_lds4(sbase + t * M, soff, at + (uint32_t)SS + (uint32_t)(wave % SW) * 256u);
     };
 
-    // scales of a stage: one per token tile and lane, one per wave (its rows
-    // lie in one block of 128)
-    const float *xsp = xs + m0;
-    int sidx[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-        sidx[j] = std::min((wc * TN + j) * 16 + li, mlast);
-    const float *wsp = ws + std::min<int64_t>(r0 + wr * TM * 16, out - 1) / F8_BLOCK * T;
-
+    const float *wsp = ws + std::min<int64_t>(r0 + wr * TM * 16, out - 1) / F8_BLOCK * T;   // (a wave's rows share a block)
     v4f acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -140,24 +173,31 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
         return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
     };
 
-    float sx[TN], sw;
-    auto load_scales = [&](int t) {
+    // The products of one stage; with `request`, the loads of stage `next` go
+    // out between them, a few after each row tile (issued together they would
+    // hold the wave back from its products).
+    auto compute = [&](const unsigned char *slot, float sw, int next, auto request) {
+        auto between = [&](int i) {
+            if constexpr (decltype(request)::value)
+#pragma unroll
+                for (int q = PER * i / TM; q < PER * (i + 1) / TM; ++q)
+                    issue(next, q);
+        };
+        const unsigned char *wa = slot + wr * TM * 16 * F8_BLOCK;
+        const unsigned char *xa = slot + SX + wc * TN * 16 * F8_BLOCK;
+        const float *sl = reinterpret_cast<const float *>(slot + SS) + wc * TN * 16 + li;
+        float s[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            sx[j] = xsp[(int64_t)t * M + sidx[j]];
-        sw = wsp[t];
-    };
-
-    auto compute = [&](int t, const float (&s)[TN]) {
-        const unsigned char *wa = lds + (t & 1) * STAGE + wr * TM * 16 * F8_BLOCK;
-        const unsigned char *xa = lds + (t & 1) * STAGE + (RT + wc * TN * 16) * F8_BLOCK;
-        if constexpr (HALF) {
+            s[j] = sl[16 * j] * sw;
+        if constexpr (!EXACT) {
             v8i a[3], b[TN];
             a[0] = fragment(wa, 0);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
                 b[j] = fragment(xa, 16 * j);
-            a[1] = fragment(wa, 16);
+            if (TM > 1)
+                a[1] = fragment(wa, 16);
             v4f p[2][TN];
             // The sums of row tile i - 1 are scaled between the products of
             // row tile i, and its fragment is read two tiles ahead; the
@@ -179,6 +219,8 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
                         acc[i - 1][j] = f8_fma(p[(i - 1) & 1][j], s[j], acc[i - 1][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                if (i < TM)
+                    between(i);
             }
         } else {
             v8h b[TN][4];
@@ -192,101 +234,430 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void gemm_f8_tile_kernel(
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
                     acc[i][j] = f8_fma(f8_mma(a, b[j]), s[j], acc[i][j]);
+                between(i);
             }
         }
     };
 
-    if (full > 0)
-        issue(0);
-    else
-        stage_tail(0);
-    load_scales(0);
-    for (int t = 0; t < T; ++t) {
-        float s[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            s[j] = sx[j] * sw;                          // (the compiler's wait for the scales goes here)
-            asm volatile("" : "+v"(s[j]));
-        }
-        // stage t has landed, and stage t - 1 is no longer read, in every wave
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (t + 1 < T) {
-            if (t + 1 < full)
-                issue(t + 1);
-            else
-                stage_tail(t + 1);
-            load_scales(t + 1);
-        }
-        compute(t, s);
+    for (int k = 0; k < NB - 1; ++k)
+        if (k < n)
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+                issue(k, q);
+    float sw = n > 0 ? wsp[t0] : 0.0f;
+    auto step = [&](int i, auto request) {
+        float w = sw;
+        asm volatile("" : "+s"(w));                     // (the compiler's wait for it goes here)
+        sw = wsp[t0 + std::min(i + 1, n - 1)];
+        compute(lds + (i % NB) * SLOT, w, i + NB - 1, request);
+    };
+    // before stage i: it has landed (younger: the NB - 2 stages behind it),
+    // and stage i - 1 is no longer read, in every wave
+    int i = 0;
+    for (; i + NB - 1 < n; ++i) {
+        f8_landed<(NB - 2) * PER>();
+        step(i, std::true_type());
     }
+    for (; i < n; ++i) {
+        const int younger = n - 1 - i;                  // at most NB - 2
+        if (NB >= 4 && younger == 2)
+            f8_landed<2 * PER>();
+        else if (NB >= 3 && younger == 1)
+            f8_landed<PER>();
+        else
+            f8_landed<0>();
+        step(i, std::false_type());
+    }
+    if (full < T && slice == slices - 1) {
+        // the short last block, through registers, zero past the end on both
+        // sides (a piece past the end is read from the row's first bytes)
+        __syncthreads();
+        const bool ok = (int)piece < in - full * F8_BLOCK;
+        const int64_t step = ok ? (int64_t)full * F8_BLOCK : -(int64_t)piece;
+        auto zero_past = [&](const uint4 &v) {
+            return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+        };
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            *reinterpret_cast<uint4 *>(lds + (wave * LW + i) * 1024 + lane * 16) =
+                zero_past(*reinterpret_cast<const uint4 *>(wbase + step + woff[i]));
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            *reinterpret_cast<uint4 *>(lds + SX + (wave * LX + i) * 1024 + lane * 16) =
+                zero_past(*reinterpret_cast<const uint4 *>(xbase + step + xoff[i]));
+        if (wave < SW)
+            reinterpret_cast<float *>(lds + SS)[wave * 64 + lane] =
+                sbase[(int64_t)full * M + std::min(wave * 64 + lane, mlast)];
+        __syncthreads();
+        compute(lds, wsp[full], 0, std::false_type());
+    }
+    f8_write_tile<TM, TN>(acc, r0 + wr * TM * 16, m0 + wc * TN * 16, li, g, out, M, y);
+}
 
-    // lane (li, g) holds rows 4 g + v of the row tile and token li of the token tile
-    const bool vec = (out & 3) == 0 && ((uintptr_t)y & (4 * sizeof(Y) - 1)) == 0;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        const int64_t m = m0 + (wc * TN + j) * 16 + li;
-        if (m >= M)
-            continue;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t r = r0 + (wr * TM + i) * 16 + 4 * g;
-            Y *p = y + m * out + r;
-            if (vec && r < out) {
-                if constexpr (HALF)
-                    *reinterpret_cast<uint2 *>(p) =
-                        make_uint2((uint32_t)f2h(acc[i][j][0]) | (uint32_t)f2h(acc[i][j][1]) << 16,
-                                   (uint32_t)f2h(acc[i][j][2]) | (uint32_t)f2h(acc[i][j][3]) << 16);
-                else
-                    *reinterpret_cast<v4f *>(p) = acc[i][j];
-            } else {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (r + v < out)
-                        p[v] = to_y<Y>(acc[i][j][v]);
-            }
-        }
+// y = the sum of the partial sums of the slices, in slice order.
+template <typename Y>
+__global__ __launch_bounds__(256) void gemm_f8_sum_kernel(const float *__restrict__ parts, int slices, int64_t n,
+                                                          Y *__restrict__ y) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = parts[i];
+        for (int z = 1; z < slices; ++z)
+            v += parts[z * n + i];
+        y[i] = to_y<Y>(v);
     }
 }
 
-template <int WM, int WN, int TM, int TN, typename Y>
+// ---------------------------------------------------------------------------
+// fp16 outputs, tiles of 256 x 256.  Two whole stages (64 KB each) leave the
+// loads in bursts that are waited for; what the tile needs is a steady flow.
+// So a block is cut into pieces that are freed and requested on their own: the
+// tokens of a block (32 KB, two slots: they are read into registers once, at
+// the end of the block before), and half its rows (16 KB: 64 rows of each row
+// of waves, five slots).  Every half block has one barrier; the wait before
+// it is for the pieces that the end of this half reads ahead, with the
+// younger loads (a known number, as loads return in order) left in flight, so
+// that a piece has three halves' time to arrive.  Fragments are read one row
+// tile ahead, the next block's token fragments into the registers of the
+// current ones as their last products are issued: after a barrier the
+// products go on without a read in between.
+
+constexpr int GL_X = 256 * F8_BLOCK;              // a slot of tokens
+constexpr int GL_W = 128 * F8_BLOCK;              // a slot of half the rows
+constexpr int GL_S = 1024;                        // a slot of the tokens' scales
+constexpr int GL_NW = 5;                          // slots of rows
+constexpr int GL_W0 = 2 * GL_X, GL_S0 = GL_W0 + GL_NW * GL_W;
+constexpr int GL_LDS = GL_S0 + 3 * GL_S;
+constexpr int GL_THREADS = 512;
+
+__global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
+    const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
+    const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, uint16_t *__restrict__ y, int tiles_m,
+    int tiles_r) {
+    constexpr int TM = 8, TN = 4;
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int lane = threadIdx.x & (RBQ_WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
+    const int wr = wave & 1, wc = wave >> 1;
+    const int li = lane & 15, g = lane >> 4;
+
+    // tiles go in bands of 8 token tiles, tokens fastest: the 32 workgroups of
+    // an XCD share 8 token tiles and 4 row tiles
+    int id = xcd_run(blockIdx.x, tiles_m * tiles_r);
+    const int band = id / (8 * tiles_r), bw = std::min(8, tiles_m - 8 * band);
+    id -= band * 8 * tiles_r;
+    const int64_t r0 = (int64_t)(id / bw) * 256, m0 = (int64_t)(8 * band + id % bw) * 256;
+
+    const uint8_t *wbase = W + r0 * in, *xbase = X + m0 * in;
+    const float *sbase = xs + m0;
+    const int rlast = (int)std::min<int64_t>(out - 1 - r0, 255), mlast = (int)std::min<int64_t>(M - 1 - m0, 255);
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+    // row of the tile that lane l loads with load i of half h: a slot has 64
+    // rows per row of waves
+    auto slot_row = [&](int h, int i, int l) {
+        const int q = (wave * 2 + i) * 8 + (l >> 3);
+        return (q >> 6) * 128 + h * 64 + (q & 63);
+    };
+    uint32_t woff[2][2], xoff[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            woff[h][i] = (uint32_t)std::min(slot_row(h, i, lane), rlast) * (uint32_t)in + piece;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        xoff[i] = (uint32_t)std::min((wave * 4 + i) * 8 + (lane >> 3), mlast) * (uint32_t)in + piece;
+    const uint32_t soff = (uint32_t)std::min((wave & 3) * 64 + lane, mlast) * 4u;   // (two waves load the same)
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(f8_lds_addr(lds));
+
+    const int full = in / F8_BLOCK;
+    // load q = 0..3 of the tokens of block t, 4 of their scales; load i of half h = 2 t + (0, 1) of the rows
+    auto issue_x = [&](int t, int q) {
+        if (q < 4)
+            f8_load_lds(xbase + (int64_t)t * F8_BLOCK, xoff[q],
+                        lds0 + (uint32_t)(t & 1) * GL_X + (uint32_t)(wave * 4 + q) * 1024u);
+        else
+            f8_load_lds4(sbase + (int64_t)t * M, soff,
+                         lds0 + GL_S0 + (uint32_t)(t % 3) * GL_S + (uint32_t)(wave & 3) * 256u);
+    };
+    auto row_slot = [&](int h) { return GL_W0 + (h % GL_NW) * GL_W; };
+    auto issue_w = [&](int h, int odd, int i) {
+        f8_load_lds(wbase + (int64_t)(h >> 1) * F8_BLOCK, woff[odd][i],
+                    lds0 + (uint32_t)row_slot(h) + (uint32_t)(wave * 2 + i) * 1024u);
+    };
+
+    const uint32_t rd_lo = (uint32_t)(li * F8_BLOCK + ((g ^ (li & 7)) * 16));
+    const uint32_t rd_hi = (uint32_t)(li * F8_BLOCK + (((g + 4) ^ (li & 7)) * 16));
+    auto fragment = [&](const unsigned char *at, int row) {
+        const uint4 lo = *reinterpret_cast<const uint4 *>(at + row * F8_BLOCK + rd_lo);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(at + row * F8_BLOCK + rd_hi);
+        return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    auto token_slot = [&](int t) { return lds + (t & 1) * GL_X + wc * TN * 16 * F8_BLOCK; };
+    auto rows_of = [&](int h) { return lds + row_slot(h) + wr * 64 * F8_BLOCK; };
+    const float *wsp = ws + std::min<int64_t>(r0 + wr * 128, out - 1) / F8_BLOCK * T;
+
+    v4f acc[TM][TN], p[2][TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        p[0][j] = p[1][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    v8i a[2], b[TN];
+    float s[TN] = {}, last[TN];                  // scales of this block, and of the one before
+
+    // The products of one half of a block, beside each the fmas of the row
+    // tile before (of the block before, at its first).  wa: this half's rows,
+    // wn: the next half's; bn: the next block's tokens; between(i): the loads
+    // to issue behind row tile i.
+    auto half = [&](const unsigned char *wa, const unsigned char *wn, const unsigned char *bn, auto odd, auto between) {
+        constexpr int O = decltype(odd)::value;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            constexpr int I0 = 4 * O;
+            const int I = I0 + i;
+            a[(I + 1) & 1] = i < 3 ? fragment(wa, 16 * (i + 1)) : fragment(wn, 0);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                p[I & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[I & 1], b[j], z, 0, 0, 0, 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (I == TM - 1)
+                    b[j] = fragment(bn, 16 * j);
+                if (I > 0)
+                    acc[I - 1][j] = f8_fma(p[(I - 1) & 1][j], s[j], acc[I - 1][j]);
+                else
+                    acc[TM - 1][j] = f8_fma(p[1][j], last[j], acc[TM - 1][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            between(i);
+        }
+    };
+    auto first_fragments = [&](const unsigned char *wa, const unsigned char *ba) {
+        a[0] = fragment(wa, 0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            b[j] = fragment(ba, 16 * j);
+    };
+
+    // requests go out in the order W 2t, X t, S t, W 2t + 1
+    if (full > 0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t >= full)
+                break;
+            issue_w(2 * t, 0, 0);
+            issue_w(2 * t, 0, 1);
+#pragma unroll
+            for (int q = 0; q < 5; ++q)
+                issue_x(t, q);
+            issue_w(2 * t + 1, 1, 0);
+            issue_w(2 * t + 1, 1, 1);
+        }
+        if (full > 1)
+            f8_landed<11>();
+        else
+            f8_landed<2>();
+        first_fragments(rows_of(0), token_slot(0));
+    }
+    float sw = full > 0 ? wsp[0] : 0.0f;
+    // Block t, with `more` full blocks (two: two or more) behind it.  Past the
+    // last one old bytes of the slots are read, for fragments that no one uses.
+    auto stage = [&](int t, auto more) {
+        constexpr int MORE = decltype(more)::value;
+        // second half of t; younger: W 2t + 2, X and S t + 1, W 2t + 3
+        f8_landed<(MORE > 0 ? 9 : 0)>();
+        asm volatile("" : "+s"(sw));                       // (the compiler's wait for it goes here)
+        const float *sl = reinterpret_cast<const float *>(lds + GL_S0 + (t % 3) * GL_S) + wc * TN * 16 + li;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            last[j] = s[j];
+            s[j] = sl[16 * j] * sw;
+        }
+        half(rows_of(2 * t), rows_of(2 * t + 1), lds, std::integral_constant<int, 0>(), [&](int i) {
+            if (MORE > 1) {
+                if (i == 0) {
+                    issue_w(2 * t + 4, 0, 0);
+                    issue_w(2 * t + 4, 0, 1);
+                } else {
+                    issue_x(t + 2, 2 * i - 2);
+                    if (i < 3)
+                        issue_x(t + 2, 2 * i - 1);
+                }
+            }
+        });
+        // W 2t + 2 and X t + 1; younger: W 2t + 3, W 2t + 4, X and S t + 2
+        f8_landed<(MORE > 1 ? 9 : MORE > 0 ? 2 : 0)>();
+        if (MORE > 0)
+            sw = wsp[t + 1];
+        half(rows_of(2 * t + 1), rows_of(2 * t + 2), token_slot(t + 1), std::integral_constant<int, 1>(), [&](int i) {
+            if (MORE > 1 && i < 2)
+                issue_w(2 * t + 5, 1, i);
+        });
+    };
+    int t = 0;
+    for (; t + 2 < full; ++t)
+        stage(t, std::integral_constant<int, 2>());
+    if (t + 1 < full)
+        stage(t++, std::integral_constant<int, 1>());
+    if (t < full)
+        stage(t, std::integral_constant<int, 0>());
+    if (full < T) {
+        // the short last block, through registers, zero past the end on both
+        // sides (a piece past the end is read from the row's first bytes)
+        __syncthreads();
+        int l = lane;
+        asm volatile("" : "+v"(l));                        // (the places are worked out anew, not kept)
+        const int c = ((l & 7) ^ (l >> 3)) * 16;
+        const bool ok = c < in - full * F8_BLOCK;
+        const int64_t at = ok ? (int64_t)full * F8_BLOCK + c : 0;
+        auto zero_past = [&](const uint4 &v) {
+            return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = std::min((wave * 4 + i) * 8 + (l >> 3), mlast);
+            const uint4 v = *reinterpret_cast<const uint4 *>(xbase + m * in + at);
+            *reinterpret_cast<uint4 *>(lds + (wave * 4 + i) * 1024 + l * 16) = zero_past(v);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t r = std::min(slot_row(h, i, l), rlast);
+                const uint4 v = *reinterpret_cast<const uint4 *>(wbase + r * in + at);
+                *reinterpret_cast<uint4 *>(lds + row_slot(h) + (wave * 2 + i) * 1024 + l * 16) = zero_past(v);
+            }
+        __syncthreads();
+        first_fragments(rows_of(0), token_slot(0));
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            last[j] = s[j];
+            s[j] = sbase[(int64_t)full * M + std::min((wc * TN + j) * 16 + li, mlast)] * wsp[full];
+        }
+        half(rows_of(0), rows_of(1), lds, std::integral_constant<int, 0>(), [](int) {});
+        half(rows_of(1), rows_of(0), lds, std::integral_constant<int, 1>(), [](int) {});
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        acc[TM - 1][j] = f8_fma(p[1][j], s[j], acc[TM - 1][j]);
+    f8_write_tile<TM, TN>(acc, r0 + wr * TM * 16, m0 + wc * TN * 16, li, g, out, M, y);
+}
+
+template <int WM, int WN, int TM, int TN, int NB, bool EXACT, typename Y>
 hipError_t launch_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
-                       Y *y, hipStream_t st) {
+                       Y *y, int slices, hipStream_t st) {
     constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
-    constexpr size_t LDS = 2 * (RT + CT) * F8_BLOCK;
-    auto kernel = gemm_f8_tile_kernel<WM, WN, TM, TN, Y>;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
-    if (e != hipSuccess)
-        return e;
-    const int64_t tiles_m = ((int64_t)M + CT - 1) / CT, total = tiles_m * (((int64_t)out + RT - 1) / RT);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(WM * WN * RBQ_WAVE), LDS, st, W, ws, out, in,
-                       f8_blocks(in), X, xs, M, y, (int)tiles_m, (int)total);
+    constexpr int LDS = NB * ((RT + CT) * F8_BLOCK + CT * 4);
+    static_assert(LDS <= 160 * 1024, "LDS of a compute unit");
+    const int64_t tiles_m = ((int64_t)M + CT - 1) / CT, tiles = tiles_m * (((int64_t)out + RT - 1) / RT);
+    hipLaunchKernelGGL((gemm_f8_tile_kernel<WM, WN, TM, TN, NB, EXACT, Y>), dim3((unsigned)(tiles * slices)),
+                       dim3(WM * WN * RBQ_WAVE), LDS, st, W, ws, out, in, f8_blocks(in), X, xs, M, y, (int)tiles_m,
+                       (int)tiles, slices);
     return hipGetLastError();
+}
+
+hipError_t launch_large(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
+                        uint16_t *y, hipStream_t st) {
+    const int tiles_m = (int)(((int64_t)M + 255) / 256), tiles_r = (int)(((int64_t)out + 255) / 256);
+    hipLaunchKernelGGL(gemm_f8_large_kernel, dim3((unsigned)(tiles_m * tiles_r)), dim3(GL_THREADS), GL_LDS, st, W, ws,
+                       out, in, f8_blocks(in), X, xs, M, y, tiles_m, tiles_r);
+    return hipGetLastError();
+}
+
+template <bool EXACT, typename Y>
+hipError_t launch_tiles(int kind, const uint8_t *W, const float *ws, int out, int in, const uint8_t *X,
+                        const float *xs, int M, Y *y, int slices, hipStream_t st) {
+    switch (kind) {
+    case 1: return launch_tile<2, 4, 4, 4, 3, EXACT, Y>(W, ws, out, in, X, xs, M, y, slices, st);
+    case 2: return launch_tile<2, 2, 4, 4, 4, EXACT, Y>(W, ws, out, in, X, xs, M, y, slices, st);
+    default: return launch_tile<2, 2, 2, 4, 4, EXACT, Y>(W, ws, out, in, X, xs, M, y, slices, st);
+    }
+}
+
+// Tile sizes (rows x tokens) and how many slices the columns are split into.
+struct f8_plan {
+    int kind, slices;
+};
+
+constexpr int F8_KINDS = 4;
+constexpr int F8_ROWS[F8_KINDS] = {256, 128, 128, 64}, F8_TOKENS[F8_KINDS] = {256, 256, 128, 128};
+
+// The choice is the least of a simple cost: every kind keeps one workgroup per
+// compute unit, so a launch takes ceil(workgroups / 256) rounds of its blocks'
+// stages and a start of 2.5 us each; slices add a second launch and the write
+// and read of the partial sums.  Stage times measured on full launches: us per
+// block 1.8, 1.05, 0.68, 0.47 (fp16 outputs; 256 x 256 serves only those), and
+// 1.95, 1.1, 0.75.  It picked the fastest kind, or one within 7 % of it, for 65 to 2048 tokens on 1000 to 14336
+// rows; e.g. 128 tokens, 4096 x 4096: 14.6 us with 64 x 128 in 4 slices, 48.9
+// with 256 x 256; 2048 tokens: 39.3 with 128 x 256, 54.9 with 256 x 256, 67.2
+// with 64 x 128; 1024 tokens, 11008 x 4096: 63.0 with 256 x 256, 73.4 with
+// 128 x 256.
+f8_plan plan_tiles(int out, int in, int M, int y_f32) {
+    static constexpr float stage[2][F8_KINDS] = {{1.8f, 1.05f, 0.68f, 0.47f}, {0.0f, 1.95f, 1.1f, 0.75f}};
+    static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
+    const int T = f8_blocks(in);
+    f8_plan best = {1, 1};
+    float least = 0.0f;
+    for (int k = y_f32 ? 1 : 0; k < F8_KINDS; ++k)
+        for (const int S : splits) {
+            if (S > 1 && (k == 0 || 2 * S > T))
+                break;
+            const int64_t tiles = (((int64_t)out + F8_ROWS[k] - 1) / F8_ROWS[k]) *
+                                  (((int64_t)M + F8_TOKENS[k] - 1) / F8_TOKENS[k]);
+            const int64_t rounds = (tiles * S + 255) / 256;
+            float cost = (float)rounds * ((float)((T + S - 1) / S) * stage[y_f32][k] + 2.5f);
+            if (S > 1)
+                cost += 4.0f + (float)S * (float)M * (float)out * (8.0f / 6.0e6f);
+            if (least == 0.0f || cost < least) {
+                least = cost;
+                best = {k, S};
+            }
+        }
+    return best;
 }
 
 }  // namespace
 
 // Byte offsets inside a tile are 32-bit and the tiles are numbered in 31 bits.
 bool gemm_f8_tile_supports(int out, int in, int M) {
-    return in <= (1 << 23) && ((int64_t)out / 128 + 1) * ((int64_t)M / 128 + 1) < (1 << 30);
+    return in <= (1 << 23) && ((int64_t)out / 64 + 1) * ((int64_t)M / 128 + 1) < (1 << 22);
 }
 
-// Large tiles where they fill the 256 compute units at least once, else tiles
-// of 128 x 128.  fp16 outputs, measured at 8192 rows,
-// 8192 columns, 4096 tokens (512 large tiles): 302 us against 366; at 5003
-// rows, 4128 columns, 777 tokens (80 large, 280 small tiles): 82 against 53.
+size_t gemm_f8_workspace_bytes(int out, int in, int M, int y_f32) {
+    if (M <= F8_FEW || !gemm_f8_tile_supports(out, in, M))
+        return 0;
+    const f8_plan p = plan_tiles(out, in, M, y_f32);
+    return p.slices > 1 ? (size_t)p.slices * (size_t)M * (size_t)out * sizeof(float) : 0;
+}
+
 hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                               int M, void *y, int y_f32, hipStream_t st) {
-    const int rt = y_f32 ? 128 : 256;
-    const bool large = ((int64_t)out + rt - 1) / rt * (((int64_t)M + 255) / 256) >= (y_f32 ? 150 : 200);
-    if (y_f32) {
-        float *o = static_cast<float *>(y);
-        return large ? launch_tile<2, 4, 4, 4, float>(W, ws, out, in, X, xs, M, o, st)
-                     : launch_tile<2, 2, 4, 4, float>(W, ws, out, in, X, xs, M, o, st);
+                               int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st) {
+    f8_plan p = plan_tiles(out, in, M, y_f32);
+    if (ws_bytes < gemm_f8_workspace_bytes(out, in, M, y_f32))
+        p.slices = 1;
+    if (p.slices == 1) {
+        if (y_f32)
+            return launch_tiles<true>(p.kind, W, ws, out, in, X, xs, M, static_cast<float *>(y), 1, st);
+        uint16_t *o = static_cast<uint16_t *>(y);
+        return p.kind == 0 ? launch_large(W, ws, out, in, X, xs, M, o, st)
+                           : launch_tiles<false>(p.kind, W, ws, out, in, X, xs, M, o, 1, st);
     }
-    uint16_t *o = static_cast<uint16_t *>(y);
-    return large ? launch_tile<2, 4, 8, 4, uint16_t>(W, ws, out, in, X, xs, M, o, st)
-                 : launch_tile<2, 2, 4, 4, uint16_t>(W, ws, out, in, X, xs, M, o, st);
+    float *parts = static_cast<float *>(workspace);
+    hipError_t e = y_f32 ? launch_tiles<true>(p.kind, W, ws, out, in, X, xs, M, parts, p.slices, st)
+                         : launch_tiles<false>(p.kind, W, ws, out, in, X, xs, M, parts, p.slices, st);
+    if (e != hipSuccess)
+        return e;
+    const int64_t n = (int64_t)M * out;
+    const dim3 grid((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16));
+    if (y_f32)
+        hipLaunchKernelGGL(gemm_f8_sum_kernel<float>, grid, dim3(256), 0, st, parts, p.slices, n,
+                           static_cast<float *>(y));
+    else
+        hipLaunchKernelGGL(gemm_f8_sum_kernel<uint16_t>, grid, dim3(256), 0, st, parts, p.slices, n,
+                           static_cast<uint16_t *>(y));
+    return hipGetLastError();
 }
 
 }  // namespace rbq

@@ -122,20 +122,24 @@ def test_f8_argument_errors():
     assert L.rbq_quantize_f8(OK + 2, 2, 64, OK, OK, None) == al
     assert L.rbq_quantize_f8(OK, 2, 64, OK + 4, OK, None) == al
     assert L.rbq_quantize_f8(None, 0, 64, None, None, None) == E.RBQ_OK
-    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 2, None) == bad
-    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, -2, OK, 0, None) == bad
-    assert L.rbq_gemm_f8(OK, OK, 8, 40, OK, OK, 2, OK, 0, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 2, None, 0, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, -2, OK, 0, None, 0, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 40, OK, OK, 2, OK, 0, None, 0, None) == bad
     for k in (0, 1, 4, 5, 7):
-        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None]
+        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None, 0, None]
         a[k] = None
         assert L.rbq_gemm_f8(*a) == bad, k
     for k, off in ((0, 8), (1, 2), (4, 8), (5, 2), (7, 1)):
-        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None]
+        a = [OK, OK, 8, 64, OK, OK, 2, OK, 0, None, 0, None]
         a[k] = OK + off
         assert L.rbq_gemm_f8(*a) == al, k
-    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK + 2, 1, None) == al
-    assert L.rbq_gemm_f8(None, None, 8, 64, None, None, 0, None, 0, None) == E.RBQ_OK
-    assert L.rbq_gemm_f8(None, None, 0, 64, None, None, 3, None, 0, None) == E.RBQ_OK
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK + 2, 1, None, 0, None) == al
+    assert L.rbq_gemm_f8(None, None, 8, 64, None, None, 0, None, 0, None, 0, None) == E.RBQ_OK
+    assert L.rbq_gemm_f8(None, None, 0, 64, None, None, 3, None, 0, None, 0, None) == E.RBQ_OK
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 0, None, 64, None) == bad
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 0, OK + 2, 64, None) == al
+    for a in ((8, 40, 2, 0), (8, 64, -1, 0), (0, 64, 300, 0), (-8, 64, 300, 0), (8, 0, 300, 0), (8, 64, 300, 2)):
+        assert L.rbq_gemm_f8_workspace_bytes(*a) == 0, a
     for k in (0, 1, 4, 5):
         a = [OK, OK, 8, 64, OK, OK, None]
         a[k] = None
@@ -197,8 +201,8 @@ def test_valid_calls_without_a_device():
     L, none = rbq.lib(), rbq.RBQ_ERR_NO_DEVICE
     assert L.rbq_encode_f8(OK, 8, 64, OK, OK, None, None) == none
     assert L.rbq_quantize_f8(OK, 2, 64, OK, OK, None) == none
-    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 0, None) == none
-    assert L.rbq_gemm_f8(None, None, 8, 0, None, None, 2, OK, 1, None) == none
+    assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, 0, None, 0, None) == none
+    assert L.rbq_gemm_f8(None, None, 8, 0, None, None, 2, OK, 1, None, 0, None) == none
     assert L.rbq_gemv_f8(OK, OK, 8, 64, OK, OK, None) == none
     assert L.rbq_qat_checkpoint(OK, 2, 64, OK, OK, None) == none
     s = rbq.shape(64, 128, 2, 0)

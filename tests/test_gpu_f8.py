@@ -8,7 +8,7 @@ each block, the joining of partial sums), each at most 2^-23 (a matrix
 instruction may cut instead of round):
   fp32:  |err| <= n 2^-23 S
   fp16:  the same, and one rounding: 2^-11 (|y| + n 2^-23 S) + 2^-25
-More than 64 tokens with fp16 outputs take the 8-bit matrix instruction, which
+More than 32 tokens with fp16 outputs take the 8-bit matrix instruction, which
 cuts the products of 8 columns at 2^-13 of the power of two below the largest:
 the other 7 lose less than that each, so an output is off by up to 7 2^-13 of
 the sum of the groups' largest products more.
@@ -145,9 +145,45 @@ def test_gemm_matches_the_oracle(out, M, inf, half):
     torch.cuda.synchronize()
     assert got is Y
     err = np.abs(Y.cpu().numpy().astype(np.float64) - y_ref)
-    tol = tolerance(S, y_ref, inf, half, f8.largest_products(w8, ws, x8, xs) if half and M > 64 else 0.0)
+    tol = tolerance(S, y_ref, inf, half, f8.largest_products(w8, ws, x8, xs) if half and M > 32 else 0.0)
     assert (err <= tol).all(), f"{(err / tol).max():.3f} of the tolerance at {np.unravel_index((err / tol).argmax(), err.shape)}"
     assert torch.equal(Y, again)                           # the same bits in every run
+
+
+# every tile kind, with and without slices: tall and wide, columns of one to
+# many blocks, with and without a short last one
+TILES = [(5003, 2500, 96), (5003, 2500, 128), (5003, 2500, 288), (5003, 2500, 384), (4999, 2561, 416),
+         (5000, 2500, 1184), (4099, 2100, 640), (4099, 2100, 4128), (2050, 1500, 800), (130, 2000, 4128),
+         (4096, 100, 4096), (4100, 129, 2080), (1003, 65, 11008), (8200, 300, 544)]
+
+
+@pytest.mark.parametrize("half", [True, False], ids=["fp16", "fp32"])
+@pytest.mark.parametrize("out,M,inf", TILES)
+def test_gemm_tiles_match_the_definition_in_64_bits(out, M, inf, half):
+    """The same bounds as above, with the sums in 64 bits on the device and
+    the cut of the 8-bit instruction bounded by the sum of all products."""
+    w8, ws, x8, xs = layer(out, inf, M, out + M + inf)
+    dt = torch.float16 if half else torch.float32
+    buf = torch.full((M * out + 4096,), float("nan"), dtype=dt, device=dev())
+    Y = buf[:M * out].view(M, out)
+    args = (t_f8(w8), t_f32(ws), t_f8(x8), t_f32(xs))
+    rbq.gemm_f8(*args, dtype=dt, Y=Y)
+    again = rbq.gemm_f8(*args, dtype=dt)
+    none = rbq.gemm_f8(*args, dtype=dt, workspace=torch.empty(0, dtype=torch.uint8, device=dev()))
+    torch.cuda.synchronize()
+    assert torch.equal(Y, again) and bool(torch.isnan(buf[M * out:]).all())
+    T = -(-inf // 128)
+    cols = torch.arange(inf, device=dev()) // 128
+    w = args[0].double() * args[1].double()[torch.arange(out, device=dev()) // 128][:, cols]
+    x = args[2].double() * args[3].double().t()[:, cols]
+    y_ref = x @ w.t().contiguous()
+    S = x.abs() @ w.abs().t().contiguous()
+    # of 8 products of one group the largest is at least an eighth of their sum and at most all of it
+    t = (inf + 3 * T + 16) * 2.0 ** -23 * S + (7 * 2.0 ** -13 * S if half else 0.0)
+    if half:
+        t = 2.0 ** -11 * (y_ref.abs() + t) + 2.0 ** -25 + t
+    for got in (Y, none):
+        assert bool(((got.double() - y_ref).abs() <= t).all()), f"{((got.double() - y_ref).abs() / t).max():.3f}"
 
 
 @pytest.mark.parametrize("M", [1, 40, 300])
@@ -317,5 +353,7 @@ def test_refusals_on_the_device():
         rbq.quantize_f8(torch.empty(3, 40, dtype=torch.float16, device=dev()))
     with pytest.raises(rbq.RbqError):                       # rows that start 2 bytes off
         rbq.quantize_f8(torch.empty(129, dtype=torch.float16, device=dev())[1:].view(2, 64))
+    with pytest.raises(ValueError):                        # a workspace on the host
+        rbq.gemm_f8(W8, WS, X8, XS, workspace=torch.empty(64, dtype=torch.uint8))
     with pytest.raises(ValueError):
         rbq.gemv_f8(W8, WS, torch.empty(65, dtype=torch.float16, device=dev()))
