@@ -724,7 +724,7 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
 
 size_t rbq_qat_backward_ckpt_workspace_bytes(rbq_shape s, int32_t M) {
     if (rbq_check_shape(s) != RBQ_OK || !rbq::qat_supports(s.num_planes) || M < 1 || s.out_features == 0 ||
-        s.in_features == 0)
+        s.in_features == 0 || s.out_features > RBQ_CKPT_MAX_FEATURES || s.in_features > RBQ_CKPT_MAX_FEATURES)
         return 0;
     return rbq::qat_backward_ckpt_workspace_bytes(M, s.out_features, s.in_features, s.num_planes, s.group_size);
 }
@@ -740,6 +740,8 @@ rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales,
         return RBQ_ERR_UNSUPPORTED;
     if (M < 0 || (dscales != nullptr && dW == nullptr) || (ws_bytes > 0 && workspace == nullptr))
         return RBQ_ERR_INVALID_ARG;
+    if (s.out_features > RBQ_CKPT_MAX_FEATURES || s.in_features > RBQ_CKPT_MAX_FEATURES)
+        return RBQ_ERR_UNSUPPORTED;
     const bool some = M > 0 && s.out_features > 0 && s.in_features > 0;
     if (!some)   // an empty sum: no activations are read
         return rbq_qat_backward(planes, scales, s, nullptr, dY, M, dX, dW, dscales, workspace, ws_bytes, status_dev,

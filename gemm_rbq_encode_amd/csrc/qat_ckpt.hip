@@ -19,6 +19,7 @@
 // quotient of two 11-bit significands in [0.25, 127] that is no tie is at
 // least 2^-12 away from every half-integer.
 #include <algorithm>
+#include <type_traits>
 
 #include "rbq.h"
 #include "rbq_device.h"
@@ -120,6 +121,7 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef v4u __attribute__((aligned(2))) v4u_a2;       // 16 bytes at any fp16
+typedef v4u __attribute__((aligned(4))) v4u_a4;       // ... at any word
 
 __device__ __forceinline__ int ck_swizzle(int k, int P) { return 2 * (((k & 3) | ((k >> 1) & 12)) & (P / 2 - 1)); }
 
@@ -159,11 +161,13 @@ __device__ __forceinline__ void ck_barrier() { asm volatile("s_waitcnt lgkmcnt(0
 constexpr int CW_BK = 64;
 constexpr int CW_TM = 8;
 
+// (At least two waves per SIMD, here and below: no accumulation registers, out
+// of which the sums would have to be copied.)
 template <int WM, int WN, int TN>
-__global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
+__global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
     const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int M,
     int out, int in, int T, float *__restrict__ dW, const uint32_t *__restrict__ planes, int K,
-    float *__restrict__ parts, int tiles_j, int total) {
+    float *__restrict__ parts, int tiles_j, int tiles, int slices) {
     constexpr int THREADS = WM * WN * RBQ_WAVE;
     constexpr int CJ = WM * 128, CR = WN * TN * 16;            // tile: columns x rows of dW
     constexpr int PJ = CJ / 8, PR = CR / 8;                    // pieces of an LDS row
@@ -171,14 +175,17 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
     constexpr int NX = CW_BK * CJ / 16 / THREADS;              // 16 codes each
     constexpr int NY = CW_BK * PR / THREADS;                   // 8 values of dY each
     static_assert(NX * THREADS * 16 == CW_BK * CJ && NY * THREADS == CW_BK * PR, "staging covers the tile");
+    static_assert(NX + NY <= CW_BK / 32 * CW_TM / 2, "every piece is staged within a stage");
     extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & (RBQ_WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / RBQ_WAVE);
     const int wj = wave % WM, wr = wave / WM;
     const int li = lane & 15, g = lane >> 4;
-    const int id = xcd_run(blockIdx.x, total);
-    const int64_t j0 = (int64_t)(id % tiles_j) * CJ, r0 = (int64_t)(id / tiles_j) * CR;
+    const int id = xcd_run(blockIdx.x, tiles * slices);
+    const int tile = id % tiles, slice = id / tiles;
+    const int64_t j0 = (int64_t)(tile % tiles_j) * CJ, r0 = (int64_t)(tile / tiles_j) * CR;
+    dW += (int64_t)slice * out * in;
 
     v4f acc[CW_TM][TN];
 #pragma unroll
@@ -187,19 +194,51 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
         for (int j = 0; j < TN; ++j)
             acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
+    // Whole stages load without a branch: columns past the last repeat column
+    // 0 and rows past the last run on into the next token's (both end up in
+    // elements of dW that do not exist).  The others, which that would take
+    // past the end of dY, check every piece; tokens past the last are zero on
+    // both sides.
+    const int64_t steps = ((int64_t)M + CW_BK - 1) / CW_BK;
+    const int64_t safe = ((int64_t)M * out - 7) / out / CW_BK;   // (below 1 where M out < 7 + out)
     v4u xr[NX], yr[NY];
     uint16_t xs[NX];
-    auto load_x = [&](int64_t m0, int u) {
+    uint32_t xoff[NX], soff[NX], yoff[NY];        // elements from the first of a stage
+#pragma unroll
+    for (int u = 0; u < NX; ++u) {
         const int c = u * THREADS + tid;
-        const int64_t m = m0 + c / (CJ / 16), j = j0 + 16 * (c % (CJ / 16));
-        const bool ok = m < M && j < in;
-        xr[u] = ok ? *reinterpret_cast<const v4u *>(codes + m * in + j) : (v4u){0u, 0u, 0u, 0u};
-        xs[u] = ok ? cscales[m * T + j / F8_BLOCK] : (uint16_t)0;
+        const int64_t j = j0 + 16 * (c % (CJ / 16));
+        const uint32_t jc = j < in ? (uint32_t)j : 0u;
+        xoff[u] = (uint32_t)(c / (CJ / 16)) * (uint32_t)in + jc;
+        soff[u] = (uint32_t)(c / (CJ / 16)) * (uint32_t)T + jc / F8_BLOCK;
+    }
+#pragma unroll
+    for (int u = 0; u < NY; ++u) {
+        const int c = u * THREADS + tid;
+        const int64_t r = r0 + 8 * (c % PR);
+        yoff[u] = (uint32_t)(c / PR) * (uint32_t)out + (r < out ? (uint32_t)r : 0u);
+    }
+    auto load_x = [&](int64_t t, int u, auto whole) {
+        const int64_t m0 = t * CW_BK;
+        const bool ok = decltype(whole)::value || m0 + (u * THREADS + tid) / (CJ / 16) < M;
+        const int8_t *p = codes + m0 * in;
+        const uint16_t *q = cscales + m0 * T;
+        if (decltype(whole)::value || ok) {
+            xr[u] = *reinterpret_cast<const v4u *>(p + xoff[u]);
+            xs[u] = q[soff[u]];
+        } else {
+            xr[u] = (v4u){0u, 0u, 0u, 0u};
+            xs[u] = 0;
+        }
     };
-    auto load_y = [&](int64_t m0, int u) {
-        const int c = u * THREADS + tid;
-        const int64_t m = m0 + c / PR;
-        yr[u] = ck_piece(dY + m * out, r0 + 8 * (c % PR), out, m < M);
+    auto load_y = [&](int64_t t, int u, auto whole) {
+        const uint16_t *p = dY + t * CW_BK * out;
+        if constexpr (decltype(whole)::value) {
+            yr[u] = *reinterpret_cast<const v4u_a2 *>(p + yoff[u]);
+        } else {
+            const int c = u * THREADS + tid;
+            yr[u] = ck_piece(p + (int64_t)(c / PR) * out, r0 + 8 * (c % PR), out, t * CW_BK + c / PR < M);
+        }
     };
     auto store_x = [&](unsigned char *at, int u) {
         const int c = u * THREADS + tid;
@@ -233,56 +272,81 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
     for (int j = 0; j < TN; ++j)
         yo[j] = XB + k0 * (CR * 2) + (((wr * TN + j) * 2) ^ ck_swizzle(k0, PR)) * 16 + 8 * (li & 3);
 
-    const int64_t steps = ((int64_t)M + CW_BK - 1) / CW_BK;
-#pragma unroll
-    for (int u = 0; u < NX; ++u) {
-        load_x(0, u);
-        store_x(lds, u);
-        load_x(CW_BK, u);
-    }
-#pragma unroll
-    for (int u = 0; u < NY; ++u) {
-        load_y(0, u);
-        store_y(lds, u);
-        load_y(CW_BK, u);
-    }
-    ck_barrier();
-    for (int64_t t = 0; t < steps; ++t) {
-        const unsigned char *cur = lds + (t & 1) * STAGE;
-        unsigned char *nxt = lds + ((t + 1) & 1) * STAGE;
-        const int64_t m2 = (t + 2) * CW_BK;
+    // stage t of this slice: its products, and between them, a piece after
+    // every second row of tiles, stage t + 1 to LDS and stage t + 2 requested
+    auto stage = [&](int64_t t, int64_t first, auto whole) {
+        const unsigned char *cur = lds + ((t - first) & 1) * STAGE;
+        unsigned char *nxt = lds + ((t - first + 1) & 1) * STAGE;
 #pragma unroll
         for (int kk = 0; kk < CW_BK / 32; ++kk) {
-            v8h b[TN];
+            v8h a[2], b[TN];
+            a[0] = ck_column(cur + xo[0] + kk * 32 * (CJ * 2), CJ * 2);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
                 b[j] = ck_column(cur + yo[j] + kk * 32 * (CR * 2), CR * 2);
-            v8h a = ck_column(cur + xo[0] + kk * 32 * (CJ * 2), CJ * 2);
 #pragma unroll
             for (int i = 0; i < CW_TM; ++i) {
-                v8h an = a;
                 if (i + 1 < CW_TM)
-                    an = ck_column(cur + xo[i + 1] + kk * 32 * (CJ * 2), CJ * 2);
+                    a[(i + 1) & 1] = ck_column(cur + xo[i + 1] + kk * 32 * (CJ * 2), CJ * 2);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[j], acc[i][j], 0, 0, 0);
-                a = an;
-                // one piece of the next stages' data after every second tile row
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[i & 1], b[j], acc[i][j], 0, 0, 0);
                 const int u = (kk * CW_TM + i) / 2;
                 if (i & 1) {
                     if (u < NX) {
                         store_x(nxt, u);
-                        load_x(m2, u);
+                        load_x(t + 2, u, whole);
                     } else if (u - NX < NY) {
                         store_y(nxt, u - NX);
-                        load_y(m2, u - NX);
+                        load_y(t + 2, u - NX, whole);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        static_assert(NX + NY <= CW_BK / 32 * CW_TM / 2, "every piece is staged within a stage");
         ck_barrier();
+    };
+    // (a slice's last stages request two past its end: checked, and unused)
+    const int64_t t_lo = steps * slice / slices, t_hi = steps * (slice + 1) / slices;
+#pragma unroll
+    for (int u = 0; u < NX; ++u) {
+        load_x(t_lo, u, std::false_type());
+        store_x(lds, u);
+        load_x(t_lo + 1, u, std::false_type());
     }
+#pragma unroll
+    for (int u = 0; u < NY; ++u) {
+        load_y(t_lo, u, std::false_type());
+        store_y(lds, u);
+        load_y(t_lo + 1, u, std::false_type());
+    }
+    ck_barrier();
+    int64_t t = t_lo;
+    for (; t + 2 < std::min(t_hi, safe); ++t)
+        stage(t, t_lo, std::true_type());
+    for (; t < t_hi; ++t)
+        stage(t, t_lo, std::false_type());
+
+    // the sign words of this wave's columns, for the scales' gradients; they
+    // arrive while dW is written
+    const int64_t words = in >> 5, w0 = (j0 + wj * 128) >> 5;
+    const bool add = parts != nullptr && w0 < words;
+    v4u sign[4][TN];
+    if (add)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < K)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int64_t r = std::min<int64_t>(r0 + (wr * TN + j) * 16 + li, out - 1);
+                    const uint32_t *p = planes + ((int64_t)k * out + r) * words + w0;
+                    if (w0 + 4 <= words)
+                        sign[k][j] = *reinterpret_cast<const v4u_a4 *>(p);
+                    else
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            sign[k][j][q] = w0 + q < words ? p[q] : 0u;
+                }
 
     // lane (li, g): columns 4 g + v of a column tile, row li of a row tile
     const bool vec = ((uintptr_t)dW & 15) == 0;
@@ -306,21 +370,22 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
             }
         }
     }
-    if (parts == nullptr || j0 + wj * 128 >= in)
+    if (!add)
         return;
-    const int64_t words = in >> 5;
-    const int64_t w0 = (j0 + wj * 128) >> 5;
-    for (int k = 0; k < K; ++k) {
+    parts += (int64_t)slice * K * out * T + w0 / 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k >= K)
+            break;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t r = r0 + (wr * TN + j) * 16 + li;
-            const uint32_t *pw = planes + ((int64_t)k * out + std::min<int64_t>(r, out - 1)) * words;
             float s = 0.0f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (w0 + q >= words)
+                if (w0 + q >= words)                       // columns past the last
                     break;
-                const uint32_t w = ~pw[w0 + q] >> (4 * g);
+                const uint32_t w = ~sign[k][j][q] >> (4 * g);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -331,21 +396,22 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE) void qat_ckpt_dw_kernel(
             s += __shfl_xor(s, 16, RBQ_WAVE);
             s += __shfl_xor(s, 32, RBQ_WAVE);
             if (g == 0 && r < out)
-                parts[((int64_t)k * out + r) * T + (j0 >> 7) + wj] = s;
+                parts[((int64_t)k * out + r) * T] = s;
         }
     }
 }
 
-// dscales[n] = the sum of T parts in order, in fp64: one wave each.
-__global__ __launch_bounds__(CK_THREADS) void qat_ckpt_sum_parts(const float *__restrict__ parts, int64_t n, int T,
-                                                                 float *__restrict__ dscales) {
+// dscales[n] = the sum in fp64, slices in order, of the T parts of a row and plane: one wave each.
+__global__ __launch_bounds__(CK_THREADS) void qat_ckpt_sum_rows(const float *__restrict__ parts, int64_t n, int T,
+                                                                int slices, float *__restrict__ dscales) {
     const int lane = threadIdx.x & (RBQ_WAVE - 1);
     const int64_t i = (int64_t)blockIdx.x * (CK_THREADS / RBQ_WAVE) + threadIdx.x / RBQ_WAVE;
     if (i >= n)
         return;                                   // whole wave
     double s = 0.0;
-    for (int t = lane; t < T; t += RBQ_WAVE)
-        s += (double)parts[i * T + t];
+    for (int z = 0; z < slices; ++z)
+        for (int t = lane; t < T; t += RBQ_WAVE)
+            s += (double)parts[(z * n + i) * T + t];
     s = wave_sum_f64(s);
     if (lane == 0)
         dscales[i] = (float)s;
@@ -375,7 +441,7 @@ __device__ __forceinline__ void ck_table(_Float16 v0, _Float16 v1, uint32_t &lo,
 }
 
 template <int TM, int K>
-__global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
+__global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
     int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
     int tiles_j, int tiles_m, int total) {
@@ -404,12 +470,23 @@ __global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
         for (int j = 0; j < TM; ++j)
             acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-    // staging: 8 pieces per token row, piece p of token m at p ^ (m & 7)
+    // staging: 8 pieces per token row, piece p of token m at p ^ (m & 7).
+    // Stages that lie whole in the slice load without a branch (tokens and
+    // columns past the last repeat the last: they end up in elements of dX
+    // that do not exist); the last one checks, zero past the end on both sides.
     v4u yr[NY];
-    auto load_y = [&](int64_t rb, int u) {
+    const uint16_t *yrow[NY];
+#pragma unroll
+    for (int u = 0; u < NY; ++u) {
         const int c = u * CX_THREADS + tid;
-        const int64_t m = m0 + (c >> 3);
-        yr[u] = ck_piece(dY + m * out, rb + 8 * (c & 7), r_hi, m < M);
+        yrow[u] = dY + std::min<int64_t>(m0 + (c >> 3), M - 1) * out + 8 * (c & 7);
+    }
+    auto load_y = [&](int64_t rb, int u, auto whole) {
+        const int c = u * CX_THREADS + tid;
+        if constexpr (decltype(whole)::value)
+            yr[u] = *reinterpret_cast<const v4u_a2 *>(yrow[u] + rb);
+        else
+            yr[u] = ck_piece(dY + (m0 + (c >> 3)) * out, rb + 8 * (c & 7), r_hi, m0 + (c >> 3) < M);
     };
     auto store_y = [&](unsigned char *at, int u) {
         const int c = u * CX_THREADS + tid;
@@ -417,37 +494,47 @@ __global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
         *reinterpret_cast<v4u *>(at + m * (CX_BK * 2) + (p ^ (m & 7)) * 16) = yr[u];
     };
     const int fr = tid >> 3, fj = tid & 7;                     // this thread's row of What and 16 columns
-    const int64_t fw = (j0 >> 5) + (fj >> 1);
+    const int64_t fw = std::min((j0 >> 5) + (fj >> 1), words - 1);
     const int64_t fg = group_size ? j0 / group_size : 0;       // 128 columns lie in one group
     uint32_t bits[K];
     uint16_t sc[K];
+    const uint32_t woff = (uint32_t)fr * (uint32_t)words + (uint32_t)fw, goff = (uint32_t)fr * (uint32_t)G + (uint32_t)fg;
     bool valid = false, ovf = false;
-    auto load_w = [&](int64_t rb) {
-        const int64_t r = rb + fr;
-        valid = r < r_hi && fw < words;
+    auto load_w = [&](int64_t rb, auto whole) {
+        valid = decltype(whole)::value || rb + fr < r_hi;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            bits[k] = valid ? planes[((int64_t)k * out + r) * words + fw] : 0u;
-            sc[k] = valid ? scales[((int64_t)k * out + r) * G + fg] : (uint16_t)0;
+            const uint32_t *p = planes + ((int64_t)k * out + rb) * words;
+            const uint16_t *q = scales + ((int64_t)k * out + rb) * G;
+            if (decltype(whole)::value || valid) {
+                bits[k] = p[woff];
+                sc[k] = q[goff];
+            } else {
+                bits[k] = 0u;
+                sc[k] = 0;
+            }
         }
     };
     uint32_t hv[8], lv[8];
-    auto form = [&]() {
+    // part q = 0 .. 3 of forming: 4 columns (with one or two planes the tables come with part 0)
+    uint32_t hl = 0, hh = 0, ll = 0, lh = 0;
+    auto form = [&](int q) {
         const int sh = 16 * (fj & 1);
         if constexpr (K <= 2) {
             const uint32_t b0 = bits[0] >> sh, b1 = K > 1 ? bits[K - 1] >> sh : 0u;
-            const float a0 = h2f(sc[0]), a1 = K > 1 ? h2f(sc[K - 1]) : 0.0f;
-            // index b0 + 2 b1: -a0 - a1, a0 - a1, a1 - a0, a0 + a1 (K = 1: only the first two, b1 = 0)
-            const float w0 = -a0 - a1, w1 = a0 - a1;
-            const uint32_t diff = (b0 ^ b1) & 0xFFFFu;
-            ovf = ovf || (valid && ((diff != 0xFFFFu && !(__builtin_fabsf(w0) < 65520.0f)) ||
-                                    (diff != 0u && !(__builtin_fabsf(w1) < 65520.0f))));
-            const _Float16 h0 = (_Float16)w0, h1 = (_Float16)w1;
-            uint32_t hl, hh, ll, lh;
-            ck_table(h0, h1, hl, hh);
-            ck_table((_Float16)(w0 - (float)h0), (_Float16)(w1 - (float)h1), ll, lh);
+            if (q == 0) {
+                const float a0 = h2f(sc[0]), a1 = K > 1 ? h2f(sc[K - 1]) : 0.0f;
+                // index b0 + 2 b1: -a0 - a1, a0 - a1, a1 - a0, a0 + a1 (K = 1: only the first two, b1 = 0)
+                const float w0 = -a0 - a1, w1 = a0 - a1;
+                const uint32_t diff = (b0 ^ b1) & 0xFFFFu;
+                ovf = ovf || (valid && ((diff != 0xFFFFu && !(__builtin_fabsf(w0) < 65520.0f)) ||
+                                        (diff != 0u && !(__builtin_fabsf(w1) < 65520.0f))));
+                const _Float16 h0 = (_Float16)w0, h1 = (_Float16)w1;
+                ck_table(h0, h1, hl, hh);
+                ck_table((_Float16)(w0 - (float)h0), (_Float16)(w1 - (float)h1), ll, lh);
+            }
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
+            for (int p = 2 * q; p < 2 * q + 2; ++p) {
                 const uint32_t e = ((b0 >> (2 * p)) & 1u) | (((b1 >> (2 * p)) & 1u) << 1);
                 const uint32_t o = ((b0 >> (2 * p + 1)) & 1u) | (((b1 >> (2 * p + 1)) & 1u) << 1);
                 const uint32_t sel = (e | o << 16) * 0x101u + 0x04000400u;
@@ -456,7 +543,7 @@ __global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
             }
         } else {
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
+            for (int p = 2 * q; p < 2 * q + 2; ++p) {
                 _Float16 h[2], l[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -491,53 +578,67 @@ __global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
     for (int kk = 0; kk < 2; ++kk)
         yo[kk] = (wm * TM * 16 + li) * (CX_BK * 2) + ((4 * kk + g) ^ (li & 7)) * 16;
 
-    const int64_t steps = (r_hi - r_lo + CX_BK - 1) / CX_BK;
-    load_w(r_lo);
-    form();
-    store_w(lds);
-    load_w(r_lo + CX_BK);
-#pragma unroll
-    for (int u = 0; u < NY; ++u) {
-        load_y(r_lo, u);
-        store_y(lds, u);
-        load_y(r_lo + CX_BK, u);
-    }
-    ck_barrier();
-    for (int64_t t = 0; t < steps; ++t) {
+    // the stage at row r of What: its products, and between them, a piece after
+    // every row of tiles, the next stage to LDS and the one after it requested
+    auto stage = [&](int64_t r, auto whole) {
+        const int64_t t = (r - r_lo) / CX_BK;
         const unsigned char *cur = lds + (t & 1) * STAGE;
         unsigned char *nxt = lds + ((t + 1) & 1) * STAGE;
-        const int64_t r2 = r_lo + (t + 2) * CX_BK;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            v8h b[TM];
+            v8h b[TM], al[2], ah[2];
+            al[0] = ck_column(cur + wo[0] + HB + kk * 32 * (CX_J * 2), CX_J * 2);
 #pragma unroll
             for (int j = 0; j < TM; ++j)
                 b[j] = *reinterpret_cast<const v8h *>(cur + yo[kk] + j * 16 * (CX_BK * 2));
+            ah[0] = ck_column(cur + wo[0] + kk * 32 * (CX_J * 2), CX_J * 2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const v8h al = ck_column(cur + wo[i] + HB + kk * 32 * (CX_J * 2), CX_J * 2);
-                const v8h ah = ck_column(cur + wo[i] + kk * 32 * (CX_J * 2), CX_J * 2);
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, b[j], acc[i][j], 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, b[j], acc[i][j], 0, 0, 0);
-                const int u = kk * 4 + i;
-                if (u == 0)
-                    form();
-                else if (u == 1) {
-                    store_w(nxt);
-                    load_w(r2);
-                } else if (u - 2 < NY) {
-                    store_y(nxt, u - 2);
-                    load_y(r2, u - 2);
+                if (i + 1 < 4) {
+                    al[(i + 1) & 1] = ck_column(cur + wo[i + 1] + HB + kk * 32 * (CX_J * 2), CX_J * 2);
+                    ah[(i + 1) & 1] = ck_column(cur + wo[i + 1] + kk * 32 * (CX_J * 2), CX_J * 2);
                 }
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al[i & 1], b[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[i & 1], b[j], acc[i][j], 0, 0, 0);
+                const int u = kk * 4 + i;
+                if (u < 4)
+                    form(u);
+                if (u == 4) {
+                    store_w(nxt);
+                    load_w(r + 2 * CX_BK, whole);
+                }
+                if (u >= 4 && u - 4 < NY) {
+                    store_y(nxt, u - 4);
+                    load_y(r + 2 * CX_BK, u - 4, whole);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        static_assert(NY <= 6, "every piece is staged within a stage");
+        static_assert(NY <= 4, "every piece is staged within a stage");
         ck_barrier();
+    };
+    load_w(r_lo, std::false_type());
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        form(q);
+    store_w(lds);
+    load_w(r_lo + CX_BK, std::false_type());
+#pragma unroll
+    for (int u = 0; u < NY; ++u) {
+        load_y(r_lo, u, std::false_type());
+        store_y(lds, u);
+        load_y(r_lo + CX_BK, u, std::false_type());
     }
+    ck_barrier();
+    int64_t r = r_lo;
+    for (; r + 3 * CX_BK <= r_hi; r += CX_BK)
+        stage(r, std::true_type());
+    for (; r < r_hi; r += CX_BK)
+        stage(r, std::false_type());
 
     const bool vec = ((uintptr_t)dX & 15) == 0;
 #pragma unroll
@@ -564,31 +665,31 @@ __global__ __launch_bounds__(CX_THREADS) void qat_ckpt_dx_kernel(
         atomicOr(status, (int)RBQ_STATUS_SCALE_OVERFLOW);
 }
 
-// dX = the sum of the S partial slices, in slice order.
+// to = the sum of the S partial slices, in slice order.
 __global__ __launch_bounds__(CK_THREADS) void qat_ckpt_sum_slices(const float *__restrict__ parts, int S, int64_t n,
-                                                                  float *__restrict__ dX) {
-    const int64_t i = (int64_t)blockIdx.x * CK_THREADS + threadIdx.x;
-    if (i >= n)
-        return;
-    float v = parts[i];
-    for (int z = 1; z < S; ++z)
-        v += parts[z * n + i];
-    dX[i] = v;
+                                                                  float *__restrict__ to) {
+    for (int64_t i = (int64_t)blockIdx.x * CK_THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * CK_THREADS) {
+        float v = parts[i];
+        for (int z = 1; z < S; ++z)
+            v += parts[z * n + i];
+        to[i] = v;
+    }
 }
 
 constexpr int LDS_MAX = 160 * 1024;
 
 template <int WM, int WN, int TN>
 hipError_t launch_dw(const uint16_t *dY, const int8_t *codes, const uint16_t *cscales, int M, int out, int in,
-                     float *dW, const uint32_t *planes, int K, float *parts, hipStream_t st) {
+                     float *dW, const uint32_t *planes, int K, float *parts, int slices, hipStream_t st) {
     constexpr int CJ = WM * 128, CR = WN * TN * 16;
     constexpr int LDS = 2 * CW_BK * (CJ + CR) * 2;
     static_assert(LDS <= LDS_MAX, "LDS of a compute unit");
-    const int64_t tiles_j = ((int64_t)in + CJ - 1) / CJ, total = tiles_j * (((int64_t)out + CR - 1) / CR);
-    if (total > 0x7FFFFFFF / (WM * WN * RBQ_WAVE))
+    const int64_t tiles_j = ((int64_t)in + CJ - 1) / CJ, tiles = tiles_j * (((int64_t)out + CR - 1) / CR);
+    if (tiles * slices > 0x7FFFFFFF / (WM * WN * RBQ_WAVE))
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((qat_ckpt_dw_kernel<WM, WN, TN>), dim3((unsigned)total), dim3(WM * WN * RBQ_WAVE), LDS, st, dY,
-                       codes, cscales, M, out, in, f8_blocks(in), dW, planes, K, parts, (int)tiles_j, (int)total);
+    hipLaunchKernelGGL((qat_ckpt_dw_kernel<WM, WN, TN>), dim3((unsigned)(tiles * slices)), dim3(WM * WN * RBQ_WAVE),
+                       LDS, st, dY, codes, cscales, M, out, in, f8_blocks(in), dW, planes, K, parts, (int)tiles_j,
+                       (int)tiles, slices);
     return hipGetLastError();
 }
 
@@ -614,24 +715,94 @@ hipError_t launch_dx(const uint16_t *dY, const uint32_t *planes, const uint16_t 
     return hipGetLastError();
 }
 
-// Tokens per dX tile in units of 64, and slices of its contraction: enough
-// workgroups for one per compute unit, at most 16 slices of at least 256 rows.
-int dx_tokens(int M) { return M > 64 ? 4 : 1; }
+// Both plans take the least of a simple cost in us: rounds of workgroups over
+// the compute units, each a start and end and its stages, and for slices a
+// second launch and the write and read of the partial sums at 5 TB/s.
 
-int dx_slices(int M, int out, int in) {
-    const int cm = 64 * dx_tokens(M);
-    const int64_t tiles = ((int64_t)in + CX_J - 1) / CX_J * (((int64_t)M + cm - 1) / cm);
-    const int64_t S = std::min<int64_t>({(256 + tiles - 1) / tiles, 16, std::max(1, out / 256)});
-    return (int)std::max<int64_t>(S, 1);
+float slice_cost(int S, int64_t n) { return S > 1 ? 4.0f + (float)n * (float)(2 * S + 1) * (4.0f / 5.0e6f) : 0.0f; }
+
+// Tokens per dX tile in units of 64: 16 tokens on 4096 x 4096 take 19 us in
+// tiles of 64; tiles of 256 multiply 16 times the zeros.
+int dx_tokens(int M) { return M > 128 ? 4 : M > 64 ? 2 : 1; }
+
+// Slices of dX's contraction.  Measured (one slice and the choice): 16 tokens,
+// 4096 x 4096: 71 and 19 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and
+// 165 us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens,
+// 11008 x 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.
+int dx_slices(int M, int out, int in, int K) {
+    static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    const int tm = dx_tokens(M);
+    const float stage = tm == 1 ? 1.1f : tm == 2 ? 1.4f : K > 2 ? 2.7f : 2.0f;
+    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + 64 * tm - 1) / (64 * tm));
+    const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
+    int best = 1;
+    float least = 0.0f;
+    for (const int S : splits) {
+        if (S > 1 && 2 * S > steps)
+            break;
+        const float cost = (float)((tiles * S + 255) / 256) * ((float)((steps + S - 1) / S) * stage + 4.0f) +
+                           slice_cost(S, (int64_t)M * in);
+        if (S == 1 || cost < least) {
+            best = S;
+            least = cost;
+        }
+    }
+    return best;
 }
 
-size_t dx_slice_bytes(int M, int out, int in) {
-    const int S = dx_slices(M, out, in);
+size_t dx_slice_bytes(int M, int out, int in, int K) {
+    const int S = dx_slices(M, out, in, K);
     return S > 1 ? (size_t)S * (size_t)M * (size_t)in * sizeof(float) : 0;
 }
 
-size_t dw_part_bytes(int out, int in, int K, int group_size) {
-    return group_size || in <= F8_BLOCK ? 0 : (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
+// dW's tiles (256 x 256, one workgroup per compute unit; or 128 x 128, two) and
+// slices of its tokens.  Measured with the scales' gradients: 2048 tokens,
+// 11008 x 4096: 248 us large, 338 small; 300 tokens, 2000 x 2048: 33 large, 20
+// small; 2000 tokens, 600 x 576: 38 us in one slice of 25 small tiles, 25 in 4.
+struct dw_plan {
+    int large, slices;
+};
+
+dw_plan plan_dw(int M, int out, int in) {
+    static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
+    const int64_t steps = ((int64_t)M + CW_BK - 1) / CW_BK;
+    dw_plan best = {1, 1};
+    float least = 0.0f;
+    for (int large = 0; large < 2; ++large)
+        for (const int S : splits) {
+            if (S > 1 && 2 * S > steps)
+                break;
+            const int edge = large ? 256 : 128;
+            const int64_t wgs = (((int64_t)in + edge - 1) / edge) * (((int64_t)out + edge - 1) / edge) * S;
+            const float n = (float)((steps + S - 1) / S);
+            float cost = large        ? (float)((wgs + 255) / 256) * (n * 1.9f + 8.0f)
+                         : wgs <= 256 ? n * 1.1f + 6.0f
+                                      : (float)((wgs + 511) / 512) * (n * 1.6f + 8.0f);
+            cost += slice_cost(S, (int64_t)out * in);
+            if (least == 0.0f || cost < least) {
+                least = cost;
+                best = {large, S};
+            }
+        }
+    return best;
+}
+
+// Partial sums of dW's slices, and behind them the parts of the scales' gradients.
+size_t dw_slice_bytes(int M, int out, int in) {
+    const int S = plan_dw(M, out, in).slices;
+    return S > 1 ? (size_t)S * (size_t)out * (size_t)in * sizeof(float) : 0;
+}
+
+size_t dw_part_bytes(int M, int out, int in, int K, int group_size) {
+    const int S = plan_dw(M, out, in).slices;
+    return S == 1 && (group_size || in <= F8_BLOCK)
+               ? 0 : (size_t)S * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
+}
+
+hipError_t launch_sum(const float *parts, int S, int64_t n, float *to, hipStream_t st) {
+    hipLaunchKernelGGL(qat_ckpt_sum_slices, dim3((unsigned)std::min<int64_t>((n + CK_THREADS - 1) / CK_THREADS, 1 << 20)),
+                       dim3(CK_THREADS), 0, st, parts, S, n, to);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -645,10 +816,10 @@ hipError_t launch_qat_checkpoint(const uint16_t *X, int M, int in, int8_t *codes
     return hipGetLastError();
 }
 
-// dW and its parts come first on the stream, the slices of dX after their sum:
-// both may use the same memory.
+// dW comes first on the stream, the slices of dX after its sums: both may use
+// the same memory.
 size_t qat_backward_ckpt_workspace_bytes(int M, int out, int in, int K, int group_size) {
-    return std::max(dx_slice_bytes(M, out, in), dw_part_bytes(out, in, K, group_size));
+    return std::max(dx_slice_bytes(M, out, in, K), dw_slice_bytes(M, out, in) + dw_part_bytes(M, out, in, K, group_size));
 }
 
 hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
@@ -657,21 +828,32 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
                                     void *workspace, size_t ws_bytes, int32_t *status, hipStream_t st) {
     hipError_t e = hipSuccess;
     if (dW != nullptr) {
-        // the sums of a tile go straight to dscales where a tile's columns
-        // are a whole group, else through the workspace; without one the
-        // scales' gradients are taken from dW in a pass of its own
-        const size_t need = dw_part_bytes(out, in, K, group_size);
-        const bool fused = dscales != nullptr && ws_bytes >= need;
-        float *parts = !fused ? nullptr : need ? static_cast<float *>(workspace) : dscales;
-        const int64_t large = ((int64_t)in + 255) / 256 * (((int64_t)out + 255) / 256);
-        e = large >= 200 ? launch_dw<2, 4, 4>(dY, x_codes, x_scales, M, out, in, dW, planes, K, parts, st)
-                         : launch_dw<1, 4, 2>(dY, x_codes, x_scales, M, out, in, dW, planes, K, parts, st);
+        // The sums of a tile go straight to dscales where a tile's columns are
+        // a whole group and the tokens are not sliced, else through the
+        // workspace.  Without one, tokens are not sliced and the scales'
+        // gradients are taken from dW in a pass of its own.
+        dw_plan p = plan_dw(M, out, in);
+        const size_t slice_bytes = dw_slice_bytes(M, out, in), part_bytes = dw_part_bytes(M, out, in, K, group_size);
+        const bool fits = ws_bytes >= slice_bytes + part_bytes;
+        if (!fits)
+            p.slices = 1;
+        const bool fused = dscales != nullptr && fits;
+        float *dst = p.slices > 1 ? static_cast<float *>(workspace) : dW;
+        float *parts = !fused ? nullptr
+                       : part_bytes ? reinterpret_cast<float *>(static_cast<char *>(workspace) + slice_bytes)
+                                    : dscales;
+        e = p.large ? launch_dw<2, 4, 4>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st)
+                    : launch_dw<1, 4, 2>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st);
+        if (e == hipSuccess && p.slices > 1)
+            e = launch_sum(dst, p.slices, (int64_t)out * in, dW, st);
         if (e != hipSuccess)
             return e;
-        if (fused && need) {
-            const int64_t n = (int64_t)K * out;
-            hipLaunchKernelGGL(qat_ckpt_sum_parts, dim3((unsigned)((n + 3) / 4)), dim3(CK_THREADS), 0, st, parts, n,
-                               f8_blocks(in), dscales);
+        const int64_t rows = (int64_t)K * out;
+        if (fused && part_bytes && group_size) {
+            e = launch_sum(parts, p.slices, rows * f8_blocks(in), dscales, st);
+        } else if (fused && part_bytes) {
+            hipLaunchKernelGGL(qat_ckpt_sum_rows, dim3((unsigned)((rows + 3) / 4)), dim3(CK_THREADS), 0, st, parts,
+                               rows, f8_blocks(in), p.slices, dscales);
             e = hipGetLastError();
         } else if (dscales != nullptr && !fused) {
             e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st);
@@ -680,21 +862,19 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
             return e;
     }
     if (dX != nullptr) {
-        int S = dx_slices(M, out, in);
-        if (ws_bytes < dx_slice_bytes(M, out, in))
+        int S = dx_slices(M, out, in, K);
+        if (ws_bytes < dx_slice_bytes(M, out, in, K))
             S = 1;
         const int64_t r_slice = (((int64_t)out + S - 1) / S + CX_BK - 1) / CX_BK * CX_BK;
         S = (int)(((int64_t)out + r_slice - 1) / r_slice);
         float *dst = S > 1 ? static_cast<float *>(workspace) : dX;
-        e = dx_tokens(M) == 4
-                ? launch_dx<4>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st)
-                : launch_dx<1>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st);
-        if (e != hipSuccess || S == 1)
-            return e;
-        const int64_t n = (int64_t)M * in;
-        hipLaunchKernelGGL(qat_ckpt_sum_slices, dim3((unsigned)((n + CK_THREADS - 1) / CK_THREADS)),
-                           dim3(CK_THREADS), 0, st, static_cast<const float *>(workspace), S, n, dX);
-        e = hipGetLastError();
+        switch (dx_tokens(M)) {
+        case 1: e = launch_dx<1>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
+        case 2: e = launch_dx<2>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
+        default: e = launch_dx<4>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
+        }
+        if (e == hipSuccess && S > 1)
+            e = launch_sum(dst, S, (int64_t)M * in, dX, st);
     }
     return e;
 }

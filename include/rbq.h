@@ -639,6 +639,9 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
 rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features, int8_t *codes, uint16_t *scales,
                               void *stream);
 
+/* Most rows and columns of a layer that rbq_qat_backward_ckpt handles. */
+#define RBQ_CKPT_MAX_FEATURES      (1 << 25)
+
 /*
  * rbq_qat_backward_ckpt -- rbq_qat_backward from a checkpoint: the same
  * gradients, with x^ in the place of X:
@@ -653,7 +656,8 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
  *   workspace  device memory of rbq_qat_backward_ckpt_workspace_bytes(s, M)
  *              bytes; rules as for rbq_qat_backward
  * Other arguments, rules (any of dX, dW may be NULL; dscales needs dW) and
- * errors as rbq_qat_backward.
+ * errors as rbq_qat_backward, and RBQ_ERR_UNSUPPORTED for more than
+ * RBQ_CKPT_MAX_FEATURES rows or columns.
  */
 size_t rbq_qat_backward_ckpt_workspace_bytes(rbq_shape s, int32_t M);
 rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, rbq_shape s,

@@ -102,7 +102,9 @@ def check_grads(got, planes, s, x, dY, group):
 
 BACKWARD = [(256, 512, 2, 0, 5), (384, 1024, 4, 128, 130), (100, 4128, 3, 0, 33), (64, 96, 1, 0, 1),
             (1000, 2048, 2, 0, 16), (1024, 1280, 4, 128, 257), (33, 160, 2, 0, 70), (513, 288, 1, 0, 65),
-            (8, 32, 2, 0, 3), (129, 128, 3, 128, 2), (264, 544, 2, 0, 511)]
+            (8, 32, 2, 0, 3), (129, 128, 3, 128, 2), (264, 544, 2, 0, 511), (3, 64, 1, 0, 200), (1, 32, 2, 0, 129),
+            (5, 96, 4, 0, 64), (600, 576, 2, 0, 1100), (601, 640, 4, 128, 1030), (1501, 384, 1, 0, 100),
+            (4100, 96, 3, 0, 20)]
 
 
 @pytest.mark.parametrize("out,inf,K,group,M", BACKWARD)
@@ -117,6 +119,39 @@ def test_backward_matches_the_oracle(out, inf, K, group, M):
     assert int(st.item()) == 0
     check_grads(got, planes, s, f8.restore(*f8.checkpoint(X)), dY, group)
     assert all(torch.equal(a, b) for a, b in zip(got, again))       # the same bits in every run
+    less = rbq.qat_backward_ckpt(*args, workspace=torch.empty(0, dtype=torch.uint8, device=dev()))
+    check_grads(less, planes, s, f8.restore(*f8.checkpoint(X)), dY, group)
+
+
+LARGE = [(4101, 4128, 2, 0, 131), (3900, 4224, 4, 128, 65), (4096, 4096, 1, 0, 320), (700, 4096, 3, 0, 700),
+         (8200, 1024, 2, 128, 257)]
+
+
+@pytest.mark.parametrize("out,inf,K,group,M", LARGE)
+def test_backward_of_large_layers_in_64_bits(out, inf, K, group, M):
+    """The bounds above, with the sums in 64 bits on the device; once with the
+    workspace and once without."""
+    planes, s, X, dY = case(out, inf, K, group, M, out + M)
+    codes, cs = rbq.qat_checkpoint(t_f16(X))
+    a = (t_planes(planes), t_f16(s), codes, cs, t_f16(dY), group)
+    x = t_f16(f8.restore(codes.cpu().numpy(), cs.cpu().numpy().view(np.uint16))).double()
+    d = t_f16(dY).double()
+    w = torch.from_numpy(qat.dequant(planes, s, group)).to(dev()).double()
+    G = inf // group if group else 1
+    dw = d.t().contiguous() @ x
+    t_dw = 2.0 * M * U * (d.abs().t().contiguous() @ x.abs()) + 1e-300
+    dx = d @ w
+    t_dx = d.abs() @ (2.0 ** -21 * w.abs() + 2.0 ** -25) + 4.0 * out * U * (d.abs() @ w.abs()) + 1e-300
+    sums = (t_dw + 128 * U * dw.abs()).view(out, G, -1).sum(2)
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=dev())):
+        gdx, gdw, gds = rbq.qat_backward_ckpt(*a, workspace=ws)
+        assert bool(((gdw.double() - dw).abs() <= t_dw).all()), "dW"
+        assert bool(((gdx.double() - dx).abs() <= t_dx).all()), "dX"
+        word = a[0].long() & 0xFFFFFFFF
+        for k in range(K):
+            sign = torch.stack([(word[k] >> b) & 1 for b in range(32)], -1).view(out, inf).double() * 2 - 1
+            ds = (sign * dw).view(out, G, -1).sum(2)
+            assert bool(((gds[k].double() - ds).abs() <= sums + 2.0 ** -23 * ds.abs() + 1e-300).all()), "dscales"
 
 
 def test_backward_of_exact_activations_is_the_fp16_backwards():
