@@ -156,7 +156,7 @@ __device__ __forceinline__ void ck_barrier() { asm volatile("s_waitcnt lgkmcnt(0
 // wave adds its 128 columns from the registers it has just computed and
 // writes one value per row and plane to parts [K][out][ceil(in / 128)], which
 // are the group gradients themselves for groups of 128 and are added in order
-// by qat_ckpt_sum_parts for scales per row.
+// at the end for scales per row.
 
 constexpr int CW_BK = 64;
 constexpr int CW_TM = 8;
@@ -399,22 +399,6 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
                 parts[((int64_t)k * out + r) * T] = s;
         }
     }
-}
-
-// dscales[n] = the sum in fp64, slices in order, of the T parts of a row and plane: one wave each.
-__global__ __launch_bounds__(CK_THREADS) void qat_ckpt_sum_rows(const float *__restrict__ parts, int64_t n, int T,
-                                                                int slices, float *__restrict__ dscales) {
-    const int lane = threadIdx.x & (RBQ_WAVE - 1);
-    const int64_t i = (int64_t)blockIdx.x * (CK_THREADS / RBQ_WAVE) + threadIdx.x / RBQ_WAVE;
-    if (i >= n)
-        return;                                   // whole wave
-    double s = 0.0;
-    for (int z = 0; z < slices; ++z)
-        for (int t = lane; t < T; t += RBQ_WAVE)
-            s += (double)parts[(z * n + i) * T + t];
-    s = wave_sum_f64(s);
-    if (lane == 0)
-        dscales[i] = (float)s;
 }
 
 // ---------------------------------------------------------------------------
@@ -665,14 +649,48 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
         atomicOr(status, (int)RBQ_STATUS_SCALE_OVERFLOW);
 }
 
-// to = the sum of the S partial slices, in slice order.
-__global__ __launch_bounds__(CK_THREADS) void qat_ckpt_sum_slices(const float *__restrict__ parts, int S, int64_t n,
-                                                                  float *__restrict__ to) {
-    for (int64_t i = (int64_t)blockIdx.x * CK_THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * CK_THREADS) {
-        float v = parts[i];
-        for (int z = 1; z < S; ++z)
-            v += parts[z * n + i];
-        to[i] = v;
+// What is left to add at the end, in one launch: up to three jobs, each with a
+// share of the workgroups.  A job sums, for each of n outputs, `slices` groups
+// of `parts` consecutive values in a fixed order: by one thread in fp32 where
+// a group is one value (slices of dW or dX, gradients of group scales), else
+// by one wave in fp64 (gradients of row scales).
+struct ck_job {
+    const float *from;
+    float *to;
+    int64_t n;
+    int slices, parts;
+    unsigned blocks;
+};
+
+struct ck_jobs {
+    ck_job job[3];
+};
+
+__global__ __launch_bounds__(CK_THREADS) void qat_ckpt_join_kernel(ck_jobs jobs) {
+    unsigned b = blockIdx.x;
+    int q = 0;
+    while (q < 2 && b >= jobs.job[q].blocks)
+        b -= jobs.job[q++].blocks;
+    const ck_job &o = jobs.job[q];
+    if (o.parts == 1) {
+        for (int64_t i = (int64_t)b * CK_THREADS + threadIdx.x; i < o.n; i += (int64_t)o.blocks * CK_THREADS) {
+            float v = o.from[i];
+            for (int z = 1; z < o.slices; ++z)
+                v += o.from[z * o.n + i];
+            o.to[i] = v;
+        }
+        return;
+    }
+    const int lane = threadIdx.x & (RBQ_WAVE - 1);
+    constexpr int WAVES = CK_THREADS / RBQ_WAVE;
+    for (int64_t i = (int64_t)b * WAVES + threadIdx.x / RBQ_WAVE; i < o.n; i += (int64_t)o.blocks * WAVES) {
+        double s = 0.0;
+        for (int z = 0; z < o.slices; ++z)
+            for (int t = lane; t < o.parts; t += RBQ_WAVE)
+                s += (double)o.from[(z * o.n + i) * o.parts + t];
+        s = wave_sum_f64(s);
+        if (lane == 0)
+            o.to[i] = (float)s;
     }
 }
 
@@ -799,10 +817,9 @@ size_t dw_part_bytes(int M, int out, int in, int K, int group_size) {
                ? 0 : (size_t)S * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
 }
 
-hipError_t launch_sum(const float *parts, int S, int64_t n, float *to, hipStream_t st) {
-    hipLaunchKernelGGL(qat_ckpt_sum_slices, dim3((unsigned)std::min<int64_t>((n + CK_THREADS - 1) / CK_THREADS, 1 << 20)),
-                       dim3(CK_THREADS), 0, st, parts, S, n, to);
-    return hipGetLastError();
+ck_job sum_job(const float *from, float *to, int64_t n, int slices, int parts) {
+    const int64_t blocks = parts == 1 ? (n + CK_THREADS - 1) / CK_THREADS : (n + 3) / 4;
+    return {from, to, n, slices, parts, (unsigned)std::min<int64_t>(blocks, 1 << 18)};
 }
 
 }  // namespace
@@ -816,65 +833,69 @@ hipError_t launch_qat_checkpoint(const uint16_t *X, int M, int in, int8_t *codes
     return hipGetLastError();
 }
 
-// dW comes first on the stream, the slices of dX after its sums: both may use
-// the same memory.
+// One after another: slices of dW, parts of the scales' gradients, slices of dX.
 size_t qat_backward_ckpt_workspace_bytes(int M, int out, int in, int K, int group_size) {
-    return std::max(dx_slice_bytes(M, out, in, K), dw_slice_bytes(M, out, in) + dw_part_bytes(M, out, in, K, group_size));
+    return dw_slice_bytes(M, out, in) + dw_part_bytes(M, out, in, K, group_size) + dx_slice_bytes(M, out, in, K);
 }
 
 hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
                                     int group_size, const int8_t *x_codes, const uint16_t *x_scales,
                                     const uint16_t *dY, int M, float *dX, float *dW, float *dscales,
                                     void *workspace, size_t ws_bytes, int32_t *status, hipStream_t st) {
+    // With less than the whole workspace nothing is sliced, and the scales'
+    // gradients that would pass through it are taken from dW in a pass of
+    // their own.
+    const bool fits = ws_bytes >= qat_backward_ckpt_workspace_bytes(M, out, in, K, group_size);
+    float *ws = static_cast<float *>(workspace);
+    ck_jobs left = {};
+    int jobs = 0;
     hipError_t e = hipSuccess;
     if (dW != nullptr) {
-        // The sums of a tile go straight to dscales where a tile's columns are
-        // a whole group and the tokens are not sliced, else through the
-        // workspace.  Without one, tokens are not sliced and the scales'
-        // gradients are taken from dW in a pass of its own.
         dw_plan p = plan_dw(M, out, in);
-        const size_t slice_bytes = dw_slice_bytes(M, out, in), part_bytes = dw_part_bytes(M, out, in, K, group_size);
-        const bool fits = ws_bytes >= slice_bytes + part_bytes;
+        const size_t part_bytes = dw_part_bytes(M, out, in, K, group_size);
         if (!fits)
             p.slices = 1;
-        const bool fused = dscales != nullptr && fits;
-        float *dst = p.slices > 1 ? static_cast<float *>(workspace) : dW;
-        float *parts = !fused ? nullptr
-                       : part_bytes ? reinterpret_cast<float *>(static_cast<char *>(workspace) + slice_bytes)
-                                    : dscales;
+        float *dst = dW, *parts = nullptr;
+        if (p.slices > 1) {
+            dst = ws;
+            left.job[jobs++] = sum_job(dst, dW, (int64_t)out * in, p.slices, 1);
+            ws += (int64_t)p.slices * out * in;
+        }
+        if (dscales != nullptr && part_bytes == 0) {
+            parts = dscales;                    // a tile's columns are a whole group, and all its tokens
+        } else if (dscales != nullptr && fits) {
+            parts = ws;
+            const int64_t rows = (int64_t)K * out;
+            left.job[jobs++] = group_size ? sum_job(parts, dscales, rows * f8_blocks(in), p.slices, 1)
+                                          : sum_job(parts, dscales, rows, p.slices, f8_blocks(in));
+            ws += part_bytes / sizeof(float);
+        }
         e = p.large ? launch_dw<2, 4, 4>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st)
                     : launch_dw<1, 4, 2>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st);
-        if (e == hipSuccess && p.slices > 1)
-            e = launch_sum(dst, p.slices, (int64_t)out * in, dW, st);
-        if (e != hipSuccess)
-            return e;
-        const int64_t rows = (int64_t)K * out;
-        if (fused && part_bytes && group_size) {
-            e = launch_sum(parts, p.slices, rows * f8_blocks(in), dscales, st);
-        } else if (fused && part_bytes) {
-            hipLaunchKernelGGL(qat_ckpt_sum_rows, dim3((unsigned)((rows + 3) / 4)), dim3(CK_THREADS), 0, st, parts,
-                               rows, f8_blocks(in), p.slices, dscales);
-            e = hipGetLastError();
-        } else if (dscales != nullptr && !fused) {
+        if (e == hipSuccess && dscales != nullptr && parts == nullptr)
             e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st);
-        }
         if (e != hipSuccess)
             return e;
     }
     if (dX != nullptr) {
-        int S = dx_slices(M, out, in, K);
-        if (ws_bytes < dx_slice_bytes(M, out, in, K))
-            S = 1;
+        int S = fits ? dx_slices(M, out, in, K) : 1;
         const int64_t r_slice = (((int64_t)out + S - 1) / S + CX_BK - 1) / CX_BK * CX_BK;
         S = (int)(((int64_t)out + r_slice - 1) / r_slice);
-        float *dst = S > 1 ? static_cast<float *>(workspace) : dX;
+        float *dst = S > 1 ? ws : dX;
+        if (S > 1)
+            left.job[jobs++] = sum_job(dst, dX, (int64_t)M * in, S, 1);
         switch (dx_tokens(M)) {
         case 1: e = launch_dx<1>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
         case 2: e = launch_dx<2>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
         default: e = launch_dx<4>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
         }
-        if (e == hipSuccess && S > 1)
-            e = launch_sum(dst, S, (int64_t)M * in, dX, st);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (jobs) {
+        const unsigned blocks = left.job[0].blocks + left.job[1].blocks + left.job[2].blocks;
+        hipLaunchKernelGGL(qat_ckpt_join_kernel, dim3(blocks), dim3(CK_THREADS), 0, st, left);
+        e = hipGetLastError();
     }
     return e;
 }
