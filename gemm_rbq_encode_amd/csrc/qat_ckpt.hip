@@ -433,6 +433,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     constexpr int YB = CM * CX_BK * 2, HB = CX_BK * CX_J * 2, STAGE = YB + 2 * HB;
     constexpr int NY = CM * (CX_BK / 8) / CX_THREADS;          // 8 values of dY each
     constexpr int PJ = CX_J / 8;
+    // stages whose loads are in flight: the short stages of few tokens need two
+    constexpr int SETS = TM == 4 ? 1 : 2;
     extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & (RBQ_WAVE - 1);
@@ -458,87 +460,98 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     // Stages that lie whole in the slice load without a branch (tokens and
     // columns past the last repeat the last: they end up in elements of dX
     // that do not exist); the last one checks, zero past the end on both sides.
-    v4u yr[NY];
+    v4u yr[SETS][NY];
     const uint16_t *yrow[NY];
 #pragma unroll
     for (int u = 0; u < NY; ++u) {
         const int c = u * CX_THREADS + tid;
         yrow[u] = dY + std::min<int64_t>(m0 + (c >> 3), M - 1) * out + 8 * (c & 7);
     }
-    auto load_y = [&](int64_t rb, int u, auto whole) {
+    auto load_y = [&](int64_t rb, int u, auto whole, int set) {
         const int c = u * CX_THREADS + tid;
         if constexpr (decltype(whole)::value)
-            yr[u] = *reinterpret_cast<const v4u_a2 *>(yrow[u] + rb);
+            yr[set][u] = *reinterpret_cast<const v4u_a2 *>(yrow[u] + rb);
         else
-            yr[u] = ck_piece(dY + (m0 + (c >> 3)) * out, rb + 8 * (c & 7), r_hi, m0 + (c >> 3) < M);
+            yr[set][u] = ck_piece(dY + (m0 + (c >> 3)) * out, rb + 8 * (c & 7), r_hi, m0 + (c >> 3) < M);
     };
-    auto store_y = [&](unsigned char *at, int u) {
+    auto store_y = [&](unsigned char *at, int u, int set) {
         const int c = u * CX_THREADS + tid;
         const int m = c >> 3, p = c & 7;
-        *reinterpret_cast<v4u *>(at + m * (CX_BK * 2) + (p ^ (m & 7)) * 16) = yr[u];
+        *reinterpret_cast<v4u *>(at + m * (CX_BK * 2) + (p ^ (m & 7)) * 16) = yr[set][u];
     };
     const int fr = tid >> 3, fj = tid & 7;                     // this thread's row of What and 16 columns
     const int64_t fw = std::min((j0 >> 5) + (fj >> 1), words - 1);
     const int64_t fg = group_size ? j0 / group_size : 0;       // 128 columns lie in one group
-    uint32_t bits[K];
-    uint16_t sc[K];
+    uint32_t bits[SETS][K];
+    uint16_t sc[SETS][K];
+    bool valid[SETS] = {}, ovf = false;
     const uint32_t woff = (uint32_t)fr * (uint32_t)words + (uint32_t)fw, goff = (uint32_t)fr * (uint32_t)G + (uint32_t)fg;
-    bool valid = false, ovf = false;
-    auto load_w = [&](int64_t rb, auto whole) {
-        valid = decltype(whole)::value || rb + fr < r_hi;
+    const int sh = 16 * (fj & 1);
+    auto load_w = [&](int64_t rb, auto whole, int set) {
+        valid[set] = decltype(whole)::value || rb + fr < r_hi;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const uint32_t *p = planes + ((int64_t)k * out + rb) * words;
             const uint16_t *q = scales + ((int64_t)k * out + rb) * G;
-            if (decltype(whole)::value || valid) {
-                bits[k] = p[woff];
-                sc[k] = q[goff];
+            if (decltype(whole)::value || valid[set]) {
+                bits[set][k] = p[woff] >> sh;
+                sc[set][k] = q[goff];
             } else {
-                bits[k] = 0u;
-                sc[k] = 0;
+                bits[set][k] = 0u;
+                sc[set][k] = 0;
             }
         }
     };
     uint32_t hv[8], lv[8];
-    // part q = 0 .. 3 of forming: 4 columns (with one or two planes the tables come with part 0)
-    uint32_t hl = 0, hh = 0, ll = 0, lh = 0;
-    auto form = [&](int q) {
-        const int sh = 16 * (fj & 1);
-        if constexpr (K <= 2) {
-            const uint32_t b0 = bits[0] >> sh, b1 = K > 1 ? bits[K - 1] >> sh : 0u;
-            if (q == 0) {
-                const float a0 = h2f(sc[0]), a1 = K > 1 ? h2f(sc[K - 1]) : 0.0f;
+    // part q = 0 .. 3 of forming: 4 columns; what is common to the row comes with part 0
+    uint32_t hl = 0, hh = 0, ll = 0, lh = 0, even = 0, odd = 0;
+    float a[K];
+    auto form = [&](int q, int set) {
+        if (q == 0) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                a[k] = h2f(sc[set][k]);
+                sum += __builtin_fabsf(a[k]);
+            }
+            // no weight of the row is beyond the sum of its scales: only
+            // where that is beyond fp16 are the weights looked at
+            if (valid[set] && !(sum < 65520.0f))
+                for (int c = 0; c < 16; ++c) {
+                    float w = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        w += (bits[set][k] >> c) & 1u ? a[k] : -a[k];
+                    ovf = ovf || !(__builtin_fabsf(w) < 65520.0f);
+                }
+            if constexpr (K <= 2) {
                 // index b0 + 2 b1: -a0 - a1, a0 - a1, a1 - a0, a0 + a1 (K = 1: only the first two, b1 = 0)
-                const float w0 = -a0 - a1, w1 = a0 - a1;
-                const uint32_t diff = (b0 ^ b1) & 0xFFFFu;
-                ovf = ovf || (valid && ((diff != 0xFFFFu && !(__builtin_fabsf(w0) < 65520.0f)) ||
-                                        (diff != 0u && !(__builtin_fabsf(w1) < 65520.0f))));
+                const uint32_t b0 = bits[set][0], b1 = K > 1 ? bits[set][K - 1] : 0u;
+                const float a1 = K > 1 ? a[K - 1] : 0.0f, w0 = -a[0] - a1, w1 = a[0] - a1;
                 const _Float16 h0 = (_Float16)w0, h1 = (_Float16)w1;
                 ck_table(h0, h1, hl, hh);
                 ck_table((_Float16)(w0 - (float)h0), (_Float16)(w1 - (float)h1), ll, lh);
+                even = (b0 & 0x5555u) | ((b1 & 0x5555u) << 1);
+                odd = ((b0 >> 1) & 0x5555u) | (b1 & 0xAAAAu);
             }
+        }
 #pragma unroll
-            for (int p = 2 * q; p < 2 * q + 2; ++p) {
-                const uint32_t e = ((b0 >> (2 * p)) & 1u) | (((b1 >> (2 * p)) & 1u) << 1);
-                const uint32_t o = ((b0 >> (2 * p + 1)) & 1u) | (((b1 >> (2 * p + 1)) & 1u) << 1);
-                const uint32_t sel = (e | o << 16) * 0x101u + 0x04000400u;
+        for (int p = 2 * q; p < 2 * q + 2; ++p) {
+            if constexpr (K <= 2) {
+                const uint32_t i = ((even >> (2 * p)) & 3u) | ((odd >> (2 * p)) & 3u) << 16;
+                const uint32_t sel = i * 0x101u + 0x04000400u;
                 hv[p] = __builtin_amdgcn_perm(hh, hl, sel);
                 lv[p] = __builtin_amdgcn_perm(lh, ll, sel);
-            }
-        } else {
-#pragma unroll
-            for (int p = 2 * q; p < 2 * q + 2; ++p) {
+            } else {
                 _Float16 h[2], l[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float w = 0.0f;
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        w += __uint_as_float(__float_as_uint(h2f(sc[k])) ^
-                                             ((~(bits[k] >> sh) << (31 - 2 * p - e)) & 0x80000000u));
-                    ovf = ovf || (valid && !(__builtin_fabsf(w) < 65520.0f));
+                        w += __uint_as_float(__float_as_uint(a[k]) ^ ((~bits[set][k] << (31 - 2 * p - e)) & 0x80000000u));
                     h[e] = (_Float16)w;
-                    l[e] = (_Float16)(w - (float)h[e]);
+                    l[e] = (_Float16)__builtin_fmaf((float)h[e], -1.0f, w);
                 }
                 hv[p] = ck_pack(h[0], h[1]);
                 lv[p] = ck_pack(l[0], l[1]);
@@ -563,9 +576,11 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
         yo[kk] = (wm * TM * 16 + li) * (CX_BK * 2) + ((4 * kk + g) ^ (li & 7)) * 16;
 
     // the stage at row r of What: its products, and between them, a piece after
-    // every row of tiles, the next stage to LDS and the one after it requested
-    auto stage = [&](int64_t r, auto whole) {
-        const int64_t t = (r - r_lo) / CX_BK;
+    // every row of tiles, the next stage (from register set `next`) to LDS and
+    // the one SETS behind it requested
+    auto stage = [&](int64_t r, auto whole, auto next) {
+        constexpr int set = decltype(next)::value;
+        const int64_t t = (r - r_lo) / CX_BK, ahead = r + (1 + SETS) * CX_BK;
         const unsigned char *cur = lds + (t & 1) * STAGE;
         unsigned char *nxt = lds + ((t + 1) & 1) * STAGE;
 #pragma unroll
@@ -590,14 +605,14 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[i & 1], b[j], acc[i][j], 0, 0, 0);
                 const int u = kk * 4 + i;
                 if (u < 4)
-                    form(u);
+                    form(u, set);
                 if (u == 4) {
                     store_w(nxt);
-                    load_w(r + 2 * CX_BK, whole);
+                    load_w(ahead, whole, set);
                 }
                 if (u >= 4 && u - 4 < NY) {
-                    store_y(nxt, u - 4);
-                    load_y(r + 2 * CX_BK, u - 4, whole);
+                    store_y(nxt, u - 4, set);
+                    load_y(ahead, u - 4, whole, set);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -605,24 +620,37 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
         static_assert(NY <= 4, "every piece is staged within a stage");
         ck_barrier();
     };
-    load_w(r_lo, std::false_type());
+    constexpr std::integral_constant<int, 0> set0;
+    constexpr std::integral_constant<int, SETS - 1> set1;     // of odd stages
+    load_w(r_lo, std::false_type(), 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        form(q);
+        form(q, 0);
     store_w(lds);
-    load_w(r_lo + CX_BK, std::false_type());
 #pragma unroll
     for (int u = 0; u < NY; ++u) {
-        load_y(r_lo, u, std::false_type());
-        store_y(lds, u);
-        load_y(r_lo + CX_BK, u, std::false_type());
+        load_y(r_lo, u, std::false_type(), 0);
+        store_y(lds, u, 0);
+    }
+#pragma unroll
+    for (int d = 1; d <= SETS; ++d) {
+        load_w(r_lo + d * CX_BK, std::false_type(), d % SETS);
+#pragma unroll
+        for (int u = 0; u < NY; ++u)
+            load_y(r_lo + d * CX_BK, u, std::false_type(), d % SETS);
     }
     ck_barrier();
     int64_t r = r_lo;
-    for (; r + 3 * CX_BK <= r_hi; r += CX_BK)
-        stage(r, std::true_type());
-    for (; r < r_hi; r += CX_BK)
-        stage(r, std::false_type());
+    for (; r + (3 + SETS) * CX_BK <= r_hi; r += 2 * CX_BK) {
+        stage(r, std::true_type(), set1);
+        stage(r + CX_BK, std::true_type(), set0);
+    }
+    for (; r < r_hi; r += CX_BK) {
+        stage(r, std::false_type(), set1);
+        r += CX_BK;
+        if (r < r_hi)
+            stage(r, std::false_type(), set0);
+    }
 
     const bool vec = ((uintptr_t)dX & 15) == 0;
 #pragma unroll
