@@ -596,11 +596,14 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
 // ---- linears in 8-bit floating point blocks of 128 ---------------------------
 
 static bool f8_shape_ok(int32_t out, int32_t in) { return out >= 0 && in >= 0 && in % 32 == 0; }
+static bool f8_too_large(int32_t out, int32_t in) { return out > RBQ_F8_MAX_FEATURES || in > RBQ_F8_MAX_FEATURES; }
 
 rbq_status rbq_encode_f8(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes, float *scales,
                          int32_t *status_dev, void *stream) {
     if (!f8_shape_ok(out_features, in_features))
         return RBQ_ERR_INVALID_ARG;
+    if (f8_too_large(out_features, in_features))
+        return RBQ_ERR_UNSUPPORTED;
     if (out_features == 0 || in_features == 0)
         return RBQ_OK;
     if (W == nullptr || codes == nullptr || scales == nullptr)
@@ -620,6 +623,8 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
                            void *stream) {
     if (M < 0 || !f8_shape_ok(0, in_features))
         return RBQ_ERR_INVALID_ARG;
+    if (f8_too_large(0, in_features))
+        return RBQ_ERR_UNSUPPORTED;
     if (M == 0 || in_features == 0)
         return RBQ_OK;
     if (X == nullptr || codes == nullptr || scales == nullptr)
@@ -635,7 +640,7 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
 
 size_t rbq_gemm_f8_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type) {
     if (M < 1 || out_features < 1 || in_features < 32 || in_features % 32 != 0 ||
-        (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
+        f8_too_large(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
         return 0;
     return rbq::gemm_f8_workspace_bytes(out_features, in_features, M, y_type == RBQ_Y_F32);
 }
@@ -646,6 +651,8 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
     if (M < 0 || !f8_shape_ok(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32) ||
         (ws_bytes > 0 && workspace == nullptr))
         return RBQ_ERR_INVALID_ARG;
+    if (f8_too_large(out_features, in_features))
+        return RBQ_ERR_UNSUPPORTED;
     if (M == 0 || out_features == 0)
         return RBQ_OK;
     if (Y == nullptr)
@@ -679,6 +686,8 @@ rbq_status rbq_gemv_f8(const uint8_t *codes, const float *scales, int32_t out_fe
                        const uint16_t *x, uint16_t *y, void *stream) {
     if (!f8_shape_ok(out_features, in_features))
         return RBQ_ERR_INVALID_ARG;
+    if (f8_too_large(out_features, in_features))
+        return RBQ_ERR_UNSUPPORTED;
     if (out_features == 0)
         return RBQ_OK;
     if (y == nullptr)
@@ -709,6 +718,8 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
                               void *stream) {
     if (M < 0 || !f8_shape_ok(0, in_features))
         return RBQ_ERR_INVALID_ARG;
+    if (in_features > RBQ_CKPT_MAX_FEATURES)
+        return RBQ_ERR_UNSUPPORTED;
     if (M == 0 || in_features == 0)
         return RBQ_OK;
     if (X == nullptr || codes == nullptr || scales == nullptr)

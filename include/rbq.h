@@ -611,6 +611,9 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
                             const uint16_t *dY, int32_t M, float *dX, float *dW, float *dscales, void *workspace,
                             size_t ws_bytes, int32_t *status, void *stream);
 
+/* Most rows and columns of a layer that the calls on checkpoints handle. */
+#define RBQ_CKPT_MAX_FEATURES      (1 << 25)
+
 /*
  * 8-bit activation checkpoints.  Training keeps the input X of every layer
  * for the weight gradient (RaBiT summary, section 4.2 and "RaBiT training"
@@ -633,14 +636,11 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
  *   codes   device, 16-byte aligned, written;  scales  device, 2-byte
  *           aligned, written.  They may not overlap X.
  *   in_features  a multiple of 32;  M == 0 or in == 0 enqueues nothing
- * Errors: RBQ_ERR_INVALID_ARG, RBQ_ERR_ALIGNMENT, RBQ_ERR_NO_DEVICE,
- * RBQ_ERR_HIP.
+ * Errors: RBQ_ERR_INVALID_ARG, RBQ_ERR_ALIGNMENT, RBQ_ERR_UNSUPPORTED
+ * (in_features > RBQ_CKPT_MAX_FEATURES), RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
  */
 rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features, int8_t *codes, uint16_t *scales,
                               void *stream);
-
-/* Most rows and columns of a layer that rbq_qat_backward_ckpt handles. */
-#define RBQ_CKPT_MAX_FEATURES      (1 << 25)
 
 /*
  * rbq_qat_backward_ckpt -- rbq_qat_backward from a checkpoint: the same
@@ -678,7 +678,8 @@ rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales,
  *   X   codes uint8 [M][in],   scales fp32 [T][M]: one per token and block of
  *       128 columns (a block's scales of all tokens side by side)
  * with T = ceil(in / 128); blocks at the edges are smaller.  A value is its
- * code times its scale.  in_features is a multiple of 32 throughout.
+ * code times its scale.  in_features is a multiple of 32 throughout; more than
+ * RBQ_F8_MAX_FEATURES rows or columns are RBQ_ERR_UNSUPPORTED.
  * The transposed layer (dX = dY W) is the product with the transposed codes
  * and the transposed scales: blocks of 128 x 128 stay blocks (out must then
  * be a multiple of 32).
@@ -688,6 +689,9 @@ rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales,
  * every rounding to nearest even.  A block with a NaN or infinite entry has
  * scale NaN and codes 0.
  * ------------------------------------------------------------------------- */
+
+/* Most rows and columns of a layer that the calls of this section handle. */
+#define RBQ_F8_MAX_FEATURES        (1 << 25)
 
 /*
  * rbq_encode_f8 -- codes and scales of a weight.

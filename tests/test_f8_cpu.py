@@ -152,6 +152,34 @@ def test_f8_argument_errors():
     assert L.rbq_gemv_f8(None, None, 0, 64, None, None, None) == E.RBQ_OK
 
 
+def test_layers_beyond_the_limit_are_refused():
+    L, un, big = rbq.lib(), rbq.RBQ_ERR_UNSUPPORTED, (1 << 25) + 32
+    assert L.rbq_encode_f8(OK, big, 64, OK, OK, None, None) == un
+    assert L.rbq_encode_f8(OK, 8, big, OK, OK, None, None) == un
+    assert L.rbq_quantize_f8(OK, 2, big, OK, OK, None) == un
+    assert L.rbq_gemm_f8(OK, OK, big, 64, OK, OK, 2, OK, 0, None, 0, None) == un
+    assert L.rbq_gemv_f8(OK, OK, 8, big, OK, OK, None) == un
+    assert L.rbq_qat_checkpoint(OK, 2, big, OK, OK, None) == un
+    for s in (rbq.shape(big, 64, 2, 0), rbq.shape(8, big, 2, 0)):
+        assert L.rbq_qat_backward_ckpt(OK, OK, s, OK, OK, OK, 4, OK, OK, OK, None, 0, None, None) == un
+        assert L.rbq_qat_backward_ckpt_workspace_bytes(s, 4) == 0
+    assert L.rbq_gemm_f8_workspace_bytes(big, 64, 300, 0) == 0
+
+
+def test_workspaces_are_no_larger_than_their_slices():
+    """A handful of slices of the outputs at most, for every size."""
+    L = rbq.lib()
+    for out in (1, 5, 500, 4096, 11008, 1 << 25):
+        for inf in (32, 512, 4128, 14336, 1 << 25):
+            for M in (1, 33, 128, 2048, 1 << 20, 2 ** 31 - 1):
+                for kind in (0, 1):
+                    n = L.rbq_gemm_f8_workspace_bytes(out, inf, M, kind)
+                    assert n % (4 * M * out) == 0 and n <= 8 * 4 * M * out
+                s = rbq.shape(out, inf, 4, 0)
+                n = L.rbq_qat_backward_ckpt_workspace_bytes(s, M)
+                assert n <= 4 * (8 * out * inf + 8 * 4 * out * (inf // 128 + 1) + 32 * M * inf)
+
+
 def test_checkpoint_argument_errors():
     L, E = rbq.lib(), rbq
     bad, al = E.RBQ_ERR_INVALID_ARG, E.RBQ_ERR_ALIGNMENT
