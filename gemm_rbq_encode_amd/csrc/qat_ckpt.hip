@@ -407,7 +407,10 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
 // Tiles of 64 TM tokens x 128 columns, 64 rows r per stage; waves 4 x 2.  A
 // thread forms 16 columns of one row.  With one or two planes a row has four
 // values, which a byte permute looks up from two 8-byte tables (hi and lo)
-// two columns at a time; with three and four the sums are formed one by one.
+// two columns at a time; with three and four it has eight and their
+// negatives, each worked out by one of the eight lanes of the row and passed
+// round, in byte tables that are looked up four columns at a time (1003
+// tokens, 5120 x 5120, K = 4: 158 us; with every sum formed by itself 183).
 
 constexpr int CX_BK = 64;
 constexpr int CX_J = 128;
@@ -422,6 +425,41 @@ __device__ __forceinline__ void ck_table(_Float16 v0, _Float16 v1, uint32_t &lo,
     const uint32_t a = ck_pack(v0, v1), b = ck_pack(v1, v0) ^ 0x80008000u;
     lo = __builtin_amdgcn_perm(b, a, 0x06040200u);
     hi = __builtin_amdgcn_perm(b, a, 0x07050301u);
+}
+
+// The same byte tables of eight values, one from each of the 8 lanes that form
+// a row (fj: the lane's place, v: fp16 hi | lo << 16): of the hi and of the lo
+// parts, the low bytes t[0], t[1] of values 0 .. 3 and 4 .. 7, the high bytes
+// t[2], t[3].  Three exchanges, each doubling what a lane holds.
+__device__ __forceinline__ void ck_table8(uint32_t v, int fj, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    auto dpp = [](uint32_t x, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xF, 0xF, false);
+    };
+    constexpr std::integral_constant<int, 0xB1> by1;       // quad_perm 1 0 3 2
+    constexpr std::integral_constant<int, 0x4E> by2;       // quad_perm 2 3 0 1
+    constexpr std::integral_constant<int, 0x141> other4;   // row_half_mirror: a lane of the other four
+    const uint32_t v1 = dpp(v, by1);
+    // bytes L0 L1 H0 H1 of the even and the odd lane (perm: bytes 0 .. 3 are the second operand's)
+    const bool b0 = fj & 1, b1 = fj & 2, b2 = fj & 4;
+    const uint32_t h2 = __builtin_amdgcn_perm(v1, v, b0 ? 0x01050004u : 0x05010400u);
+    const uint32_t l2 = __builtin_amdgcn_perm(v1, v, b0 ? 0x03070206u : 0x07030602u);
+    const uint32_t h3 = dpp(h2, by2), l3 = dpp(l2, by2);
+    const uint32_t sl = b1 ? 0x01000504u : 0x05040100u, sh = b1 ? 0x03020706u : 0x07060302u;
+    const uint32_t own[4] = {__builtin_amdgcn_perm(h3, h2, sl), __builtin_amdgcn_perm(h3, h2, sh),
+                             __builtin_amdgcn_perm(l3, l2, sl), __builtin_amdgcn_perm(l3, l2, sh)};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t o = dpp(own[q], other4);
+        uint32_t *t = (q < 2 ? hi : lo) + 2 * (q & 1);
+        t[0] = b2 ? o : own[q];
+        t[1] = b2 ? own[q] : o;
+    }
+}
+
+// The four nibbles of a 16-bit number, one to a byte.
+__device__ __forceinline__ uint32_t ck_nibbles(uint32_t x) {
+    const uint32_t z = __builtin_amdgcn_perm(0u, x, 0x0C010C00u);       // bytes 0 and 1 to 0 and 2
+    return (z & 0x000F000Fu) | ((z << 4) & 0x0F000F00u);
 }
 
 template <int TM, int K>
@@ -504,7 +542,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     };
     uint32_t hv[8], lv[8];
     // part q = 0 .. 3 of forming: 4 columns; what is common to the row comes with part 0
-    uint32_t hl = 0, hh = 0, ll = 0, lh = 0, even = 0, odd = 0;
+    uint32_t hl = 0, hh = 0, ll = 0, lh = 0, even = 0, odd = 0;        // K <= 2
+    uint32_t ht[4], lt[4], nib[K], hp[2], lp[2];                       // K >= 3
     float a[K];
     auto form = [&](int q, int set) {
         if (q == 0) {
@@ -533,28 +572,58 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
                 ck_table((_Float16)(w0 - (float)h0), (_Float16)(w1 - (float)h1), ll, lh);
                 even = (b0 & 0x5555u) | ((b1 & 0x5555u) << 1);
                 odd = ((b0 >> 1) & 0x5555u) | (b1 & 0xAAAAu);
+            } else {
+                // the values with the last plane's bit set (the others are
+                // their negatives), by the bits that differ from it
+                float w = fj & 1 ? -a[0] : a[0];
+#pragma unroll
+                for (int k = 1; k + 1 < K; ++k)
+                    w += fj >> k & 1 ? -a[k] : a[k];
+                w += a[K - 1];
+                const _Float16 h = (_Float16)w;
+                ck_table8(ck_pack(h, (_Float16)(w - (float)h)), fj, ht, lt);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    nib[k] = ck_nibbles(k + 1 < K ? bits[set][k] ^ bits[set][K - 1] : ~bits[set][k]);
             }
         }
+        if constexpr (K <= 2) {
 #pragma unroll
-        for (int p = 2 * q; p < 2 * q + 2; ++p) {
-            if constexpr (K <= 2) {
+            for (int p = 2 * q; p < 2 * q + 2; ++p) {
                 const uint32_t i = ((even >> (2 * p)) & 3u) | ((odd >> (2 * p)) & 3u) << 16;
                 const uint32_t sel = i * 0x101u + 0x04000400u;
                 hv[p] = __builtin_amdgcn_perm(hh, hl, sel);
                 lv[p] = __builtin_amdgcn_perm(lh, ll, sel);
+            }
+        } else {
+            // columns q, q + 4, q + 8, q + 12: a byte of the index each
+            uint32_t sel = (nib[0] >> q) & 0x01010101u;
+#pragma unroll
+            for (int k = 1; k + 1 < K; ++k)
+                sel |= ((nib[k] >> q) & 0x01010101u) << k;
+            const uint32_t sign = ((nib[K - 1] >> q) & 0x01010101u) << 7;
+            const uint32_t h0 = __builtin_amdgcn_perm(ht[1], ht[0], sel);
+            const uint32_t h1 = __builtin_amdgcn_perm(ht[3], ht[2], sel) ^ sign;
+            const uint32_t l0 = __builtin_amdgcn_perm(lt[1], lt[0], sel);
+            const uint32_t l1 = __builtin_amdgcn_perm(lt[3], lt[2], sel) ^ sign;
+            // columns q and q + 4, q + 8 and q + 12; with those of the column before, the pairs
+            const uint32_t ha = __builtin_amdgcn_perm(h1, h0, 0x05010400u), hb = __builtin_amdgcn_perm(h1, h0, 0x07030602u);
+            const uint32_t la = __builtin_amdgcn_perm(l1, l0, 0x05010400u), lb = __builtin_amdgcn_perm(l1, l0, 0x07030602u);
+            if (q & 1) {
+                const int p = q >> 1;
+                hv[p] = __builtin_amdgcn_perm(ha, hp[0], 0x05040100u);
+                hv[p + 2] = __builtin_amdgcn_perm(ha, hp[0], 0x07060302u);
+                hv[p + 4] = __builtin_amdgcn_perm(hb, hp[1], 0x05040100u);
+                hv[p + 6] = __builtin_amdgcn_perm(hb, hp[1], 0x07060302u);
+                lv[p] = __builtin_amdgcn_perm(la, lp[0], 0x05040100u);
+                lv[p + 2] = __builtin_amdgcn_perm(la, lp[0], 0x07060302u);
+                lv[p + 4] = __builtin_amdgcn_perm(lb, lp[1], 0x05040100u);
+                lv[p + 6] = __builtin_amdgcn_perm(lb, lp[1], 0x07060302u);
             } else {
-                _Float16 h[2], l[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float w = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        w += __uint_as_float(__float_as_uint(a[k]) ^ ((~bits[set][k] << (31 - 2 * p - e)) & 0x80000000u));
-                    h[e] = (_Float16)w;
-                    l[e] = (_Float16)__builtin_fmaf((float)h[e], -1.0f, w);
-                }
-                hv[p] = ck_pack(h[0], h[1]);
-                lv[p] = ck_pack(l[0], l[1]);
+                hp[0] = ha;
+                hp[1] = hb;
+                lp[0] = la;
+                lp[1] = lb;
             }
         }
     };
@@ -778,7 +847,7 @@ int dx_tokens(int M) { return M > 128 ? 4 : M > 64 ? 2 : 1; }
 int dx_slices(int M, int out, int in, int K) {
     static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
     const int tm = dx_tokens(M);
-    const float stage = tm == 1 ? 1.1f : tm == 2 ? 1.4f : K > 2 ? 2.7f : 2.0f;
+    const float stage = tm == 1 ? 1.1f : tm == 2 ? 1.4f : K > 2 ? 2.4f : 2.0f;
     const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + 64 * tm - 1) / (64 * tm));
     const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
     int best = 1;
