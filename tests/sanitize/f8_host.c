@@ -37,8 +37,8 @@ static void sizes(void)
                 const uint64_t out = (uint64_t)OUTS[o], in = (uint64_t)INS[i], M = (uint64_t)TOKENS[m];
                 for (int y = 0; y <= 1; ++y) {
                     const size_t n = rbq_gemm_f8_workspace_bytes(OUTS[o], INS[i], TOKENS[m], y);
-                    CHECK(n % (4 * M * out) == 0);
-                    CHECK(n <= 8 * 4 * M * out);
+                    CHECK(n % 16 == 0);
+                    CHECK(n <= 34 * ((M + 255) / 256 * 256) * ((out + 127) / 128 * 128));
                     CHECK(M > 32 || n == 0);
                 }
                 for (int K = 1; K <= 4; ++K)

@@ -174,7 +174,7 @@ def test_workspaces_are_no_larger_than_their_slices():
             for M in (1, 33, 128, 2048, 1 << 20, 2 ** 31 - 1):
                 for kind in (0, 1):
                     n = L.rbq_gemm_f8_workspace_bytes(out, inf, M, kind)
-                    assert n % (4 * M * out) == 0 and n <= 8 * 4 * M * out
+                    assert n % 16 == 0 and n <= 8 * 4 * -(-M // 256) * 256 * -(-out // 128) * 128 * 1.05
                 s = rbq.shape(out, inf, 4, 0)
                 n = L.rbq_qat_backward_ckpt_workspace_bytes(s, M)
                 assert n <= 4 * (8 * out * inf + 8 * 4 * out * (inf // 128 + 1) + 32 * M * inf)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import gemm_rbq_encode_amd as rbq
-import workloads
+import test_gpu_f8
 from oracle import f8
 from test_gpu_qat_ckpt import case, check_grads, dev, t_f16, t_planes
 
@@ -190,3 +190,12 @@ def test_the_same_input_twice():
     p = planes.cpu().numpy().view(np.uint32)
     xb = x.cpu().numpy().view(np.uint16)
     check_grads(d, p, scales.cpu().numpy().view(np.uint16), f8.restore(*f8.checkpoint(xb)), xb, 0)
+
+
+@pytest.mark.parametrize("out,M,inf", [(5003, 777, 4128), (7568, 1066, 3040)])
+def test_gemm_of_whole_and_sliced_tiles(out, M, inf):
+    """More tiles than compute units, the last ones split: within the bounds
+    of the other tiles, with the workspace and without."""
+    need = rbq.lib().rbq_gemm_f8_workspace_bytes(out, inf, M, rbq.RBQ_Y_F32)
+    assert 0 < need < 4 * M * out
+    test_gpu_f8.test_gemm_tiles_match_the_definition_in_64_bits(out, M, inf, False)
