@@ -4,9 +4,9 @@
 //
 // A workgroup computes a tile of W's rows by tokens.  Both operands pass
 // through LDS by direct global-to-LDS loads of 16 bytes a lane: in tiles of up
-// to 128 x 256 as a ring of two to four stages of one block of 128 columns
-// each, one barrier per stage; in tiles of 256 x 256 as pieces of a block that
-// are freed and requested on their own.  The loads are inline assembly without
+// to 128 x 256 as a ring of three or four stages of one block of 128 columns
+// each, one barrier per stage; in the large ones as pieces of a block that are
+// freed and requested on their own.  The loads are inline assembly without
 // register results and their waits are explicit (the compiler would wait for
 // them before every LDS read); no other vector memory access is in flight in
 // the main loops, so that the counts are exact.
@@ -361,18 +361,23 @@ __global__ __launch_bounds__(256) void gemm_f8_sum_kernel(const float *__restric
 }
 
 // ---------------------------------------------------------------------------
-// fp16 outputs, tiles of 256 x 256.  Two whole stages (64 KB each) leave the
-// loads in bursts that are waited for; what the tile needs is a steady flow.
-// So a block is cut into pieces that are freed and requested on their own: the
-// tokens of a block (32 KB, two slots: they are read into registers once, at
-// the end of the block before), and half its rows (16 KB: 64 rows of each row
-// of waves, five slots).  Every half block has one barrier; the wait before
-// it is for the pieces that the end of this half reads ahead, with the
-// younger loads (a known number, as loads return in order) left in flight, so
-// that a piece has three halves' time to arrive.  Fragments are read one row
-// tile ahead, the next block's token fragments into the registers of the
-// current ones as their last products are issued: after a barrier the
-// products go on without a read in between.
+// fp16 outputs, tiles of 32 TM rows (256, 224 or 192) by 256 tokens.  Two
+// whole stages (64 KB each) leave the loads in bursts that are waited for;
+// what the tile needs is a steady flow.  So a block is cut into pieces that are
+// freed and requested on their own: the tokens of a block (32 KB, two slots:
+// they are read into registers once, at the end of the block before), and half
+// its rows (16 KB or less, five slots: row tiles 0 .. 3 of each row of waves,
+// and the others).  Every half block has one barrier; the wait before it is
+// for the pieces that the end of this half reads ahead, with the younger loads
+// (a known number, as loads return in order) left in flight, so that a piece
+// has three halves' time to arrive.  Fragments are read one row tile ahead,
+// the next block's token fragments into the registers of the current ones as
+// their last products are issued: after a barrier the products go on without a
+// read in between.
+//
+// The smaller tiles fill rounds that tiles of 256 rows would leave part empty.
+// A wave's 96 or 112 rows may lie in two of the weights' scale blocks, so the
+// scales are chosen by row tile (four products more per row tile).
 
 constexpr int GL_X = 256 * F8_BLOCK;              // a slot of tokens
 constexpr int GL_W = 128 * F8_BLOCK;              // a slot of half the rows
@@ -382,11 +387,16 @@ constexpr int GL_W0 = 2 * GL_X, GL_S0 = GL_W0 + GL_NW * GL_W;
 constexpr int GL_LDS = GL_S0 + 3 * GL_S;
 constexpr int GL_THREADS = 512;
 
+template <int TM>
 __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
     const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
     const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, uint16_t *__restrict__ y, int tiles_m,
     int tiles_r) {
-    constexpr int TM = 8, TN = 4;
+    constexpr int TN = 4, RT = 32 * TM, WR = 16 * TM;   // rows of the tile, of a wave
+    constexpr bool SPLIT = WR != F8_BLOCK;              // a wave's rows may lie in two scale blocks
+    constexpr int LO = TM > 6 ? 2 : 1;                  // loads of a wave for the second half's rows
+    constexpr int PO = 32 * LO;                         // its rows per row of waves in a slot
+    static_assert(TM >= 6 && TM <= 8 && PO >= WR - 64, "row tiles");
     extern __shared__ __align__(16) unsigned char lds[];
     const int lane = threadIdx.x & (RBQ_WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
@@ -398,23 +408,27 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
     int id = xcd_run(blockIdx.x, tiles_m * tiles_r);
     const int band = id / (8 * tiles_r), bw = std::min(8, tiles_m - 8 * band);
     id -= band * 8 * tiles_r;
-    const int64_t r0 = (int64_t)(id / bw) * 256, m0 = (int64_t)(8 * band + id % bw) * 256;
+    const int64_t r0 = (int64_t)(id / bw) * RT, m0 = (int64_t)(8 * band + id % bw) * 256;
 
     const uint8_t *wbase = W + r0 * in, *xbase = X + m0 * in;
     const float *sbase = xs + m0;
-    const int rlast = (int)std::min<int64_t>(out - 1 - r0, 255), mlast = (int)std::min<int64_t>(M - 1 - m0, 255);
+    const int rlast = (int)std::min<int64_t>(out - 1 - r0, RT - 1), mlast = (int)std::min<int64_t>(M - 1 - m0, 255);
     const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
-    // row of the tile that lane l loads with load i of half h: a slot has 64
-    // rows per row of waves
+    // row of the tile that lane l loads with load i of half h (with 224 rows, a
+    // quarter of the second half's places repeat a row and are not read)
     auto slot_row = [&](int h, int i, int l) {
-        const int q = (wave * 2 + i) * 8 + (l >> 3);
-        return (q >> 6) * 128 + h * 64 + (q & 63);
+        if (h == 0) {
+            const int q = (wave * 2 + i) * 8 + (l >> 3);
+            return (q >> 6) * WR + (q & 63);
+        }
+        const int q = (wave * LO + i) * 8 + (l >> 3);
+        return q / PO * WR + 64 + std::min(q % PO, WR - 65);
     };
     uint32_t woff[2][2], xoff[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < (h == 0 ? 2 : LO); ++i)
             woff[h][i] = (uint32_t)std::min(slot_row(h, i, lane), rlast) * (uint32_t)in + piece;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -435,7 +449,7 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
     auto row_slot = [&](int h) { return GL_W0 + (h % GL_NW) * GL_W; };
     auto issue_w = [&](int h, int odd, int i) {
         f8_load_lds(wbase + (int64_t)(h >> 1) * F8_BLOCK, woff[odd][i],
-                    lds0 + (uint32_t)row_slot(h) + (uint32_t)(wave * 2 + i) * 1024u);
+                    lds0 + (uint32_t)row_slot(h) + (uint32_t)(wave * (odd ? LO : 2) + i) * 1024u);
     };
 
     const uint32_t rd_lo = (uint32_t)(li * F8_BLOCK + ((g ^ (li & 7)) * 16));
@@ -446,8 +460,12 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
         return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
     };
     auto token_slot = [&](int t) { return lds + (t & 1) * GL_X + wc * TN * 16 * F8_BLOCK; };
-    auto rows_of = [&](int h) { return lds + row_slot(h) + wr * 64 * F8_BLOCK; };
-    const float *wsp = ws + std::min<int64_t>(r0 + wr * 128, out - 1) / F8_BLOCK * T;
+    auto rows_of = [&](int h, int odd) { return lds + row_slot(h) + wr * (odd ? PO : 64) * F8_BLOCK; };
+    // scale blocks of the wave's first and last row tile, and the first row tile of the second
+    const int64_t rw = std::min<int64_t>(r0 + wr * WR, out - 1), rb = rw / F8_BLOCK;
+    const float *wsp = ws + rb * T;
+    const int second = SPLIT ? (int)((rb + 1) * F8_BLOCK - rw) / 16 : TM;
+    const int64_t next_block = SPLIT && second < TM && (rb + 1) * F8_BLOCK < out ? T : 0;
 
     v4f acc[TM][TN], p[2][TN];
 #pragma unroll
@@ -457,41 +475,72 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
             acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
         p[0][j] = p[1][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
     }
-    v8i a[2], b[TN];
-    float s[TN] = {}, last[TN];                  // scales of this block, and of the one before
+    // Row tile i's products are in p[i & 1] and its sums taken beside those of
+    // row tile i + 1; the last one of an odd number takes its own at once, and
+    // has a fragment of its own, so that the next block finds the turns as
+    // this one did.
+    constexpr bool ODD = TM & 1;
+    v8i a[2 + ODD], b[TN];
+    auto at = [](int i) { return ODD && i == TM - 1 ? 2 : i & 1; };
+    // scales of the tokens in this block (times the row's, where a wave has
+    // one), of the last row tile in the block before, and of the rows
+    float s[TN] = {}, last[TN], sw[2];
+    auto row_scale = [&](int i) { return i < second ? sw[0] : sw[1]; };
 
     // The products of one half of a block, beside each the fmas of the row
     // tile before (of the block before, at its first).  wa: this half's rows,
     // wn: the next half's; bn: the next block's tokens; between(i): the loads
     // to issue behind row tile i.
-    auto half = [&](const unsigned char *wa, const unsigned char *wn, const unsigned char *bn, auto odd, auto between) {
-        constexpr int O = decltype(odd)::value;
+    auto half = [&](const unsigned char *wa, const unsigned char *wn, const unsigned char *bn, auto odd,
+                    auto between) {
+        constexpr int I0 = 4 * decltype(odd)::value, N = decltype(odd)::value ? TM - 4 : 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            constexpr int I0 = 4 * O;
+        for (int i = 0; i < N; ++i) {
             const int I = I0 + i;
-            a[(I + 1) & 1] = i < 3 ? fragment(wa, 16 * (i + 1)) : fragment(wn, 0);
+            a[I + 1 < TM ? at(I + 1) : 0] = i + 1 < N ? fragment(wa, 16 * (i + 1)) : fragment(wn, 0);
+            float f[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                f[j] = I == 0 ? last[j] : SPLIT ? s[j] * row_scale(I - 1) : s[j];
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                p[I & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[I & 1], b[j], z, 0, 0, 0, 0, 0, 0);
+                p[I & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[at(I)], b[j], z, 0, 0, 0, 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
                 if (I == TM - 1)
                     b[j] = fragment(bn, 16 * j);
                 if (I > 0)
-                    acc[I - 1][j] = f8_fma(p[(I - 1) & 1][j], s[j], acc[I - 1][j]);
-                else
-                    acc[TM - 1][j] = f8_fma(p[1][j], last[j], acc[TM - 1][j]);
+                    acc[I - 1][j] = f8_fma(p[(I - 1) & 1][j], f[j], acc[I - 1][j]);
+                else if (!ODD)
+                    acc[TM - 1][j] = f8_fma(p[1][j], f[j], acc[TM - 1][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             between(i);
         }
+        if (ODD && decltype(odd)::value)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[TM - 1][j] = f8_fma(p[0][j], s[j] * row_scale(TM - 1), acc[TM - 1][j]);
     };
     auto first_fragments = [&](const unsigned char *wa, const unsigned char *ba) {
         a[0] = fragment(wa, 0);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             b[j] = fragment(ba, 16 * j);
+    };
+    // the scales of a block: those of the tokens from sl, of the rows in sw
+    auto take_scales = [&](auto scale) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            last[j] = s[j];
+            s[j] = SPLIT ? scale(j) : scale(j) * sw[0];
+        }
+    };
+    auto keep_last = [&]() {                     // (before the rows' scales of the next block are taken)
+        if (SPLIT && !ODD)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                s[j] *= row_scale(TM - 1);
     };
 
     // requests go out in the order W 2t, X t, S t, W 2t + 1
@@ -505,30 +554,31 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
 #pragma unroll
             for (int q = 0; q < 5; ++q)
                 issue_x(t, q);
-            issue_w(2 * t + 1, 1, 0);
-            issue_w(2 * t + 1, 1, 1);
+#pragma unroll
+            for (int i = 0; i < LO; ++i)
+                issue_w(2 * t + 1, 1, i);
         }
         if (full > 1)
-            f8_landed<11>();
+            f8_landed<7 + 2 * LO>();
         else
-            f8_landed<2>();
-        first_fragments(rows_of(0), token_slot(0));
+            f8_landed<LO>();
+        first_fragments(rows_of(0, 0), token_slot(0));
     }
-    float sw = full > 0 ? wsp[0] : 0.0f;
+    sw[0] = full > 0 ? wsp[0] : 0.0f;
+    sw[1] = SPLIT && full > 0 ? wsp[next_block] : sw[0];
+    constexpr std::integral_constant<int, 0> c0;
+    constexpr std::integral_constant<int, 1> c1;
+    constexpr std::integral_constant<int, 2> c2;
     // Block t, with `more` full blocks (two: two or more) behind it.  Past the
     // last one old bytes of the slots are read, for fragments that no one uses.
     auto stage = [&](int t, auto more) {
         constexpr int MORE = decltype(more)::value;
         // second half of t; younger: W 2t + 2, X and S t + 1, W 2t + 3
-        f8_landed<(MORE > 0 ? 9 : 0)>();
-        asm volatile("" : "+s"(sw));                       // (the compiler's wait for it goes here)
+        f8_landed<(MORE > 0 ? 7 + LO : 0)>();
+        asm volatile("" : "+s"(sw[0]), "+s"(sw[1]));       // (the compiler's wait for them goes here)
         const float *sl = reinterpret_cast<const float *>(lds + GL_S0 + (t % 3) * GL_S) + wc * TN * 16 + li;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            last[j] = s[j];
-            s[j] = sl[16 * j] * sw;
-        }
-        half(rows_of(2 * t), rows_of(2 * t + 1), lds, std::integral_constant<int, 0>(), [&](int i) {
+        take_scales([&](int j) { return sl[16 * j]; });
+        half(rows_of(2 * t, 0), rows_of(2 * t + 1, 1), lds, c0, [&](int i) {
             if (MORE > 1) {
                 if (i == 0) {
                     issue_w(2 * t + 4, 0, 0);
@@ -541,21 +591,28 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
             }
         });
         // W 2t + 2 and X t + 1; younger: W 2t + 3, W 2t + 4, X and S t + 2
-        f8_landed<(MORE > 1 ? 9 : MORE > 0 ? 2 : 0)>();
-        if (MORE > 0)
-            sw = wsp[t + 1];
-        half(rows_of(2 * t + 1), rows_of(2 * t + 2), token_slot(t + 1), std::integral_constant<int, 1>(), [&](int i) {
-            if (MORE > 1 && i < 2)
+        f8_landed<(MORE > 1 ? 7 + LO : MORE > 0 ? LO : 0)>();
+        float sn[2] = {sw[0], sw[1]};
+        if (MORE > 0) {
+            sn[0] = wsp[t + 1];
+            if (SPLIT)
+                sn[1] = wsp[next_block + t + 1];
+        }
+        half(rows_of(2 * t + 1, 1), rows_of(2 * t + 2, 0), token_slot(t + 1), c1, [&](int i) {
+            if (MORE > 1 && i < LO)
                 issue_w(2 * t + 5, 1, i);
         });
+        keep_last();
+        sw[0] = sn[0];
+        sw[1] = sn[1];
     };
     int t = 0;
     for (; t + 2 < full; ++t)
-        stage(t, std::integral_constant<int, 2>());
+        stage(t, c2);
     if (t + 1 < full)
-        stage(t++, std::integral_constant<int, 1>());
+        stage(t++, c1);
     if (t < full)
-        stage(t, std::integral_constant<int, 0>());
+        stage(t, c0);
     if (full < T) {
         // the short last block, through registers, zero past the end on both
         // sides (a piece past the end is read from the row's first bytes)
@@ -577,28 +634,33 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < (h == 0 ? 2 : LO); ++i) {
                 const int64_t r = std::min(slot_row(h, i, l), rlast);
                 const uint4 v = *reinterpret_cast<const uint4 *>(wbase + r * in + at);
-                *reinterpret_cast<uint4 *>(lds + row_slot(h) + (wave * 2 + i) * 1024 + l * 16) = zero_past(v);
+                *reinterpret_cast<uint4 *>(lds + row_slot(h) + (wave * (h == 0 ? 2 : LO) + i) * 1024 + l * 16) =
+                    zero_past(v);
             }
         __syncthreads();
-        first_fragments(rows_of(0), token_slot(0));
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            last[j] = s[j];
-            s[j] = sbase[(int64_t)full * M + std::min((wc * TN + j) * 16 + li, mlast)] * wsp[full];
-        }
-        half(rows_of(0), rows_of(1), lds, std::integral_constant<int, 0>(), [](int) {});
-        half(rows_of(1), rows_of(0), lds, std::integral_constant<int, 1>(), [](int) {});
+        first_fragments(rows_of(0, 0), token_slot(0));
+        sw[0] = wsp[full];
+        sw[1] = wsp[next_block + full];
+        take_scales([&](int j) { return sbase[(int64_t)full * M + std::min((wc * TN + j) * 16 + li, mlast)]; });
+        half(rows_of(0, 0), rows_of(1, 1), lds, c0, [](int) {});
+        half(rows_of(1, 1), rows_of(0, 0), lds, c1, [](int) {});
+        keep_last();
     }
+    if (!ODD)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-        acc[TM - 1][j] = f8_fma(p[1][j], s[j], acc[TM - 1][j]);
-    f8_write_tile<TM, TN>(acc, r0 + wr * TM * 16, m0 + wc * TN * 16, li, g, out, M, y);
+        for (int j = 0; j < TN; ++j)
+            acc[TM - 1][j] = f8_fma(p[1][j], s[j], acc[TM - 1][j]);
+    f8_write_tile<TM, TN>(acc, r0 + wr * WR, m0 + wc * TN * 16, li, g, out, M, y);
 }
 
-// Tile sizes (rows x tokens), tiles computed whole, and slices of the others.
+// Kinds of tiles (rows x tokens); the first are those of the large kernel.
+constexpr int F8_LARGE = 3, F8_KINDS = 6;
+constexpr int F8_ROWS[F8_KINDS] = {256, 224, 192, 128, 128, 64}, F8_TOKENS[F8_KINDS] = {256, 256, 256, 256, 128, 128};
+
+// The kind, tiles computed whole, and slices of the others.
 struct f8_plan {
     int kind, whole, slices;
 };
@@ -622,11 +684,12 @@ hipError_t launch_tile(const uint8_t *W, const float *ws, int out, int in, const
     return hipGetLastError();
 }
 
+template <int TM>
 hipError_t launch_large(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
                         uint16_t *y, hipStream_t st) {
-    const int tiles_m = (int)(((int64_t)M + 255) / 256), tiles_r = (int)(((int64_t)out + 255) / 256);
-    hipLaunchKernelGGL(gemm_f8_large_kernel, dim3((unsigned)(tiles_m * tiles_r)), dim3(GL_THREADS), GL_LDS, st, W, ws,
-                       out, in, f8_blocks(in), X, xs, M, y, tiles_m, tiles_r);
+    const int tiles_m = (int)(((int64_t)M + 255) / 256), tiles_r = (int)(((int64_t)out + 32 * TM - 1) / (32 * TM));
+    hipLaunchKernelGGL((gemm_f8_large_kernel<TM>), dim3((unsigned)(tiles_m * tiles_r)), dim3(GL_THREADS), GL_LDS, st,
+                       W, ws, out, in, f8_blocks(in), X, xs, M, y, tiles_m, tiles_r);
     return hipGetLastError();
 }
 
@@ -634,41 +697,43 @@ template <typename Y>
 hipError_t launch_tiles(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
                         Y *y, float *parts, f8_plan p, hipStream_t st) {
     switch (p.kind) {
-    case 1: return launch_tile<2, 4, 4, 4, 3>(W, ws, out, in, X, xs, M, y, parts, p, st);
-    case 2: return launch_tile<2, 2, 4, 4, 4>(W, ws, out, in, X, xs, M, y, parts, p, st);
+    case F8_LARGE: return launch_tile<2, 4, 4, 4, 3>(W, ws, out, in, X, xs, M, y, parts, p, st);
+    case F8_LARGE + 1: return launch_tile<2, 2, 4, 4, 4>(W, ws, out, in, X, xs, M, y, parts, p, st);
     default: return launch_tile<2, 2, 2, 4, 4>(W, ws, out, in, X, xs, M, y, parts, p, st);
     }
 }
-
-constexpr int F8_KINDS = 4;
-constexpr int F8_ROWS[F8_KINDS] = {256, 128, 128, 64}, F8_TOKENS[F8_KINDS] = {256, 256, 128, 128};
 
 // The choice is the least of a simple cost: every kind keeps one workgroup per
 // compute unit, so a launch takes ceil(workgroups / 256) rounds of its blocks'
 // stages and a start of 2.5 us each; slices add a second launch and the write
 // and read of the partial sums.  Stage times measured on full launches: us per
-// block 1.8, 1.05, 0.68, 0.47 (fp16 outputs; 256 x 256 serves only those), and
-// 1.95, 1.1, 0.75.  It picked the fastest kind, or one within 7 % of it, for 65
+// block 1.8, 1.62, 1.42, 1.05, 0.68, 0.47 (fp16 outputs; the large tiles serve
+// only those), and 1.95, 1.1, 0.75.  It picked the fastest kind, or one within 7 % of it, for 65
 // to 2048 tokens on 1000 to 14336 rows; e.g. 128 tokens, 4096 x 4096: 14.6 us
 // with 64 x 128 in 4 slices, 48.9 with 256 x 256; 2048 tokens: 39.3 with
 // 128 x 256, 54.9 with 256 x 256, 67.2 with 64 x 128; 1024 tokens, 11008 x
-// 4096: 63.0 with 256 x 256, 73.4 with 128 x 256.  Slices for the last round
+// 4096: 63.0 with 256 x 256, 73.4 with 128 x 256.  Tiles of 192 rows, one round
+// in place of one and a third or of a part empty one: 2048 tokens, 6144 x 4096:
+// 64.2 us with 256 rows, 59.1 with 192; 1024 tokens, 11008 x 4096: 63.3 and
+// 56.8; of 224: 2048 tokens, 11008 x 4096: 120.3 and 113.2; 14336 x 4096: 133.3
+// and 131.2.  Slices for the last round
 // only: fp32 outputs, 777 tokens, 5003 x 4128 (256 + 24 tiles of 128 x 128):
 // 73.0 us without, 63.1 with them; 1066 tokens, 7568 x 3040: 85.5 and 74;
 // fp16, 300 tokens, 11008 x 4096: 37.3 and 33.2.
 f8_plan plan_tiles(int out, int in, int M, int y_f32) {
-    static constexpr float stage[2][F8_KINDS] = {{1.8f, 1.05f, 0.68f, 0.47f}, {0.0f, 1.95f, 1.1f, 0.75f}};
+    static constexpr float stage[2][F8_KINDS] = {{1.8f, 1.62f, 1.42f, 1.05f, 0.68f, 0.47f},
+                                                 {0.0f, 0.0f, 0.0f, 1.95f, 1.1f, 0.75f}};
     static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
     const int T = f8_blocks(in);
-    f8_plan best = {1, 0, 1};
+    f8_plan best = {F8_LARGE, 0, 1};
     float least = 0.0f;
-    for (int k = y_f32 ? 1 : 0; k < F8_KINDS; ++k) {
+    for (int k = y_f32 ? F8_LARGE : 0; k < F8_KINDS; ++k) {
         const int64_t tiles = (((int64_t)out + F8_ROWS[k] - 1) / F8_ROWS[k]) *
                               (((int64_t)M + F8_TOKENS[k] - 1) / F8_TOKENS[k]);
         // (the whole rounds computed whole, or every tile cut)
         for (int64_t whole = tiles / 256 * 256;; whole = 0) {
             for (const int S : splits) {
-                if (S > 1 && (k == 0 || 2 * S > T))
+                if (S > 1 && (k < F8_LARGE || 2 * S > T))
                     break;
                 const int64_t cut = tiles - whole;
                 float cost = (float)(whole / 256) * ((float)T * stage[y_f32][k] + 2.5f) +
@@ -713,8 +778,12 @@ hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int i
     if (y_f32)
         return launch_tiles(W, ws, out, in, X, xs, M, static_cast<float *>(y), parts, p, st);
     uint16_t *o = static_cast<uint16_t *>(y);
-    return p.kind == 0 ? launch_large(W, ws, out, in, X, xs, M, o, st)
-                       : launch_tiles(W, ws, out, in, X, xs, M, o, parts, p, st);
+    switch (p.kind) {
+    case 0: return launch_large<8>(W, ws, out, in, X, xs, M, o, st);
+    case 1: return launch_large<7>(W, ws, out, in, X, xs, M, o, st);
+    case 2: return launch_large<6>(W, ws, out, in, X, xs, M, o, st);
+    default: return launch_tiles(W, ws, out, in, X, xs, M, o, parts, p, st);
+    }
 }
 
 }  // namespace rbq

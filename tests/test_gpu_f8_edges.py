@@ -199,3 +199,14 @@ def test_gemm_of_whole_and_sliced_tiles(out, M, inf):
     need = rbq.lib().rbq_gemm_f8_workspace_bytes(out, inf, M, rbq.RBQ_Y_F32)
     assert 0 < need < 4 * M * out
     test_gpu_f8.test_gemm_tiles_match_the_definition_in_64_bits(out, M, inf, False)
+
+
+# one round of tiles of 256, 224 and 192 rows by 256 tokens; no, one and
+# several whole blocks of columns, with and without a short last one
+HEIGHTS = [(out, M, inf) for out, M in [(8191, 2047), (7168, 2041), (7001, 2048), (6140, 2000), (6144, 2048)]
+           for inf in (64, 128, 288, 384, 640)] + [(7167, 2048, 2144), (6143, 2048, 2144), (8190, 2048, 2144)]
+
+
+@pytest.mark.parametrize("out,M,inf", HEIGHTS)
+def test_gemm_tiles_of_every_height(out, M, inf):
+    test_gpu_f8.test_gemm_tiles_match_the_definition_in_64_bits(out, M, inf, True)
