@@ -161,13 +161,13 @@ __device__ __forceinline__ void ck_barrier() { asm volatile("s_waitcnt lgkmcnt(0
 constexpr int CW_BK = 64;
 constexpr int CW_TM = 8;
 
-// (At least two waves per SIMD, here and below: no accumulation registers, out
-// of which the sums would have to be copied.)
-template <int WM, int WN, int TN>
-__global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
-    const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int M,
-    int out, int in, int T, float *__restrict__ dW, const uint32_t *__restrict__ planes, int K,
-    float *__restrict__ parts, int tiles_j, int tiles, int slices) {
+// ONE: a single stage (up to 64 tokens): one buffer, and no staging between
+// the products.  KP: planes whose sign words a lane holds.
+template <int WM, int WN, int TN, bool ONE, int KP>
+__device__ __forceinline__ void ck_dw(
+    unsigned char *lds, int id, const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes,
+    const uint16_t *__restrict__ cscales, int M, int out, int in, int T, float *__restrict__ dW,
+    const uint32_t *__restrict__ planes, int K, float *__restrict__ parts, int tiles_j, int tiles, int slices) {
     constexpr int THREADS = WM * WN * RBQ_WAVE;
     constexpr int CJ = WM * 128, CR = WN * TN * 16;            // tile: columns x rows of dW
     constexpr int PJ = CJ / 8, PR = CR / 8;                    // pieces of an LDS row
@@ -176,13 +176,11 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
     constexpr int NY = CW_BK * PR / THREADS;                   // 8 values of dY each
     static_assert(NX * THREADS * 16 == CW_BK * CJ && NY * THREADS == CW_BK * PR, "staging covers the tile");
     static_assert(NX + NY <= CW_BK / 32 * CW_TM / 2, "every piece is staged within a stage");
-    extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & (RBQ_WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / RBQ_WAVE);
     const int wj = wave % WM, wr = wave / WM;
     const int li = lane & 15, g = lane >> 4;
-    const int id = xcd_run(blockIdx.x, tiles * slices);
     const int tile = id % tiles, slice = id / tiles;
     const int64_t j0 = (int64_t)(tile % tiles_j) * CJ, r0 = (int64_t)(tile / tiles_j) * CR;
     dW += (int64_t)slice * out * in;
@@ -292,7 +290,7 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
                 for (int j = 0; j < TN; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[i & 1], b[j], acc[i][j], 0, 0, 0);
                 const int u = (kk * CW_TM + i) / 2;
-                if (i & 1) {
+                if (!ONE && (i & 1)) {
                     if (u < NX) {
                         store_x(nxt, u);
                         load_x(t + 2, u, whole);
@@ -304,37 +302,19 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        ck_barrier();
+        if (!ONE)
+            ck_barrier();
     };
-    // (a slice's last stages request two past its end: checked, and unused)
-    const int64_t t_lo = steps * slice / slices, t_hi = steps * (slice + 1) / slices;
-#pragma unroll
-    for (int u = 0; u < NX; ++u) {
-        load_x(t_lo, u, std::false_type());
-        store_x(lds, u);
-        load_x(t_lo + 1, u, std::false_type());
-    }
-#pragma unroll
-    for (int u = 0; u < NY; ++u) {
-        load_y(t_lo, u, std::false_type());
-        store_y(lds, u);
-        load_y(t_lo + 1, u, std::false_type());
-    }
-    ck_barrier();
-    int64_t t = t_lo;
-    for (; t + 2 < std::min(t_hi, safe); ++t)
-        stage(t, t_lo, std::true_type());
-    for (; t < t_hi; ++t)
-        stage(t, t_lo, std::false_type());
-
     // the sign words of this wave's columns, for the scales' gradients; they
     // arrive while dW is written
     const int64_t words = in >> 5, w0 = (j0 + wj * 128) >> 5;
     const bool add = parts != nullptr && w0 < words;
-    v4u sign[4][TN];
-    if (add)
+    v4u sign[KP][TN];
+    auto load_signs = [&]() {
+        if (!add)
+            return;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < KP; ++k)
             if (k < K)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
@@ -347,6 +327,46 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
                         for (int q = 0; q < 4; ++q)
                             sign[k][j][q] = w0 + q < words ? p[q] : 0u;
                 }
+    };
+    if constexpr (ONE) {
+#pragma unroll
+        for (int u = 0; u < NX; ++u)
+            load_x(0, u, std::false_type());
+#pragma unroll
+        for (int u = 0; u < NY; ++u)
+            load_y(0, u, std::false_type());
+#pragma unroll
+        for (int u = 0; u < NX; ++u)
+            store_x(lds, u);
+#pragma unroll
+        for (int u = 0; u < NY; ++u)
+            store_y(lds, u);
+        load_signs();
+        ck_barrier();
+        stage(0, 0, std::false_type());
+    } else {
+        // (a slice's last stages request two past its end: checked, and unused)
+        const int64_t t_lo = steps * slice / slices, t_hi = steps * (slice + 1) / slices;
+#pragma unroll
+        for (int u = 0; u < NX; ++u) {
+            load_x(t_lo, u, std::false_type());
+            store_x(lds, u);
+            load_x(t_lo + 1, u, std::false_type());
+        }
+#pragma unroll
+        for (int u = 0; u < NY; ++u) {
+            load_y(t_lo, u, std::false_type());
+            store_y(lds, u);
+            load_y(t_lo + 1, u, std::false_type());
+        }
+        ck_barrier();
+        int64_t t = t_lo;
+        for (; t + 2 < std::min(t_hi, safe); ++t)
+            stage(t, t_lo, std::true_type());
+        for (; t < t_hi; ++t)
+            stage(t, t_lo, std::false_type());
+        load_signs();
+    }
 
     // lane (li, g): columns 4 g + v of a column tile, row li of a row tile
     const bool vec = ((uintptr_t)dW & 15) == 0;
@@ -374,7 +394,7 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
         return;
     parts += (int64_t)slice * K * out * T + w0 / 4;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < KP; ++k) {
         if (k >= K)
             break;
 #pragma unroll
@@ -399,6 +419,18 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
                 parts[((int64_t)k * out + r) * T] = s;
         }
     }
+}
+
+// (At least two waves per SIMD, here and below: no accumulation registers, out
+// of which the sums would have to be copied.)
+template <int WM, int WN, int TN>
+__global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
+    const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int M,
+    int out, int in, int T, float *__restrict__ dW, const uint32_t *__restrict__ planes, int K,
+    float *__restrict__ parts, int tiles_j, int tiles, int slices) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    ck_dw<WM, WN, TN, false, 4>(lds, xcd_run(blockIdx.x, tiles * slices), dY, codes, cscales, M, out, in, T, dW,
+                                planes, K, parts, tiles_j, tiles, slices);
 }
 
 // ---------------------------------------------------------------------------
@@ -462,24 +494,23 @@ __device__ __forceinline__ uint32_t ck_nibbles(uint32_t x) {
     return (z & 0x000F000Fu) | ((z << 4) & 0x0F000F00u);
 }
 
-template <int TM, int K>
-__global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
-    const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
-    int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
-    int tiles_j, int tiles_m, int total) {
-    constexpr int CM = 64 * TM;
+template <int WM, int TM, int K>
+__device__ __forceinline__ void ck_dx(
+    unsigned char *lds, int id, const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes,
+    const uint16_t *__restrict__ scales, int M, int out, int in, int group_size, int64_t r_slice,
+    float *__restrict__ dX, int32_t *__restrict__ status, int tiles_j, int tiles_m) {
+    constexpr int WJ = CX_THREADS / RBQ_WAVE / WM, TJ = CX_J / 16 / WJ;   // waves and their tiles along the columns
+    constexpr int CM = 16 * WM * TM;
     constexpr int YB = CM * CX_BK * 2, HB = CX_BK * CX_J * 2, STAGE = YB + 2 * HB;
-    constexpr int NY = CM * (CX_BK / 8) / CX_THREADS;          // 8 values of dY each
+    constexpr int YP = CM * (CX_BK / 8), NY = (YP + CX_THREADS - 1) / CX_THREADS;   // 8 values of dY each
     constexpr int PJ = CX_J / 8;
     // stages whose loads are in flight: the short stages of few tokens need two
-    constexpr int SETS = TM == 4 ? 1 : 2;
-    extern __shared__ __align__(16) unsigned char lds[];
+    constexpr int SETS = CM == 256 ? 1 : 2;
     const int tid = threadIdx.x;
     const int lane = tid & (RBQ_WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / RBQ_WAVE);
-    const int wm = wave & 3, wj = wave >> 2;
+    const int wm = wave % WM, wj = wave / WM;
     const int li = lane & 15, g = lane >> 4;
-    const int id = xcd_run(blockIdx.x, total);
     const int z = id / (tiles_j * tiles_m);
     const int64_t j0 = (int64_t)(id % tiles_j) * CX_J, m0 = (int64_t)(id / tiles_j % tiles_m) * CM;
     const int64_t words = in >> 5;
@@ -487,9 +518,9 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     const int64_t r_lo = z * r_slice, r_hi = std::min<int64_t>(out, r_lo + r_slice);
     dX += (int64_t)z * M * in;
 
-    v4f acc[4][TM];
+    v4f acc[TJ][TM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TJ; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j)
             acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
@@ -515,7 +546,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     auto store_y = [&](unsigned char *at, int u, int set) {
         const int c = u * CX_THREADS + tid;
         const int m = c >> 3, p = c & 7;
-        *reinterpret_cast<v4u *>(at + m * (CX_BK * 2) + (p ^ (m & 7)) * 16) = yr[set][u];
+        if (c < YP)
+            *reinterpret_cast<v4u *>(at + m * (CX_BK * 2) + (p ^ (m & 7)) * 16) = yr[set][u];
     };
     const int fr = tid >> 3, fj = tid & 7;                     // this thread's row of What and 16 columns
     const int64_t fw = std::min((j0 >> 5) + (fj >> 1), words - 1);
@@ -636,10 +668,10 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     };
 
     const int k0 = 8 * g + (li >> 2);
-    uint32_t wo[4], yo[2];
+    uint32_t wo[TJ], yo[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        wo[i] = YB + k0 * (CX_J * 2) + (((wj * 4 + i) * 2) ^ ck_swizzle(k0, PJ)) * 16 + 8 * (li & 3);
+    for (int i = 0; i < TJ; ++i)
+        wo[i] = YB + k0 * (CX_J * 2) + (((wj * TJ + i) * 2) ^ ck_swizzle(k0, PJ)) * 16 + 8 * (li & 3);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
         yo[kk] = (wm * TM * 16 + li) * (CX_BK * 2) + ((4 * kk + g) ^ (li & 7)) * 16;
@@ -661,8 +693,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
                 b[j] = *reinterpret_cast<const v8h *>(cur + yo[kk] + j * 16 * (CX_BK * 2));
             ah[0] = ck_column(cur + wo[0] + kk * 32 * (CX_J * 2), CX_J * 2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i + 1 < 4) {
+            for (int i = 0; i < TJ; ++i) {
+                if (i + 1 < TJ) {
                     al[(i + 1) & 1] = ck_column(cur + wo[i + 1] + HB + kk * 32 * (CX_J * 2), CX_J * 2);
                     ah[(i + 1) & 1] = ck_column(cur + wo[i + 1] + kk * 32 * (CX_J * 2), CX_J * 2);
                 }
@@ -672,16 +704,19 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
 #pragma unroll
                 for (int j = 0; j < TM; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[i & 1], b[j], acc[i][j], 0, 0, 0);
-                const int u = kk * 4 + i;
-                if (u < 4)
-                    form(u, set);
-                if (u == 4) {
-                    store_w(nxt);
-                    load_w(ahead, whole, set);
-                }
-                if (u >= 4 && u - 4 < NY) {
-                    store_y(nxt, u - 4, set);
-                    load_y(ahead, u - 4, whole, set);
+                // (8 places for the pieces)
+#pragma unroll
+                for (int u = (kk * TJ + i) * 4 / TJ; u < (kk * TJ + i + 1) * 4 / TJ; ++u) {
+                    if (u < 4)
+                        form(u, set);
+                    if (u == 4) {
+                        store_w(nxt);
+                        load_w(ahead, whole, set);
+                    }
+                    if (u >= 4 && u - 4 < NY) {
+                        store_y(nxt, u - 4, set);
+                        load_y(ahead, u - 4, whole, set);
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -728,8 +763,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
         if (m >= M)
             continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t c = j0 + (wj * 4 + i) * 16 + 4 * g;
+        for (int i = 0; i < TJ; ++i) {
+            const int64_t c = j0 + (wj * TJ + i) * 16 + 4 * g;
             float *p = dX + m * in + c;
             if (c < in) {
                 if (vec) {
@@ -744,6 +779,35 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
     }
     if (status != nullptr && __ballot(ovf) != 0 && lane == 0)
         atomicOr(status, (int)RBQ_STATUS_SCALE_OVERFLOW);
+}
+
+template <int WM, int TM, int K>
+__global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
+    const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
+    int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
+    int tiles_j, int tiles_m, int total) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    ck_dx<WM, TM, K>(lds, xcd_run(blockIdx.x, total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
+                     status, tiles_j, tiles_m);
+}
+
+// Up to 64 tokens: both in one launch, two workgroups to a compute unit.  The
+// write of dW bounds one, the start of every stage the other, so they go well
+// beside each other; either may have no workgroups.  dX: the waves lie along
+// the columns, so that each weight is read from LDS by one wave only.
+template <int TM, int K>
+__global__ __launch_bounds__(CX_THREADS, 4) void qat_ckpt_few_kernel(
+    const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
+    int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
+    int x_tiles, int x_total, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int T,
+    float *__restrict__ dW, float *__restrict__ parts, int w_tiles_j, int w_tiles) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    if ((int)blockIdx.x < x_total)
+        ck_dx<1, TM, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
+                        status, x_tiles, 1);
+    else
+        ck_dw<1, 8, 2, true, K>(lds, xcd_run(blockIdx.x - x_total, w_tiles), dY, codes, cscales, M, out, in, T, dW,
+                                planes, K, parts, w_tiles_j, w_tiles, 1);
 }
 
 // What is left to add at the end, in one launch: up to three jobs, each with a
@@ -793,39 +857,85 @@ __global__ __launch_bounds__(CK_THREADS) void qat_ckpt_join_kernel(ck_jobs jobs)
 
 constexpr int LDS_MAX = 160 * 1024;
 
+// The calls' arguments and where their partial sums go.
+struct ck_call {
+    const uint16_t *dY;
+    const uint32_t *planes;
+    const uint16_t *scales;
+    const int8_t *codes;
+    const uint16_t *cscales;
+    int M, out, in, K, group_size;
+    float *dX, *dW, *parts;                // dX and dW: the results, or slices of them
+    int dx_slices, dw_slices;
+    int32_t *status;
+    hipStream_t st;
+};
+
+constexpr int64_t CK_GRID = 0x7FFFFFFF / CX_THREADS;
+
+// Rows of What per slice of dX's contraction.
+int64_t dx_rows(const ck_call &c) {
+    return (((int64_t)c.out + c.dx_slices - 1) / c.dx_slices + CX_BK - 1) / CX_BK * CX_BK;
+}
+
 template <int WM, int WN, int TN>
-hipError_t launch_dw(const uint16_t *dY, const int8_t *codes, const uint16_t *cscales, int M, int out, int in,
-                     float *dW, const uint32_t *planes, int K, float *parts, int slices, hipStream_t st) {
+hipError_t launch_dw(const ck_call &c) {
     constexpr int CJ = WM * 128, CR = WN * TN * 16;
     constexpr int LDS = 2 * CW_BK * (CJ + CR) * 2;
     static_assert(LDS <= LDS_MAX, "LDS of a compute unit");
-    const int64_t tiles_j = ((int64_t)in + CJ - 1) / CJ, tiles = tiles_j * (((int64_t)out + CR - 1) / CR);
-    if (tiles * slices > 0x7FFFFFFF / (WM * WN * RBQ_WAVE))
+    const int64_t tiles_j = ((int64_t)c.in + CJ - 1) / CJ, tiles = tiles_j * (((int64_t)c.out + CR - 1) / CR);
+    if (tiles * c.dw_slices > CK_GRID)
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((qat_ckpt_dw_kernel<WM, WN, TN>), dim3((unsigned)(tiles * slices)), dim3(WM * WN * RBQ_WAVE),
-                       LDS, st, dY, codes, cscales, M, out, in, f8_blocks(in), dW, planes, K, parts, (int)tiles_j,
-                       (int)tiles, slices);
+    hipLaunchKernelGGL((qat_ckpt_dw_kernel<WM, WN, TN>), dim3((unsigned)(tiles * c.dw_slices)),
+                       dim3(WM * WN * RBQ_WAVE), LDS, c.st, c.dY, c.codes, c.cscales, c.M, c.out, c.in,
+                       f8_blocks(c.in), c.dW, c.planes, c.K, c.parts, (int)tiles_j, (int)tiles, c.dw_slices);
     return hipGetLastError();
 }
 
-template <int TM>
-hipError_t launch_dx(const uint16_t *dY, const uint32_t *planes, const uint16_t *scales, int M, int out, int in,
-                     int K, int group_size, int S, int64_t r_slice, float *dX, int32_t *status, hipStream_t st) {
-    constexpr int LDS = 2 * (64 * TM * CX_BK * 2 + 2 * CX_BK * CX_J * 2);
+template <int WM, int TM>
+hipError_t launch_dx(const ck_call &c) {
+    constexpr int CM = 16 * WM * TM, LDS = 2 * (CM * CX_BK * 2 + 2 * CX_BK * CX_J * 2);
     static_assert(LDS <= LDS_MAX, "LDS of a compute unit");
-    const int64_t tiles_j = ((int64_t)in + CX_J - 1) / CX_J, tiles_m = ((int64_t)M + 64 * TM - 1) / (64 * TM);
-    const int64_t total = tiles_j * tiles_m * S;
-    if (total > 0x7FFFFFFF / CX_THREADS)
+    const int64_t tiles_j = ((int64_t)c.in + CX_J - 1) / CX_J, tiles_m = ((int64_t)c.M + CM - 1) / CM;
+    const int64_t total = tiles_j * tiles_m * c.dx_slices;
+    if (total > CK_GRID)
         return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(CX_THREADS), LDS, st, dY, planes, scales, M, out, in,
-                           group_size, r_slice, dX, status, (int)tiles_j, (int)tiles_m, (int)total);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(CX_THREADS), LDS, c.st, c.dY, c.planes, c.scales, c.M,
+                           c.out, c.in, c.group_size, dx_rows(c), c.dX, c.status, (int)tiles_j, (int)tiles_m,
+                           (int)total);
     };
-    switch (K) {
-    case 1: go(qat_ckpt_dx_kernel<TM, 1>); break;
-    case 2: go(qat_ckpt_dx_kernel<TM, 2>); break;
-    case 3: go(qat_ckpt_dx_kernel<TM, 3>); break;
-    default: go(qat_ckpt_dx_kernel<TM, 4>); break;
+    switch (c.K) {
+    case 1: go(qat_ckpt_dx_kernel<WM, TM, 1>); break;
+    case 2: go(qat_ckpt_dx_kernel<WM, TM, 2>); break;
+    case 3: go(qat_ckpt_dx_kernel<WM, TM, 3>); break;
+    default: go(qat_ckpt_dx_kernel<WM, TM, 4>); break;
+    }
+    return hipGetLastError();
+}
+
+// Either of dX and dW may be null.
+template <int TM>
+hipError_t launch_few(const ck_call &c) {
+    constexpr int LDS_X = 2 * (16 * TM * CX_BK * 2 + 2 * CX_BK * CX_J * 2), LDS_W = CW_BK * (128 + 256) * 2;
+    constexpr int LDS = LDS_X > LDS_W ? LDS_X : LDS_W;
+    static_assert(2 * LDS <= LDS_MAX, "LDS of a compute unit");
+    const int64_t tiles_j = ((int64_t)c.in + 127) / 128;
+    const int64_t x_total = c.dX != nullptr ? tiles_j * c.dx_slices : 0;
+    const int64_t w_tiles = c.dW != nullptr ? tiles_j * (((int64_t)c.out + 255) / 256) : 0;
+    if (x_total + w_tiles > CK_GRID)
+        return hipErrorInvalidConfiguration;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(x_total + w_tiles)), dim3(CX_THREADS), LDS, c.st, c.dY, c.planes,
+                           c.scales, c.M, c.out, c.in, c.group_size, dx_rows(c), c.dX, c.status, (int)tiles_j,
+                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.parts, (int)tiles_j,
+                           (int)w_tiles);
+    };
+    switch (c.K) {
+    case 1: go(qat_ckpt_few_kernel<TM, 1>); break;
+    case 2: go(qat_ckpt_few_kernel<TM, 2>); break;
+    case 3: go(qat_ckpt_few_kernel<TM, 3>); break;
+    default: go(qat_ckpt_few_kernel<TM, 4>); break;
     }
     return hipGetLastError();
 }
@@ -836,26 +946,29 @@ hipError_t launch_dx(const uint16_t *dY, const uint32_t *planes, const uint16_t 
 
 float slice_cost(int S, int64_t n) { return S > 1 ? 4.0f + (float)n * (float)(2 * S + 1) * (4.0f / 5.0e6f) : 0.0f; }
 
-// Tokens per dX tile in units of 64: 16 tokens on 4096 x 4096 take 19 us in
-// tiles of 64; tiles of 256 multiply 16 times the zeros.
-int dx_tokens(int M) { return M > 128 ? 4 : M > 64 ? 2 : 1; }
+// Tokens per dX tile.
+int dx_tokens(int M) { return M > 128 ? 256 : M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
 
 // Slices of dX's contraction.  Measured (one slice and the choice): 16 tokens,
-// 4096 x 4096: 71 and 19 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and
-// 165 us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens,
-// 11008 x 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.
-int dx_slices(int M, int out, int in, int K) {
+// 4096 x 4096: 48 and 16 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and 158
+// us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens, 11008 x
+// 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.  Up to 64
+// tokens with dW in the same launch, its workgroups want room too: both
+// outputs, 16 tokens, 4096 x 4096: 28.5 us in 4 slices, 31.0 in 8; 4096 x
+// 11008: 56 in 2, 64 in 1, 67 in 8.
+int dx_slices(int M, int out, int in, int K, bool with_dw) {
     static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
     const int tm = dx_tokens(M);
-    const float stage = tm == 1 ? 1.1f : tm == 2 ? 1.4f : K > 2 ? 2.4f : 2.0f;
-    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + 64 * tm - 1) / (64 * tm));
+    const float stage = tm <= 64 ? 0.8f : tm == 128 ? 1.4f : K > 2 ? 2.4f : 2.0f;
+    const int64_t room = with_dw && tm <= 64 ? 176 : 256;
+    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + tm - 1) / tm);
     const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
     int best = 1;
     float least = 0.0f;
     for (const int S : splits) {
         if (S > 1 && 2 * S > steps)
             break;
-        const float cost = (float)((tiles * S + 255) / 256) * ((float)((steps + S - 1) / S) * stage + 4.0f) +
+        const float cost = (float)((tiles * S + room - 1) / room) * ((float)((steps + S - 1) / S) * stage + 4.0f) +
                            slice_cost(S, (int64_t)M * in);
         if (S == 1 || cost < least) {
             best = S;
@@ -866,12 +979,12 @@ int dx_slices(int M, int out, int in, int K) {
 }
 
 size_t dx_slice_bytes(int M, int out, int in, int K) {
-    const int S = dx_slices(M, out, in, K);
+    const int S = std::max(dx_slices(M, out, in, K, false), dx_slices(M, out, in, K, true));
     return S > 1 ? (size_t)S * (size_t)M * (size_t)in * sizeof(float) : 0;
 }
 
 // dW's tiles (256 x 256, one workgroup per compute unit; or 128 x 128, two) and
-// slices of its tokens.  Measured with the scales' gradients: 2048 tokens,
+// slices of its tokens, of which up to 64 have a kernel of their own.  Measured with the scales' gradients: 2048 tokens,
 // 11008 x 4096: 248 us large, 338 small; 300 tokens, 2000 x 2048: 33 large, 20
 // small; 2000 tokens, 600 x 576: 38 us in one slice of 25 small tiles, 25 in 4.
 struct dw_plan {
@@ -881,6 +994,8 @@ struct dw_plan {
 dw_plan plan_dw(int M, int out, int in) {
     static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
     const int64_t steps = ((int64_t)M + CW_BK - 1) / CW_BK;
+    if (steps == 1)
+        return {0, 1};
     dw_plan best = {1, 1};
     float least = 0.0f;
     for (int large = 0; large < 2; ++large)
@@ -943,52 +1058,48 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     // gradients that would pass through it are taken from dW in a pass of
     // their own.
     const bool fits = ws_bytes >= qat_backward_ckpt_workspace_bytes(M, out, in, K, group_size);
+    const size_t part_bytes = dw_part_bytes(M, out, in, K, group_size);
     float *ws = static_cast<float *>(workspace);
     ck_jobs left = {};
     int jobs = 0;
+    const dw_plan p = plan_dw(M, out, in);
+    ck_call c = {dY, planes, scales, x_codes, x_scales, M, out, in, K, group_size, dX, dW, nullptr,
+                 fits ? dx_slices(M, out, in, K, dW != nullptr) : 1, fits ? p.slices : 1, status, st};
+    c.dx_slices = (int)((out + dx_rows(c) - 1) / dx_rows(c));        // (none of them empty)
+    if (dW != nullptr && c.dw_slices > 1) {
+        c.dW = ws;
+        left.job[jobs++] = sum_job(ws, dW, (int64_t)out * in, c.dw_slices, 1);
+        ws += (int64_t)c.dw_slices * out * in;
+    }
+    if (dscales != nullptr && part_bytes == 0) {
+        c.parts = dscales;                  // a tile's columns are a whole group, and all its tokens
+    } else if (dscales != nullptr && fits) {
+        c.parts = ws;
+        const int64_t rows = (int64_t)K * out;
+        left.job[jobs++] = group_size ? sum_job(ws, dscales, rows * f8_blocks(in), c.dw_slices, 1)
+                                      : sum_job(ws, dscales, rows, c.dw_slices, f8_blocks(in));
+        ws += part_bytes / sizeof(float);
+    }
+    if (dX != nullptr && c.dx_slices > 1) {
+        c.dX = ws;
+        left.job[jobs++] = sum_job(ws, dX, (int64_t)M * in, c.dx_slices, 1);
+    }
     hipError_t e = hipSuccess;
-    if (dW != nullptr) {
-        dw_plan p = plan_dw(M, out, in);
-        const size_t part_bytes = dw_part_bytes(M, out, in, K, group_size);
-        if (!fits)
-            p.slices = 1;
-        float *dst = dW, *parts = nullptr;
-        if (p.slices > 1) {
-            dst = ws;
-            left.job[jobs++] = sum_job(dst, dW, (int64_t)out * in, p.slices, 1);
-            ws += (int64_t)p.slices * out * in;
-        }
-        if (dscales != nullptr && part_bytes == 0) {
-            parts = dscales;                    // a tile's columns are a whole group, and all its tokens
-        } else if (dscales != nullptr && fits) {
-            parts = ws;
-            const int64_t rows = (int64_t)K * out;
-            left.job[jobs++] = group_size ? sum_job(parts, dscales, rows * f8_blocks(in), p.slices, 1)
-                                          : sum_job(parts, dscales, rows, p.slices, f8_blocks(in));
-            ws += part_bytes / sizeof(float);
-        }
-        e = p.large ? launch_dw<2, 4, 4>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st)
-                    : launch_dw<1, 4, 2>(dY, x_codes, x_scales, M, out, in, dst, planes, K, parts, p.slices, st);
-        if (e == hipSuccess && dscales != nullptr && parts == nullptr)
-            e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st);
-        if (e != hipSuccess)
-            return e;
+    switch (dx_tokens(M)) {
+    case 16: e = launch_few<1>(c); break;
+    case 32: e = launch_few<2>(c); break;
+    case 64: e = launch_few<4>(c); break;
+    default:
+        if (dW != nullptr)
+            e = p.large ? launch_dw<2, 4, 4>(c) : launch_dw<1, 4, 2>(c);
+        if (e == hipSuccess && dX != nullptr)
+            e = M > 128 ? launch_dx<4, 4>(c) : launch_dx<4, 2>(c);
+        break;
     }
-    if (dX != nullptr) {
-        int S = fits ? dx_slices(M, out, in, K) : 1;
-        const int64_t r_slice = (((int64_t)out + S - 1) / S + CX_BK - 1) / CX_BK * CX_BK;
-        S = (int)(((int64_t)out + r_slice - 1) / r_slice);
-        float *dst = S > 1 ? ws : dX;
-        if (S > 1)
-            left.job[jobs++] = sum_job(dst, dX, (int64_t)M * in, S, 1);
-        switch (dx_tokens(M)) {
-        case 1: e = launch_dx<1>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
-        case 2: e = launch_dx<2>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
-        default: e = launch_dx<4>(dY, planes, scales, M, out, in, K, group_size, S, r_slice, dst, status, st); break;
-        }
-        if (e != hipSuccess)
-            return e;
-    }
+    if (e == hipSuccess && dscales != nullptr && c.parts == nullptr)
+        e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st);
+    if (e != hipSuccess)
+        return e;
     if (jobs) {
         const unsigned blocks = left.job[0].blocks + left.job[1].blocks + left.job[2].blocks;
         hipLaunchKernelGGL(qat_ckpt_join_kernel, dim3(blocks), dim3(CK_THREADS), 0, st, left);
