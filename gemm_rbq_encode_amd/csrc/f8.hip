@@ -25,7 +25,9 @@ constexpr int FQ_THREADS = 256;
 // tokens: 16 lanes hold one block (8 consecutive fp16 each, one 16-byte load),
 // so the maximum is four DPP rotations inside a row of 16 lanes and needs no
 // LDS.  A workgroup takes 16 tokens x 4 blocks; the four loads of a lane are
-// issued together.  Bound by the read of X and the write of the codes.
+// issued together.  Bound by the read of X and the write of the codes: 2048 x
+// 14336 takes 15.4 us, 5.8 TB/s (26.8 us where X has to come from HBM past
+// another kernel's unwritten lines); 4 x 4096, 4.6 us, is a launch.
 constexpr int FQ_ROWS = FQ_THREADS / 16;
 constexpr int FQ_BLOCKS = 4;
 
@@ -63,7 +65,8 @@ __global__ __launch_bounds__(FQ_THREADS) void quantize_f8_kernel(const uint16_t 
 
 // ---------------------------------------------------------------------------
 // weights: one workgroup per 128 x 128 block, held in 64 registers per thread
-// between the maximum and the codes, so W is read once.
+// between the maximum and the codes, so W is read once.  Bound by that read:
+// 14336 x 4096 takes 53.5 us, 5.5 TB/s of W and codes.
 
 __global__ __launch_bounds__(FQ_THREADS) void encode_f8_kernel(const float *__restrict__ W, int out, int in, int T,
                                                                uint8_t *__restrict__ codes,
@@ -122,6 +125,9 @@ __global__ __launch_bounds__(FQ_THREADS) void encode_f8_kernel(const float *__re
 // 16g.. and 64 + 16g.. of row i of both operands: any assignment of columns
 // gives the same sum as long as both sides share it, and this one makes a
 // load 64 contiguous bytes per row.
+//
+// One token, 11008 x 4096: 9.9 us, 4.6 TB/s of W; 16 tokens, 4096 x 11008: 13.3
+// us, 3.4 TB/s (the tokens' 176 KB are read by each of the 256 workgroups).
 
 // Every wave keeps U blocks in flight: the loads of block u + U of its own are
 // issued as soon as block u's registers are free.

