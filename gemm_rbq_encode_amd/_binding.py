@@ -495,32 +495,56 @@ def _one_device(*tensors) -> torch.device:
     return dev
 
 
-class _Launch:
+class _Here:
+    """Context of a call on the current device and stream: the stream's handle."""
+    __slots__ = ("_index",)
+
+    def __init__(self, index: int):
+        self._index = index
+
+    def __enter__(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self._index)       # current_stream without the object
+
+    def __exit__(self, *exc):
+        pass
+
+
+class _There:
     """Context of a call for tensors on `dev`: that device is current, and so is
     the stream the call is for, so that buffers made inside belong to it.
     Enters as the stream's handle."""
-    __slots__ = ("_dev", "_ctx")
+    __slots__ = ("_index", "_ctx")
 
-    def __init__(self, dev: torch.device, stream=None):
-        self._dev = dev
-        self._ctx = None
-        if stream is not None or dev.index != torch.cuda.current_device():
-            self._ctx = [torch.cuda.device(dev)]
-            if stream is not None:
-                if not hasattr(stream, "cuda_stream"):
-                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
-                self._ctx.append(torch.cuda.stream(stream))
+    def __init__(self, dev: torch.device, stream):
+        self._index = dev.index
+        self._ctx = [torch.cuda.device(dev)]
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            self._ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self) -> int:
-        if self._ctx is not None:
-            for c in self._ctx:
-                c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self._dev.index)   # current_stream without the object
+        for c in self._ctx:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            for c in reversed(self._ctx):
-                c.__exit__(*exc)
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+_here: dict = {}
+
+
+def _launch(dev: torch.device, stream=None):
+    """The context of a call for tensors on `dev`."""
+    i = dev.index
+    if stream is not None or i != torch._C._cuda_getDevice():        # (a tensor is there: the runtime is up)
+        return _There(dev, stream)
+    h = _here.get(i)
+    if h is None:
+        h = _here[i] = _Here(i)
+    return h
 
 
 def _blocks(n: int) -> int:
@@ -533,12 +557,14 @@ def _nbytes(workspace: torch.Tensor) -> int:
     return workspace.numel() * workspace.element_size()
 
 
-def _out(t: torch.Tensor | None, size: tuple, dtype, name: str, dev: torch.device) -> torch.Tensor:
-    """The given output tensor, checked, or a new one."""
+def _out(t: torch.Tensor | None, size: tuple, dtype, name: str, dev: torch.device,
+         like: torch.Tensor | None = None) -> torch.Tensor:
+    """The given output tensor, checked, or a new one (`like`: a contiguous
+    tensor of its size, which is the quicker way to one)."""
     if t is None:
-        return torch.empty(size, dtype=dtype, device=dev)
+        return torch.empty(size, dtype=dtype, device=dev) if like is None else torch.empty_like(like, dtype=dtype)
     _dev(t, dtype, name)
-    if tuple(t.shape) != size:
+    if t.shape != size:
         raise ValueError(f"{name} must be {list(size)}, got {list(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
@@ -557,8 +583,8 @@ def encode_f8(W: torch.Tensor, *, status: torch.Tensor | None = None, codes: tor
     if status is not None:
         _dev(status, torch.int32, "status")
     dev = _one_device(W, status)
-    with _Launch(dev, stream) as st:
-        codes = _out(codes, (out_f, in_f), torch.float8_e4m3fn, "codes", dev)
+    with _launch(dev, stream) as st:
+        codes = _out(codes, (out_f, in_f), torch.float8_e4m3fn, "codes", dev, W)
         scales = _out(scales, (_blocks(out_f), _blocks(in_f)), torch.float32, "scales", dev)
         check(lib().rbq_encode_f8(W.data_ptr(), out_f, in_f, codes.data_ptr(), scales.data_ptr(),
                                   None if status is None else status.data_ptr(), st), "rbq_encode_f8")
@@ -574,8 +600,8 @@ def quantize_f8(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales: t
         raise ValueError("X must be [M][in]")
     M, in_f = X.shape
     dev = X.device
-    with _Launch(dev, stream) as st:
-        codes = _out(codes, (M, in_f), torch.float8_e4m3fn, "codes", dev)
+    with _launch(dev, stream) as st:
+        codes = _out(codes, (M, in_f), torch.float8_e4m3fn, "codes", dev, X)
         scales = _out(scales, (_blocks(in_f), M), torch.float32, "scales", dev)
         check(lib().rbq_quantize_f8(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
               "rbq_quantize_f8")
@@ -585,7 +611,7 @@ def quantize_f8(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales: t
 def _f8_layer(codes: torch.Tensor, scales: torch.Tensor):
     _dev(codes, torch.float8_e4m3fn, "codes")
     _dev(scales, torch.float32, "scales")
-    if codes.dim() != 2 or tuple(scales.shape) != (_blocks(codes.shape[0]), _blocks(codes.shape[1])):
+    if codes.dim() != 2 or scales.shape != (_blocks(codes.shape[0]), _blocks(codes.shape[1])):
         raise ValueError("codes must be [out][in] and scales [ceil(out/128)][ceil(in/128)]")
     return codes.shape
 
@@ -601,13 +627,13 @@ def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_
     if x_codes.dim() != 2 or x_codes.shape[1] != in_f:
         raise ValueError(f"x_codes must be [M][{in_f}], got {tuple(x_codes.shape)}")
     M = x_codes.shape[0]
-    if tuple(x_scales.shape) != (_blocks(in_f), M):
+    if x_scales.shape != (_blocks(in_f), M):
         raise ValueError(f"x_scales must be [{_blocks(in_f)}][{M}], got {tuple(x_scales.shape)}")
     if dtype not in (torch.float16, torch.float32):
         raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
     dev = _one_device(codes, scales, x_codes, x_scales, workspace)
     kind = RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16
-    with _Launch(dev, stream) as st:
+    with _launch(dev, stream) as st:
         Y = _out(Y, (M, out_f), dtype, "Y", dev)
         if workspace is None and M > 32:      # none is needed for fewer
             need = int(lib().rbq_gemm_f8_workspace_bytes(out_f, in_f, M, kind))
@@ -627,7 +653,7 @@ def gemv_f8(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, *, y: to
     if x.numel() != in_f:
         raise ValueError(f"x must have {in_f} elements")
     dev = _one_device(codes, scales, x)
-    with _Launch(dev, stream) as st:
+    with _launch(dev, stream) as st:
         y = _out(y, (out_f,), torch.float16, "y", dev)
         check(lib().rbq_gemv_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x.data_ptr(), y.data_ptr(), st),
               "rbq_gemv_f8")
@@ -643,8 +669,8 @@ def qat_checkpoint(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales
         raise ValueError("X must be [M][in]")
     M, in_f = X.shape
     dev = X.device
-    with _Launch(dev, stream) as st:
-        codes = _out(codes, (M, in_f), torch.int8, "codes", dev)
+    with _launch(dev, stream) as st:
+        codes = _out(codes, (M, in_f), torch.int8, "codes", dev, X)
         scales = _out(scales, (M, _blocks(in_f)), torch.float16, "scales", dev)
         check(lib().rbq_qat_checkpoint(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
               "rbq_qat_checkpoint")
@@ -670,8 +696,7 @@ def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch
     s = shape(out_f, in_f, K, group_size)
     check(lib().rbq_check_shape(s), "rbq_qat_backward_ckpt")
     M = dY.shape[0]
-    if tuple(dY.shape) != (M, out_f) or tuple(x_codes.shape) != (M, in_f) or \
-            tuple(x_scales.shape) != (M, _blocks(in_f)):
+    if dY.shape != (M, out_f) or x_codes.shape != (M, in_f) or x_scales.shape != (M, _blocks(in_f)):
         raise ValueError("x_codes must be [M][in], x_scales [M][ceil(in/128)] and dY [M][out]")
     if scales.numel() * 2 != scales_bytes(s):
         raise ValueError("scales do not match the shape")
@@ -679,7 +704,7 @@ def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch
         _dev(status, torch.int32, "status")
     dev = _one_device(planes, scales, x_codes, x_scales, dY, workspace, status)
     ptr = (lambda t: None if t is None else t.data_ptr())
-    with _Launch(dev, stream) as st:
+    with _launch(dev, stream) as st:
         dX = torch.empty((M, in_f), dtype=torch.float32, device=dev) if need_dx else None
         dW = torch.empty((out_f, in_f), dtype=torch.float32, device=dev) if (need_dw or need_dscales) else None
         ds = torch.empty((K, out_f, groups_per_row(in_f, group_size)), dtype=torch.float32, device=dev) \
