@@ -655,6 +655,9 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
  *   dY       device fp16 [M][out], 2-byte aligned
  *   workspace  device memory of rbq_qat_backward_ckpt_workspace_bytes(s, M)
  *              bytes; rules as for rbq_qat_backward
+ * Outputs and the workspace may not overlap anything else.  The order of the
+ * fp32 sums depends on the sizes, the workspace given and on whether dW is
+ * asked for along with dX, not on the run.
  * Other arguments, rules (any of dX, dW may be NULL; dscales needs dW) and
  * errors as rbq_qat_backward, and RBQ_ERR_UNSUPPORTED for more than
  * RBQ_CKPT_MAX_FEATURES rows or columns.
@@ -679,7 +682,8 @@ rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales,
  *       128 columns (a block's scales of all tokens side by side)
  * with T = ceil(in / 128); blocks at the edges are smaller.  A value is its
  * code times its scale.  in_features is a multiple of 32 throughout; more than
- * RBQ_F8_MAX_FEATURES rows or columns are RBQ_ERR_UNSUPPORTED.
+ * RBQ_F8_MAX_FEATURES rows or columns are RBQ_ERR_UNSUPPORTED.  What a call
+ * writes (outputs, workspace) may not overlap anything else it is given.
  * The transposed layer (dX = dY W) is the product with the transposed codes
  * and the transposed scales: blocks of 128 x 128 stay blocks (out must then
  * be a multiple of 32).
