@@ -40,7 +40,8 @@
 // power leaves: 2048 tokens, 14336 x 4096: 127 us, 1.9 PFLOP/s (a library
 // product of this size with one scale for the whole matrix: 103 us); 4096
 // tokens, 8192 x 8192: 254 us, 2.2 PFLOP/s.  fp32 outputs run at the fp16
-// rate: 777 tokens, 5003 x 4128: 56.8 us, 565 TFLOP/s.
+// rate: 777 tokens, 5003 x 4128: 56 us, 570 TFLOP/s; 2048 tokens, 14336 x 4096:
+// 231 us, 1.04 PFLOP/s, which is the fp16 instruction's under its power.
 #include <algorithm>
 #include <type_traits>
 
@@ -253,19 +254,68 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void gemm_f8_tile_kernel(
                     between(i);
             }
         } else {
-            v8h b[TN][4];
+            // A product of fp16 takes as long as four vector instructions: one
+            // issues it, and the conversions of what comes next (of the other
+            // tokens beside row tile 0, of the next rows) and the fmas of the
+            // row tile before go between, held there by the scheduling barriers.
+            static_assert(TN == 4, "the places between the products");
+            v8h a[2][4], b[TN][4];
+            v8i ra[2], rb[2] = {fragment(xa, 0), fragment(xa, 16)};
+            v4f p[2][TN];
+            // pair k = 0 .. 15 of a fragment
+            auto pair = [&](v8h (&h)[4], const v8i &u, int k) {
+                const v2h c = k & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u[k >> 1], 1.0f, true)
+                                    : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u[k >> 1], 1.0f, false);
+                h[k >> 2][2 * (k & 3)] = c.x;
+                h[k >> 2][2 * (k & 3) + 1] = c.y;
+            };
+            ra[0] = fragment(wa, 0);
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                f8_to_f16(fragment(xa, 16 * j), b[j]);
+            for (int k = 0; k < 16; ++k)
+                pair(b[0], rb[0], k);
+            rb[0] = fragment(xa, 32);
+            if (TM > 1)
+                ra[1] = fragment(wa, 16);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                pair(a[0], ra[0], k);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                v8h a[4];
-                f8_to_f16(fragment(wa, 16 * i), a);
+                if (i + 2 < TM)
+                    ra[i & 1] = fragment(wa, 16 * (i + 2));
+                auto step = [&](int j, int q, int n) {             // the n-th of the 4 TN products of this row tile
+                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    p[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[i & 1][q], b[j][q], q ? p[i & 1][j] : z, 0,
+                                                                         0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (i == 0 && j + 1 < TN)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = f8_fma(f8_mma(a, b[j]), s[j], acc[i][j]);
+                        for (int e = 0; e < 4; ++e)
+                            pair(b[j + 1 < TN ? j + 1 : 0], rb[(j + 1) & 1], 4 * q + e);
+                    if (i == 0 && q == 3 && j + 3 < TN)
+                        rb[(j + 1) & 1] = fragment(xa, 16 * (j + 3));
+                    if (i + 1 < TM && n < 16)
+                        pair(a[(i + 1) & 1], ra[(i + 1) & 1], n);
+                    if (i > 0) {
+                        v4f &o = acc[i > 0 ? i - 1 : 0][n >> 2];
+                        o[n & 3] = __builtin_fmaf(p[(i - 1) & 1][n >> 2][n & 3], s[n >> 2], o[n & 3]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                if (i == 0) {
+#pragma unroll
+                    for (int n = 0; n < 4 * TN; ++n)
+                        step(n >> 2, n & 3, n);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4 * TN; ++n)
+                        step(n % TN, n / TN, n);
+                }
                 between(i);
             }
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[TM - 1][j] = f8_fma(p[(TM - 1) & 1][j], s[j], acc[TM - 1][j]);
         }
     };
 
