@@ -800,6 +800,23 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
                      status, tiles_j, tiles_m);
 }
 
+// Large tiles of both in one launch, one workgroup to a compute unit: dW's
+// begin on the units that dX's last round leaves free.
+template <int K>
+__global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_both_kernel(
+    const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
+    int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
+    int x_tiles_j, int x_tiles_m, int x_total, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales,
+    int T, float *__restrict__ dW, float *__restrict__ parts, int w_tiles_j, int w_tiles, int w_slices) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    if ((int)blockIdx.x < x_total)
+        ck_dx<4, 4, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
+                       status, x_tiles_j, x_tiles_m);
+    else
+        ck_dw<2, 4, 4, false, 4>(lds, xcd_run(blockIdx.x - x_total, w_tiles * w_slices), dY, codes, cscales, M, out,
+                                 in, T, dW, planes, K, parts, w_tiles_j, w_tiles, w_slices);
+}
+
 // Up to 64 tokens: both in one launch, two workgroups to a compute unit.  The
 // write of dW bounds one, the start of every stage the other, so they go well
 // beside each other; either may have no workgroups.  dX: the waves lie along
@@ -925,6 +942,29 @@ hipError_t launch_dx(const ck_call &c) {
     return hipGetLastError();
 }
 
+hipError_t launch_both(const ck_call &c) {
+    constexpr int LDS = 2 * CW_BK * (256 + 256) * 2;
+    static_assert(LDS == 2 * (256 * CX_BK * 2 + 2 * CX_BK * CX_J * 2) && LDS <= LDS_MAX, "LDS of a compute unit");
+    const int64_t x_tiles_j = ((int64_t)c.in + CX_J - 1) / CX_J, x_tiles_m = ((int64_t)c.M + 255) / 256;
+    const int64_t w_tiles_j = ((int64_t)c.in + 255) / 256, w_tiles = w_tiles_j * (((int64_t)c.out + 255) / 256);
+    const int64_t x_total = x_tiles_j * x_tiles_m * c.dx_slices, total = x_total + w_tiles * c.dw_slices;
+    if (total > CK_GRID)
+        return hipErrorInvalidConfiguration;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(CX_THREADS), LDS, c.st, c.dY, c.planes, c.scales, c.M,
+                           c.out, c.in, c.group_size, dx_rows(c), c.dX, c.status, (int)x_tiles_j, (int)x_tiles_m,
+                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.parts, (int)w_tiles_j,
+                           (int)w_tiles, c.dw_slices);
+    };
+    switch (c.K) {
+    case 1: go(qat_ckpt_both_kernel<1>); break;
+    case 2: go(qat_ckpt_both_kernel<2>); break;
+    case 3: go(qat_ckpt_both_kernel<3>); break;
+    default: go(qat_ckpt_both_kernel<4>); break;
+    }
+    return hipGetLastError();
+}
+
 // Either of dX and dW may be null.
 template <int TM>
 hipError_t launch_few(const ck_call &c) {
@@ -960,40 +1000,6 @@ float slice_cost(int S, int64_t n) { return S > 1 ? 4.0f + (float)n * (float)(2 
 // Tokens per dX tile.
 int dx_tokens(int M) { return M > 128 ? 256 : M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
 
-// Slices of dX's contraction.  Measured (one slice and the choice): 16 tokens,
-// 4096 x 4096: 48 and 16 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and 158
-// us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens, 11008 x
-// 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.  Up to 64
-// tokens with dW in the same launch, its workgroups want room too: both
-// outputs, 16 tokens, 4096 x 4096: 28.5 us in 4 slices, 31.0 in 8; 4096 x
-// 11008: 56 in 2, 64 in 1, 67 in 8.
-int dx_slices(int M, int out, int in, int K, bool with_dw) {
-    static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-    const int tm = dx_tokens(M);
-    const float stage = tm <= 64 ? 0.8f : tm == 128 ? 1.4f : K > 2 ? 2.4f : 2.0f;
-    const int64_t room = with_dw && tm <= 64 ? 176 : 256;
-    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + tm - 1) / tm);
-    const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
-    int best = 1;
-    float least = 0.0f;
-    for (const int S : splits) {
-        if (S > 1 && 2 * S > steps)
-            break;
-        const float cost = (float)((tiles * S + room - 1) / room) * ((float)((steps + S - 1) / S) * stage + 4.0f) +
-                           slice_cost(S, (int64_t)M * in);
-        if (S == 1 || cost < least) {
-            best = S;
-            least = cost;
-        }
-    }
-    return best;
-}
-
-size_t dx_slice_bytes(int M, int out, int in, int K) {
-    const int S = std::max(dx_slices(M, out, in, K, false), dx_slices(M, out, in, K, true));
-    return S > 1 ? (size_t)S * (size_t)M * (size_t)in * sizeof(float) : 0;
-}
-
 // dW's tiles (256 x 256, one workgroup per compute unit; or 128 x 128, two) and
 // slices of its tokens, of which up to 64 have a kernel of their own.  Measured with the scales' gradients: 2048 tokens,
 // 11008 x 4096: 248 us large, 338 small; 300 tokens, 2000 x 2048: 33 large, 20
@@ -1001,6 +1007,24 @@ size_t dx_slice_bytes(int M, int out, int in, int K) {
 struct dw_plan {
     int large, slices;
 };
+
+// Workgroups, stages of one, and its time (with a compute unit to itself).
+int64_t dw_tiles(int out, int in, dw_plan p) {
+    const int64_t edge = p.large ? 256 : 128;
+    return ((in + edge - 1) / edge) * ((out + edge - 1) / edge) * p.slices;
+}
+
+int64_t dw_stages(int M, dw_plan p) {
+    return (((int64_t)M + CW_BK - 1) / CW_BK + p.slices - 1) / p.slices;
+}
+
+float dw_tile_cost(int M, dw_plan p) {
+    return p.large ? (float)dw_stages(M, p) * 1.9f + 8.0f : (float)dw_stages(M, p) * 1.1f + 6.0f;
+}
+
+// Whether dX and dW go in one launch of large tiles (300 tokens, 8192 x 4096,
+// K = 3: 143 us, 151 in two launches, though dX's fill whole rounds there).
+bool both_large(int M, dw_plan p) { return p.large && M > 128; }
 
 dw_plan plan_dw(int M, int out, int in) {
     static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
@@ -1013,12 +1037,11 @@ dw_plan plan_dw(int M, int out, int in) {
         for (const int S : splits) {
             if (S > 1 && 2 * S > steps)
                 break;
-            const int edge = large ? 256 : 128;
-            const int64_t wgs = (((int64_t)in + edge - 1) / edge) * (((int64_t)out + edge - 1) / edge) * S;
-            const float n = (float)((steps + S - 1) / S);
-            float cost = large        ? (float)((wgs + 255) / 256) * (n * 1.9f + 8.0f)
-                         : wgs <= 256 ? n * 1.1f + 6.0f
-                                      : (float)((wgs + 511) / 512) * (n * 1.6f + 8.0f);
+            const dw_plan p = {large, S};
+            const int64_t wgs = dw_tiles(out, in, p);
+            float cost = large        ? (float)((wgs + 255) / 256) * dw_tile_cost(M, p)
+                         : wgs <= 256 ? dw_tile_cost(M, p)
+                                      : (float)((wgs + 511) / 512) * ((float)dw_stages(M, p) * 1.6f + 8.0f);
             cost += slice_cost(S, (int64_t)out * in);
             if (least == 0.0f || cost < least) {
                 least = cost;
@@ -1026,6 +1049,49 @@ dw_plan plan_dw(int M, int out, int in) {
             }
         }
     return best;
+}
+
+// Slices of dX's contraction.  Measured (one slice and the choice): 16 tokens,
+// 4096 x 4096: 48 and 16 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and 158
+// us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens, 11008 x
+// 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.  Up to 64
+// tokens with dW in the same launch, its workgroups want room too: both
+// outputs, 16 tokens, 4096 x 4096: 28.5 us in 4 slices, 31.0 in 8; 4096 x
+// 11008: 56 in 2, 64 in 1, 67 in 8.  Large tiles of both in one launch: dW's
+// fill the units that dX's leave, so that fewer slices do (1003 tokens, 5120 x
+// 5120, K = 4, both outputs: 231 us in 1 slice, 261 in 3 and two launches; 700
+// tokens, 5000 x 4096: 132 us, 160 in two launches).
+int dx_slices(int M, int out, int in, int K, bool with_dw) {
+    static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    const int tm = dx_tokens(M);
+    const float stage = tm <= 64 ? 0.8f : tm == 128 ? 1.4f : K > 2 ? 2.4f : 2.0f;
+    const int64_t room = with_dw && tm <= 64 ? 176 : 256;
+    const dw_plan w = plan_dw(M, out, in);
+    const bool both = with_dw && both_large(M, w);
+    const float tw = dw_tile_cost(M, w), work_w = (float)dw_tiles(out, in, w) * tw;
+    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + tm - 1) / tm);
+    const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
+    int best = 1;
+    float least = 0.0f;
+    for (const int S : splits) {
+        if (S > 1 && 2 * S > steps)
+            break;
+        const float tx = (float)((steps + S - 1) / S) * stage + 4.0f;
+        float cost = (float)((tiles * S + room - 1) / room) * tx;
+        if (both)                                                  // (and uneven ends)
+            cost = std::max(cost, ((float)(tiles * S) * tx + work_w) / 256.0f + 0.5f * tw + 0.2f * tx);
+        cost += slice_cost(S, (int64_t)M * in);
+        if (S == 1 || cost < least) {
+            best = S;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+size_t dx_slice_bytes(int M, int out, int in, int K) {
+    const int S = std::max(dx_slices(M, out, in, K, false), dx_slices(M, out, in, K, true));
+    return S > 1 ? (size_t)S * (size_t)M * (size_t)in * sizeof(float) : 0;
 }
 
 // Partial sums of dW's slices, and behind them the parts of the scales' gradients.
@@ -1101,6 +1167,10 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     case 32: e = launch_few<2>(c); break;
     case 64: e = launch_few<4>(c); break;
     default:
+        if (dW != nullptr && dX != nullptr && both_large(M, p)) {
+            e = launch_both(c);
+            break;
+        }
         if (dW != nullptr)
             e = p.large ? launch_dw<2, 4, 4>(c) : launch_dw<1, 4, 2>(c);
         if (e == hipSuccess && dX != nullptr)
