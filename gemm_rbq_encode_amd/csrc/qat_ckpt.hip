@@ -802,7 +802,7 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_dx_kernel(
 
 // Large tiles of both in one launch, one workgroup to a compute unit: dW's
 // begin on the units that dX's last round leaves free.
-template <int K>
+template <int TM, int K>
 __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_both_kernel(
     const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
     int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
@@ -810,7 +810,7 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_both_kernel(
     int T, float *__restrict__ dW, float *__restrict__ parts, int w_tiles_j, int w_tiles, int w_slices) {
     extern __shared__ __align__(16) unsigned char lds[];
     if ((int)blockIdx.x < x_total)
-        ck_dx<4, 4, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
+        ck_dx<4, TM, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
                        status, x_tiles_j, x_tiles_m);
     else
         ck_dw<2, 4, 4, false, 4>(lds, xcd_run(blockIdx.x - x_total, w_tiles * w_slices), dY, codes, cscales, M, out,
@@ -942,10 +942,11 @@ hipError_t launch_dx(const ck_call &c) {
     return hipGetLastError();
 }
 
+template <int TM>
 hipError_t launch_both(const ck_call &c) {
-    constexpr int LDS = 2 * CW_BK * (256 + 256) * 2;
-    static_assert(LDS == 2 * (256 * CX_BK * 2 + 2 * CX_BK * CX_J * 2) && LDS <= LDS_MAX, "LDS of a compute unit");
-    const int64_t x_tiles_j = ((int64_t)c.in + CX_J - 1) / CX_J, x_tiles_m = ((int64_t)c.M + 255) / 256;
+    constexpr int CM = 64 * TM, LDS = 2 * CW_BK * (256 + 256) * 2;
+    static_assert(LDS >= 2 * (CM * CX_BK * 2 + 2 * CX_BK * CX_J * 2) && LDS <= LDS_MAX, "LDS of a compute unit");
+    const int64_t x_tiles_j = ((int64_t)c.in + CX_J - 1) / CX_J, x_tiles_m = ((int64_t)c.M + CM - 1) / CM;
     const int64_t w_tiles_j = ((int64_t)c.in + 255) / 256, w_tiles = w_tiles_j * (((int64_t)c.out + 255) / 256);
     const int64_t x_total = x_tiles_j * x_tiles_m * c.dx_slices, total = x_total + w_tiles * c.dw_slices;
     if (total > CK_GRID)
@@ -957,10 +958,10 @@ hipError_t launch_both(const ck_call &c) {
                            (int)w_tiles, c.dw_slices);
     };
     switch (c.K) {
-    case 1: go(qat_ckpt_both_kernel<1>); break;
-    case 2: go(qat_ckpt_both_kernel<2>); break;
-    case 3: go(qat_ckpt_both_kernel<3>); break;
-    default: go(qat_ckpt_both_kernel<4>); break;
+    case 1: go(qat_ckpt_both_kernel<TM, 1>); break;
+    case 2: go(qat_ckpt_both_kernel<TM, 2>); break;
+    case 3: go(qat_ckpt_both_kernel<TM, 3>); break;
+    default: go(qat_ckpt_both_kernel<TM, 4>); break;
     }
     return hipGetLastError();
 }
@@ -991,119 +992,132 @@ hipError_t launch_few(const ck_call &c) {
     return hipGetLastError();
 }
 
-// Both plans take the least of a simple cost in us: rounds of workgroups over
-// the compute units, each a start and end and its stages, and for slices a
-// second launch and the write and read of the partial sums at 5 TB/s.
+// How a call is split up.  Every choice is the least of a simple cost in us:
+// rounds of workgroups over the compute units, each a start and end and its
+// stages, and for slices a second launch and the write and read of the partial
+// sums at 5 TB/s.
+constexpr int CK_SPLITS[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+constexpr int CK_UNITS = 256;
+
+struct ck_plan {
+    int dx_slices;            // of dX's contraction
+    int dw_large, dw_slices;  // dW's tiles (256 x 256, one workgroup per compute unit, or 128 x 128, two), slices of its tokens
+    bool both;                // one launch of dX and large tiles of dW
+};
 
 float slice_cost(int S, int64_t n) { return S > 1 ? 4.0f + (float)n * (float)(2 * S + 1) * (4.0f / 5.0e6f) : 0.0f; }
+
+int64_t ck_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // Tokens per dX tile.
 int dx_tokens(int M) { return M > 128 ? 256 : M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
 
-// dW's tiles (256 x 256, one workgroup per compute unit; or 128 x 128, two) and
-// slices of its tokens, of which up to 64 have a kernel of their own.  Measured with the scales' gradients: 2048 tokens,
-// 11008 x 4096: 248 us large, 338 small; 300 tokens, 2000 x 2048: 33 large, 20
-// small; 2000 tokens, 600 x 576: 38 us in one slice of 25 small tiles, 25 in 4.
-struct dw_plan {
-    int large, slices;
-};
+// dX: workgroups, and the time of one; stage times by tokens and planes.
+int64_t dx_groups(int M, int in, int S) { return ck_div(in, CX_J) * ck_div(M, dx_tokens(M)) * S; }
 
-// Workgroups, stages of one, and its time (with a compute unit to itself).
-int64_t dw_tiles(int out, int in, dw_plan p) {
-    const int64_t edge = p.large ? 256 : 128;
-    return ((in + edge - 1) / edge) * ((out + edge - 1) / edge) * p.slices;
-}
-
-int64_t dw_stages(int M, dw_plan p) {
-    return (((int64_t)M + CW_BK - 1) / CW_BK + p.slices - 1) / p.slices;
-}
-
-float dw_tile_cost(int M, dw_plan p) {
-    return p.large ? (float)dw_stages(M, p) * 1.9f + 8.0f : (float)dw_stages(M, p) * 1.1f + 6.0f;
-}
-
-// Whether dX and dW go in one launch of large tiles (300 tokens, 8192 x 4096,
-// K = 3: 143 us, 151 in two launches, though dX's fill whole rounds there).
-bool both_large(int M, dw_plan p) { return p.large && M > 128; }
-
-dw_plan plan_dw(int M, int out, int in) {
-    static constexpr int splits[] = {1, 2, 3, 4, 6, 8};
-    const int64_t steps = ((int64_t)M + CW_BK - 1) / CW_BK;
-    if (steps == 1)
-        return {0, 1};
-    dw_plan best = {1, 1};
-    float least = 0.0f;
-    for (int large = 0; large < 2; ++large)
-        for (const int S : splits) {
-            if (S > 1 && 2 * S > steps)
-                break;
-            const dw_plan p = {large, S};
-            const int64_t wgs = dw_tiles(out, in, p);
-            float cost = large        ? (float)((wgs + 255) / 256) * dw_tile_cost(M, p)
-                         : wgs <= 256 ? dw_tile_cost(M, p)
-                                      : (float)((wgs + 511) / 512) * ((float)dw_stages(M, p) * 1.6f + 8.0f);
-            cost += slice_cost(S, (int64_t)out * in);
-            if (least == 0.0f || cost < least) {
-                least = cost;
-                best = {large, S};
-            }
-        }
-    return best;
-}
-
-// Slices of dX's contraction.  Measured (one slice and the choice): 16 tokens,
-// 4096 x 4096: 48 and 16 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and 158
-// us in 3 (160 workgroups leave 96 compute units idle); 2048 tokens, 11008 x
-// 4096: 339 us in 1, 352 in 2.  Stage times by tokens and planes.  Up to 64
-// tokens with dW in the same launch, its workgroups want room too: both
-// outputs, 16 tokens, 4096 x 4096: 28.5 us in 4 slices, 31.0 in 8; 4096 x
-// 11008: 56 in 2, 64 in 1, 67 in 8.  Large tiles of both in one launch: dW's
-// fill the units that dX's leave, so that fewer slices do (1003 tokens, 5120 x
-// 5120, K = 4, both outputs: 231 us in 1 slice, 261 in 3 and two launches; 700
-// tokens, 5000 x 4096: 132 us, 160 in two launches).
-int dx_slices(int M, int out, int in, int K, bool with_dw) {
-    static constexpr int splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+float dx_time(int M, int out, int K, int S) {
     const int tm = dx_tokens(M);
     const float stage = tm <= 64 ? 0.8f : tm == 128 ? 1.4f : K > 2 ? 2.4f : 2.0f;
-    const int64_t room = with_dw && tm <= 64 ? 176 : 256;
-    const dw_plan w = plan_dw(M, out, in);
-    const bool both = with_dw && both_large(M, w);
-    const float tw = dw_tile_cost(M, w), work_w = (float)dw_tiles(out, in, w) * tw;
-    const int64_t tiles = (((int64_t)in + CX_J - 1) / CX_J) * (((int64_t)M + tm - 1) / tm);
-    const int64_t steps = ((int64_t)out + CX_BK - 1) / CX_BK;
-    int best = 1;
-    float least = 0.0f;
-    for (const int S : splits) {
-        if (S > 1 && 2 * S > steps)
+    return (float)ck_div(ck_div(out, CX_BK), S) * stage + (tm <= 64 ? 4.0f : 8.0f);
+}
+
+// dW: the same.
+int64_t dw_groups(int out, int in, int large, int S) {
+    const int edge = large ? 256 : 128;
+    return ck_div(in, edge) * ck_div(out, edge) * S;
+}
+
+float dw_time(int M, int large, int S, bool two) {
+    return (float)ck_div(ck_div(M, CW_BK), S) * (large ? 1.9f : two ? 1.6f : 1.1f) + (large ? 20.0f : two ? 14.0f : 10.0f);
+}
+
+// Each by itself.  Measured, dX (one slice and the choice): 16 tokens, 4096 x
+// 4096: 48 and 16 us in 8; 1003 tokens, 5120 x 5120, K = 4: 191 and 158 us in 3
+// (160 workgroups leave 96 compute units idle); 2048 tokens, 11008 x 4096: 339
+// us in 1, 352 in 2.  dW with the scales' gradients: 2048 tokens, 11008 x 4096:
+// 248 us large, 338 small; 300 tokens, 2000 x 2048: 33 large, 20 small; 2000
+// tokens, 600 x 576: 38 us in one slice of 25 small tiles, 25 in 4.
+//
+// Both in one launch.  Up to 64 tokens, where dW is written in one stage: 16
+// tokens, 4096 x 4096: 28.5 us with dX in 4 slices, 31.0 in 8; 4096 x 11008: 56
+// in 2, 64 in 1, 67 in 8; so dX takes 176 of the 256 units.  More tokens: dW's
+// workgroups fill the units that dX's leave, so that fewer slices do: 1003
+// tokens, 5120 x 5120, K = 4: 231 us in 1 slice, 261 in 3 and two launches; 300
+// tokens, 8192 x 4096, K = 3: 143 us, 151 in two launches; 955 tokens, 2896 x
+// 1536, K = 1: 54 us in 3 slices, 86 in 1, 75 in two launches.  Over 17 such
+// sizes the choice is the fastest or within 8 % of it.
+ck_plan plan_backward(int M, int out, int in, int K, bool dx, bool dw) {
+    ck_plan best = {1, 0, 1, false};
+    const int64_t steps = ck_div(out, CX_BK), stages = ck_div(M, CW_BK);
+    const bool few = M <= CW_BK;
+    float dx_least = 0.0f, dw_least = 0.0f;
+    for (const int S : CK_SPLITS) {
+        if (!dx || (S > 1 && 2 * S > steps))
             break;
-        const float tx = (float)((steps + S - 1) / S) * stage + 4.0f;
-        float cost = (float)((tiles * S + room - 1) / room) * tx;
-        if (both)                                                  // (and uneven ends)
-            cost = std::max(cost, ((float)(tiles * S) * tx + work_w) / 256.0f + 0.5f * tw + 0.2f * tx);
-        cost += slice_cost(S, (int64_t)M * in);
-        if (S == 1 || cost < least) {
-            best = S;
-            least = cost;
+        const int room = few && dw ? 176 : CK_UNITS;
+        const float cost = (float)ck_div(dx_groups(M, in, S), room) * dx_time(M, out, K, S) +
+                           slice_cost(S, (int64_t)M * in);
+        if (S == 1 || cost < dx_least) {
+            best.dx_slices = S;
+            dx_least = cost;
+        }
+    }
+    if (few || !dw)
+        return best;
+    for (int large = 1; large >= 0; --large)
+        for (const int S : CK_SPLITS) {
+            if (S > 8 || (S > 1 && 2 * S > stages))
+                break;
+            const int64_t groups = dw_groups(out, in, large, S);
+            const bool two = !large && groups > CK_UNITS;
+            const float cost = (float)ck_div(groups, two ? 2 * CK_UNITS : CK_UNITS) * dw_time(M, large, S, two) +
+                               slice_cost(S, (int64_t)out * in);
+            if (dw_least == 0.0f || cost < dw_least) {
+                best.dw_large = large;
+                best.dw_slices = S;
+                dw_least = cost;
+            }
+        }
+    if (!dx)
+        return best;
+    float least = dx_least + dw_least + 3.0f;
+    for (const int Sw : CK_SPLITS) {
+        if (Sw > 8 || (Sw > 1 && 2 * Sw > stages))
+            break;
+        const float tw = dw_time(M, 1, Sw, false);
+        const int64_t nw = dw_groups(out, in, 1, Sw);
+        for (const int S : CK_SPLITS) {
+            if (S > 1 && 2 * S > steps)
+                break;
+            // the units that dX's last round leaves begin with dW
+            const float tx = dx_time(M, out, K, S);
+            const int64_t nx = dx_groups(M, in, S), late = nx % CK_UNITS;
+            float cost = (float)(nx / CK_UNITS) * tx;
+            cost += late == 0 ? (float)ck_div(nw, CK_UNITS) * tw
+                              : std::max(std::max(tx, tw), ((float)late * tx + (float)nw * tw) / CK_UNITS + 0.4f * tw);
+            cost += slice_cost(S, (int64_t)M * in) + slice_cost(Sw, (int64_t)out * in);
+            if (cost < least) {
+                best = {S, 1, Sw, true};
+                least = cost;
+            }
         }
     }
     return best;
 }
 
-size_t dx_slice_bytes(int M, int out, int in, int K) {
-    const int S = std::max(dx_slices(M, out, in, K, false), dx_slices(M, out, in, K, true));
-    return S > 1 ? (size_t)S * (size_t)M * (size_t)in * sizeof(float) : 0;
+// Partial sums of dW's slices, the parts of the scales' gradients, and dX's
+// slices, one after another.
+size_t dw_slice_bytes(const ck_plan &p, int out, int in) {
+    return p.dw_slices > 1 ? (size_t)p.dw_slices * (size_t)out * (size_t)in * sizeof(float) : 0;
 }
 
-// Partial sums of dW's slices, and behind them the parts of the scales' gradients.
-size_t dw_slice_bytes(int M, int out, int in) {
-    const int S = plan_dw(M, out, in).slices;
-    return S > 1 ? (size_t)S * (size_t)out * (size_t)in * sizeof(float) : 0;
+size_t dw_part_bytes(const ck_plan &p, int out, int in, int K, int group_size) {
+    return p.dw_slices == 1 && (group_size || in <= F8_BLOCK)
+               ? 0 : (size_t)p.dw_slices * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
 }
 
-size_t dw_part_bytes(int M, int out, int in, int K, int group_size) {
-    const int S = plan_dw(M, out, in).slices;
-    return S == 1 && (group_size || in <= F8_BLOCK)
-               ? 0 : (size_t)S * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
+size_t dx_slice_bytes(const ck_plan &p, int M, int in) {
+    return p.dx_slices > 1 ? (size_t)p.dx_slices * (size_t)M * (size_t)in * sizeof(float) : 0;
 }
 
 ck_job sum_job(const float *from, float *to, int64_t n, int slices, int parts) {
@@ -1122,9 +1136,17 @@ hipError_t launch_qat_checkpoint(const uint16_t *X, int M, int in, int8_t *codes
     return hipGetLastError();
 }
 
-// One after another: slices of dW, parts of the scales' gradients, slices of dX.
+// Enough for any of the outputs.
 size_t qat_backward_ckpt_workspace_bytes(int M, int out, int in, int K, int group_size) {
-    return dw_slice_bytes(M, out, in) + dw_part_bytes(M, out, in, K, group_size) + dx_slice_bytes(M, out, in, K);
+    size_t most = 0;
+    for (int ask = 1; ask < 4; ++ask) {
+        const ck_plan p = plan_backward(M, out, in, K, ask & 1, ask & 2);
+        size_t n = ask & 1 ? dx_slice_bytes(p, M, in) : 0;
+        if (ask & 2)
+            n += dw_slice_bytes(p, out, in) + dw_part_bytes(p, out, in, K, group_size);
+        most = std::max(most, n);
+    }
+    return most;
 }
 
 hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales, int out, int in, int K,
@@ -1135,13 +1157,15 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     // gradients that would pass through it are taken from dW in a pass of
     // their own.
     const bool fits = ws_bytes >= qat_backward_ckpt_workspace_bytes(M, out, in, K, group_size);
-    const size_t part_bytes = dw_part_bytes(M, out, in, K, group_size);
+    ck_plan p = plan_backward(M, out, in, K, dX != nullptr, dW != nullptr);
+    const size_t part_bytes = dw_part_bytes(p, out, in, K, group_size);
+    if (!fits)
+        p.dx_slices = p.dw_slices = 1;
     float *ws = static_cast<float *>(workspace);
     ck_jobs left = {};
     int jobs = 0;
-    const dw_plan p = plan_dw(M, out, in);
     ck_call c = {dY, planes, scales, x_codes, x_scales, M, out, in, K, group_size, dX, dW, nullptr,
-                 fits ? dx_slices(M, out, in, K, dW != nullptr) : 1, fits ? p.slices : 1, status, st};
+                 p.dx_slices, p.dw_slices, status, st};
     c.dx_slices = (int)((out + dx_rows(c) - 1) / dx_rows(c));        // (none of them empty)
     if (dW != nullptr && c.dw_slices > 1) {
         c.dW = ws;
@@ -1167,12 +1191,12 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     case 32: e = launch_few<2>(c); break;
     case 64: e = launch_few<4>(c); break;
     default:
-        if (dW != nullptr && dX != nullptr && both_large(M, p)) {
-            e = launch_both(c);
+        if (p.both) {
+            e = M > 128 ? launch_both<4>(c) : launch_both<2>(c);
             break;
         }
         if (dW != nullptr)
-            e = p.large ? launch_dw<2, 4, 4>(c) : launch_dw<1, 4, 2>(c);
+            e = p.dw_large ? launch_dw<2, 4, 4>(c) : launch_dw<1, 4, 2>(c);
         if (e == hipSuccess && dX != nullptr)
             e = M > 128 ? launch_dx<4, 4>(c) : launch_dx<4, 2>(c);
         break;

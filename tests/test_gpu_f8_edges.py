@@ -210,3 +210,22 @@ HEIGHTS = [(out, M, inf) for out, M in [(8191, 2047), (7168, 2041), (7001, 2048)
 @pytest.mark.parametrize("out,M,inf", HEIGHTS)
 def test_gemm_tiles_of_every_height(out, M, inf):
     test_gpu_f8.test_gemm_tiles_match_the_definition_in_64_bits(out, M, inf, True)
+
+
+@pytest.mark.parametrize("out,inf,K,group,M", [(600, 576, 2, 0, 1100), (100, 160, 1, 0, 70), (1030, 640, 4, 128, 300),
+                                               (257, 1056, 3, 0, 130), (2050, 2048, 2, 0, 128)])
+def test_gradients_asked_for_one_by_one(out, inf, K, group, M):
+    """Kernels of their own serve dX alone and dW with or without the scales'
+    gradients; with the workspace and without."""
+    planes, s, X, dY = case(out, inf, K, group, M, out + 3 * M)
+    a = (t_planes(planes), t_f16(s), *rbq.qat_checkpoint(t_f16(X)), t_f16(dY), group)
+    x = f8.restore(*f8.checkpoint(X))
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=dev())):
+        dx = rbq.qat_backward_ckpt(*a, need_dw=False, need_dscales=False, workspace=ws)
+        dw = rbq.qat_backward_ckpt(*a, need_dx=False, need_dscales=False, workspace=ws)
+        ds = rbq.qat_backward_ckpt(*a, need_dx=False, workspace=ws)
+        both = rbq.qat_backward_ckpt(*a, need_dscales=False, workspace=ws)
+        torch.cuda.synchronize()
+        assert dx[1:] == (None, None) and (dw[0], dw[2]) == (None, None) and ds[0] is None and both[2] is None
+        for got in (dx, dw, ds, both):
+            check_grads(got, planes, s, x, dY, group)
