@@ -495,56 +495,32 @@ def _one_device(*tensors) -> torch.device:
     return dev
 
 
-class _Here:
-    """Context of a call on the current device and stream: the stream's handle."""
-    __slots__ = ("_index",)
-
-    def __init__(self, index: int):
-        self._index = index
-
-    def __enter__(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self._index)       # current_stream without the object
-
-    def __exit__(self, *exc):
-        pass
+# the current device, and the handle of a device's current stream, without the
+# objects (a call's tensors are there: the runtime is up)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _There:
-    """Context of a call for tensors on `dev`: that device is current, and so is
-    the stream the call is for, so that buffers made inside belong to it.
-    Enters as the stream's handle."""
-    __slots__ = ("_index", "_ctx")
+    """Inside, `dev` is the current device, and `stream` (if given) its current
+    stream, so that buffers made belong to them."""
+    __slots__ = ("_ctx",)
 
     def __init__(self, dev: torch.device, stream):
-        self._index = dev.index
         self._ctx = [torch.cuda.device(dev)]
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=dev)
             self._ctx.append(torch.cuda.stream(stream))
 
-    def __enter__(self) -> int:
+    def __enter__(self):
         for c in self._ctx:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def __exit__(self, *exc):
         for c in reversed(self._ctx):
             c.__exit__(*exc)
-
-
-_here: dict = {}
-
-
-def _launch(dev: torch.device, stream=None):
-    """The context of a call for tensors on `dev`."""
-    i = dev.index
-    if stream is not None or i != torch._C._cuda_getDevice():        # (a tensor is there: the runtime is up)
-        return _There(dev, stream)
-    h = _here.get(i)
-    if h is None:
-        h = _here[i] = _Here(i)
-    return h
 
 
 def _blocks(n: int) -> int:
@@ -583,11 +559,14 @@ def encode_f8(W: torch.Tensor, *, status: torch.Tensor | None = None, codes: tor
     if status is not None:
         _dev(status, torch.int32, "status")
     dev = _one_device(W, status)
-    with _launch(dev, stream) as st:
-        codes = _out(codes, (out_f, in_f), torch.float8_e4m3fn, "codes", dev, W)
-        scales = _out(scales, (_blocks(out_f), _blocks(in_f)), torch.float32, "scales", dev)
-        check(lib().rbq_encode_f8(W.data_ptr(), out_f, in_f, codes.data_ptr(), scales.data_ptr(),
-                                  None if status is None else status.data_ptr(), st), "rbq_encode_f8")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return encode_f8(W, status=status, codes=codes, scales=scales)
+    st = _current_stream(dev.index)
+    codes = _out(codes, (out_f, in_f), torch.float8_e4m3fn, "codes", dev, W)
+    scales = _out(scales, (_blocks(out_f), _blocks(in_f)), torch.float32, "scales", dev)
+    check(lib().rbq_encode_f8(W.data_ptr(), out_f, in_f, codes.data_ptr(), scales.data_ptr(),
+                              None if status is None else status.data_ptr(), st), "rbq_encode_f8")
     return codes, scales
 
 
@@ -600,11 +579,14 @@ def quantize_f8(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales: t
         raise ValueError("X must be [M][in]")
     M, in_f = X.shape
     dev = X.device
-    with _launch(dev, stream) as st:
-        codes = _out(codes, (M, in_f), torch.float8_e4m3fn, "codes", dev, X)
-        scales = _out(scales, (_blocks(in_f), M), torch.float32, "scales", dev)
-        check(lib().rbq_quantize_f8(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
-              "rbq_quantize_f8")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return quantize_f8(X, codes=codes, scales=scales)
+    st = _current_stream(dev.index)
+    codes = _out(codes, (M, in_f), torch.float8_e4m3fn, "codes", dev, X)
+    scales = _out(scales, (_blocks(in_f), M), torch.float32, "scales", dev)
+    check(lib().rbq_quantize_f8(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
+          "rbq_quantize_f8")
     return codes, scales
 
 
@@ -633,15 +615,18 @@ def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_
         raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
     dev = _one_device(codes, scales, x_codes, x_scales, workspace)
     kind = RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16
-    with _launch(dev, stream) as st:
-        Y = _out(Y, (M, out_f), dtype, "Y", dev)
-        if workspace is None and M > 32:      # none is needed for fewer
-            need = int(lib().rbq_gemm_f8_workspace_bytes(out_f, in_f, M, kind))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
-        check(lib().rbq_gemm_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x_codes.data_ptr(),
-                                x_scales.data_ptr(), M, Y.data_ptr(), kind, wp, wn, st), "rbq_gemm_f8")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return gemm_f8(codes, scales, x_codes, x_scales, dtype=dtype, Y=Y, workspace=workspace)
+    st = _current_stream(dev.index)
+    Y = _out(Y, (M, out_f), dtype, "Y", dev)
+    if workspace is None and M > 32:      # none is needed for fewer
+        need = int(lib().rbq_gemm_f8_workspace_bytes(out_f, in_f, M, kind))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
+    check(lib().rbq_gemm_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x_codes.data_ptr(),
+                            x_scales.data_ptr(), M, Y.data_ptr(), kind, wp, wn, st), "rbq_gemm_f8")
     return Y
 
 
@@ -653,10 +638,13 @@ def gemv_f8(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, *, y: to
     if x.numel() != in_f:
         raise ValueError(f"x must have {in_f} elements")
     dev = _one_device(codes, scales, x)
-    with _launch(dev, stream) as st:
-        y = _out(y, (out_f,), torch.float16, "y", dev)
-        check(lib().rbq_gemv_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x.data_ptr(), y.data_ptr(), st),
-              "rbq_gemv_f8")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return gemv_f8(codes, scales, x, y=y)
+    st = _current_stream(dev.index)
+    y = _out(y, (out_f,), torch.float16, "y", dev)
+    check(lib().rbq_gemv_f8(codes.data_ptr(), scales.data_ptr(), out_f, in_f, x.data_ptr(), y.data_ptr(), st),
+          "rbq_gemv_f8")
     return y
 
 
@@ -669,11 +657,14 @@ def qat_checkpoint(X: torch.Tensor, *, codes: torch.Tensor | None = None, scales
         raise ValueError("X must be [M][in]")
     M, in_f = X.shape
     dev = X.device
-    with _launch(dev, stream) as st:
-        codes = _out(codes, (M, in_f), torch.int8, "codes", dev, X)
-        scales = _out(scales, (M, _blocks(in_f)), torch.float16, "scales", dev)
-        check(lib().rbq_qat_checkpoint(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
-              "rbq_qat_checkpoint")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return qat_checkpoint(X, codes=codes, scales=scales)
+    st = _current_stream(dev.index)
+    codes = _out(codes, (M, in_f), torch.int8, "codes", dev, X)
+    scales = _out(scales, (M, _blocks(in_f)), torch.float16, "scales", dev)
+    check(lib().rbq_qat_checkpoint(X.data_ptr(), M, in_f, codes.data_ptr(), scales.data_ptr(), st),
+          "rbq_qat_checkpoint")
     return codes, scales
 
 
@@ -704,18 +695,22 @@ def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch
         _dev(status, torch.int32, "status")
     dev = _one_device(planes, scales, x_codes, x_scales, dY, workspace, status)
     ptr = (lambda t: None if t is None else t.data_ptr())
-    with _launch(dev, stream) as st:
-        dX = torch.empty((M, in_f), dtype=torch.float32, device=dev) if need_dx else None
-        dW = torch.empty((out_f, in_f), dtype=torch.float32, device=dev) if (need_dw or need_dscales) else None
-        ds = torch.empty((K, out_f, groups_per_row(in_f, group_size)), dtype=torch.float32, device=dev) \
-            if need_dscales else None
-        need = int(lib().rbq_qat_backward_ckpt_workspace_bytes(s, M))
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wn = _nbytes(workspace) if workspace is not None else 0
-        check(lib().rbq_qat_backward_ckpt(planes.data_ptr(), scales.data_ptr(), s, x_codes.data_ptr(),
-                                          x_scales.data_ptr(), dY.data_ptr(), M, ptr(dX), ptr(dW), ptr(ds),
-                                          ptr(workspace), wn, ptr(status), st), "rbq_qat_backward_ckpt")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return qat_backward_ckpt(planes, scales, x_codes, x_scales, dY, group_size, need_dx=need_dx,
+                                     need_dw=need_dw, need_dscales=need_dscales, workspace=workspace, status=status)
+    st = _current_stream(dev.index)
+    dX = torch.empty((M, in_f), dtype=torch.float32, device=dev) if need_dx else None
+    dW = torch.empty((out_f, in_f), dtype=torch.float32, device=dev) if (need_dw or need_dscales) else None
+    ds = torch.empty((K, out_f, groups_per_row(in_f, group_size)), dtype=torch.float32, device=dev) \
+        if need_dscales else None
+    need = int(lib().rbq_qat_backward_ckpt_workspace_bytes(s, M))
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wn = _nbytes(workspace) if workspace is not None else 0
+    check(lib().rbq_qat_backward_ckpt(planes.data_ptr(), scales.data_ptr(), s, x_codes.data_ptr(),
+                                      x_scales.data_ptr(), dY.data_ptr(), M, ptr(dX), ptr(dW), ptr(ds),
+                                      ptr(workspace), wn, ptr(status), st), "rbq_qat_backward_ckpt")
     return dX, (dW if need_dw else None), ds
 
 

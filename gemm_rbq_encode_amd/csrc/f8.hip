@@ -24,33 +24,29 @@ constexpr int FQ_THREADS = 256;
 // ---------------------------------------------------------------------------
 // tokens: 16 lanes hold one block (8 consecutive fp16 each, one 16-byte load),
 // so the maximum is four DPP rotations inside a row of 16 lanes and needs no
-// LDS.  A workgroup takes 16 tokens x 4 blocks; the four loads of a lane are
-// issued together.  Bound by the read of X and the write of the codes: 2048 x
-// 14336 takes 15.4 us, 5.8 TB/s (26.8 us where X has to come from HBM past
-// another kernel's unwritten lines); 4 x 4096, 4.6 us, is a launch.
-constexpr int FQ_ROWS = FQ_THREADS / 16;
-constexpr int FQ_BLOCKS = 4;
+// LDS.  A workgroup takes 16 tokens x 4 blocks, the four loads of a lane issued
+// together, or 1 x 16, one block a lane, which takes less time from the load to
+// the codes.  Bound by the read of X and the write of the codes: 2048 x 14336
+// takes 15.4 us, 5.8 TB/s (26.4 us where X has to come from HBM past another
+// kernel's unwritten lines).
 
+template <int B>
 __global__ __launch_bounds__(FQ_THREADS) void quantize_f8_kernel(const uint16_t *__restrict__ X, int M, int in,
-                                                                 int T, int64_t units,
-                                                                 uint8_t *__restrict__ codes,
+                                                                 int T, uint8_t *__restrict__ codes,
                                                                  float *__restrict__ scales) {
-    const int li = threadIdx.x & 15;
-    const int tg = (T + FQ_BLOCKS - 1) / FQ_BLOCKS;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t m = u / tg * FQ_ROWS + (threadIdx.x >> 4);
-        const int t0 = (int)(u % tg) * FQ_BLOCKS;
-        if (m >= M)
-            continue;
+    constexpr int ROWS = f8_rows(B);
+    const int li = threadIdx.x & 15, sub = threadIdx.x >> 4;
+    const int t0 = B == 1 ? (int)blockIdx.x * 16 + sub : (int)blockIdx.x * B;
+    for (int64_t m = (int64_t)blockIdx.y * ROWS + (B == 1 ? 0 : sub); m < M; m += (int64_t)gridDim.y * ROWS) {
         const uint16_t *row = X + m * in;
-        uint4 v[FQ_BLOCKS];
+        uint4 v[B];
 #pragma unroll
-        for (int b = 0; b < FQ_BLOCKS; ++b) {
+        for (int b = 0; b < B; ++b) {
             const int64_t c = (int64_t)(t0 + b) * F8_BLOCK + 8 * li;
             v[b] = c < in ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int b = 0; b < FQ_BLOCKS; ++b) {
+        for (int b = 0; b < B; ++b) {
             const int64_t c = (int64_t)(t0 + b) * F8_BLOCK + 8 * li;
             const uint32_t top = row16_max_u32(absmax8_f16(v[b]));
             float scale, inv;
@@ -385,10 +381,15 @@ hipError_t launch_few_tokens(const uint8_t *W, const float *ws, int out, int in,
 }  // namespace
 
 hipError_t launch_quantize_f8(const uint16_t *X, int M, int in, uint8_t *codes, float *scales, hipStream_t st) {
+    // 4 x 4096: 2.0 us with one block a lane, 2.6 with four; 2048 x 4096: 6.1 and
+    // 6.5; 4096 x 4096: 10.5 and 9.9
     const int T = f8_blocks(in);
-    const int64_t units = ((int64_t)M + FQ_ROWS - 1) / FQ_ROWS * ((T + FQ_BLOCKS - 1) / FQ_BLOCKS);
-    hipLaunchKernelGGL(quantize_f8_kernel, dim3((unsigned)std::min<int64_t>(units, 1 << 22)), dim3(FQ_THREADS), 0,
-                       st, X, M, in, T, units, codes, scales);
+    if (f8_spread(M, T, 65536))
+        hipLaunchKernelGGL(quantize_f8_kernel<1>, f8_token_grid(M, T, 1), dim3(FQ_THREADS), 0, st, X, M, in, T, codes,
+                           scales);
+    else
+        hipLaunchKernelGGL(quantize_f8_kernel<4>, f8_token_grid(M, T, 4), dim3(FQ_THREADS), 0, st, X, M, in, T, codes,
+                           scales);
     return hipGetLastError();
 }
 

@@ -12,6 +12,23 @@ constexpr float F8_MAX = 448.0f;
 
 inline __host__ __device__ int f8_blocks(int n) { return (n >> 7) + ((n & 127) != 0); }
 
+// Kernels over tokens in blocks of 128: workgroups of 256 threads, 16 lanes to
+// a block, take f8_rows(B) tokens x B blocks a lane; grid x the blocks, y the
+// tokens (from 65535 on, in a loop).
+constexpr __host__ __device__ int f8_rows(int B) { return B == 1 ? 1 : 16; }
+
+inline dim3 f8_token_grid(int M, int T, int B) {
+    const int cols = B == 1 ? 16 : B;
+    const int64_t rows = ((int64_t)M + f8_rows(B) - 1) / f8_rows(B);
+    return dim3((unsigned)((T + cols - 1) / cols), (unsigned)(rows < 65535 ? rows : 65535));
+}
+
+// One block a lane, for the least time from the load to the codes: up to `most`
+// blocks, and with rows of fewer than 16, of which lanes are left over, few.
+inline bool f8_spread(int M, int T, int64_t most) {
+    return (int64_t)M * T <= (T < 16 ? 4096 : most);
+}
+
 // Tile of workgroup `id` of `total`: consecutive workgroups go to consecutive
 // XCDs, so each of the 8 takes a run of consecutive tiles, which share
 // operands in its L2.
