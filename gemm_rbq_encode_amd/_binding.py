@@ -512,6 +512,8 @@ class _There:
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            elif stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the call's tensors are on {dev}")
             self._ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):

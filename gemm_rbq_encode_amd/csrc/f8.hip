@@ -396,7 +396,10 @@ hipError_t launch_quantize_f8(const uint16_t *X, int M, int in, uint8_t *codes, 
 hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, float *scales, int32_t *status,
                             hipStream_t st) {
     const int T = f8_blocks(in);
-    hipLaunchKernelGGL(encode_f8_kernel, dim3((unsigned)T * (unsigned)f8_blocks(out)), dim3(FQ_THREADS), 0, st, W,
+    const int64_t groups = (int64_t)T * f8_blocks(out);
+    if (groups > 0x7FFFFFFF / FQ_THREADS)
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(encode_f8_kernel, dim3((unsigned)groups), dim3(FQ_THREADS), 0, st, W,
                        out, in, T, codes, scales, status);
     return hipGetLastError();
 }

@@ -7,6 +7,7 @@ import torch
 
 import gemm_rbq_encode_amd as rbq
 import workloads
+from gemm_rbq_encode_amd import _binding
 from oracle import f8
 
 pytestmark = pytest.mark.cpu
@@ -164,6 +165,14 @@ def test_layers_beyond_the_limit_are_refused():
         assert L.rbq_qat_backward_ckpt(OK, OK, s, OK, OK, OK, 4, OK, OK, OK, None, 0, None, None) == un
         assert L.rbq_qat_backward_ckpt_workspace_bytes(s, 4) == 0
     assert L.rbq_gemm_f8_workspace_bytes(big, 64, 300, 0) == 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        cuda_stream, device = 1, torch.device("cuda:1")
+
+    with pytest.raises(ValueError):
+        _binding._There(torch.device("cuda:0"), Stream())
 
 
 def test_workspaces_are_no_larger_than_their_slices():
