@@ -367,8 +367,8 @@ hipError_t launch_few(const uint8_t *W, const float *ws, int out, int in, const 
 // often, fewer rows make more workgroups: 16 tokens on 4096 x 4096, 11008 x
 // 4096 and 14336 x 4096 take 7.3, 15.8 and 20.0 us with 16 rows against 8.8,
 // 16.3 and 17.7 with 32.  Two blocks in flight and 8 waves: 3 or 4 blocks take
-// 3 to 30 % longer, 16 waves between 3 % less and 16 % more.  More than 32 tokens come here only where the tiled
-// kernels' offsets do not reach.
+// 3 to 30 % longer, 16 waves between 3 % less and 16 % more.  More than 32
+// tokens come here only where the tiled kernels' offsets do not reach.
 template <typename Y>
 hipError_t launch_few_tokens(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
                              int M, Y *y, hipStream_t st) {
