@@ -59,14 +59,16 @@ __device__ __forceinline__ uint32_t f8_lds_addr(const void *p) {
 }
 
 // 16 bytes from base + voff to LDS [m0 + 16 lane].  M0 is set here; nothing
-// else in this kernel reads it.
+// else in this kernel reads it.  A load to LDS may read M0 one wait state after
+// a scalar write at the earliest, and the compiler places such waits around
+// inline assembly, not inside it: hence the s_nop.
 __device__ __forceinline__ void f8_load_lds(const void *base, uint32_t voff, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
 }
 
 // 4 bytes from base + voff to LDS [m0 + 4 lane].
 __device__ __forceinline__ void f8_load_lds4(const void *base, uint32_t voff, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory");
 }
 
 // All but the N youngest loads have landed, in every wave.

@@ -231,15 +231,17 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
 
 // The two loads below set M0 themselves; nothing else in the kernels that
 // use them reads M0 (no LDS-DMA builtins, message or relative-move
-// instructions), so the compiler keeps no value there.
+// instructions), so the compiler keeps no value there.  A load to LDS may read
+// M0 one wait state after a scalar write at the earliest, and the compiler
+// places such waits around inline assembly, not inside it: hence the s_nop.
 // 16 bytes from base + voff to LDS [m0 + 16 lane]
 __device__ __forceinline__ void dma16(const void *base, uint32_t voff, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0)
                  : "memory");
 }
 // 4 bytes from base + voff to LDS [m0 + 4 lane]
 __device__ __forceinline__ void dma4(const void *base, uint32_t voff, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0)
                  : "memory");
 }
 

@@ -140,7 +140,8 @@ __global__ __launch_bounds__(SP_THREADS, 1) void gemm_splitf_kernel(
         const int q = lane ^ m;
         const int piece = min((c0 + c) * 64 + q, npieces - 1);
         const uint32_t voff = (uint32_t)((min(m, M - 1) * in + 8 * piece) * 2);
-        asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(X),
+        // (the s_nop: a load to LDS reads M0 one wait state after its write at the earliest)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(X),
                      "s"(xl + (uint32_t)(c * SF_XCHUNK + m * 1024))
                      : "memory");
     }
