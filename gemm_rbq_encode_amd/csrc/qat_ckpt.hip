@@ -119,6 +119,7 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef v4u __attribute__((aligned(2))) v4u_a2;       // 16 bytes at any fp16
 typedef v4u __attribute__((aligned(4))) v4u_a4;       // ... at any word
+typedef double __attribute__((aligned(4))) f64_a4;
 
 __device__ __forceinline__ int ck_swizzle(int k, int P) { return 2 * (((k & 3) | ((k >> 1) & 12)) & (P / 2 - 1)); }
 
@@ -149,11 +150,11 @@ __device__ __forceinline__ void ck_barrier() { asm volatile("s_waitcnt lgkmcnt(0
 // each 128 columns x 16 TN rows of dW; the columns are the side that a lane
 // holds four of, so dW is written 16 bytes a lane.
 //
-// The gradients of the scales are sums of +-dW over groups of columns: each
-// wave adds its 128 columns from the registers it has just computed and
-// writes one value per row and plane to parts [K][out][ceil(in / 128)], which
-// are the group gradients themselves for groups of 128 and are added in order
-// at the end for scales per row.
+// The gradients of the scales are sums of +-dW over groups of columns, in fp64
+// as in qat.hip (entries of one size cancel): each wave adds its 128 columns
+// from the registers it has just computed, which is a whole gradient where
+// that is a group and all tokens, and else one fp64 value per row and plane of
+// parts [slice][K][out][ceil(in / 128)], added in order at the end.
 //
 // Bound by the matrix instructions and their power: 2048 tokens, 11008 x 4096:
 // 225 us, 820 TFLOP/s, and 237 with the scales' gradients (688 tiles are 2.7
@@ -169,7 +170,8 @@ template <int WM, int WN, int TN, bool ONE, int KP>
 __device__ __forceinline__ void ck_dw(
     unsigned char *lds, int id, const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes,
     const uint16_t *__restrict__ cscales, int M, int out, int in, int T, float *__restrict__ dW,
-    const uint32_t *__restrict__ planes, int K, float *__restrict__ parts, int tiles_j, int tiles, int slices) {
+    const uint32_t *__restrict__ planes, int K, float *__restrict__ grads, f64_a4 *__restrict__ parts, int tiles_j,
+    int tiles, int slices) {
     constexpr int THREADS = WM * WN * RBQ_WAVE;
     constexpr int CJ = WM * 128, CR = WN * TN * 16;            // tile: columns x rows of dW
     constexpr int PJ = CJ / 8, PR = CR / 8;                    // pieces of an LDS row
@@ -310,7 +312,7 @@ __device__ __forceinline__ void ck_dw(
     // the sign words of this wave's columns, for the scales' gradients; they
     // arrive while dW is written
     const int64_t words = in >> 5, w0 = (j0 + wj * 128) >> 5;
-    const bool add = parts != nullptr && w0 < words;
+    const bool add = (grads != nullptr || parts != nullptr) && w0 < words;
     v4u sign[KP][TN];
     auto load_signs = [&]() {
         if (!add)
@@ -394,31 +396,52 @@ __device__ __forceinline__ void ck_dw(
     }
     if (!add)
         return;
-    parts += (int64_t)slice * K * out * T + w0 / 4;
+    const int64_t at = (int64_t)slice * K * out * T + w0 / 4;
 #pragma unroll
-    for (int k = 0; k < KP; ++k) {
-        if (k >= K)
-            break;
+    for (int j = 0; j < TN; ++j) {
+        const int64_t r = r0 + (wr * TN + j) * 16 + li;
+        double s[KP];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t r = r0 + (wr * TN + j) * 16 + li;
-            float s = 0.0f;
+        for (int k = 0; k < KP; ++k)
+            s[k] = 0.0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (w0 + q >= words)                       // columns past the last
-                    break;
-                const uint32_t w = ~sign[k][j][q] >> (4 * g);
+        for (int q = 0; q < 4; ++q) {
+            if (w0 + q >= words)                           // columns past the last
+                break;
+            // (a half at a time, for the registers)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                double d[4];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        s += __uint_as_float(__float_as_uint(acc[2 * q + h][j][v]) ^
-                                             ((w << (31 - 16 * h - v)) & 0x80000000u));
+                for (int v = 0; v < 4; ++v)
+                    d[v] = (double)acc[2 * q + h][j][v];
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    if (k >= K)
+                        break;
+                    const uint32_t w = ~sign[k][j][q] >> (4 * g);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)                // + d or - d: the high word of +-1.0
+                        s[k] = __builtin_fma(
+                            d[v], __hiloint2double((int)(((w << (31 - 16 * h - v)) & 0x80000000u) | 0x3FF00000u), 0), s[k]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            s += __shfl_xor(s, 16, RBQ_WAVE);
-            s += __shfl_xor(s, 32, RBQ_WAVE);
-            if (g == 0 && r < out)
-                parts[((int64_t)k * out + r) * T] = s;
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            if (k >= K)
+                break;
+            double v = s[k];
+            v += __shfl_xor(v, 16, RBQ_WAVE);
+            v += __shfl_xor(v, 32, RBQ_WAVE);
+            const int64_t o = at + ((int64_t)k * out + r) * T;
+            if (g == 0 && r < out) {
+                if (grads != nullptr)
+                    grads[o] = (float)v;
+                else
+                    parts[o] = v;
+            }
         }
     }
 }
@@ -429,10 +452,10 @@ template <int WM, int WN, int TN>
 __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
     const uint16_t *__restrict__ dY, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int M,
     int out, int in, int T, float *__restrict__ dW, const uint32_t *__restrict__ planes, int K,
-    float *__restrict__ parts, int tiles_j, int tiles, int slices) {
+    float *__restrict__ grads, f64_a4 *__restrict__ parts, int tiles_j, int tiles, int slices) {
     extern __shared__ __align__(16) unsigned char lds[];
     ck_dw<WM, WN, TN, false, 4>(lds, xcd_run(blockIdx.x, tiles * slices), dY, codes, cscales, M, out, in, T, dW,
-                                planes, K, parts, tiles_j, tiles, slices);
+                                planes, K, grads, parts, tiles_j, tiles, slices);
 }
 
 // ---------------------------------------------------------------------------
@@ -802,14 +825,15 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_both_kernel(
     const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
     int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
     int x_tiles_j, int x_tiles_m, int x_total, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales,
-    int T, float *__restrict__ dW, float *__restrict__ parts, int w_tiles_j, int w_tiles, int w_slices) {
+    int T, float *__restrict__ dW, float *__restrict__ grads, f64_a4 *__restrict__ parts, int w_tiles_j, int w_tiles,
+    int w_slices) {
     extern __shared__ __align__(16) unsigned char lds[];
     if ((int)blockIdx.x < x_total)
         ck_dx<4, TM, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
                        status, x_tiles_j, x_tiles_m);
     else
         ck_dw<2, 4, 4, false, 4>(lds, xcd_run(blockIdx.x - x_total, w_tiles * w_slices), dY, codes, cscales, M, out,
-                                 in, T, dW, planes, K, parts, w_tiles_j, w_tiles, w_slices);
+                                 in, T, dW, planes, K, grads, parts, w_tiles_j, w_tiles, w_slices);
 }
 
 // Up to 64 tokens: both in one launch, two workgroups to a compute unit.  The
@@ -823,23 +847,23 @@ __global__ __launch_bounds__(CX_THREADS, 4) void qat_ckpt_few_kernel(
     const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,
     int out, int in, int group_size, int64_t r_slice, float *__restrict__ dX, int32_t *__restrict__ status,
     int x_tiles, int x_total, const int8_t *__restrict__ codes, const uint16_t *__restrict__ cscales, int T,
-    float *__restrict__ dW, float *__restrict__ parts, int w_tiles_j, int w_tiles) {
+    float *__restrict__ dW, float *__restrict__ grads, f64_a4 *__restrict__ parts, int w_tiles_j, int w_tiles) {
     extern __shared__ __align__(16) unsigned char lds[];
     if ((int)blockIdx.x < x_total)
         ck_dx<1, TM, K>(lds, xcd_run(blockIdx.x, x_total), dY, planes, scales, M, out, in, group_size, r_slice, dX,
                         status, x_tiles, 1);
     else
         ck_dw<1, 8, 2, true, K>(lds, xcd_run(blockIdx.x - x_total, w_tiles), dY, codes, cscales, M, out, in, T, dW,
-                                planes, K, parts, w_tiles_j, w_tiles, 1);
+                                planes, K, grads, parts, w_tiles_j, w_tiles, 1);
 }
 
 // What is left to add at the end, in one launch: up to three jobs, each with a
-// share of the workgroups.  A job sums, for each of n outputs, `slices` groups
-// of `parts` consecutive values in a fixed order: by one thread in fp32 where
-// a group is one value (slices of dW or dX, gradients of group scales), else
-// by one wave in fp64 (gradients of row scales).
+// share of the workgroups.  A job sums, for each of n outputs, `slices` fp32
+// values in order (slices of dW or dX; parts = 0), or `slices` groups of
+// `parts` consecutive fp64 values in a fixed order (the scales' gradients): by
+// one thread where a group is one value, else by one wave.
 struct ck_job {
-    const float *from;
+    const void *from;
     float *to;
     int64_t n;
     int slices, parts;
@@ -856,12 +880,24 @@ __global__ __launch_bounds__(CK_THREADS) void qat_ckpt_join_kernel(ck_jobs jobs)
     while (q < 2 && b >= jobs.job[q].blocks)
         b -= jobs.job[q++].blocks;
     const ck_job &o = jobs.job[q];
-    if (o.parts == 1) {
-        for (int64_t i = (int64_t)b * CK_THREADS + threadIdx.x; i < o.n; i += (int64_t)o.blocks * CK_THREADS) {
-            float v = o.from[i];
+    const int64_t first = (int64_t)b * CK_THREADS + threadIdx.x, stride = (int64_t)o.blocks * CK_THREADS;
+    if (o.parts == 0) {
+        const float *from = static_cast<const float *>(o.from);
+        for (int64_t i = first; i < o.n; i += stride) {
+            float v = from[i];
             for (int z = 1; z < o.slices; ++z)
-                v += o.from[z * o.n + i];
+                v += from[z * o.n + i];
             o.to[i] = v;
+        }
+        return;
+    }
+    const f64_a4 *from = static_cast<const f64_a4 *>(o.from);
+    if (o.parts == 1) {
+        for (int64_t i = first; i < o.n; i += stride) {
+            double v = from[i];
+            for (int z = 1; z < o.slices; ++z)
+                v += from[z * o.n + i];
+            o.to[i] = (float)v;
         }
         return;
     }
@@ -871,7 +907,7 @@ __global__ __launch_bounds__(CK_THREADS) void qat_ckpt_join_kernel(ck_jobs jobs)
         double s = 0.0;
         for (int z = 0; z < o.slices; ++z)
             for (int t = lane; t < o.parts; t += RBQ_WAVE)
-                s += (double)o.from[(z * o.n + i) * o.parts + t];
+                s += from[(z * o.n + i) * o.parts + t];
         s = wave_sum_f64(s);
         if (lane == 0)
             o.to[i] = (float)s;
@@ -888,7 +924,9 @@ struct ck_call {
     const int8_t *codes;
     const uint16_t *cscales;
     int M, out, in, K, group_size;
-    float *dX, *dW, *parts;                // dX and dW: the results, or slices of them
+    float *dX, *dW;                        // the results, or slices of them
+    float *grads;                          // the scales' gradients, or null and
+    f64_a4 *parts;                         // parts of them, or null
     int dx_slices, dw_slices;
     int32_t *status;
     hipStream_t st;
@@ -911,7 +949,7 @@ hipError_t launch_dw(const ck_call &c) {
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((qat_ckpt_dw_kernel<WM, WN, TN>), dim3((unsigned)(tiles * c.dw_slices)),
                        dim3(WM * WN * RBQ_WAVE), LDS, c.st, c.dY, c.codes, c.cscales, c.M, c.out, c.in,
-                       f8_blocks(c.in), c.dW, c.planes, c.K, c.parts, (int)tiles_j, (int)tiles, c.dw_slices);
+                       f8_blocks(c.in), c.dW, c.planes, c.K, c.grads, c.parts, (int)tiles_j, (int)tiles, c.dw_slices);
     return hipGetLastError();
 }
 
@@ -949,7 +987,7 @@ hipError_t launch_both(const ck_call &c) {
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(CX_THREADS), LDS, c.st, c.dY, c.planes, c.scales, c.M,
                            c.out, c.in, c.group_size, dx_rows(c), c.dX, c.status, (int)x_tiles_j, (int)x_tiles_m,
-                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.parts, (int)w_tiles_j,
+                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.grads, c.parts, (int)w_tiles_j,
                            (int)w_tiles, c.dw_slices);
     };
     switch (c.K) {
@@ -975,7 +1013,7 @@ hipError_t launch_few(const ck_call &c) {
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)(x_total + w_tiles)), dim3(CX_THREADS), LDS, c.st, c.dY, c.planes,
                            c.scales, c.M, c.out, c.in, c.group_size, dx_rows(c), c.dX, c.status, (int)tiles_j,
-                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.parts, (int)tiles_j,
+                           (int)x_total, c.codes, c.cscales, f8_blocks(c.in), c.dW, c.grads, c.parts, (int)tiles_j,
                            (int)w_tiles);
     };
     switch (c.K) {
@@ -1108,15 +1146,15 @@ size_t dw_slice_bytes(const ck_plan &p, int out, int in) {
 
 size_t dw_part_bytes(const ck_plan &p, int out, int in, int K, int group_size) {
     return p.dw_slices == 1 && (group_size || in <= F8_BLOCK)
-               ? 0 : (size_t)p.dw_slices * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(float);
+               ? 0 : (size_t)p.dw_slices * (size_t)K * (size_t)out * (size_t)f8_blocks(in) * sizeof(double);
 }
 
 size_t dx_slice_bytes(const ck_plan &p, int M, int in) {
     return p.dx_slices > 1 ? (size_t)p.dx_slices * (size_t)M * (size_t)in * sizeof(float) : 0;
 }
 
-ck_job sum_job(const float *from, float *to, int64_t n, int slices, int parts) {
-    const int64_t blocks = parts == 1 ? (n + CK_THREADS - 1) / CK_THREADS : (n + 3) / 4;
+ck_job sum_job(const void *from, float *to, int64_t n, int slices, int parts) {
+    const int64_t blocks = parts <= 1 ? (n + CK_THREADS - 1) / CK_THREADS : (n + 3) / 4;
     return {from, to, n, slices, parts, (unsigned)std::min<int64_t>(blocks, 1 << 18)};
 }
 
@@ -1164,18 +1202,18 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     float *ws = static_cast<float *>(workspace);
     ck_jobs left = {};
     int jobs = 0;
-    ck_call c = {dY, planes, scales, x_codes, x_scales, M, out, in, K, group_size, dX, dW, nullptr,
+    ck_call c = {dY, planes, scales, x_codes, x_scales, M, out, in, K, group_size, dX, dW, nullptr, nullptr,
                  p.dx_slices, p.dw_slices, status, st};
     c.dx_slices = (int)((out + dx_rows(c) - 1) / dx_rows(c));        // (none of them empty)
     if (dW != nullptr && c.dw_slices > 1) {
         c.dW = ws;
-        left.job[jobs++] = sum_job(ws, dW, (int64_t)out * in, c.dw_slices, 1);
+        left.job[jobs++] = sum_job(ws, dW, (int64_t)out * in, c.dw_slices, 0);
         ws += (int64_t)c.dw_slices * out * in;
     }
     if (dscales != nullptr && part_bytes == 0) {
-        c.parts = dscales;                  // a tile's columns are a whole group, and all its tokens
+        c.grads = dscales;                  // a tile's columns are a whole group, and all its tokens
     } else if (dscales != nullptr && fits) {
-        c.parts = ws;
+        c.parts = reinterpret_cast<f64_a4 *>(ws);
         const int64_t rows = (int64_t)K * out;
         left.job[jobs++] = group_size ? sum_job(ws, dscales, rows * f8_blocks(in), c.dw_slices, 1)
                                       : sum_job(ws, dscales, rows, c.dw_slices, f8_blocks(in));
@@ -1183,7 +1221,7 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
     }
     if (dX != nullptr && c.dx_slices > 1) {
         c.dX = ws;
-        left.job[jobs++] = sum_job(ws, dX, (int64_t)M * in, c.dx_slices, 1);
+        left.job[jobs++] = sum_job(ws, dX, (int64_t)M * in, c.dx_slices, 0);
     }
     hipError_t e = hipSuccess;
     switch (dx_tokens(M)) {
@@ -1201,7 +1239,7 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
             e = M > 128 ? launch_dx<4, 4>(c) : launch_dx<4, 2>(c);
         break;
     }
-    if (e == hipSuccess && dscales != nullptr && c.parts == nullptr)
+    if (e == hipSuccess && dscales != nullptr && c.grads == nullptr && c.parts == nullptr)
         e = launch_qat_dscales(planes, out, in, K, group_size, dW, dscales, st);
     if (e != hipSuccess)
         return e;

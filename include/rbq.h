@@ -646,7 +646,9 @@ rbq_status rbq_qat_checkpoint(const uint16_t *X, int32_t M, int32_t in_features,
  * rbq_qat_backward_ckpt -- rbq_qat_backward from a checkpoint: the same
  * gradients, with x^ in the place of X:
  *   dW[r][j]       = sum_m dY[m][r] x^[m][j]          fp32 [out][in]
- *   dscales, dX    as rbq_qat_backward (dX does not read the checkpoint)
+ *   dscales, dX    as rbq_qat_backward (dX does not read the checkpoint):
+ *                  dscales sums the fp32 dW, or the fp32 slices that dW is
+ *                  added from, in fp64
  * Each product of two fp16 numbers is exact and the sums are fp32, so dW
  * carries no error beyond the checkpoint's own and the fp32 accumulation.
  *   x_codes, x_scales  device, as rbq_qat_checkpoint wrote them; x_codes
