@@ -574,7 +574,7 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
     const bool want_dw = dW != nullptr && s.out_features > 0 && s.in_features > 0;
     if (!want_dx && !want_dw)
         return RBQ_OK;
-    if (M > 0 && dY == nullptr)
+    if (M > 0 && s.out_features > 0 && dY == nullptr)
         return RBQ_ERR_INVALID_ARG;
     if (want_dw && M > 0 && X == nullptr)
         return RBQ_ERR_INVALID_ARG;

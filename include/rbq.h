@@ -589,7 +589,8 @@ rbq_status rbq_qat_forward(const float *W, const uint16_t *scales, rbq_shape s, 
  *                                                      fp32 [K][out][G]
  *   dX[m][j]       = sum_r dY[m][r] What[r][j]        fp32 [M][in]
  * Any of dX, dW may be NULL (not computed); dscales needs dW.  X, dY fp16
- * [M][in], [M][out]; planes and scales as written by the forward.  dW is
+ * [M][in], [M][out] (dY may be NULL where out is 0: dX is 0); planes and scales
+ * as written by the forward.  dW is
  * exact products with fp32 accumulation; dscales sums the fp32 dW in fp64;
  * dX forms What in fp32 and multiplies its two fp16 parts (relative 2^-22,
  * absolute 2^-25 where the lower part is subnormal) with fp32 accumulation.

@@ -244,3 +244,14 @@ def test_valid_calls_without_a_device():
     assert L.rbq_qat_checkpoint(OK, 2, 64, OK, OK, None) == none
     s = rbq.shape(64, 128, 2, 0)
     assert L.rbq_qat_backward_ckpt(OK, OK, s, OK, OK, OK, 4, OK, OK, OK, None, 0, None, None) == none
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="only meaningful without a GPU")
+def test_a_layer_without_rows_needs_no_output_gradient():
+    """dY [M][0] may have no address (an empty tensor's is NULL): dX = 0 is an empty sum."""
+    L, s = rbq.lib(), rbq.shape(0, 128, 2, 0)
+    for call in (L.rbq_qat_backward_ckpt(None, None, s, None, None, None, 4, OK, None, None, None, 0, None, None),
+                 L.rbq_qat_backward(None, None, s, None, None, 4, OK, None, None, None, 0, None, None)):
+        assert call == rbq.RBQ_ERR_NO_DEVICE
+    s = rbq.shape(8, 128, 2, 0)
+    assert L.rbq_qat_backward(OK, OK, s, OK, None, 4, OK, None, None, None, 0, None, None) == rbq.RBQ_ERR_INVALID_ARG
