@@ -337,30 +337,30 @@ __global__ __launch_bounds__(QC_THREADS) void qat_dscales_kernel(const float *__
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / RBQ_WAVE));
     const int G = group_size ? in / group_size : 1;
     const int n = group_size ? group_size : in;
-    const long seg = (long)blockIdx.x * QC_WAVES + wave;
-    if (seg >= (long)out * G)
-        return;                               // whole wave
-    const int r = (int)(seg / G), t = (int)(seg - (long)r * G);
     const int words = in >> 5;
     const size_t plane_stride = (size_t)out * words;
-    const float *wrow = dW + (size_t)r * in;
-    double s[K];
+    for (int64_t seg = (int64_t)blockIdx.x * QC_WAVES + wave; seg < (int64_t)out * G;
+         seg += (int64_t)gridDim.x * QC_WAVES) {
+        const int r = (int)(seg / G), t = (int)(seg - (int64_t)r * G);
+        const float *wrow = dW + (size_t)r * in;
+        double s[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        s[k] = 0.0;
-    for (int c = t * n + lane; c < (t + 1) * n; c += RBQ_WAVE) {
-        const double w = (double)wrow[c];
+        for (int k = 0; k < K; ++k)
+            s[k] = 0.0;
+        for (int c = t * n + lane; c < (t + 1) * n; c += RBQ_WAVE) {
+            const double w = (double)wrow[c];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const uint32_t word = planes[(size_t)k * plane_stride + (size_t)r * words + (c >> 5)];
+                s[k] += ((word >> (c & 31)) & 1u) ? w : -w;
+            }
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const uint32_t word = planes[(size_t)k * plane_stride + (size_t)r * words + (c >> 5)];
-            s[k] += ((word >> (c & 31)) & 1u) ? w : -w;
+            const double tot = wave_sum_f64(s[k]);
+            if (lane == 0)
+                dscales[((size_t)k * out + r) * G + t] = (float)tot;
         }
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const double tot = wave_sum_f64(s[k]);
-        if (lane == 0)
-            dscales[((size_t)k * out + r) * G + t] = (float)tot;
     }
 }
 
@@ -376,16 +376,18 @@ __global__ void qat_sum_slices(const float *__restrict__ parts, int S, size_t n,
 }
 
 __global__ void qat_fill_zero_f32(float *p, size_t n) {
-    const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n)
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
         p[i] = 0.0f;
 }
+
+// Workgroups of 256 threads of a launch that has work for `groups` of them:
+// 2^32 threads and more wrap round without an error, so the kernel loops.
+unsigned qat_groups(int64_t groups) { return (unsigned)std::min<int64_t>(groups, 1 << 20); }
 
 hipError_t fill_zero(float *p, size_t n, hipStream_t st) {
     if (n == 0)
         return hipSuccess;
-    const size_t blocks = (n + 255) / 256;
-    hipLaunchKernelGGL(qat_fill_zero_f32, dim3((unsigned)blocks), dim3(256), 0, st, p, n);
+    hipLaunchKernelGGL(qat_fill_zero_f32, dim3(qat_groups((int64_t)((n + 255) / 256))), dim3(256), 0, st, p, n);
     return hipGetLastError();
 }
 
@@ -429,7 +431,7 @@ hipError_t launch_qat_encode(const float *W, int out, int in, int K, int group_s
 hipError_t launch_qat_dscales(const uint32_t *planes, int out, int in, int K, int group_size, const float *dW,
                               float *dscales, hipStream_t st) {
     const int G = group_size ? in / group_size : 1;
-    const dim3 grid((unsigned)(((long)out * G + QC_WAVES - 1) / QC_WAVES));
+    const dim3 grid(qat_groups(((int64_t)out * G + QC_WAVES - 1) / QC_WAVES));
     switch (K) {
     case 1: hipLaunchKernelGGL(qat_dscales_kernel<1>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
     case 2: hipLaunchKernelGGL(qat_dscales_kernel<2>, grid, dim3(QC_THREADS), 0, st, dW, planes, out, in, group_size, dscales); break;
