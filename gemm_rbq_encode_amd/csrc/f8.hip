@@ -14,6 +14,7 @@
 #include "rbq_device.h"
 #include "rbq_kernels.h"
 #include "f8_device.h"
+#include "f8_plan.h"
 
 namespace rbq {
 
