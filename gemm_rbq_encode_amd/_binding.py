@@ -38,6 +38,7 @@ RBQ_LAYOUT_ROWS = 0
 RBQ_LAYOUT_TILES = 1
 RBQ_Y_F16 = 0
 RBQ_Y_F32 = 1
+RBQ_Y_EXACT = 0x100
 
 PATH_AUTO, PATH_VALU, PATH_DECODE, PATH_PREFILL, PATH_STREAM, PATH_FLAT, PATH_GROUP, PATH_SPLIT = (
     0, 1, 2, 3, 4, 5, 6, 7)
@@ -601,10 +602,12 @@ def _f8_layer(codes: torch.Tensor, scales: torch.Tensor):
 
 
 def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor, *,
-            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None,
+            dtype: torch.dtype = torch.float16, exact: bool = False, Y: torch.Tensor | None = None,
             workspace: torch.Tensor | None = None, stream=None):
     """rbq_gemm_f8: Y [M][out] (float16 or float32) of the layer of encode_f8
-    and the tokens of quantize_f8."""
+    and the tokens of quantize_f8.  Without `exact`, float16 outputs of more
+    than 32 tokens take the 8-bit matrix instruction, which cuts small products
+    beside large ones; with it, every product is exact, as for float32."""
     out_f, in_f = _f8_layer(codes, scales)
     _dev(x_codes, torch.float8_e4m3fn, "x_codes")
     _dev(x_scales, torch.float32, "x_scales")
@@ -616,10 +619,10 @@ def gemm_f8(codes: torch.Tensor, scales: torch.Tensor, x_codes: torch.Tensor, x_
     if dtype not in (torch.float16, torch.float32):
         raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
     dev = _one_device(codes, scales, x_codes, x_scales, workspace)
-    kind = RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16
+    kind = RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16 | (RBQ_Y_EXACT if exact else 0)
     if stream is not None or dev.index != _current_device():
         with _There(dev, stream):
-            return gemm_f8(codes, scales, x_codes, x_scales, dtype=dtype, Y=Y, workspace=workspace)
+            return gemm_f8(codes, scales, x_codes, x_scales, dtype=dtype, exact=exact, Y=Y, workspace=workspace)
     st = _current_stream(dev.index)
     Y = _out(Y, (M, out_f), dtype, "Y", dev)
     if workspace is None and M > 32:      # none is needed for fewer

@@ -596,6 +596,8 @@ rbq_status rbq_qat_backward(const uint32_t *planes, const uint16_t *scales, rbq_
 // ---- linears in 8-bit floating point blocks of 128 ---------------------------
 
 static bool f8_shape_ok(int32_t out, int32_t in) { return out >= 0 && in >= 0 && in % 32 == 0; }
+// fp16 or fp32 outputs, RBQ_Y_EXACT or-ed in or not
+static bool f8_type_ok(uint32_t y_type) { return (y_type & ~RBQ_Y_EXACT) <= RBQ_Y_F32; }
 static bool f8_too_large(int32_t out, int32_t in) { return out > RBQ_F8_MAX_FEATURES || in > RBQ_F8_MAX_FEATURES; }
 
 rbq_status rbq_encode_f8(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes, float *scales,
@@ -640,15 +642,15 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
 
 size_t rbq_gemm_f8_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type) {
     if (M < 1 || out_features < 1 || in_features < 32 || in_features % 32 != 0 ||
-        f8_too_large(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32))
+        f8_too_large(out_features, in_features) || !f8_type_ok(y_type))
         return 0;
-    return rbq::gemm_f8_workspace_bytes(out_features, in_features, M, y_type == RBQ_Y_F32);
+    return rbq::gemm_f8_workspace_bytes(out_features, in_features, M, y_type != RBQ_Y_F16);
 }
 
 rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
                        const uint8_t *x_codes, const float *x_scales, int32_t M, void *Y, uint32_t y_type,
                        void *workspace, size_t ws_bytes, void *stream) {
-    if (M < 0 || !f8_shape_ok(out_features, in_features) || (y_type != RBQ_Y_F16 && y_type != RBQ_Y_F32) ||
+    if (M < 0 || !f8_shape_ok(out_features, in_features) || !f8_type_ok(y_type) ||
         (ws_bytes > 0 && workspace == nullptr))
         return RBQ_ERR_INVALID_ARG;
     if (f8_too_large(out_features, in_features))
@@ -657,7 +659,8 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
         return RBQ_OK;
     if (Y == nullptr)
         return RBQ_ERR_INVALID_ARG;
-    if (!aligned(Y, y_type == RBQ_Y_F32 ? 4 : 2))
+    const bool f32 = (y_type & RBQ_Y_F32) != 0;
+    if (!aligned(Y, f32 ? 4 : 2))
         return RBQ_ERR_ALIGNMENT;
     rbq_status st;
     hipError_t e;
@@ -665,9 +668,8 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
         if ((st = device_present()) != RBQ_OK)
             return st;
         const size_t n = (size_t)M * (size_t)out_features;
-        e = y_type == RBQ_Y_F32 ? rbq::launch_fill_zero_f32(static_cast<float *>(Y), n, (hipStream_t)stream)
-                                : rbq::launch_fill_zero_u16(static_cast<uint16_t *>(Y), (int64_t)n,
-                                                            (hipStream_t)stream);
+        e = f32 ? rbq::launch_fill_zero_f32(static_cast<float *>(Y), n, (hipStream_t)stream)
+                : rbq::launch_fill_zero_u16(static_cast<uint16_t *>(Y), (int64_t)n, (hipStream_t)stream);
         return e == hipSuccess ? RBQ_OK : hip_fail(e);
     }
     if (codes == nullptr || scales == nullptr || x_codes == nullptr || x_scales == nullptr)
@@ -678,7 +680,7 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
     if ((st = device_present()) != RBQ_OK)
         return st;
     e = rbq::launch_gemm_f8(codes, scales, out_features, in_features, x_codes, x_scales, M, Y,
-                            y_type == RBQ_Y_F32, workspace, ws_bytes, (hipStream_t)stream);
+                            f32, (y_type & RBQ_Y_EXACT) != 0, workspace, ws_bytes, (hipStream_t)stream);
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 

@@ -407,9 +407,9 @@ hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, flo
 }
 
 hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                          int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st) {
+                          int M, void *y, int y_f32, int exact, void *workspace, size_t ws_bytes, hipStream_t st) {
     if (M > F8_FEW && gemm_f8_tile_supports(out, in, M))
-        return launch_gemm_f8_tile(W, ws, out, in, X, xs, M, y, y_f32, workspace, ws_bytes, st);
+        return launch_gemm_f8_tile(W, ws, out, in, X, xs, M, y, y_f32, y_f32 || exact, workspace, ws_bytes, st);
     return y_f32 ? launch_few_tokens(W, ws, out, in, X, xs, M, static_cast<float *>(y), st)
                  : launch_few_tokens(W, ws, out, in, X, xs, M, static_cast<uint16_t *>(y), st);
 }

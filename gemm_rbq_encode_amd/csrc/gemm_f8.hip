@@ -32,14 +32,15 @@
 //    adds the groups in fp32.  A group is off by less than 7 * 2^-13 of its
 //    largest product, about a seventieth of the 2^-4 that an e4m3 operand is
 //    off itself; it buys twice the rate of the fp16 instruction.
-//  * fp32 outputs: the codes converted to fp16 (exact) in registers and
-//    v_mfma_f32_16x16x32_f16: exact products, fp32 sums.
+//  * fp32 outputs, and fp16 ones of which the caller asks it: the codes
+//    converted to fp16 (exact) in registers and v_mfma_f32_16x16x32_f16: exact
+//    products, fp32 sums.
 // Either way the block's sums are scaled by xs ws in one fp32 fma each.
 //
 // Large tiles are bound by the matrix instructions at the clock that their
 // power leaves: 2048 tokens, 14336 x 4096: 125 us, 1.9 PFLOP/s (a library
 // product of this size with one scale for the whole matrix: 103 us); 4096
-// tokens, 8192 x 8192: 254 us, 2.2 PFLOP/s.  fp32 outputs run at the fp16
+// tokens, 8192 x 8192: 254 us, 2.2 PFLOP/s.  Exact products run at the fp16
 // rate: 777 tokens, 5003 x 4128: 55 us, 580 TFLOP/s; 2048 tokens, 14336 x 4096:
 // 231 us, 1.04 PFLOP/s, which is the fp16 instruction's under its power.
 #include <algorithm>
@@ -130,12 +131,11 @@ __device__ __forceinline__ void f8_write_tile(const v4f (&acc)[TM][TN], int64_t 
 template <int RT, int CT>
 constexpr int F8_PART = RT * CT + 320;       // (a power of two apart, all would be written to the same channels at once)
 
-template <int WM, int WN, int TM, int TN, int NB, typename Y>
+template <int WM, int WN, int TM, int TN, int NB, bool EXACT, typename Y>
 __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void gemm_f8_tile_kernel(
     const uint8_t *__restrict__ W, const float *__restrict__ ws, int out, int in, int T,
     const uint8_t *__restrict__ X, const float *__restrict__ xs, int M, Y *__restrict__ y,
     float *__restrict__ parts, int tiles_m, int tiles, int whole, int slices) {
-    constexpr bool EXACT = sizeof(Y) == 4;
     constexpr int WAVES = WM * WN;
     constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
     constexpr int SX = RT * F8_BLOCK, SS = SX + CT * F8_BLOCK, SLOT = SS + CT * 4;   // rows, tokens, scales
@@ -715,7 +715,7 @@ __global__ __launch_bounds__(GL_THREADS) void gemm_f8_large_kernel(
     f8_write_tile<TM, TN>(acc, r0 + wr * WR, m0 + wc * TN * 16, li, g, out, M, y);
 }
 
-template <int WM, int WN, int TM, int TN, int NB, typename Y>
+template <int WM, int WN, int TM, int TN, int NB, bool EXACT, typename Y>
 hipError_t launch_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
                        Y *y, float *parts, f8_plan p, hipStream_t st) {
     constexpr int RT = WM * TM * 16, CT = WN * TN * 16;
@@ -723,7 +723,7 @@ hipError_t launch_tile(const uint8_t *W, const float *ws, int out, int in, const
     static_assert(LDS <= 160 * 1024, "LDS of a compute unit");
     const int tiles_m = (int)(((int64_t)M + CT - 1) / CT), tiles = tiles_m * (int)(((int64_t)out + RT - 1) / RT);
     const int64_t groups = p.whole + (int64_t)(tiles - p.whole) * p.slices;
-    hipLaunchKernelGGL((gemm_f8_tile_kernel<WM, WN, TM, TN, NB, Y>), dim3((unsigned)groups), dim3(WM * WN * RBQ_WAVE),
+    hipLaunchKernelGGL((gemm_f8_tile_kernel<WM, WN, TM, TN, NB, EXACT, Y>), dim3((unsigned)groups), dim3(WM * WN * RBQ_WAVE),
                        LDS, st, W, ws, out, in, f8_blocks(in), X, xs, M, y, parts, tiles_m, tiles, p.whole, p.slices);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.slices == 1)
@@ -743,41 +743,43 @@ hipError_t launch_large(const uint8_t *W, const float *ws, int out, int in, cons
     return hipGetLastError();
 }
 
-template <typename Y>
+template <bool EXACT, typename Y>
 hipError_t launch_tiles(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs, int M,
                         Y *y, float *parts, f8_plan p, hipStream_t st) {
     switch (p.kind) {
-    case F8_LARGE: return launch_tile<2, 4, 4, 4, 3>(W, ws, out, in, X, xs, M, y, parts, p, st);
-    case F8_LARGE + 1: return launch_tile<2, 2, 4, 4, 4>(W, ws, out, in, X, xs, M, y, parts, p, st);
-    default: return launch_tile<2, 2, 2, 4, 4>(W, ws, out, in, X, xs, M, y, parts, p, st);
+    case F8_LARGE: return launch_tile<2, 4, 4, 4, 3, EXACT>(W, ws, out, in, X, xs, M, y, parts, p, st);
+    case F8_LARGE + 1: return launch_tile<2, 2, 4, 4, 4, EXACT>(W, ws, out, in, X, xs, M, y, parts, p, st);
+    default: return launch_tile<2, 2, 2, 4, 4, EXACT>(W, ws, out, in, X, xs, M, y, parts, p, st);
     }
 }
 
 }  // namespace
 
-size_t gemm_f8_workspace_bytes(int out, int in, int M, int y_f32) {
+size_t gemm_f8_workspace_bytes(int out, int in, int M, int exact) {
     if (M <= F8_FEW || !gemm_f8_tile_supports(out, in, M))
         return 0;
-    const f8_plan p = plan_tiles(out, in, M, y_f32);
+    const f8_plan p = plan_tiles(out, in, M, exact);
     const int64_t rows = F8_ROWS[p.kind], tokens = F8_TOKENS[p.kind];
     const int64_t tiles = (out + rows - 1) / rows * ((M + tokens - 1) / tokens);
     return p.slices > 1 ? (size_t)((tiles - p.whole) * p.slices * (rows * tokens + F8_PART<0, 0>)) * sizeof(float) : 0;
 }
 
 hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                               int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st) {
-    f8_plan p = plan_tiles(out, in, M, y_f32);
-    if (ws_bytes < gemm_f8_workspace_bytes(out, in, M, y_f32))
+                               int M, void *y, int y_f32, int exact, void *workspace, size_t ws_bytes, hipStream_t st) {
+    f8_plan p = plan_tiles(out, in, M, exact);
+    if (ws_bytes < gemm_f8_workspace_bytes(out, in, M, exact))
         p.slices = 1;
     float *parts = static_cast<float *>(workspace);
     if (y_f32)
-        return launch_tiles(W, ws, out, in, X, xs, M, static_cast<float *>(y), parts, p, st);
+        return launch_tiles<true>(W, ws, out, in, X, xs, M, static_cast<float *>(y), parts, p, st);
     uint16_t *o = static_cast<uint16_t *>(y);
+    if (exact)
+        return launch_tiles<true>(W, ws, out, in, X, xs, M, o, parts, p, st);
     switch (p.kind) {
     case 0: return launch_large<8>(W, ws, out, in, X, xs, M, o, st);
     case 1: return launch_large<7>(W, ws, out, in, X, xs, M, o, st);
     case 2: return launch_large<6>(W, ws, out, in, X, xs, M, o, st);
-    default: return launch_tiles(W, ws, out, in, X, xs, M, o, parts, p, st);
+    default: return launch_tiles<false>(W, ws, out, in, X, xs, M, o, parts, p, st);
     }
 }
 

@@ -131,12 +131,12 @@ hipError_t launch_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scal
 hipError_t launch_encode_f8(const float *W, int out, int in, uint8_t *codes, float *scales, int32_t *status,
                             hipStream_t st);
 hipError_t launch_quantize_f8(const uint16_t *X, int M, int in, uint8_t *codes, float *scales, hipStream_t st);
-size_t gemm_f8_workspace_bytes(int out, int in, int M, int y_f32);
+size_t gemm_f8_workspace_bytes(int out, int in, int M, int exact);
 hipError_t launch_gemm_f8(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                          int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st);
+                          int M, void *y, int y_f32, int exact, void *workspace, size_t ws_bytes, hipStream_t st);
 // More tokens than F8_FEW (gemm_f8.hip; f8_plan.h).
 hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
-                               int M, void *y, int y_f32, void *workspace, size_t ws_bytes, hipStream_t st);
+                               int M, void *y, int y_f32, int exact, void *workspace, size_t ws_bytes, hipStream_t st);
 hipError_t launch_gemv_f8(const uint8_t *W, const float *ws, int out, int in, const uint16_t *x, uint16_t *y,
                           hipStream_t st);
 

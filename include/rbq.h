@@ -717,24 +717,30 @@ rbq_status rbq_encode_f8(const float *W, int32_t out_features, int32_t in_featur
 rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, uint8_t *codes, float *scales,
                            void *stream);
 
-/* Output types of rbq_gemm_f8. */
-#define RBQ_Y_F16 0u
-#define RBQ_Y_F32 1u
+/* Output types of rbq_gemm_f8, and a flag that may be or-ed in: exact products
+ * for binary16 outputs of any number of tokens too (at half the rate). */
+#define RBQ_Y_F16   0u
+#define RBQ_Y_F32   1u
+#define RBQ_Y_EXACT 0x100u
 
 /*
  * rbq_gemm_f8 -- the product of M quantised tokens:
  *   Y[m][r] = sum_t xs[t][m] ws[r/128][t] sum_{j in block t} x[m][j] w[r][j]
  * over the codes' values; the sums are fp32 and each output is rounded once
  * to its type.  The products are exact, except for binary16 outputs of more
- * than 32 tokens, which take the 8-bit matrix instruction: of the products of
- * 8 consecutive columns it drops what lies below 2^-13 of the power of two
- * under the largest (an error below 7 2^-13 of the largest product of each 8;
- * the codes themselves are off by 2^-4).
+ * than 32 tokens without RBQ_Y_EXACT, which take the 8-bit matrix instruction:
+ * of the products of 8 consecutive columns it drops what lies below 2^-13 of
+ * the power of two under the largest (an error below 7 2^-13 of the largest
+ * product of each 8; the codes themselves are off by 2^-4).  (Sizes beyond the
+ * tiled kernels, in > 2^23 or more than about 2^22 tiles of 64 x 128, are
+ * multiplied exactly in any case.)
  *   codes, scales      the layer; codes 16-byte, scales 4-byte aligned
  *   x_codes, x_scales  the tokens; x_codes 16-byte, x_scales 4-byte aligned
  *   M       tokens, >= 0 (0 enqueues nothing)
  *   Y       device [M][out], written: binary16 (RBQ_Y_F16, 2-byte aligned) or
  *           fp32 (RBQ_Y_F32, 4-byte aligned)
+ *   y_type  RBQ_Y_F16 or RBQ_Y_F32, with or without RBQ_Y_EXACT (which changes
+ *           nothing for fp32 outputs); the same for the workspace's size
  *   workspace  device memory of rbq_gemm_f8_workspace_bytes(..) bytes, 4-byte
  *           aligned, any contents (0 for few and for many tokens): in between
  *           the columns are split over workgroups whose fp32 partial sums it

@@ -255,3 +255,20 @@ def test_a_layer_without_rows_needs_no_output_gradient():
         assert call == rbq.RBQ_ERR_NO_DEVICE
     s = rbq.shape(8, 128, 2, 0)
     assert L.rbq_qat_backward(OK, OK, s, OK, None, 4, OK, None, None, None, 0, None, None) == rbq.RBQ_ERR_INVALID_ARG
+
+
+def test_types_of_product_outputs():
+    """RBQ_Y_EXACT goes with either type and nothing else does; exact products
+    are split alike for both types."""
+    L, E = rbq.lib(), rbq
+    for kind in (2, 3, 4, 0x101 + 1, 0x200, 0x1000, 0xFFFFFFFF):
+        assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK, kind, None, 0, None) == E.RBQ_ERR_INVALID_ARG, kind
+        assert L.rbq_gemm_f8_workspace_bytes(1024, 8192, 64, kind) == 0
+    for kind in (E.RBQ_Y_F16, E.RBQ_Y_F32, E.RBQ_Y_F16 | E.RBQ_Y_EXACT, E.RBQ_Y_F32 | E.RBQ_Y_EXACT):
+        assert L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 0, OK, kind, None, 0, None) == E.RBQ_OK
+        odd = L.rbq_gemm_f8(OK, OK, 8, 64, OK, OK, 2, OK + 2, kind, None, 0, None)
+        assert (odd == E.RBQ_ERR_ALIGNMENT) == bool(kind & E.RBQ_Y_F32)
+    for M in (33, 300, 777, 2048):
+        f32 = L.rbq_gemm_f8_workspace_bytes(5003, 4128, M, E.RBQ_Y_F32)
+        assert L.rbq_gemm_f8_workspace_bytes(5003, 4128, M, E.RBQ_Y_F16 | E.RBQ_Y_EXACT) == f32
+        assert L.rbq_gemm_f8_workspace_bytes(5003, 4128, M, E.RBQ_Y_F32 | E.RBQ_Y_EXACT) == f32
