@@ -28,8 +28,9 @@ constexpr int FQ_THREADS = 256;
 // LDS.  A workgroup takes 16 tokens x 4 blocks, the four loads of a lane issued
 // together, or 1 x 16, one block a lane, which takes less time from the load to
 // the codes.  Bound by the read of X and the write of the codes: 2048 x 14336
-// takes 15.4 us, 5.8 TB/s (26.4 us where X has to come from HBM past another
-// kernel's unwritten lines).
+// takes 15.4 us, 5.8 TB/s, over three inputs in turn, which the 256 MB cache
+// holds in part; 18.3 us, 4.8 TB/s, over eight (705 MB), and 26 us where X has
+// to come past another kernel's unwritten lines.
 
 template <int B>
 __global__ __launch_bounds__(FQ_THREADS) void quantize_f8_kernel(const uint16_t *__restrict__ X, int M, int in,
@@ -63,7 +64,8 @@ __global__ __launch_bounds__(FQ_THREADS) void quantize_f8_kernel(const uint16_t 
 // ---------------------------------------------------------------------------
 // weights: one workgroup per 128 x 128 block, held in 64 registers per thread
 // between the maximum and the codes, so W is read once.  Bound by that read:
-// 14336 x 4096 takes 53.5 us, 5.5 TB/s of W and codes.
+// 14336 x 4096 takes 53.5 us, 5.5 TB/s of W and codes (three inputs in turn are
+// 880 MB: from HBM).
 
 __global__ __launch_bounds__(FQ_THREADS) void encode_f8_kernel(const float *__restrict__ W, int out, int in, int T,
                                                                uint8_t *__restrict__ codes,
@@ -123,8 +125,11 @@ __global__ __launch_bounds__(FQ_THREADS) void encode_f8_kernel(const float *__re
 // gives the same sum as long as both sides share it, and this one makes a
 // load 64 contiguous bytes per row.
 //
-// One token, 11008 x 4096: 9.9 us, 4.6 TB/s of W; 16 tokens, 4096 x 11008: 13.3
-// us, 3.4 TB/s (the tokens' 176 KB are read by each of the 256 workgroups).
+// Over 640 MB of layers in turn, so that W comes from HBM: one token, 11008 x
+// 4096: 11.1 us, 4.1 TB/s of W; 32000 x 4096: 26.2 us, 5.0 TB/s; 16 tokens, 4096 x
+// 11008: 15.1 us, 3.0 TB/s (the tokens' 176 KB are read by each of the 256
+// workgroups).  Three layers in turn, which stay in the 256 MB cache: 9.9 and
+// 13.3 us for the first and the last.
 
 // Every wave keeps U blocks in flight: the loads of block u + U of its own are
 // issued as soon as block u's registers are free.
@@ -365,11 +370,21 @@ hipError_t launch_few(const uint8_t *W, const float *ws, int out, int in, const 
 }
 
 // Rows per workgroup and blocks in flight.  More rows read the tokens less
-// often, fewer rows make more workgroups: 16 tokens on 4096 x 4096, 11008 x
-// 4096 and 14336 x 4096 take 7.3, 15.8 and 20.0 us with 16 rows against 8.8,
-// 16.3 and 17.7 with 32.  Two blocks in flight and 8 waves: 3 or 4 blocks take
-// 3 to 30 % longer, 16 waves between 3 % less and 16 % more.  More than 32
-// tokens come here only where the tiled kernels' offsets do not reach.
+// often, fewer rows make more workgroups; us with 16 and with 32 rows, W from
+// HBM, 4096 columns (1, 16 and 32 tokens):
+//    1000 rows    5.8  7.5     7.0  8.9     8.9 11.1
+//    4096         6.9  8.3     7.3  9.1     9.2 11.3
+//    5003         8.7  9.0    11.5 10.2    15.5 12.6
+//    8192         9.3  9.7    12.9 10.6    15.6 11.8
+//   11008        13.1 15.1    16.1 16.8    21.7 21.3
+//   14336        15.3 16.3    20.3 18.2    27.5 21.9
+//   22016        22.2 23.7    28.5 26.3    39.4 31.9
+// (4096 rows of 11008 and 14336 columns: 16 rows by 15 to 32 %.)  From 12288 rows
+// on 32 are the better choice for all but one token; between 5000 and 8192, where
+// they make one round of 16 rows' two, they would be from a few tokens on too, by
+// 10 to 25 %.  Two blocks in flight and 8 waves: 3 or 4 blocks take 3 to 30 %
+// longer, 16 waves between 3 % less and 16 % more.  More than F8_FEW tokens come
+// here only where the tiled kernels' offsets do not reach.
 template <typename Y>
 hipError_t launch_few_tokens(const uint8_t *W, const float *ws, int out, int in, const uint8_t *X, const float *xs,
                              int M, Y *y, hipStream_t st) {

@@ -38,11 +38,11 @@
 // Either way the block's sums are scaled by xs ws in one fp32 fma each.
 //
 // Large tiles are bound by the matrix instructions at the clock that their
-// power leaves: 2048 tokens, 14336 x 4096: 125 us, 1.9 PFLOP/s (a library
+// power leaves: 2048 tokens, 14336 x 4096: 124 to 128 us, 1.9 PFLOP/s (a library
 // product of this size with one scale for the whole matrix: 103 us); 4096
 // tokens, 8192 x 8192: 254 us, 2.2 PFLOP/s.  Exact products run at the fp16
-// rate: 777 tokens, 5003 x 4128: 55 us, 580 TFLOP/s; 2048 tokens, 14336 x 4096:
-// 231 us, 1.04 PFLOP/s, which is the fp16 instruction's under its power.
+// rate: 777 tokens, 5003 x 4128: 56 us, 570 TFLOP/s; 2048 tokens, 14336 x 4096:
+// 230 us, 1.05 PFLOP/s, which is the fp16 instruction's under its power.
 #include <algorithm>
 #include <type_traits>
 

@@ -158,9 +158,12 @@ __device__ __forceinline__ void ck_barrier() { asm volatile("s_waitcnt lgkmcnt(0
 // parts [slice][K][out][ceil(in / 128)], added in order at the end.
 //
 // Bound by the matrix instructions and their power: 2048 tokens, 11008 x 4096:
-// 225 us, 820 TFLOP/s, and 237 with the scales' gradients (688 tiles are 2.7
-// rounds of 256 compute units).  LDS is not what counts: an order of its
-// writes without bank conflicts (17 % of its cycles) takes the same time.
+// 213 us, 866 TFLOP/s, and 240 with the scales' gradients (688 tiles are 2.7
+// rounds of 256 compute units).  Their fp64 sums cost 1 to 3 % of a whole
+// backward more than fp32 sums would (300 tokens, 8192 x 4096, K = 3: 134 us
+// and 131), and up to 13 % of dW and the gradients alone (300 tokens, 11008 x
+// 4096: 98 and 87).  LDS is not what counts: an order of its writes without
+// bank conflicts (17 % of its cycles) takes the same time.
 
 constexpr int CW_TM = 8;
 
@@ -467,9 +470,9 @@ __global__ __launch_bounds__(WM *WN *RBQ_WAVE, 2) void qat_ckpt_dw_kernel(
 // two columns at a time; with three and four it has eight and their
 // negatives, each worked out by one of the eight lanes of the row and passed
 // round, in byte tables that are looked up four columns at a time (1003
-// tokens, 5120 x 5120, K = 4: 158 us; with every sum formed by itself 183).
-// Bound by the matrix instructions: 2048 tokens, 11008 x 4096: 350 us, 1.06
-// PFLOP/s over both parts.
+// tokens, 5120 x 5120, K = 4: 145 us in 3 slices; with every sum formed by
+// itself 25 more).  Bound by the matrix instructions: 2048 tokens, 11008 x 4096:
+// 296 us, 1.25 PFLOP/s over both parts.
 
 constexpr int CX_THREADS = 512;
 
@@ -838,8 +841,8 @@ __global__ __launch_bounds__(CX_THREADS, 2) void qat_ckpt_both_kernel(
 // write of dW bounds one, the start of every stage the other, so they go well
 // beside each other; either may have no workgroups.  dX: the waves lie along
 // the columns, so that each weight is read from LDS by one wave only.  16
-// tokens, 4096 x 4096: 28.7 us for all three outputs (one after the other:
-// 37.3), against 13 for the write of dW alone.
+// tokens, 4096 x 4096: 28 us for all three outputs (one after the other: 37),
+// against 14.4 for dW alone.
 template <int TM, int K>
 __global__ __launch_bounds__(CX_THREADS, 4) void qat_ckpt_few_kernel(
     const uint16_t *__restrict__ dY, const uint32_t *__restrict__ planes, const uint16_t *__restrict__ scales, int M,

@@ -727,13 +727,14 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
  * rbq_gemm_f8 -- the product of M quantised tokens:
  *   Y[m][r] = sum_t xs[t][m] ws[r/128][t] sum_{j in block t} x[m][j] w[r][j]
  * over the codes' values; the sums are fp32 and each output is rounded once
- * to its type.  The products are exact, except for binary16 outputs of more
- * than 32 tokens without RBQ_Y_EXACT, which take the 8-bit matrix instruction:
- * of the products of 8 consecutive columns it drops what lies below 2^-13 of
- * the power of two under the largest (an error below 7 2^-13 of the largest
- * product of each 8; the codes themselves are off by 2^-4).  (Sizes beyond the
- * tiled kernels, in > 2^23 or more than about 2^22 tiles of 64 x 128, are
- * multiplied exactly in any case.)
+ * to its type.  A block's two scales are multiplied first, in fp32 (a product
+ * of scales below 2^-126 loses bits).  The products of codes are exact, except
+ * for binary16 outputs of more than 32 tokens without RBQ_Y_EXACT, which take
+ * the 8-bit matrix instruction: of the products of 8 consecutive columns it
+ * drops what lies below 2^-13 of the power of two under the largest (an error
+ * below 7 2^-13 of the largest product of each 8; the codes themselves are off
+ * by 2^-4).  Sizes beyond the tiled kernels (in > 2^23, or more than about 2^22
+ * tiles of 64 x 128) are multiplied exactly in any case.
  *   codes, scales      the layer; codes 16-byte, scales 4-byte aligned
  *   x_codes, x_scales  the tokens; x_codes 16-byte, x_scales 4-byte aligned
  *   M       tokens, >= 0 (0 enqueues nothing)
@@ -742,12 +743,13 @@ rbq_status rbq_quantize_f8(const uint16_t *X, int32_t M, int32_t in_features, ui
  *   y_type  RBQ_Y_F16 or RBQ_Y_F32, with or without RBQ_Y_EXACT (which changes
  *           nothing for fp32 outputs); the same for the workspace's size
  *   workspace  device memory of rbq_gemm_f8_workspace_bytes(..) bytes, 4-byte
- *           aligned, any contents (0 for few and for many tokens): in between
- *           the columns are split over workgroups whose fp32 partial sums it
- *           holds, added in order by a second kernel (deterministic); with a
- *           smaller workspace (or NULL with ws_bytes 0) they are not split,
- *           which is slower.  Calls that share one must be ordered on one
- *           stream.
+ *           aligned, any contents: 0 up to 32 tokens, and for more whatever
+ *           the query says, at any number of tokens.  Where it is not 0, the
+ *           columns of all or of the last tiles are split over workgroups
+ *           whose fp32 partial sums it holds, added in order by a second
+ *           kernel (deterministic); with a smaller workspace (or NULL with
+ *           ws_bytes 0) they are not split, which is slower and adds in another
+ *           order.  Calls that share one must be ordered on one stream.
  * in == 0 writes Y = 0.  Errors: RBQ_ERR_INVALID_ARG (an unknown y_type, or
  * ws_bytes > 0 with a NULL workspace, among them), RBQ_ERR_ALIGNMENT,
  * RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
