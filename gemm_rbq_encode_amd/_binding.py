@@ -465,7 +465,7 @@ def qat_backward(planes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, dY
     if X.shape != (M, in_f) or dY.shape != (M, out_f):
         raise ValueError("X must be [M][in] and dY [M][out]")
     dev = planes.device
-    G = in_f // group_size if group_size else 1
+    G = groups_per_row(in_f, group_size)
     dX = torch.empty((M, in_f), dtype=torch.float32, device=dev) if need_dx else None
     dW = torch.empty((out_f, in_f), dtype=torch.float32, device=dev) if (need_dw or need_dscales) else None
     ds = torch.empty((K, out_f, G), dtype=torch.float32, device=dev) if need_dscales else None
