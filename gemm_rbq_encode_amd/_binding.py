@@ -39,6 +39,13 @@ RBQ_LAYOUT_TILES = 1
 RBQ_Y_F16 = 0
 RBQ_Y_F32 = 1
 RBQ_Y_EXACT = 0x100
+RBQ_L_F16 = 0
+RBQ_L_F32 = 1
+RBQ_L_BF16 = 2
+RBQ_STATUS_BAD_TOKEN = 64
+RBQ_VOCAB_MAX = 1 << 24
+RBQ_TOP_MAX = 128
+RBQ_DISTILL_TAIL = 1
 
 PATH_AUTO, PATH_VALU, PATH_DECODE, PATH_PREFILL, PATH_STREAM, PATH_FLAT, PATH_GROUP, PATH_SPLIT = (
     0, 1, 2, 3, 4, 5, 6, 7)
@@ -141,6 +148,33 @@ _SIGNATURES = {
                                                       ctypes.c_uint32]),
     "rbq_gemv_f8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_encode_q4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_gemm_q4_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                      ctypes.c_uint32]),
+    "rbq_gemm_q4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                   ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                   ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "rbq_token_logprobs_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "rbq_token_logprobs": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_token_logprobs_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int32,
+                                                   ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_distill_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "rbq_distill_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "rbq_distill_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int32,
+                                            ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_probe_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
     "rbq_tiles_bytes": (ctypes.c_size_t, [Shape]),
     "rbq_pack_tiles": (ctypes.c_int, [ctypes.c_void_p, Shape, ctypes.c_void_p, ctypes.c_void_p]),
@@ -717,6 +751,258 @@ def qat_backward_ckpt(planes: torch.Tensor, scales: torch.Tensor, x_codes: torch
                                       x_scales.data_ptr(), dY.data_ptr(), M, ptr(dX), ptr(dW), ptr(ds),
                                       ptr(workspace), wn, ptr(status), st), "rbq_qat_backward_ckpt")
     return dX, (dW if need_dw else None), ds
+
+
+def encode_q4(W: torch.Tensor, *, zeros: bool = False, status: torch.Tensor | None = None, stream=None):
+    """rbq_encode_q4: fp32 W [out][in] -> (codes uint8 [out][in/2], two columns
+    a byte, scales float16 [out][ceil(in/128)], zero points uint8 of the same
+    size, or None where `zeros` is false).  `status` (int32, 1 element)
+    receives RBQ_STATUS_* bits."""
+    _dev(W, torch.float32, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be [out][in]")
+    out_f, in_f = W.shape
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(W, status)
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return encode_q4(W, zeros=zeros, status=status)
+    st = _current_stream(dev.index)
+    codes = torch.empty((out_f, in_f // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((out_f, _blocks(in_f)), dtype=torch.float16, device=dev)
+    points = torch.empty((out_f, _blocks(in_f)), dtype=torch.uint8, device=dev) if zeros else None
+    check(lib().rbq_encode_q4(W.data_ptr(), out_f, in_f, codes.data_ptr(), scales.data_ptr(), _ptr(points),
+                              _ptr(status), st), "rbq_encode_q4")
+    return codes, scales, points
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _q4_layer(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None):
+    _dev(codes, torch.uint8, "codes")
+    _dev(scales, torch.float16, "scales")
+    if codes.dim() != 2 or scales.shape != (codes.shape[0], _blocks(2 * codes.shape[1])):
+        raise ValueError("codes must be [out][in/2] and scales [out][ceil(in/128)]")
+    if zeros is not None:
+        _dev(zeros, torch.uint8, "zeros")
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must be [out][ceil(in/128)]")
+    return codes.shape[0], 2 * codes.shape[1]
+
+
+def _y_type(dtype: torch.dtype) -> int:
+    if dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"dtype must be torch.float16 or torch.float32, got {dtype}")
+    return RBQ_Y_F32 if dtype == torch.float32 else RBQ_Y_F16
+
+
+def gemm_q4(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, zeros: torch.Tensor | None = None, *,
+            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None):
+    """rbq_gemm_q4: Y [M][out] (float16 or float32) of the layer of encode_q4 and
+    fp16 tokens X [M][in]; zeros None: all zero points are 8."""
+    out_f, in_f = _q4_layer(codes, scales, zeros)
+    _dev(X, torch.float16, "X")
+    if X.dim() != 2 or X.shape[1] != in_f:
+        raise ValueError(f"X must be [M][{in_f}], got {tuple(X.shape)}")
+    M = X.shape[0]
+    kind = _y_type(dtype)
+    dev = _one_device(codes, scales, X, zeros, workspace)
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return gemm_q4(codes, scales, X, zeros, dtype=dtype, Y=Y, workspace=workspace)
+    st = _current_stream(dev.index)
+    Y = _out(Y, (M, out_f), dtype, "Y", dev)
+    if workspace is None:
+        need = int(lib().rbq_gemm_q4_workspace_bytes(out_f, in_f, M, kind))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
+    check(lib().rbq_gemm_q4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), out_f, in_f, X.data_ptr(), M,
+                            Y.data_ptr(), kind, wp, wn, st), "rbq_gemm_q4")
+    return Y
+
+
+def gemv_q4(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, zeros: torch.Tensor | None = None, *,
+            dtype: torch.dtype = torch.float16, y: torch.Tensor | None = None, stream=None):
+    """rbq_gemm_q4 of one fp16 token x [in]: y [out]."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 1:
+        raise ValueError("x must be a tensor [in]")
+    if y is not None and (not isinstance(y, torch.Tensor) or y.dim() != 1):
+        raise ValueError("y must be a tensor [out]")
+    return gemm_q4(codes, scales, x.unsqueeze(0), zeros, dtype=dtype, Y=None if y is None else y.unsqueeze(0),
+                   stream=stream).view(-1)
+
+
+_L_TYPES = {torch.float16: RBQ_L_F16, torch.float32: RBQ_L_F32, torch.bfloat16: RBQ_L_BF16}
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(type, M, vocab, row stride) of logits [M][vocab] whose rows are contiguous
+    and may lie apart (a slice of a wider tensor)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dtype not in _L_TYPES:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [M][vocab]")
+    M, vocab = t.shape
+    if (vocab > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < vocab):
+        raise ValueError(f"the rows of {name} must be contiguous and lie apart")
+    return _L_TYPES[t.dtype], M, vocab, t.stride(0) if M > 1 else vocab
+
+
+def _per_row(t: torch.Tensor | None, dtype, size: tuple, name: str, dev: torch.device) -> int | None:
+    """Address of an optional contiguous tensor of that size."""
+    if t is None:
+        return None
+    _dev(t, dtype, name)
+    if t.shape != size:
+        raise ValueError(f"{name} must be {list(size)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the logits are on {dev}")
+    return t.data_ptr()
+
+
+def _d_logits(t: torch.Tensor | None, logits: torch.Tensor):
+    """The gradient's tensor, checked or made, and its row stride."""
+    if t is None:
+        t = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    kind, M, vocab, stride = _rows(t, "d_logits")
+    if t.shape != logits.shape or t.dtype != logits.dtype or t.device != logits.device:
+        raise ValueError("d_logits must be like the logits")
+    return t, stride
+
+
+def _room(workspace: torch.Tensor | None, need: int, dev: torch.device):
+    """(tensor to keep, address, bytes) of the given workspace, or of a new one."""
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return (None, None, 0) if workspace is None else (workspace, workspace.data_ptr(), _nbytes(workspace))
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *, top: int = 0,
+                   temperature: float = 1.0, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, stream=None):
+    """rbq_token_logprobs: of logits [M][vocab] (float16, bfloat16 or float32; rows
+    may lie apart) and int64 targets [M] (negative: none; or None)
+    (logp [M] or None, entropy [M], top_logp [M][top], top_index int32
+    [M][top]), float32, at the given temperature."""
+    kind, M, vocab, stride = _rows(logits, "logits")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(logits, targets, workspace, status)
+    tp = _per_row(targets, torch.int64, (M,), "targets", dev)
+    top = int(top)
+    if not 0 <= top <= RBQ_TOP_MAX:
+        raise ValueError(f"top must be 0 .. {RBQ_TOP_MAX}")
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return token_logprobs(logits, targets, top=top, temperature=temperature, workspace=workspace,
+                                  status=status)
+    st = _current_stream(dev.index)
+    logp = None if targets is None else torch.empty(M, dtype=torch.float32, device=dev)
+    entropy = torch.empty(M, dtype=torch.float32, device=dev)
+    top_logp = torch.empty((M, top), dtype=torch.float32, device=dev)
+    top_index = torch.empty((M, top), dtype=torch.int32, device=dev)
+    keep, wp, wn = _room(workspace, int(lib().rbq_token_logprobs_workspace_bytes(M, vocab, top)), dev)
+    check(lib().rbq_token_logprobs(logits.data_ptr(), kind, M, vocab, stride, temperature, tp, _ptr(logp),
+                                   entropy.data_ptr(), top, top_logp.data_ptr(), top_index.data_ptr(), wp, wn,
+                                   _ptr(status), st), "rbq_token_logprobs")
+    return logp, entropy, top_logp, top_index
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor | None, d_logp: torch.Tensor | None,
+                            d_entropy: torch.Tensor | None = None, *, temperature: float = 1.0,
+                            d_logits: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None, stream=None):
+    """rbq_token_logprobs_backward: (d_logits, logp [M] or None, entropy [M]) with
+    the gradient of sum d_logp logp + d_entropy entropy in the logits' type
+    (float32 weights [M], either may be None); d_logits may be the logits."""
+    kind, M, vocab, stride = _rows(logits, "logits")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(logits, targets, d_logp, d_entropy, workspace, status)
+    tp = _per_row(targets, torch.int64, (M,), "targets", dev)
+    ap = _per_row(d_logp, torch.float32, (M,), "d_logp", dev)
+    bp = _per_row(d_entropy, torch.float32, (M,), "d_entropy", dev)
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return token_logprobs_backward(logits, targets, d_logp, d_entropy, temperature=temperature,
+                                           d_logits=d_logits, workspace=workspace, status=status)
+    st = _current_stream(dev.index)
+    d_logits, d_stride = _d_logits(d_logits, logits)
+    logp = None if targets is None else torch.empty(M, dtype=torch.float32, device=dev)
+    entropy = torch.empty(M, dtype=torch.float32, device=dev)
+    keep, wp, wn = _room(workspace, int(lib().rbq_token_logprobs_workspace_bytes(M, vocab, 0)), dev)
+    check(lib().rbq_token_logprobs_backward(logits.data_ptr(), kind, M, vocab, stride, temperature, tp, ap, bp,
+                                            d_logits.data_ptr(), d_stride, _ptr(logp), entropy.data_ptr(), wp, wn,
+                                            _ptr(status), st), "rbq_token_logprobs_backward")
+    return d_logits, logp, entropy
+
+
+def _teacher(index: torch.Tensor, t_logp: torch.Tensor, M: int, dev: torch.device):
+    if not isinstance(index, torch.Tensor) or index.dim() != 2 or index.shape[0] != M:
+        raise ValueError("index must be [M][slots]")
+    if index.shape[1] > RBQ_TOP_MAX:
+        raise ValueError(f"at most {RBQ_TOP_MAX} slots a row")
+    size = tuple(index.shape)
+    return (_per_row(index, torch.int32, size, "index", dev), _per_row(t_logp, torch.float32, size, "t_logp", dev),
+            size[1])
+
+
+def distill_forward(logits: torch.Tensor, index: torch.Tensor, t_logp: torch.Tensor, *, temperature: float = 1.0,
+                    tail: bool = False, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    stream=None):
+    """rbq_distill_forward: the divergence [M] (float32) of the student's logits
+    [M][vocab] from a teacher's int32 index and float32 t_logp [M][slots], as
+    token_logprobs gives them (top_index, top_logp); `tail`: the teacher's
+    remaining mass is one more class."""
+    kind, M, vocab, stride = _rows(logits, "logits")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(logits, index, t_logp, workspace, status)
+    ip, lp, slots = _teacher(index, t_logp, M, dev)
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return distill_forward(logits, index, t_logp, temperature=temperature, tail=tail, workspace=workspace,
+                                   status=status)
+    st = _current_stream(dev.index)
+    loss = torch.empty(M, dtype=torch.float32, device=dev)
+    keep, wp, wn = _room(workspace, int(lib().rbq_distill_workspace_bytes(M, vocab, slots)), dev)
+    check(lib().rbq_distill_forward(logits.data_ptr(), kind, M, vocab, stride, temperature, ip, lp, slots,
+                                    RBQ_DISTILL_TAIL if tail else 0, loss.data_ptr(), wp, wn, _ptr(status), st),
+          "rbq_distill_forward")
+    return loss
+
+
+def distill_backward(logits: torch.Tensor, index: torch.Tensor, t_logp: torch.Tensor, d_loss: torch.Tensor, *,
+                     temperature: float = 1.0, tail: bool = False, d_logits: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """rbq_distill_backward: (d_logits, loss [M]) with the gradient of
+    sum d_loss loss (float32 d_loss [M]) in the logits' type; d_logits may be
+    the logits.  Other arguments as distill_forward."""
+    kind, M, vocab, stride = _rows(logits, "logits")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+    dev = _one_device(logits, index, t_logp, d_loss, workspace, status)
+    ip, lp, slots = _teacher(index, t_logp, M, dev)
+    dp = _per_row(d_loss, torch.float32, (M,), "d_loss", dev)
+    if stream is not None or dev.index != _current_device():
+        with _There(dev, stream):
+            return distill_backward(logits, index, t_logp, d_loss, temperature=temperature, tail=tail,
+                                    d_logits=d_logits, workspace=workspace, status=status)
+    st = _current_stream(dev.index)
+    d_logits, d_stride = _d_logits(d_logits, logits)
+    loss = torch.empty(M, dtype=torch.float32, device=dev)
+    keep, wp, wn = _room(workspace, int(lib().rbq_distill_workspace_bytes(M, vocab, slots)), dev)
+    check(lib().rbq_distill_backward(logits.data_ptr(), kind, M, vocab, stride, temperature, ip, lp, slots,
+                                     RBQ_DISTILL_TAIL if tail else 0, dp, d_logits.data_ptr(), d_stride,
+                                     loss.data_ptr(), wp, wn, _ptr(status), st), "rbq_distill_backward")
+    return d_logits, loss
 
 
 def probe_read(buf: torch.Tensor, sink: torch.Tensor, nbytes: int | None = None, *, stream=None) -> None:

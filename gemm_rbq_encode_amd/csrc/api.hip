@@ -8,6 +8,7 @@
 
 #include "rbq.h"
 #include "rbq_kernels.h"
+#include "logits_plan.h"
 
 namespace {
 
@@ -773,6 +774,234 @@ rbq_status rbq_qat_backward_ckpt(const uint32_t *planes, const uint16_t *scales,
     hipError_t e = rbq::launch_qat_backward_ckpt(planes, scales, s.out_features, s.in_features, s.num_planes,
                                                  s.group_size, x_codes, x_scales, dY, M, dX, dW, dscales, workspace,
                                                  ws_bytes, status_dev, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+// ---- linears in 4 bits -------------------------------------------------------
+
+static bool q4_too_large(int32_t out, int32_t in) {
+    return out > RBQ_Q4_MAX_FEATURES || in > RBQ_Q4_MAX_FEATURES ||
+           (int64_t)out * (((int64_t)in + 127) / 128) >= ((int64_t)1 << 31);
+}
+
+rbq_status rbq_encode_q4(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes,
+                         uint16_t *scales, uint8_t *zeros, int32_t *status_dev, void *stream) {
+    if (!f8_shape_ok(out_features, in_features))
+        return RBQ_ERR_INVALID_ARG;
+    if (q4_too_large(out_features, in_features))
+        return RBQ_ERR_UNSUPPORTED;
+    if (out_features == 0 || in_features == 0)
+        return RBQ_OK;
+    if (W == nullptr || codes == nullptr || scales == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(status_dev, 4))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st = device_present();
+    if (st != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_encode_q4(W, out_features, in_features, codes, scales, zeros, status_dev,
+                                         (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+size_t rbq_gemm_q4_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type) {
+    (void)out_features, (void)in_features, (void)M, (void)y_type;
+    return 0;
+}
+
+rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int32_t out_features,
+                       int32_t in_features, const uint16_t *X, int32_t M, void *Y, uint32_t y_type,
+                       void *workspace, size_t ws_bytes, void *stream) {
+    if (M < 0 || !f8_shape_ok(out_features, in_features) || y_type > RBQ_Y_F32 ||
+        (ws_bytes > 0 && workspace == nullptr))
+        return RBQ_ERR_INVALID_ARG;
+    if (q4_too_large(out_features, in_features))
+        return RBQ_ERR_UNSUPPORTED;
+    if (M == 0 || out_features == 0)
+        return RBQ_OK;
+    if (Y == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(Y, y_type == RBQ_Y_F32 ? 4 : 2) || !aligned(workspace, 16))
+        return RBQ_ERR_ALIGNMENT;
+    rbq_status st;
+    hipError_t e;
+    if (in_features == 0) {
+        if ((st = device_present()) != RBQ_OK)
+            return st;
+        const size_t n = (size_t)M * (size_t)out_features;
+        e = y_type == RBQ_Y_F32 ? rbq::launch_fill_zero_f32((float *)Y, n, (hipStream_t)stream)
+                                : rbq::launch_fill_zero_u16((uint16_t *)Y, (int64_t)n, (hipStream_t)stream);
+        return e == hipSuccess ? RBQ_OK : hip_fail(e);
+    }
+    if (codes == nullptr || scales == nullptr || X == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 2) || !aligned(X, 16))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    e = rbq::launch_gemm_q4(codes, scales, zeros, out_features, in_features, X, M, Y, y_type == RBQ_Y_F32,
+                            (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+// ---- operators on logits ------------------------------------------------------
+
+static size_t logits_bytes(uint32_t type) { return type == RBQ_L_F32 ? 4 : 2; }
+
+// What all of them check; RBQ_OK with *done set where there is nothing to do.
+static rbq_status logits_check(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                               float temperature, int32_t entries, const void *workspace, size_t ws_bytes,
+                               const int32_t *status_dev, bool *done) {
+    *done = false;
+    if (type > RBQ_L_BF16 || M < 0 || vocab < 1 || row_stride < vocab || entries < 0 ||
+        !(temperature >= 1e-6f && temperature <= 1e6f) || (ws_bytes > 0 && workspace == nullptr))
+        return RBQ_ERR_INVALID_ARG;
+    if (vocab > RBQ_VOCAB_MAX || entries > RBQ_TOP_MAX || row_stride > ((int64_t)1 << 31))
+        return RBQ_ERR_UNSUPPORTED;
+    if (M == 0) {
+        *done = true;
+        return RBQ_OK;
+    }
+    if (logits == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(logits, logits_bytes(type)) || !aligned(workspace, 16) || !aligned(status_dev, 4))
+        return RBQ_ERR_ALIGNMENT;
+    return RBQ_OK;
+}
+
+// d_logits: the logits themselves, or apart from them.
+static rbq_status logits_gradient_check(const void *logits, const void *d_logits, uint32_t type, int32_t M,
+                                        int32_t vocab, int64_t row_stride, int64_t d_row_stride) {
+    if (d_logits == nullptr || d_row_stride < vocab)
+        return RBQ_ERR_INVALID_ARG;
+    if (d_row_stride > ((int64_t)1 << 31))
+        return RBQ_ERR_UNSUPPORTED;
+    if (!aligned(d_logits, logits_bytes(type)))
+        return RBQ_ERR_ALIGNMENT;
+    const uintptr_t b = logits_bytes(type), x0 = (uintptr_t)logits, d0 = (uintptr_t)d_logits;
+    const uintptr_t x1 = x0 + ((uintptr_t)(M - 1) * (uintptr_t)row_stride + (uintptr_t)vocab) * b;
+    const uintptr_t d1 = d0 + ((uintptr_t)(M - 1) * (uintptr_t)d_row_stride + (uintptr_t)vocab) * b;
+    if (x0 < d1 && d0 < x1 && !(x0 == d0 && row_stride == d_row_stride))
+        return RBQ_ERR_INVALID_ARG;
+    return RBQ_OK;
+}
+
+size_t rbq_token_logprobs_workspace_bytes(int32_t M, int32_t vocab, int32_t top) {
+    if (M < 1 || vocab < 1 || vocab > RBQ_VOCAB_MAX || top < 0 || top > RBQ_TOP_MAX)
+        return 0;
+    return rbq::logits_workspace_bytes(M, vocab, top, 0);
+}
+
+rbq_status rbq_token_logprobs(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                              float temperature, const int64_t *targets, float *logp, float *entropy, int32_t top,
+                              float *top_logp, int32_t *top_index, void *workspace, size_t ws_bytes,
+                              int32_t *status_dev, void *stream) {
+    bool done;
+    rbq_status st = logits_check(logits, type, M, vocab, row_stride, temperature, top, workspace, ws_bytes,
+                                 status_dev, &done);
+    if (st != RBQ_OK || done)
+        return st;
+    if ((logp != nullptr && targets == nullptr) || (top > 0 && (top_logp == nullptr || top_index == nullptr)))
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(targets, 8) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(top_logp, 4) ||
+        !aligned(top_index, 4))
+        return RBQ_ERR_ALIGNMENT;
+    if (logp == nullptr && entropy == nullptr && top == 0)
+        return RBQ_OK;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_token_logprobs(logits, type, M, vocab, row_stride, temperature, targets, logp, entropy,
+                                              top, top_logp, top_index, workspace, ws_bytes, status_dev,
+                                              (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+rbq_status rbq_token_logprobs_backward(const void *logits, uint32_t type, int32_t M, int32_t vocab,
+                                       int64_t row_stride, float temperature, const int64_t *targets,
+                                       const float *d_logp, const float *d_entropy, void *d_logits,
+                                       int64_t d_row_stride, float *logp, float *entropy, void *workspace,
+                                       size_t ws_bytes, int32_t *status_dev, void *stream) {
+    bool done;
+    rbq_status st = logits_check(logits, type, M, vocab, row_stride, temperature, 0, workspace, ws_bytes, status_dev,
+                                 &done);
+    if (st != RBQ_OK || done)
+        return st;
+    if ((d_logp == nullptr && d_entropy == nullptr) ||
+        ((logp != nullptr || d_logp != nullptr) && targets == nullptr))
+        return RBQ_ERR_INVALID_ARG;
+    st = logits_gradient_check(logits, d_logits, type, M, vocab, row_stride, d_row_stride);
+    if (st != RBQ_OK)
+        return st;
+    if (!aligned(targets, 8) || !aligned(d_logp, 4) || !aligned(d_entropy, 4) || !aligned(logp, 4) ||
+        !aligned(entropy, 4))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_token_logprobs_backward(logits, type, M, vocab, row_stride, temperature, targets,
+                                                       d_logp, d_entropy, d_logits, d_row_stride, logp, entropy,
+                                                       workspace, ws_bytes, status_dev, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+size_t rbq_distill_workspace_bytes(int32_t M, int32_t vocab, int32_t slots) {
+    if (M < 1 || vocab < 1 || vocab > RBQ_VOCAB_MAX || slots < 0 || slots > RBQ_TOP_MAX)
+        return 0;
+    return rbq::logits_workspace_bytes(M, vocab, 0, slots);
+}
+
+static rbq_status distill_check(const int32_t *index, const float *t_logp, int32_t slots, uint32_t flags,
+                                const float *loss) {
+    if ((flags & ~RBQ_DISTILL_TAIL) != 0 || (slots > 0 && (index == nullptr || t_logp == nullptr)))
+        return RBQ_ERR_INVALID_ARG;
+    if (!aligned(index, 4) || !aligned(t_logp, 4) || !aligned(loss, 4))
+        return RBQ_ERR_ALIGNMENT;
+    return RBQ_OK;
+}
+
+rbq_status rbq_distill_forward(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                               float temperature, const int32_t *index, const float *t_logp, int32_t slots,
+                               uint32_t flags, float *loss, void *workspace, size_t ws_bytes, int32_t *status_dev,
+                               void *stream) {
+    bool done;
+    rbq_status st = logits_check(logits, type, M, vocab, row_stride, temperature, slots, workspace, ws_bytes,
+                                 status_dev, &done);
+    if (st != RBQ_OK || done)
+        return st;
+    if (loss == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if ((st = distill_check(index, t_logp, slots, flags, loss)) != RBQ_OK)
+        return st;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_distill(logits, type, M, vocab, row_stride, temperature, index, t_logp, slots,
+                                       (flags & RBQ_DISTILL_TAIL) != 0, loss, nullptr, nullptr, 0, workspace,
+                                       ws_bytes, status_dev, (hipStream_t)stream);
+    return e == hipSuccess ? RBQ_OK : hip_fail(e);
+}
+
+rbq_status rbq_distill_backward(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                                float temperature, const int32_t *index, const float *t_logp, int32_t slots,
+                                uint32_t flags, const float *d_loss, void *d_logits, int64_t d_row_stride,
+                                float *loss, void *workspace, size_t ws_bytes, int32_t *status_dev, void *stream) {
+    bool done;
+    rbq_status st = logits_check(logits, type, M, vocab, row_stride, temperature, slots, workspace, ws_bytes,
+                                 status_dev, &done);
+    if (st != RBQ_OK || done)
+        return st;
+    if (d_loss == nullptr)
+        return RBQ_ERR_INVALID_ARG;
+    if ((st = distill_check(index, t_logp, slots, flags, loss)) != RBQ_OK)
+        return st;
+    st = logits_gradient_check(logits, d_logits, type, M, vocab, row_stride, d_row_stride);
+    if (st != RBQ_OK)
+        return st;
+    if (!aligned(d_loss, 4))
+        return RBQ_ERR_ALIGNMENT;
+    if ((st = device_present()) != RBQ_OK)
+        return st;
+    hipError_t e = rbq::launch_distill(logits, type, M, vocab, row_stride, temperature, index, t_logp, slots,
+                                       (flags & RBQ_DISTILL_TAIL) != 0, loss, d_loss, d_logits, d_row_stride,
+                                       workspace, ws_bytes, status_dev, (hipStream_t)stream);
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 

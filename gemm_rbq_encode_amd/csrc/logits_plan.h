@@ -1,0 +1,32 @@
+// logits_plan.h -- how the rows of logits are cut over workgroups.  Host
+// arithmetic only, so that a test can ask it without a GPU.
+#pragma once
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+namespace rbq {
+
+constexpr int LG_THREADS = 512;      // threads of a workgroup on logits
+constexpr int LG_VEC = 8;            // consecutive logits a thread takes at a time
+constexpr int LG_SLICES_MAX = 256;   // slices of a row
+
+// Slices of a row: enough that M rows make about four workgroups per compute
+// unit, each thread with one vector at least.
+inline int logits_slices(int M, int vocab) {
+    const int64_t vectors = ((int64_t)vocab + LG_VEC - 1) / LG_VEC;
+    const int64_t want = std::min<int64_t>((1024 + (int64_t)M - 1) / M, LG_SLICES_MAX);
+    const int64_t most = (vectors + LG_THREADS - 1) / LG_THREADS;
+    return (int)std::max<int64_t>(1, std::min(want, most));
+}
+
+// Bytes of the partial results of all slices, 0 where a row is one slice: per
+// slice a running maximum, two sums and the target's logit, and `top` keys of 8
+// bytes; per row the logits of `slots` named tokens.
+inline size_t logits_workspace_bytes(int M, int vocab, int top, int slots) {
+    const int S = logits_slices(M, vocab);
+    return S == 1 ? 0 : (size_t)M * ((size_t)S * (16u + 8u * (size_t)top) + 4u * (size_t)slots);
+}
+
+}  // namespace rbq

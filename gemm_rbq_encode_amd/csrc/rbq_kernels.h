@@ -140,6 +140,28 @@ hipError_t launch_gemm_f8_tile(const uint8_t *W, const float *ws, int out, int i
 hipError_t launch_gemv_f8(const uint8_t *W, const float *ws, int out, int in, const uint16_t *x, uint16_t *y,
                           hipStream_t st);
 
+// Linears in 4 bits with group scales (q4.hip); out, in, M >= 1; zeros may be
+// null (symmetric).
+hipError_t launch_encode_q4(const float *W, int out, int in, uint8_t *codes, uint16_t *scales, uint8_t *zeros,
+                            int32_t *status, hipStream_t st);
+hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
+                          const uint16_t *X, int M, void *Y, int y_f32, hipStream_t st);
+
+// Operators on rows of logits (logits.hip); M, V >= 1, strides in entries.
+hipError_t launch_token_logprobs(const void *x, uint32_t type, int M, int V, int64_t stride, float temperature,
+                                 const int64_t *targets, float *logp, float *entropy, int top, float *top_logp,
+                                 int32_t *top_index, void *workspace, size_t bytes, int32_t *status, hipStream_t st);
+hipError_t launch_token_logprobs_backward(const void *x, uint32_t type, int M, int V, int64_t stride,
+                                          float temperature, const int64_t *targets, const float *d_logp,
+                                          const float *d_entropy, void *dx, int64_t d_stride, float *logp,
+                                          float *entropy, void *workspace, size_t bytes, int32_t *status,
+                                          hipStream_t st);
+// dx may be null (loss alone).
+hipError_t launch_distill(const void *x, uint32_t type, int M, int V, int64_t stride, float temperature,
+                          const int32_t *index, const float *t_logp, int slots, int tail, float *loss,
+                          const float *d_loss, void *dx, int64_t d_stride, void *workspace, size_t bytes,
+                          int32_t *status, hipStream_t st);
+
 // Streaming-read probe (probe.hip): one launch reading `bytes` bytes.
 hipError_t launch_probe_read(const void *buf, size_t bytes, uint32_t *sink, hipStream_t st);
 

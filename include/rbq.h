@@ -768,6 +768,186 @@ rbq_status rbq_gemm_f8(const uint8_t *codes, const float *scales, int32_t out_fe
 rbq_status rbq_gemv_f8(const uint8_t *codes, const float *scales, int32_t out_features, int32_t in_features,
                        const uint16_t *x, uint16_t *y, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Linears in 4 bits with group scales.
+ *
+ * The format that a model of four planes with scales per group of 128 is
+ * compared with and started from (QBB summary: 4-bit checkpoints, "W(4x1)A16
+ * g128"), and half the bytes of the 8-bit layers for a head or a teacher that
+ * bears it:
+ *   codes   uint8 [out][in/2], row-major; byte b of a row holds column 2b in
+ *           its low four bits and column 2b + 1 in its high ones
+ *   scales  binary16 bits [out][T], T = ceil(in / 128): one per row and group of
+ *           128 consecutive columns, the last group shorter where in % 128 != 0
+ *   zeros   uint8 [out][T], the groups' zero points, or NULL: all 8
+ * A weight is w^ = (code - zero) scale.  in_features is a multiple of 32; more
+ * than RBQ_Q4_MAX_FEATURES rows or columns, or 2^31 groups and more, are
+ * RBQ_ERR_UNSUPPORTED.  What a call writes may not overlap anything else it is
+ * given.
+ *
+ * Quantisation of a group, every rounding to nearest even, fl32 one fp32
+ * operation each, scales kept within 2^-24 .. 65504:
+ *   with zeros     lo = min(0, min w), hi = max(0, max w)
+ *                  scale = fp16(fl32(fl32(hi - lo) / 15))
+ *                  zero  = rint(fl32(-lo / scale)), at most 15
+ *   without        scale = fp16(fl32(max |w| / 7)), zero = 8
+ *   code = rint(fl32(w / scale)) + zero, within 0 .. 15
+ * A group with a NaN or infinite entry has scale NaN, zero 0 and codes 0.
+ * ------------------------------------------------------------------------- */
+
+/* Most rows and columns of a layer that the calls of this section handle. */
+#define RBQ_Q4_MAX_FEATURES        (1 << 25)
+
+/*
+ * rbq_encode_q4 -- codes, scales and (where given) zero points of a weight.
+ *   W       device fp32 [out][in], 16-byte aligned (read only)
+ *   codes   device, 16-byte aligned, written;  scales  device, 2-byte aligned,
+ *           written;  zeros  device, written, or NULL: symmetric
+ *   status_dev  device int32 or NULL: RBQ_STATUS_NONFINITE_W is OR-ed in
+ * out == 0 or in == 0 enqueues nothing.  Errors: RBQ_ERR_INVALID_ARG,
+ * RBQ_ERR_ALIGNMENT, RBQ_ERR_UNSUPPORTED, RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
+ */
+rbq_status rbq_encode_q4(const float *W, int32_t out_features, int32_t in_features, uint8_t *codes,
+                         uint16_t *scales, uint8_t *zeros, int32_t *status_dev, void *stream);
+
+/*
+ * rbq_gemm_q4 -- the product with M fp16 tokens:
+ *   Y[m][r] = sum_t scale[r][t] sum_{j in group t} (code[r][j] - zero[r][t]) X[m][j]
+ * Every product inside a group is exact; the sums, the scaling and the sum over
+ * the groups are fp32, and each output is rounded once to its type.
+ *   codes, scales, zeros  the layer (zeros NULL: all 8); codes 16-byte, scales
+ *                         2-byte aligned
+ *   X       device fp16 [M][in], 16-byte aligned
+ *   M       tokens, >= 0 (0 enqueues nothing)
+ *   Y       device [M][out], written: binary16 (RBQ_Y_F16, 2-byte aligned) or
+ *           fp32 (RBQ_Y_F32, 4-byte aligned)
+ *   workspace  device memory of rbq_gemm_q4_workspace_bytes(..) bytes, 16-byte
+ *           aligned, any contents (0 for many sizes).  Where it is not 0, the
+ *           columns are split over workgroups whose fp32 partial sums it holds,
+ *           added in order by a second kernel (deterministic); with a smaller
+ *           workspace (or NULL with ws_bytes 0) they are not split, which is
+ *           slower and adds in another order.  Calls that share one must be
+ *           ordered on one stream.
+ * in == 0 writes Y = 0.  Errors: RBQ_ERR_INVALID_ARG, RBQ_ERR_ALIGNMENT,
+ * RBQ_ERR_UNSUPPORTED, RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
+ */
+size_t rbq_gemm_q4_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type);
+rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int32_t out_features,
+                       int32_t in_features, const uint16_t *X, int32_t M, void *Y, uint32_t y_type,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators on logits: the output end of a model.
+ *
+ * The pages train the binarized model against a full-precision teacher
+ * (distillation: RaBiT summary, "task" losses; QBB summary, distillation of the
+ * scales) and judge it by its log probabilities (perplexity).  logits is
+ * device [M][vocab], a row every `row_stride` entries (>= vocab; rows may start
+ * at any entry), of type RBQ_L_F16, RBQ_L_F32 or RBQ_L_BF16.  With T the
+ * temperature (> 0, 1e-6 .. 1e6), p = softmax(logits / T), computed in fp32
+ * relative to the row's maximum.
+ *
+ * Entries of -inf are masked: p = 0.  A row of nothing else is empty: its log
+ * probabilities are -inf, its entropy 0, its gradients 0.  A row with a NaN or
+ * +inf entry has NaN outputs and gradients, and alternatives of index -1.  A
+ * token number of `vocab` or more sets RBQ_STATUS_BAD_TOKEN in status_dev, and
+ * that row's outputs and gradients that depend on it are NaN.
+ *
+ * workspace: 16-byte aligned device memory of the query's size, any contents.
+ * With few rows, each is cut into slices over workgroups whose partial results
+ * it holds, joined in order by a second kernel; where it is smaller (or NULL with
+ * ws_bytes 0) rows are not cut, which is slower and adds in another order.  Calls
+ * that share one must be ordered on one stream.  Every call gives the same bits
+ * in every run.  Outputs and the workspace may not overlap anything else, but
+ * d_logits may be the logits themselves (the same address and stride).
+ * ------------------------------------------------------------------------- */
+#define RBQ_L_F16  0u
+#define RBQ_L_F32  1u
+#define RBQ_L_BF16 2u
+
+#define RBQ_VOCAB_MAX  (1 << 24)   /* longest row */
+#define RBQ_TOP_MAX    128         /* most alternatives, and slots of a teacher */
+
+#define RBQ_STATUS_BAD_TOKEN 64u   /* a token number of the vocabulary's size or more */
+
+/*
+ * rbq_token_logprobs -- per row:
+ *   logp[m]       ln p[target[m]]; 0 where the target is negative (none)
+ *   entropy[m]    -sum_v p_v ln p_v
+ *   top_index[m][j], top_logp[m][j], j < top: the largest entries downwards,
+ *                 among equal ones the lowest index first, and their log
+ *                 probabilities.  Masked entries are no alternatives: behind the
+ *                 last one the index is -1 and the log probability -inf.
+ *   targets   device int64 [M] (needed with logp), 8-byte aligned
+ *   logp, entropy, top_logp  device fp32, top_index device int32; logp and
+ *             entropy may be NULL; top 0 .. RBQ_TOP_MAX
+ * M == 0 enqueues nothing.  Errors: RBQ_ERR_INVALID_ARG, RBQ_ERR_ALIGNMENT,
+ * RBQ_ERR_UNSUPPORTED (vocab > RBQ_VOCAB_MAX, top > RBQ_TOP_MAX),
+ * RBQ_ERR_NO_DEVICE, RBQ_ERR_HIP.
+ */
+size_t rbq_token_logprobs_workspace_bytes(int32_t M, int32_t vocab, int32_t top);
+rbq_status rbq_token_logprobs(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                              float temperature, const int64_t *targets, float *logp, float *entropy, int32_t top,
+                              float *top_logp, int32_t *top_index, void *workspace, size_t ws_bytes,
+                              int32_t *status_dev, void *stream);
+
+/*
+ * rbq_token_logprobs_backward -- the gradient of
+ * sum_m d_logp[m] logp[m] + d_entropy[m] entropy[m]:
+ *   d_logits[m][v] = (1/T) (d_logp ([v = target] - p_v) - d_entropy p_v (ln p_v + entropy))
+ * in the type of the logits, a row every `d_row_stride` entries.  The row's sums
+ * are formed anew, so nothing is kept from the forward call; logp and entropy
+ * are written where given.
+ *   d_logp, d_entropy  device fp32 [M]; either may be NULL (0), not both.  A row
+ *             whose weights are 0 (d_logp counts as 0 without a target) gets the
+ *             gradient 0, whatever it holds.
+ *   targets   needed with d_logp or logp
+ *   workspace rbq_token_logprobs_workspace_bytes(M, vocab, 0)
+ * Errors as rbq_token_logprobs.
+ */
+rbq_status rbq_token_logprobs_backward(const void *logits, uint32_t type, int32_t M, int32_t vocab,
+                                       int64_t row_stride, float temperature, const int64_t *targets,
+                                       const float *d_logp, const float *d_entropy, void *d_logits,
+                                       int64_t d_row_stride, float *logp, float *entropy, void *workspace,
+                                       size_t ws_bytes, int32_t *status_dev, void *stream);
+
+/* Flags of the distillation calls: the teacher's mass beside its slots is one
+ * more class. */
+#define RBQ_DISTILL_TAIL 1u
+
+/*
+ * rbq_distill_forward, rbq_distill_backward -- Kullback-Leibler divergence of the
+ * student's logits from a teacher known by the log probabilities of some tokens
+ * of each row, as rbq_token_logprobs writes them (top_index, top_logp, at the
+ * same temperature):
+ *   index   device int32 [M][slots], t_logp  device fp32 [M][slots]; a slot with
+ *           a negative index or log probability -inf is not used.  A token named
+ *           twice counts with both.
+ *   without RBQ_DISTILL_TAIL  p_j = e^t_j / sum_i e^t_i (t up to a constant of
+ *           the row), loss = sum_j p_j (ln p_j - ln q_j), q the student's p of
+ *           the token; a row without slots has loss and gradient 0
+ *   with it p_j = e^t_j, and the rest r = max(0, 1 - sum p) is compared with the
+ *           student's mass on all tokens not named:
+ *           loss = sum_j p_j (ln p_j - ln q_j) + r (ln r - ln q_rest)
+ * A class with p = 0 counts 0; where q = 0 < p the loss is +inf.
+ *   d_loss    device fp32 [M]: d_logits is the gradient of sum_m d_loss[m] loss[m]
+ *             in the type of the logits (a factor T^2, where wanted, belongs
+ *             into d_loss); a row with d_loss 0 gets 0, whatever it holds
+ *   loss      device fp32 [M]; may be NULL in the backward call
+ * The backward call forms the row's sums anew: a training step needs it alone.
+ * What depends on the slots alone is computed in fp64.  slots 0 .. RBQ_TOP_MAX;
+ * other arguments and errors as rbq_token_logprobs.
+ */
+size_t rbq_distill_workspace_bytes(int32_t M, int32_t vocab, int32_t slots);
+rbq_status rbq_distill_forward(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                               float temperature, const int32_t *index, const float *t_logp, int32_t slots,
+                               uint32_t flags, float *loss, void *workspace, size_t ws_bytes, int32_t *status_dev,
+                               void *stream);
+rbq_status rbq_distill_backward(const void *logits, uint32_t type, int32_t M, int32_t vocab, int64_t row_stride,
+                                float temperature, const int32_t *index, const float *t_logp, int32_t slots,
+                                uint32_t flags, const float *d_loss, void *d_logits, int64_t d_row_stride,
+                                float *loss, void *workspace, size_t ws_bytes, int32_t *status_dev, void *stream);
+
 /*
  * rbq_probe_read -- measurement aid, not a step of the method: one launch that
  * reads `bytes` bytes at `buf` from device memory with 16-byte non-temporal
