@@ -20,7 +20,7 @@ SOURCES = ["api.hip", "encode.hip", "encode_dual.hip", "gemm_valu.hip", "gemm_de
            "gemm_flat.hip", "gemm_group.hip", "gemm_split.hip", "gemm_prefill.hip", "refit.hip",
            "rebin.hip", "gemv_program.hip", "probe.hip", "qat.hip", "tiles.hip",
            "f8.hip", "gemm_f8.hip", "qat_ckpt.hip", "q4.hip", "logits.hip",
-           "distill.hip"]
+           "distill.hip", "gemm_q4.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

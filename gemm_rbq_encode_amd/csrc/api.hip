@@ -805,8 +805,10 @@ rbq_status rbq_encode_q4(const float *W, int32_t out_features, int32_t in_featur
 }
 
 size_t rbq_gemm_q4_workspace_bytes(int32_t out_features, int32_t in_features, int32_t M, uint32_t y_type) {
-    (void)out_features, (void)in_features, (void)M, (void)y_type;
-    return 0;
+    if (M < 1 || !f8_shape_ok(out_features, in_features) || out_features == 0 || in_features == 0 ||
+        q4_too_large(out_features, in_features) || y_type > RBQ_Y_F32)
+        return 0;
+    return rbq::gemm_q4_workspace_bytes(out_features, in_features, M);
 }
 
 rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int32_t out_features,
@@ -840,7 +842,7 @@ rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8
     if ((st = device_present()) != RBQ_OK)
         return st;
     e = rbq::launch_gemm_q4(codes, scales, zeros, out_features, in_features, X, M, Y, y_type == RBQ_Y_F32,
-                            (hipStream_t)stream);
+                            workspace, ws_bytes, (hipStream_t)stream);
     return e == hipSuccess ? RBQ_OK : hip_fail(e);
 }
 

@@ -1,0 +1,256 @@
+// gemm_q4.hip -- the many-token product of a layer in 4 bits with group scales:
+//   Y[m][r] = sum_t s[r][t] sum_{j in group t} (c[r][j] - z[r][t]) X[m][j]
+#include <hip/hip_runtime.h>
+
+#include "rbq.h"
+#include "rbq_kernels.h"
+#include "f8_device.h"
+#include "q4_device.h"
+#include "q4_plan.h"
+
+namespace rbq {
+
+namespace {
+
+__device__ __forceinline__ auto q4_buffer(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
+}
+
+// Where the 16-byte piece q of token m lies among its 16 in LDS.
+__device__ __forceinline__ int q4_place(int q, int m) {
+    return ((q & 3) * 4 + (q >> 2)) ^ m ^ (m & 1) << 1;
+}
+
+template <typename Y>
+__device__ __forceinline__ Y q4_to(float v) {
+    if constexpr (sizeof(Y) == 2)
+        return (Y)f2h(v);
+    else
+        return (Y)v;
+}
+
+// Tiles of 64 WM rows by 64 WN tokens, a wave 64 x 64 of them; a group of 128
+// columns a stage.  The tokens of a stage go through registers, where they are
+// put into the operands' order, to one of two buffers in LDS (256 bytes a token,
+// the 16-byte piece q of token m at q ^ (m & 15), so that 16 tokens' reads of one
+// piece and 16 pieces' writes of one token hit every bank once).  The codes of a
+// wave's rows go straight to its registers, 16 bytes a lane and row tile, and are
+// unpacked there for 64 tokens each.  Both are requested a stage ahead.
+template <int WM, int WN, bool ZEROS, typename Y>
+__global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
+    const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros, int out,
+    int in, int T, const uint16_t *__restrict__ X, int M, Y *__restrict__ y, float *__restrict__ parts, int tiles_m,
+    int tiles_r, int slices) {
+    constexpr int TM = 4, TN = 4, THREADS = WM * WN * 64, RT = WM * 64, CT = WN * 64;
+    constexpr int PIECES = CT * 16 / THREADS;       // 16-byte pieces of X a thread stages
+    __shared__ __align__(16) uint8_t lds[2][CT * 256];
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WM, wc = wave / WM;
+
+    // tiles in bands of 8 token tiles, tokens fastest: the workgroups of an XCD
+    // share tokens and rows
+    int id = xcd_run(blockIdx.x, tiles_m * tiles_r * slices);
+    const int slice = __builtin_amdgcn_readfirstlane(id % slices);
+    id /= slices;
+    const int band = id / (8 * tiles_r), bw = min(8, tiles_m - 8 * band);
+    id -= band * 8 * tiles_r;
+    const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane(id / bw) * RT;
+    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(8 * band + id % bw) * CT;
+    const int t0 = __builtin_amdgcn_readfirstlane(T / slices * slice + min(slice, T % slices));
+    const int t1 = t0 + __builtin_amdgcn_readfirstlane(T / slices + (slice < T % slices));
+
+    // Loads through buffer descriptors of the tile's rows and tokens: what lies
+    // past the last one reads as 0, and the parts of an address that all lanes
+    // share are scalar.
+    const uint32_t rows = (uint32_t)min((int64_t)RT, (int64_t)out - r0), toks = (uint32_t)min((int64_t)CT, (int64_t)M - m0);
+    const auto wbuf = q4_buffer(codes + r0 * (in / 2), rows * (uint32_t)(in / 2));
+    const auto sbuf = q4_buffer(scales + r0 * T, rows * (uint32_t)T * 2u);
+    const auto zbuf = q4_buffer(ZEROS ? zeros + r0 * T : codes, rows * (uint32_t)T);
+    const auto xbuf = q4_buffer(X + m0 * in, toks * (uint32_t)in * 2u);
+    const uint32_t woff = (uint32_t)li * (uint32_t)(in / 2) + g * 16, soff = (uint32_t)li * (uint32_t)T;
+    const uint32_t xoff = (uint32_t)(tid >> 4) * (uint32_t)in * 2u + (tid & 15) * 16;
+    // (a thread's tokens are THREADS / 16 apart, a multiple of 16)
+    const uint32_t xat = (uint32_t)((tid >> 4) * 256 + (q4_place(tid & 15, tid >> 4 & 15) * 16));
+
+    // A group goes through the row tiles one by one: beside the 16 products of row
+    // tile i stand the scaling of the sums of tile i - 1 and the unpacking of tile
+    // i + 1, whose raw codes make room for the next group's.  The tokens' operands
+    // of a group stay in registers and are replaced by the next group's as the last
+    // row tile uses them.
+    const q4_bits bits;
+    uint4 wraw[TM], xraw[PIECES];
+    uint32_t sraw[TM], zraw[TM];
+    float s[2];
+    q4_f16x8 a[TN][4], b[2][4];
+    q4_f32x4 acc[TM][TN] = {}, p[2][TN] = {};
+    auto request_w = [&](int t, int i) __attribute__((always_inline)) {
+        const uint32_t row = (uint32_t)(wr * 64 + i * 16);
+        wraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff, row * (uint32_t)(in / 2) + t * 64, 0));
+        sraw[i] = __builtin_amdgcn_raw_buffer_load_b16(sbuf, soff * 2u, (row * (uint32_t)T + t) * 2u, 0);
+        if (ZEROS)
+            zraw[i] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, soff, row * (uint32_t)T + t, 0);
+    };
+    auto request_x = [&](int t) __attribute__((always_inline)) {
+        const uint32_t at = t * 128 + (tid & 15) * 8 < in ? xoff : 0x80000000u;     // (past a row's end: 0)
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            xraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, (uint32_t)(i * (THREADS / 16)) * (uint32_t)in * 2u + t * 256, 0));
+    };
+    auto stage_x = [&](int buffer) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            *(q4_f16x8 *)(lds[buffer] + xat + i * (THREADS / 16) * 256) = q4_order(xraw[i]);
+    };
+    auto read = [&](int buffer, int n, int j) __attribute__((always_inline)) {
+        a[n][j] = *(const q4_f16x8 *)(lds[buffer] + (wc * 64 + li) * 256 + n * 16 * 256 + q4_place(4 * g + j, li) * 16);
+    };
+    auto unpack = [&](int i) __attribute__((always_inline)) {
+        s[i & 1] = h2f((uint16_t)sraw[i]);
+        asm("" : "+v"(s[i & 1]));       // (converted here, or the raw scale's register would be waited for early)
+        q4_unpack(bits, wraw[i], ZEROS ? zraw[i] : 8, b[i & 1]);
+    };
+    auto scale = [&](int i, float by) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc[i][n][k] = __builtin_fmaf(p[i & 1][n][k], by, acc[i][n][k]);
+    };
+
+    const int last = t1 - 1;
+    if (t0 < t1) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            request_w(t0, i);
+        request_x(t0);
+        stage_x(0);
+        request_x(min(t0 + 1, last));
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                read(0, n, j);
+        unpack(0);
+        request_w(min(t0 + 1, last), 0);
+    }
+    float before = 0.0f;        // the scale of the last row tile of the group before
+    for (int t = t0; t < t1; ++t) {
+        const int next = min(t + 1, last), buffer = (t + 1 - t0) & 1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (i == TM - 1)
+                __syncthreads();
+            const float by = i == 0 ? before : s[(i - 1) & 1];
+            unpack((i + 1) % TM);
+            request_w(i + 1 < TM ? next : min(t + 2, last), (i + 1) % TM);
+            if (i == TM - 2) {
+                stage_x(buffer);
+                request_x(min(t + 2, last));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const q4_f32x4 none = {};
+                    p[i & 1][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[n][j], b[i & 1][j], j == 0 ? none : p[i & 1][n], 0, 0, 0);
+                    if (i == TM - 1)
+                        read(buffer, n, j);
+                }
+            scale((i + TM - 1) % TM, by);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);        // a product,
+                __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);        // other work
+                if (i == TM - 1)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // and a read
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        before = s[(TM - 1) & 1];
+    }
+    scale(TM - 1, before);
+    const bool whole = slices == 1;
+    float *part = parts + (int64_t)slice * M * out;
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t m = m0 + wc * 64 + n * 16 + 4 * g + k;
+            if (m >= M)
+                continue;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int64_t r = r0 + wr * 64 + i * 16 + li;
+                if (r < out) {
+                    if (whole)
+                        y[m * out + r] = q4_to<Y>(acc[i][n][k]);
+                    else
+                        part[m * out + r] = acc[i][n][k];
+                }
+            }
+        }
+}
+
+// Y = the slices' sums, in their order.
+template <typename Y>
+__global__ __launch_bounds__(256) void gemm_q4_sum_kernel(const float *__restrict__ parts, int64_t n, int slices,
+                                                          Y *__restrict__ y) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = parts[i];
+        for (int s = 1; s < slices; ++s)
+            v += parts[s * n + i];
+        y[i] = q4_to<Y>(v);
+    }
+}
+
+template <int WM, int WN, bool ZEROS, typename Y>
+hipError_t launch_tile(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
+                       const uint16_t *X, int M, Y *y, float *parts, int slices, hipStream_t st) {
+    const int tiles_m = (M + WN * 64 - 1) / (WN * 64), tiles_r = (out + WM * 64 - 1) / (WM * 64);
+    gemm_q4_tile_kernel<WM, WN, ZEROS, Y><<<(unsigned)(tiles_m * tiles_r * slices), WM * WN * 64, 0, st>>>(
+        codes, scales, zeros, out, in, (in + 127) / 128, X, M, y, parts, tiles_m, tiles_r, slices);
+    if (slices > 1) {
+        const int64_t n = (int64_t)M * out;
+        gemm_q4_sum_kernel<Y><<<(unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16), 256, 0, st>>>(parts, n, slices, y);
+    }
+    return hipGetLastError();
+}
+
+template <typename Y>
+hipError_t launch_typed(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
+                        const uint16_t *X, int M, Y *y, float *parts, q4_plan p, hipStream_t st) {
+    auto run = [&](auto wm, auto wn) {
+        constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
+        return zeros != nullptr
+                   ? launch_tile<WM, WN, true>(codes, scales, zeros, out, in, X, M, y, parts, p.slices, st)
+                   : launch_tile<WM, WN, false>(codes, scales, zeros, out, in, X, M, y, parts, p.slices, st);
+    };
+    constexpr std::integral_constant<int, 1> one;
+    switch (p.kind) {
+    case Q4_512: return run(std::integral_constant<int, 8>{}, one);
+    default: return run(std::integral_constant<int, 4>{}, one);
+    }
+}
+
+}  // namespace
+
+size_t gemm_q4_workspace_bytes(int out, int in, int M) {
+    if (!q4_tiled(out, in, M))
+        return 0;
+    const q4_plan p = plan_q4(out, in, M);
+    return p.slices > 1 ? (size_t)p.slices * (size_t)M * (size_t)out * sizeof(float) : 0;
+}
+
+hipError_t launch_gemm_q4_tile(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
+                               const uint16_t *X, int M, void *y, int y_f32, void *workspace, size_t ws_bytes,
+                               hipStream_t st) {
+    q4_plan p = plan_q4(out, in, M);
+    if (ws_bytes < gemm_q4_workspace_bytes(out, in, M))
+        p.slices = 1;
+    float *parts = static_cast<float *>(workspace);
+    return y_f32 ? launch_typed(codes, scales, zeros, out, in, X, M, static_cast<float *>(y), parts, p, st)
+                 : launch_typed(codes, scales, zeros, out, in, X, M, static_cast<uint16_t *>(y), parts, p, st);
+}
+
+}  // namespace rbq

@@ -9,6 +9,7 @@
 #include "rbq_device.h"
 #include "rbq_kernels.h"
 #include "q4_device.h"
+#include "q4_plan.h"
 
 namespace rbq {
 
@@ -126,6 +127,7 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
 #pragma unroll
     for (int i = 0; i < MT; ++i)
         x[i] = X + (int64_t)min(m0 + 16 * i + (lane & 15), M - 1) * in + kb * 32;
+    const q4_bits bits;
     q4_f32x4 acc[MT] = {};
     for (int t0 = wave * Q4_AHEAD; t0 < T; t0 += Q4_WAVES * Q4_AHEAD) {
         uint4 raw[Q4_AHEAD];
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
                 break;
             const bool here = t * 128 + kb * 32 < in;
             q4_f16x8 b[4];
-            q4_unpack(raw[i], zp[i], b);
+            q4_unpack(bits, raw[i], zp[i], b);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 q4_f32x4 g = {};
@@ -197,7 +199,10 @@ hipError_t launch_encode_q4(const float *W, int out, int in, uint8_t *codes, uin
 }
 
 hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
-                          const uint16_t *X, int M, void *Y, int y_f32, hipStream_t st) {
+                          const uint16_t *X, int M, void *Y, int y_f32, void *workspace, size_t ws_bytes,
+                          hipStream_t st) {
+    if (q4_tiled(out, in, M))
+        return launch_gemm_q4_tile(codes, scales, zeros, out, in, X, M, Y, y_f32, workspace, ws_bytes, st);
     const int T = (in + 127) / 128;
     auto run = [&](auto mt, auto wide, auto zero) {
         constexpr int MT = decltype(mt)::value;

@@ -19,18 +19,25 @@ typedef float q4_f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ q4_f16x2 q4_pair(uint32_t v) { return __builtin_bit_cast(q4_f16x2, v); }
 
+// The bits and exponents in registers: as literals they would make two
+// instructions of every and-or.
+struct q4_bits {
+    uint32_t low = 0x000F000Fu, high = 0x00F000F0u, e1024 = 0x64006400u, e64 = 0x54005400u;
+    __device__ __forceinline__ q4_bits() { asm("" : "+s"(low), "+s"(high), "+v"(e1024), "+v"(e64)); }
+};
+
 // Codes of 32 columns with zero point z -> four operands of 8 columns.
-__device__ __forceinline__ void q4_unpack(uint4 raw, int z, q4_f16x8 (&b)[4]) {
-    const _Float16 high = (_Float16)(-(float)(1024 + z)), low = (_Float16)(-(float)(64 + z));
-    const q4_f16x2 h = {high, high}, l = {low, low};
+__device__ __forceinline__ void q4_unpack(const q4_bits &k, uint4 raw, uint32_t z, q4_f16x8 (&b)[4]) {
+    // -(1024 + z) and -(64 + z): their last places are 1 and 1/16
+    const q4_f16x2 f = q4_pair(0xE400E400u + (z & 15) * 0x10001u), n = q4_pair(0xD400D400u + (z & 15) * 0x100010u);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t u = w[i] >> 8;
-        const q4_f16x2 p0 = q4_pair((w[i] & 0x000F000Fu) | 0x64006400u) + h;
-        const q4_f16x2 p1 = q4_pair((w[i] & 0x00F000F0u) | 0x54005400u) + l;
-        const q4_f16x2 p2 = q4_pair((u & 0x000F000Fu) | 0x64006400u) + h;
-        const q4_f16x2 p3 = q4_pair((u & 0x00F000F0u) | 0x54005400u) + l;
+        const q4_f16x2 p0 = q4_pair((w[i] & k.low) | k.e1024) + f;
+        const q4_f16x2 p1 = q4_pair((w[i] & k.high) | k.e64) + n;
+        const q4_f16x2 p2 = q4_pair((u & k.low) | k.e1024) + f;
+        const q4_f16x2 p3 = q4_pair((u & k.high) | k.e64) + n;
         b[i] = q4_f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
     }
 }

@@ -144,8 +144,14 @@ hipError_t launch_gemv_f8(const uint8_t *W, const float *ws, int out, int in, co
 // null (symmetric).
 hipError_t launch_encode_q4(const float *W, int out, int in, uint8_t *codes, uint16_t *scales, uint8_t *zeros,
                             int32_t *status, hipStream_t st);
+size_t gemm_q4_workspace_bytes(int out, int in, int M);
 hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
-                          const uint16_t *X, int M, void *Y, int y_f32, hipStream_t st);
+                          const uint16_t *X, int M, void *Y, int y_f32, void *workspace, size_t ws_bytes,
+                          hipStream_t st);
+// More tokens than the few-token kernel takes (gemm_q4.hip; q4_plan.h).
+hipError_t launch_gemm_q4_tile(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
+                               const uint16_t *X, int M, void *y, int y_f32, void *workspace, size_t ws_bytes,
+                               hipStream_t st);
 
 // Operators on rows of logits (logits.hip); M, V >= 1, strides in entries.
 hipError_t launch_token_logprobs(const void *x, uint32_t type, int M, int V, int64_t stride, float temperature,

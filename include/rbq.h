@@ -779,7 +779,8 @@ rbq_status rbq_gemv_f8(const uint8_t *codes, const float *scales, int32_t out_fe
  *           its low four bits and column 2b + 1 in its high ones
  *   scales  binary16 bits [out][T], T = ceil(in / 128): one per row and group of
  *           128 consecutive columns, the last group shorter where in % 128 != 0
- *   zeros   uint8 [out][T], the groups' zero points, or NULL: all 8
+ *   zeros   uint8 [out][T], the groups' zero points (the low four bits count),
+ *           or NULL: all 8
  * A weight is w^ = (code - zero) scale.  in_features is a multiple of 32; more
  * than RBQ_Q4_MAX_FEATURES rows or columns, or 2^31 groups and more, are
  * RBQ_ERR_UNSUPPORTED.  What a call writes may not overlap anything else it is
