@@ -856,7 +856,7 @@ static rbq_status logits_check(const void *logits, uint32_t type, int32_t M, int
                                const int32_t *status_dev, bool *done) {
     *done = false;
     if (type > RBQ_L_BF16 || M < 0 || vocab < 1 || row_stride < vocab || entries < 0 ||
-        !(temperature >= 1e-6f && temperature <= 1e6f) || (ws_bytes > 0 && workspace == nullptr))
+        !(temperature >= 1e-3f && temperature <= 1e3f) || (ws_bytes > 0 && workspace == nullptr))
         return RBQ_ERR_INVALID_ARG;
     if (vocab > RBQ_VOCAB_MAX || entries > RBQ_TOP_MAX || row_stride > ((int64_t)1 << 31))
         return RBQ_ERR_UNSUPPORTED;

@@ -50,15 +50,68 @@ __device__ __forceinline__ double lg_block_sum(double v, double (*red)[2], int w
     return t;
 }
 
-// mode 0: a whole row per workgroup; 1: the sums of a slice; 2: what follows
-// from the slices' sums.  GRAD: the gradient of a slice is written (modes 0, 2).
-template <typename T, int KIND, bool GRAD>
-__global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_distill_args p, int mode) {
-    __shared__ float4 part[LG_SLICES_MAX];
+// The workgroup's sums over a slice; the bits of the named tokens in it are set
+// in `map`, a chunk of LG_MAP vectors at a time.
+template <typename T, int KIND, bool QUICK>
+__device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const lg_range &r, const lg_slots &sl,
+                                               int slots, float c, uint32_t *map, float4 *part) {
+    const int tid = threadIdx.x;
+    lg_sums<QUICK> s;
+    float best;
+    int where;
+    if constexpr (KIND == LG_NAMED) {
+        for (int v0 = r.v0; v0 < r.v1; v0 += LG_MAP) {
+            lg_range q = r;
+            q.v0 = v0;
+            q.v1 = min(r.v1, v0 + LG_MAP);
+            for (int i = tid; i < (q.v1 - q.v0 + 3) / 4; i += LG_THREADS)
+                map[i] = 0;
+            __syncthreads();
+            if (tid < slots) {
+                const int i = sl.index[tid];
+                const int bit = i - q.v0 * LG_VEC;
+                if (i >= 0 && bit >= 0 && i / LG_VEC < q.v1)
+                    atomicOr(&map[bit >> 5], 1u << (bit & 31));
+            }
+            __syncthreads();
+            lg_walk<T, 0> walk(x, q);
+            lg_stream<T, KIND, false>(walk, c, (const uint8_t *)map, q.v0, s, best, where);
+            __syncthreads();
+        }
+    } else {
+        lg_walk<T, 0> walk(x, r);
+        lg_stream<T, KIND, false>(walk, c, nullptr, 0, s, best, where);
+    }
+    const lg_sums<QUICK> t = lg_join_block<KIND>(s, c, part);
+    if constexpr (QUICK)
+        if (!lg_good(t))
+            return {t.m, __builtin_nanf(""), 0.0f, true};
+    return lg_row_of(t);
+}
+
+// dx = e w of a slice.
+template <typename T, bool QUICK>
+__device__ __forceinline__ void distill_write(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
+                                              float m, float c, float w) {
+    lg_walk<T, 0> walk(x, r);
+    walk.down(dx, [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LG_VEC; ++i)
+            e[i] = __builtin_amdgcn_exp2f(lg_exponent<QUICK>(e[i], m, c)) * w;
+    });
+}
+
+// WHOLE: a row per workgroup; SUMS: the sums of a slice; REST: what follows from
+// the slices' sums.  GRAD: the gradient of a slice is written (WHOLE, REST).
+enum { DS_WHOLE = 0, DS_SUMS = 1, DS_REST = 2 };
+
+template <typename T, int KIND, int MODE, bool GRAD>
+__global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_distill_args p) {
+    __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : LG_WAVES];
     __shared__ lg_slots sl;
     extern __shared__ uint32_t map[];
     const int tid = threadIdx.x;
-    const int per_row = mode == 2 && !GRAD ? 1 : a.slices;
+    const int per_row = MODE == DS_REST && !GRAD ? 1 : a.slices;
     for (int64_t u = blockIdx.x; u < (int64_t)a.M * per_row; u += gridDim.x) {
         const int row = (int)(u / per_row), slice = (int)(u - (int64_t)row * per_row);
         const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
@@ -83,9 +136,9 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
                 sl.any = 1;
                 // (x may be the gradient's buffer: the slices keep the logits beside their sums)
                 float *kept = a.named + (int64_t)row * p.slots + tid;
-                if (mode == 0)
+                if (MODE == DS_WHOLE)
                     sl.x[tid] = T::one(x[i]);
-                else if (mode == 2)
+                else if (MODE == DS_REST)
                     sl.x[tid] = *kept;
                 else if (i / LG_VEC >= r.v0 && i / LG_VEC < r.v1)
                     *kept = T::one(x[i]);
@@ -94,52 +147,29 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
         }
         __syncthreads();
         // the row's sums
-        lg_sums t;
-        if (mode == 2) {
+        lg_row t;
+        if constexpr (MODE == DS_REST) {
             for (int i = tid; i < a.slices; i += LG_THREADS)
                 part[i] = a.sums[(int64_t)row * a.slices + i];
             __syncthreads();
-            t = lg_join_slices<KIND>(part, a.slices, a.c);
-        } else {
-            lg_sums s;
-            float best;
-            int where;
-            if constexpr (KIND == LG_NAMED) {
-                for (int v0 = r.v0; v0 < r.v1; v0 += LG_MAP) {
-                    lg_range q = r;
-                    q.v0 = v0;
-                    q.v1 = min(r.v1, v0 + LG_MAP);
-                    for (int i = tid; i < (q.v1 - q.v0 + 3) / 4; i += LG_THREADS)
-                        map[i] = 0;
-                    __syncthreads();
-                    if (tid < p.slots) {
-                        const int i = sl.index[tid];
-                        const int bit = i - q.v0 * LG_VEC;
-                        if (i >= 0 && bit >= 0 && i / LG_VEC < q.v1)
-                            atomicOr(&map[bit >> 5], 1u << (bit & 31));
-                    }
-                    __syncthreads();
-                    lg_stream<T, KIND, false>(x, q, a.c, (const uint8_t *)map, s, best, where);
-                    __syncthreads();
-                }
-            } else {
-                lg_stream<T, KIND, false>(x, r, a.c, nullptr, s, best, where);
-            }
-            t = lg_join_block<KIND>(s, a.c, part);
-        }
-        if (mode == 1) {
+            t = lg_row_of(lg_join_list<KIND, false>(part, a.slices, a.c));
+        } else if constexpr (MODE == DS_SUMS) {
+            t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
             if (tid == 0)
-                a.sums[u] = make_float4(t.m, t.a, t.b, 0.0f);
+                a.sums[u] = make_float4(t.m, t.S, t.b, 0.0f);
             __syncthreads();
             continue;
+        } else {
+            t = distill_sums<T, KIND, true>(x, r, sl, p.slots, a.c, map, part);
+            if (t.S != t.S) {
+                __syncthreads();
+                t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
+            }
         }
         // the teacher's side
         double top = 0.0;
         if (KIND != LG_NAMED) {     // normalised over the slots: relative to the largest
-            float big = (float)lp;
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1)
-                big = fmaxf(big, __shfl_xor(big, o));
+            const float big = lg_wave_max((float)lp);
             if ((tid & 63) == 0)
                 sl.red[tid >> 6][0] = big;
             __syncthreads();
@@ -163,16 +193,16 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
             rest = rest > 0.0 ? rest : rest != rest ? rest : 0.0;
         }
         // the student's side, the loss
-        const double S = KIND == LG_NAMED ? (double)t.a + (double)t.b : (double)t.a;
-        const double logS = log(S), c = (double)a.c * 0.6931471805599453;
+        const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
+        const double logS = log(S), c = (double)a.c;
         double term = 0.0;
-        if (used && pj != 0.0)
-            term = pj * (lpj - (S == 0.0 ? -__builtin_inf() : ((double)sl.x[tid] - (double)t.m) * c - logS));
+        if (used && pj != 0.0) {
+            const double xj = sl.x[tid], m = t.m, d = t.quick ? xj * c - m : (xj - m) * c;
+            term = pj * (lpj - (S == 0.0 ? -__builtin_inf() : d * 0.6931471805599453 - logS));
+        }
         double loss = lg_block_sum(term, sl.red, 1);
         if (KIND == LG_NAMED && rest != 0.0)
-            loss += rest * (log(rest) - (log((double)t.a) - logS));
-        if (KIND == LG_NAMED && rest != 0.0 && S == 0.0)
-            loss = __builtin_inf();
+            loss = S == 0.0 ? __builtin_inf() : loss + rest * (log(rest) - (log((double)t.S) - logS));
         if (sl.bad)
             loss = __builtin_nan("");
         if (tid == 0 && slice == 0 && p.loss != nullptr)
@@ -185,25 +215,21 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
             } else {
                 const double by = sl.bad ? __builtin_nan("") : (double)d * (double)a.inv_t;
                 const double all = by * (P + rest) / S;         // per e of a named token
-                const double away = KIND == LG_NAMED && rest != 0.0 && t.a != 0.0f ? by * rest / (double)t.a : 0.0;
-                const float w = (float)(all - away);
-                const float m = t.m, cc = a.c;
+                const double away = KIND == LG_NAMED && rest != 0.0 && t.S != 0.0f ? by * rest / (double)t.S : 0.0;
                 if (used)
                     sl.p[tid] = pj;
                 __syncthreads();    // every slot's logit has been read: dx may be x
-                auto f = [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int i = 0; i < LG_VEC; ++i)
-                        e[i] = __builtin_amdgcn_exp2f((e[i] - m) * cc) * w;
-                };
-                lg_map<T>(x, dx, r, f);
+                if (MODE == DS_WHOLE && t.quick)
+                    distill_write<T, true>(x, dx, r, t.m, a.c, (float)(all - away));
+                else
+                    distill_write<T, false>(x, dx, r, t.m, a.c, (float)(all - away));
                 __syncthreads();    // then the named tokens, each thread a slot; a token named twice gets both in each
                 if (used && sl.index[tid] / LG_VEC >= r.v0 && sl.index[tid] / LG_VEC < r.v1) {
                     const int i = sl.index[tid];
                     double mine = 0.0;
                     for (int j = 0; j < p.slots; ++j)
                         mine += sl.index[j] == i ? sl.p[j] : 0.0;
-                    const double e = exp(((double)sl.x[tid] - (double)m) * c);
+                    const double e = __builtin_amdgcn_exp2f(t.exponent(sl.x[tid], a.c));
                     dx[i] = T::of((float)(e * all - by * mine));
                 }
             }
@@ -218,10 +244,10 @@ hipError_t distill_of(lg_row_args a, const lg_distill_args &p, hipStream_t st) {
     const int vectors = (a.V + LG_VEC - 1) / LG_VEC, each = (vectors + a.slices - 1) / a.slices;
     const size_t map = KIND == LG_NAMED ? (size_t)((each < LG_MAP ? each : LG_MAP) + 3) / 4 * 4 : 0;
     if (a.slices == 1) {
-        distill_kernel<T, KIND, GRAD><<<grid, LG_THREADS, map, st>>>(a, p, 0);
+        distill_kernel<T, KIND, DS_WHOLE, GRAD><<<grid, LG_THREADS, map, st>>>(a, p);
     } else {
-        distill_kernel<T, KIND, false><<<grid, LG_THREADS, map, st>>>(a, p, 1);
-        distill_kernel<T, KIND, GRAD><<<GRAD ? grid : rows, LG_THREADS, 0, st>>>(a, p, 2);
+        distill_kernel<T, KIND, DS_SUMS, false><<<grid, LG_THREADS, map, st>>>(a, p);
+        distill_kernel<T, KIND, DS_REST, GRAD><<<GRAD ? grid : rows, LG_THREADS, 0, st>>>(a, p);
     }
     return hipGetLastError();
 }

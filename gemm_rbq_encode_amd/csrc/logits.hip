@@ -83,33 +83,28 @@ struct lg_logp_args {
     int64_t d_stride;
 };
 
-// What the sums of a row say.
-struct lg_row {
-    float m, logS, H, S;    // log2 S; entropy in nats
+// A row's sums and what follows from them.
+struct lg_logp_row : lg_row {
+    float logS, H;          // log2 S; entropy in nats
     bool empty;             // no entry above -inf
+    __device__ __forceinline__ lg_logp_row(const lg_row &r) : lg_row(r) {
+        empty = S == 0.0f;
+        logS = log2f(S);
+        H = empty ? 0.0f : fmaxf(logS - b / S, 0.0f) * LN2;
+        if (S != S)
+            H = S;
+    }
+    // (The lowest values a mask may use have infinite exponents, and log
+    // probabilities that are finite.)
+    __device__ __forceinline__ float logp(float v, float c, float inv_t) const {
+        const float d = exponent(v, c);
+        return d >= LG_LOWEST ? (d - logS) * LN2 : quick ? v * inv_t : __builtin_fmaf(-LN2, logS, (v - m) * inv_t);
+    }
 };
-
-__device__ __forceinline__ lg_row lg_row_of(const lg_sums &t) {
-    lg_row r;
-    r.m = t.m;
-    r.S = t.a;
-    r.empty = t.a == 0.0f;
-    r.logS = log2f(t.a);
-    r.H = r.empty ? 0.0f : fmaxf(r.logS - t.b / t.a, 0.0f) * LN2;
-    if (t.a != t.a)
-        r.H = t.a;
-    return r;
-}
-
-// (Not ln 2 times the exponent: that is infinite for the lowest values a mask may
-// use, whose log probability is finite.)
-__device__ __forceinline__ float lg_logp(const lg_row &r, float v, float inv_t) {
-    return __builtin_fmaf(-LN2, r.logS, (v - r.m) * inv_t);
-}
 
 // The log probability of a row's target with logit v: 0 for none (negative), NaN
 // for one beyond the vocabulary.
-__device__ __forceinline__ float lg_target(const lg_row &r, float v, int64_t target, const lg_row_args &a) {
+__device__ __forceinline__ float lg_target(const lg_logp_row &r, float v, int64_t target, const lg_row_args &a) {
     if (target < 0)
         return 0.0f;
     if (target >= a.V) {
@@ -117,13 +112,13 @@ __device__ __forceinline__ float lg_target(const lg_row &r, float v, int64_t tar
             atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
         return __builtin_nanf("");
     }
-    return r.empty ? -__builtin_inff() : lg_logp(r, v, a.inv_t);
+    return r.empty ? -__builtin_inff() : r.logp(v, a.c, a.inv_t);
 }
 
 // What thread 0 writes of a row.  The target's logit is found in the row, or,
 // where rows are cut, beside the sums of the slice that holds it: x may be the
 // gradient's buffer, which other slices' workgroups are writing by then.
-__device__ __forceinline__ void lg_write_logp(const lg_row &r, float v, int64_t target, int row, const lg_row_args &a,
+__device__ __forceinline__ void lg_write_logp(const lg_logp_row &r, float v, int64_t target, int row, const lg_row_args &a,
                                               const lg_logp_args &p) {
     if (p.logp != nullptr)
         p.logp[row] = lg_target(r, v, target, a);
@@ -135,20 +130,39 @@ __device__ __forceinline__ float lg_kept(const float4 *part, int64_t target, con
     return lg_inside(target, a.V) ? part[(int)target / LG_VEC / lg_each(a.V, a.slices)].w : 0.0f;
 }
 
-__device__ __forceinline__ void lg_write_top(const lg_row &r, const uint64_t *list, int row, float inv_t,
+__device__ __forceinline__ void lg_write_top(const lg_logp_row &r, const uint64_t *list, int row, float c, float inv_t,
                                              const lg_logp_args &p) {
     for (int j = threadIdx.x; j < p.top; j += blockDim.x) {
         const uint64_t key = list[j];
         const bool broken = r.S != r.S;
         p.top_logp[(int64_t)row * p.top + j] = broken   ? r.S
                                                : key == 0 ? -__builtin_inff()
-                                                          : lg_logp(r, lg_value(key), inv_t);
+                                                          : r.logp(lg_value(key), c, inv_t);
         p.top_index[(int64_t)row * p.top + j] = broken || key == 0 ? -1 : lg_index(key);
     }
 }
 
-// One slice of a row per workgroup: sums and largest entries.  E = 0: none.
-template <typename T, int E>
+// The sums of a whole row: quickly, and once more where that was not good.
+template <typename T, bool TOP, int KEEP>
+__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T, KEEP> &walk, float c, float4 *part, float &best, int &where) {
+    {
+        lg_sums<true> s;
+        lg_stream<T, LG_ENTROPY, TOP>(walk, c, nullptr, 0, s, best, where);
+        const lg_sums<true> t = lg_join_block<LG_ENTROPY>(s, c, part);
+        if (lg_good(t))
+            return lg_row_of(t);
+    }
+    __syncthreads();
+    lg_sums<false> s;
+    float b2;
+    int w2;
+    lg_stream<T, LG_ENTROPY, false>(walk, c, nullptr, 0, s, b2, w2);
+    return lg_row_of(lg_join_block<LG_ENTROPY>(s, c, part));
+}
+
+// The sums of a slice per workgroup (SLICED), or a whole row, and its largest
+// entries.  E = 0: none.
+template <typename T, int E, bool SLICED>
 __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_logp_args p) {
     constexpr int N = LG_WAVES * 64 * (E > 0 ? E : 1);
     __shared__ float4 part[LG_WAVES];
@@ -158,28 +172,34 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_
         const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
         const lg_range r = lg_slice(a.V, a.slices, slice);
         const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
-        lg_sums s;
         float best = -__builtin_inff();
         int where = 0;
-        lg_stream<T, LG_ENTROPY, (E > 0)>(x, r, a.c, nullptr, s, best, where);
+        lg_walk<T, 0> walk(x, r);
+        lg_row sums;
+        if constexpr (SLICED) {
+            lg_sums<false> s;
+            lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, 0, s, best, where);
+            sums = lg_row_of(lg_join_block<LG_ENTROPY>(s, a.c, part));
+        } else {
+            sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where);
+        }
         if constexpr (E > 0)
             lg_select<T, E>(x, r, p.top, best, where, lists, waiting);
-        const lg_sums t = lg_join_block<LG_ENTROPY>(s, a.c, part);
-        if (a.slices > 1) {
+        if constexpr (SLICED) {
             if (threadIdx.x == 0) {
                 const bool here = lg_inside(target, a.V) && target >= (int64_t)r.v0 * LG_VEC &&
                                   target < (int64_t)r.v1 * LG_VEC;
-                a.sums[u] = make_float4(t.m, t.a, t.b, here ? T::one(x[target]) : 0.0f);
+                a.sums[u] = make_float4(sums.m, sums.S, sums.b, here ? T::one(x[target]) : 0.0f);
             }
             if constexpr (E > 0)
                 for (int j = threadIdx.x; j < p.top; j += LG_THREADS)
                     a.keys[u * p.top + j] = lists[j];
         } else {
-            const lg_row w = lg_row_of(t);
+            const lg_logp_row w(sums);
             if (threadIdx.x == 0)
                 lg_write_logp(w, lg_inside(target, a.V) ? T::one(x[target]) : 0.0f, target, row, a, p);
             if constexpr (E > 0)
-                lg_write_top(w, lists, row, a.inv_t, p);
+                lg_write_top(w, lists, row, a.c, a.inv_t, p);
         }
         __syncthreads();    // before the next unit writes LDS
     }
@@ -215,23 +235,41 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a
             lg_block_merge<E, LG_WAVES>(best, lists);
         }
         __syncthreads();
-        const lg_row w = lg_row_of(lg_join_slices<LG_ENTROPY>(part, a.slices, a.c));
+        const lg_logp_row w(lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c)));
         if (threadIdx.x == 0) {
             const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
             lg_write_logp(w, lg_kept(part, target, a), target, row, a, p);
         }
         if constexpr (E > 0)
-            lg_write_top(w, lists, row, a.inv_t, p);
+            lg_write_top(w, lists, row, a.c, a.inv_t, p);
         __syncthreads();
     }
 }
 
 // The gradient of sum_m a_m logp_m + b_m H_m:
 //   dx_v = (a ([v = target] - p_v) - b p_v (ln p_v + H)) / T
-// with p_v = e_v / S and ln p_v = ln 2 ((x_v - m) c - log2 S), so that the part
-// without the target is e_v (w0 + w1 (x_v - m) c).  With one slice the sums are
-// formed here, and the second pass over the row finds it in the caches.
-template <typename T>
+// with p_v = e_v / S and ln p_v = ln 2 (d_v - log2 S), so that the part without
+// the target is e_v (w0 + w1 d_v).  Where rows are whole the sums are formed here,
+// and the second pass over the row finds it in the caches.
+template <typename T, bool QUICK, bool ENTROPY, int KEEP>
+__device__ __forceinline__ void lg_logp_grad(lg_walk<T, KEEP> &walk, typename T::bits *dx, float m, float c, float w0,
+                                             float w1, int at, int in, float own) {
+    walk.down(dx, [&](float(&e)[LG_VEC], int v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LG_VEC; ++i) {
+            const float d = lg_exponent<QUICK>(e[i], m, c);
+            const float g = __builtin_amdgcn_exp2f(d);
+            e[i] = ENTROPY ? g * __builtin_fmaf(w1, fmaxf(d, LG_FAR), w0) : g * w0;
+        }
+        if (v == at) {
+#pragma unroll
+            for (int i = 0; i < LG_VEC; ++i)
+                e[i] += i == in ? own : 0.0f;
+        }
+    });
+}
+
+template <typename T, int KEEP, bool SLICED, bool ENTROPY>
 __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
     __shared__ float4 part[LG_SLICES_MAX];
     for (int64_t u = blockIdx.x; u < (int64_t)a.M * a.slices; u += gridDim.x) {
@@ -241,56 +279,46 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a
         const lg_range r = lg_slice(a.V, a.slices, slice);
         const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
         const float wa = p.d_logp == nullptr || target < 0 ? 0.0f : p.d_logp[row];
-        const float wb = p.d_entropy == nullptr ? 0.0f : p.d_entropy[row];
+        const float wb = ENTROPY ? p.d_entropy[row] : 0.0f;
         const bool none = wa == 0.0f && wb == 0.0f;
-        if (!none || p.logp != nullptr || p.entropy != nullptr) {
-            lg_sums t;
-            if (a.slices > 1) {
-                for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
-                    part[i] = a.sums[(int64_t)row * a.slices + i];
-                __syncthreads();
-                t = lg_join_slices<LG_ENTROPY>(part, a.slices, a.c);
-            } else {
-                lg_sums s;
-                float best;
-                int where;
-                lg_stream<T, LG_ENTROPY, false>(x, r, a.c, nullptr, s, best, where);
-                t = lg_join_block<LG_ENTROPY>(s, a.c, part);
-            }
-            const lg_row w = lg_row_of(t);
-            if (slice == 0 && threadIdx.x == 0)
-                lg_write_logp(w,
-                              a.slices > 1                ? lg_kept(part, target, a)
-                              : lg_inside(target, a.V) ? T::one(x[target])
-                                                         : 0.0f,
-                              target, row, a, p);
-            if (!none && !w.empty) {
-                const float scale = a.inv_t / w.S;
-                const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
-                const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
-                const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
-                const float own = wa * a.inv_t;
-                __syncthreads();    // the target's entry has been read: dx may be x
-                auto f = [&](float(&e)[LG_VEC], int v) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int i = 0; i < LG_VEC; ++i) {
-                        const float d = (e[i] - w.m) * a.c;
-                        const float g = __builtin_amdgcn_exp2f(d);
-                        e[i] = wb == 0.0f ? g * w0 : g * __builtin_fmaf(w1, fmaxf(d, LG_FAR), w0);
-                    }
-                    if (v == at) {
-#pragma unroll
-                        for (int i = 0; i < LG_VEC; ++i)
-                            e[i] += i == in ? own : 0.0f;
-                    }
-                };
-                lg_map<T>(x, dx, r, f);
-                __syncthreads();
-                continue;
-            }
-            __syncthreads();
+        if (none && p.logp == nullptr && p.entropy == nullptr) {
+            lg_zero<T>(dx, r);
+            continue;
         }
-        lg_zero<T>(dx, r);
+        lg_walk<T, KEEP> walk(x, r);
+        lg_row sums;
+        if constexpr (SLICED) {
+            for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
+                part[i] = a.sums[(int64_t)row * a.slices + i];
+            __syncthreads();
+            sums = lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c));
+        } else {
+            float best;
+            int where;
+            sums = lg_whole_row<T, false>(walk, a.c, part, best, where);
+        }
+        const lg_logp_row w(sums);
+        if (slice == 0 && threadIdx.x == 0)
+            lg_write_logp(w,
+                          SLICED                      ? lg_kept(part, target, a)
+                          : lg_inside(target, a.V) ? T::one(x[target])
+                                                     : 0.0f,
+                          target, row, a, p);
+        if (none || w.empty) {
+            lg_zero<T>(dx, r);
+        } else {
+            const float scale = a.inv_t / w.S;
+            const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
+            const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
+            const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
+            const float own = wa * a.inv_t;
+            __syncthreads();    // the target's entry has been read: dx may be x
+            if (!SLICED && w.quick)
+                lg_logp_grad<T, true, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
+            else
+                lg_logp_grad<T, false, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
+        }
+        __syncthreads();
     }
 }
 
@@ -299,9 +327,12 @@ hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     const unsigned grid = lg_grid((int64_t)a.M * a.slices), rows = lg_grid(a.M);
     auto run = [&](auto e) {
         constexpr int E = decltype(e)::value;
-        logprobs_kernel<T, E><<<grid, LG_THREADS, 0, st>>>(a, p);
-        if (a.slices > 1)
+        if (a.slices > 1) {
+            logprobs_kernel<T, E, true><<<grid, LG_THREADS, 0, st>>>(a, p);
             logprobs_join_kernel<E><<<rows, LG_THREADS, 0, st>>>(a, p);
+        } else {
+            logprobs_kernel<T, E, false><<<grid, LG_THREADS, 0, st>>>(a, p);
+        }
     };
     if (p.top == 0)
         run(std::integral_constant<int, 0>{});
@@ -315,9 +346,18 @@ hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
 template <typename T>
 hipError_t logprobs_grad_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     const unsigned grid = lg_grid((int64_t)a.M * a.slices);
-    if (a.slices > 1)
-        logprobs_kernel<T, 0><<<grid, LG_THREADS, 0, st>>>(a, p);
-    logprobs_grad_kernel<T><<<grid, LG_THREADS, 0, st>>>(a, p);
+    const bool entropy = p.d_entropy != nullptr;
+    if (a.slices > 1) {
+        logprobs_kernel<T, 0, true><<<grid, LG_THREADS, 0, st>>>(a, p);
+        if (entropy)
+            logprobs_grad_kernel<T, 0, true, true><<<grid, LG_THREADS, 0, st>>>(a, p);
+        else
+            logprobs_grad_kernel<T, 0, true, false><<<grid, LG_THREADS, 0, st>>>(a, p);
+    } else if (entropy) {
+        logprobs_grad_kernel<T, LG_KEEP, false, true><<<grid, LG_THREADS, 0, st>>>(a, p);
+    } else {
+        logprobs_grad_kernel<T, LG_KEEP, false, false><<<grid, LG_THREADS, 0, st>>>(a, p);
+    }
     return hipGetLastError();
 }
 

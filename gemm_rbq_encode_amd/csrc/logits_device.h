@@ -79,9 +79,9 @@ __device__ __forceinline__ void lg_store(typename T::bits *p, const float (&x)[L
             a[i] = (uint32_t)T::of(x[2 * i]) | (uint32_t)T::of(x[2 * i + 1]) << 16;
         }
     }
-    *(lg_u32x4 *)p = a;
+    __builtin_nontemporal_store(a, (lg_u32x4 *)p);
     if constexpr (sizeof(typename T::bits) == 4)
-        *(lg_u32x4 *)(p + 4) = b;
+        __builtin_nontemporal_store(b, (lg_u32x4 *)(p + 4));
 }
 
 // The first n < LG_VEC entries at p, -inf behind them.
@@ -100,27 +100,75 @@ __device__ __forceinline__ void lg_store_part(typename T::bits *p, int n, const 
             p[i] = T::of(x[i]);
 }
 
+// ---- lanes --------------------------------------------------------------------
+//
+// Sums and maxima over a wave by DPP: inside quads, mirrored halves and rows of
+// 16, then row 15 -> next row and lane 31 -> upper half; lane 63 has the whole.
+
+#define LG_DPP(old, v, ctrl, rows) \
+    __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v), ctrl, rows, 0xF, false))
+
+__device__ __forceinline__ float lg_lane63(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ float lg_wave_sum(float v) {
+    v += LG_DPP(0.0f, v, 0xB1, 0xF);
+    v += LG_DPP(0.0f, v, 0x4E, 0xF);
+    v += LG_DPP(0.0f, v, 0x141, 0xF);
+    v += LG_DPP(0.0f, v, 0x140, 0xF);
+    v += LG_DPP(0.0f, v, RBQ_DPP_ROW_BCAST15, 0xA);
+    v += LG_DPP(0.0f, v, RBQ_DPP_ROW_BCAST31, 0xC);
+    return lg_lane63(v);
+}
+__device__ __forceinline__ float lg_wave_max(float v) {
+    v = fmaxf(v, LG_DPP(v, v, 0xB1, 0xF));
+    v = fmaxf(v, LG_DPP(v, v, 0x4E, 0xF));
+    v = fmaxf(v, LG_DPP(v, v, 0x141, 0xF));
+    v = fmaxf(v, LG_DPP(v, v, 0x140, 0xF));
+    v = fmaxf(v, LG_DPP(v, v, RBQ_DPP_ROW_BCAST15, 0xA));
+    v = fmaxf(v, LG_DPP(v, v, RBQ_DPP_ROW_BCAST31, 0xC));
+    return lg_lane63(v);
+}
+
 // ---- running sums ---------------------------------------------------------------
 //
-// e(x) = 2^((x - m) c) with c = log2(e) / T.  m follows the maximum lazily: it
-// moves when an entry lies more than LG_SLACK / c above it, so e is at most
-// 2^LG_SLACK and nothing overflows.  The difference is taken before the product:
-// rows of the type's lowest value have finite differences where products with c
-// would be infinite.
+// e(x) = 2^d relative to a reference that follows the maximum lazily: it moves
+// when an entry lies more than LG_SLACK above it (in the exponent), so e stays
+// small and nothing overflows.  With c = log2(e) / T there are two ways to d:
+//  * QUICK   d = x c - r, one fma, r = the product top c as it was rounded (what
+//            that loses is the same for all entries, and cancels in e / S).  It
+//            starts at -LG_FLOOR and is good for rows whose reference ends within
+//            -LG_FLOOR / 2 .. LG_FLOOR (there the rounding of r is at most 4) and
+//            whose sum is a positive number: lg_good.
+//  * otherwise  d = (x - m) c: the difference first, so that rows of the type's
+//            lowest value have finite exponents where products with c would be
+//            infinite.  Rows that are not good are done once more this way.
 
 constexpr float LG_SLACK = 4.0f;
+constexpr float LG_FLOOR = 67108864.0f;     // 2^26
 
-// Kinds of the two sums: of e and of e (x - m) c; of e alone; of e over the
-// entries whose bit of a map is clear and over those whose bit is set.
+// Kinds of the two sums: of e and of e d; of e alone; of e over the entries
+// whose bit of a map is clear and over those whose bit is set.
 enum { LG_ENTROPY = 0, LG_PLAIN = 1, LG_NAMED = 2 };
 
+template <bool QUICK>
 struct lg_sums {
-    float m = LG_LOWEST, a = 0.0f, b = 0.0f;
+    float m = QUICK ? -LG_FLOOR : LG_LOWEST, a = 0.0f, b = 0.0f;
 };
 
-template <int KIND>
-__device__ __forceinline__ void lg_move(lg_sums &s, float m, float c) {
-    const float d = fmaxf((s.m - m) * c, LG_FAR);
+template <bool QUICK>
+__device__ __forceinline__ float lg_exponent(float x, float m, float c) {
+    return QUICK ? __builtin_fmaf(x, c, -m) : (x - m) * c;
+}
+
+__device__ __forceinline__ bool lg_good(const lg_sums<true> &s) {
+    const float all = s.a + __builtin_fabsf(s.b);      // (the second sum is no less than -1 of the first's logarithm)
+    return s.m > -0.5f * LG_FLOOR && s.m < LG_FLOOR && all > 0.0f && all < __builtin_inff();
+}
+
+template <int KIND, bool QUICK>
+__device__ __forceinline__ void lg_move(lg_sums<QUICK> &s, float m, float c) {
+    const float d = fmaxf(QUICK ? s.m - m : (s.m - m) * c, LG_FAR);
     const float f = __builtin_amdgcn_exp2f(d);
     if constexpr (KIND == LG_ENTROPY)
         s.b = f * __builtin_fmaf(s.a, d, s.b);
@@ -130,18 +178,21 @@ __device__ __forceinline__ void lg_move(lg_sums &s, float m, float c) {
     s.m = m;
 }
 
-template <int KIND>
-__device__ __forceinline__ float lg_add(lg_sums &s, const float (&x)[LG_VEC], float c, float slack, uint32_t named) {
-    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (__any(top > s.m + slack)) {
-        if (top > s.m + slack)
-            lg_move<KIND>(s, top, c);
+// `slack`: LG_SLACK in the reference's unit.
+template <int KIND, bool QUICK>
+__device__ __forceinline__ float lg_add(lg_sums<QUICK> &s, const float (&x)[LG_VEC], float c, float slack,
+                                        uint32_t named) {
+    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    const float at = QUICK ? top * c : top;
+    if (__any(at > s.m + slack)) {
+        if (at > s.m + slack)
+            lg_move<KIND>(s, at, c);
     }
     if constexpr (KIND == LG_NAMED) {
         if (__any(named != 0)) {
 #pragma unroll
             for (int i = 0; i < LG_VEC; ++i) {
-                const float e = __builtin_amdgcn_exp2f((x[i] - s.m) * c);
+                const float e = __builtin_amdgcn_exp2f(lg_exponent<QUICK>(x[i], s.m, c));
                 const bool in = named >> i & 1;
                 s.a += in ? 0.0f : e;
                 s.b += in ? e : 0.0f;
@@ -151,7 +202,7 @@ __device__ __forceinline__ float lg_add(lg_sums &s, const float (&x)[LG_VEC], fl
     }
 #pragma unroll
     for (int i = 0; i < LG_VEC; ++i) {
-        const float d = (x[i] - s.m) * c;
+        const float d = lg_exponent<QUICK>(x[i], s.m, c);
         const float e = __builtin_amdgcn_exp2f(d);
         s.a += e;
         if constexpr (KIND == LG_ENTROPY)
@@ -162,25 +213,21 @@ __device__ __forceinline__ float lg_add(lg_sums &s, const float (&x)[LG_VEC], fl
 
 // All lanes' sums (in every lane).  An infinite entry makes m infinite and a
 // NaN; fmaxf passes NaN by, the sums keep it.
-template <int KIND>
-__device__ __forceinline__ lg_sums lg_join_wave(lg_sums s, float c) {
-    float m = s.m;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor(m, o));
-    lg_move<KIND>(s, m, c);
-    s.a = wave_sum_f32(s.a);
+template <int KIND, bool QUICK>
+__device__ __forceinline__ lg_sums<QUICK> lg_join_wave(lg_sums<QUICK> s, float c) {
+    lg_move<KIND>(s, lg_wave_max(s.m), c);
+    s.a = lg_wave_sum(s.a);
     if constexpr (KIND != LG_PLAIN)
-        s.b = wave_sum_f32(s.b);
+        s.b = lg_wave_sum(s.b);
     return s;
 }
 
-// The sums of a row's slices joined, by every wave for itself.
-template <int KIND>
-__device__ __forceinline__ lg_sums lg_join_slices(const float4 *v, int n, float c) {
-    lg_sums t;
+// n sums joined, by every wave for itself.
+template <int KIND, bool QUICK>
+__device__ __forceinline__ lg_sums<QUICK> lg_join_list(const float4 *v, int n, float c) {
+    lg_sums<QUICK> t;
     for (int i = threadIdx.x & 63; i < n; i += 64) {
-        lg_sums s;
+        lg_sums<QUICK> s;
         s.m = v[i].x, s.a = v[i].y, s.b = v[i].z;
         const float m = fmaxf(s.m, t.m);
         lg_move<KIND>(s, m, c);
@@ -191,30 +238,14 @@ __device__ __forceinline__ lg_sums lg_join_slices(const float4 *v, int n, float 
     return lg_join_wave<KIND>(t, c);
 }
 
-// n sums joined in their order.
-template <int KIND>
-__device__ __forceinline__ lg_sums lg_join_list(const float4 *v, int n, float c) {
-    lg_sums t;
-    for (int i = 0; i < n; ++i)
-        t.m = fmaxf(t.m, v[i].x);
-    for (int i = 0; i < n; ++i) {
-        lg_sums s;
-        s.m = v[i].x, s.a = v[i].y, s.b = v[i].z;
-        lg_move<KIND>(s, t.m, c);
-        t.a += s.a;
-        t.b += s.b;
-    }
-    return t;
-}
-
 // All threads' sums (in every thread); `part` holds one float4 per wave.
-template <int KIND>
-__device__ __forceinline__ lg_sums lg_join_block(const lg_sums &s, float c, float4 *part) {
-    const lg_sums w = lg_join_wave<KIND>(s, c);
+template <int KIND, bool QUICK>
+__device__ __forceinline__ lg_sums<QUICK> lg_join_block(const lg_sums<QUICK> &s, float c, float4 *part) {
+    const lg_sums<QUICK> w = lg_join_wave<KIND>(s, c);
     if ((threadIdx.x & 63) == 0)
         part[threadIdx.x >> 6] = make_float4(w.m, w.a, w.b, 0.0f);
     __syncthreads();
-    return lg_join_list<KIND>(part, LG_WAVES, c);
+    return lg_join_list<KIND, QUICK>(part, LG_WAVES, c);
 }
 
 // ---- the largest entries ----------------------------------------------------------
@@ -394,82 +425,156 @@ __device__ __forceinline__ lg_range lg_slice(int V, int slices, int s) {
     return r;
 }
 
-// The thread's sums over its vectors of [v0, v1), and, with TOP, its largest
-// entry and the first vector that holds it.  `map` (LG_NAMED): a byte per
-// vector from v0 on.
-template <typename T, int KIND, bool TOP>
-__device__ __forceinline__ void lg_stream(const typename T::bits *x, const lg_range &r, float c, const uint8_t *map,
-                                          lg_sums &s, float &best, int &where) {
-    const float slack = LG_SLACK / c;
-    const int end = min(r.v1, r.whole);
-    int v = r.v0 + (int)threadIdx.x;
-    constexpr int AHEAD = 4;
-    auto take = [&](const float(&e)[LG_VEC], int at) __attribute__((always_inline)) {
+// A thread's vectors of a slice: those of `turns` whole turns of the workgroup,
+// one more where `more`, and the row's last one, part empty, where `part`.  The
+// last KEEP of the whole turns can stay in registers between two passes.
+template <typename T, int KEEP>
+struct lg_walk {
+    static constexpr int AHEAD = 4;
+    const typename T::bits *x;
+    int v, turns, loose, rest;      // first vector; loose: turns that are not kept
+    bool more, part;
+    typename T::raw kept[KEEP > 0 ? KEEP : 1];
+
+    __device__ __forceinline__ lg_walk(const typename T::bits *row, const lg_range &r) : x(row) {
+        const int end = min(r.v1, r.whole);
+        v = r.v0 + (int)threadIdx.x;
+        turns = max(0, end - r.v0) / LG_THREADS;
+        loose = max(0, turns - KEEP);
+        const int last = v + turns * LG_THREADS;
+        more = last < end;
+        part = (more ? last + LG_THREADS : last) == r.whole && r.v1 > r.whole;
+        rest = r.rest;
+    }
+    __device__ __forceinline__ const typename T::bits *at(int turn) const {
+        return x + (int64_t)(v + turn * LG_THREADS) * LG_VEC;
+    }
+    // f(values, vector) of all, upwards
+    template <typename F>
+    __device__ __forceinline__ void up(F f) {
+        int t = 0;
+        for (; t + AHEAD <= loose; t += AHEAD) {
+            typename T::raw raw[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                raw[i] = lg_load<T>(at(t + i));
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                float e[LG_VEC];
+                lg_values<T>(raw[i], e);
+                f(e, v + (t + i) * LG_THREADS);
+            }
+        }
+        for (; t < loose; ++t)
+            one(t, f);
+        if constexpr (KEEP > 0) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (loose + i < turns)
+                    kept[i] = lg_load<T>(at(loose + i));
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (loose + i < turns) {
+                    float e[LG_VEC];
+                    lg_values<T>(kept[i], e);
+                    f(e, v + (loose + i) * LG_THREADS);
+                }
+        }
+        if (more)
+            one(turns, f);
+        if (part) {
+            float e[LG_VEC];
+            lg_load_part<T>(at(turns + more), rest, e);
+            f(e, v + (turns + more) * LG_THREADS);
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void one(int t, F f) {
+        float e[LG_VEC];
+        lg_values<T>(lg_load<T>(at(t)), e);
+        f(e, v + t * LG_THREADS);
+    }
+    // out = f(values, vector) of all, downwards: what was read last is still in
+    // the caches.  A thread writes what it has read itself, so `out` may be x.
+    // The stores leave the caches to what will be read again.
+    template <typename F>
+    __device__ __forceinline__ void down(typename T::bits *out, F f) {
+        if (part) {
+            float e[LG_VEC];
+            const int64_t at_ = (int64_t)(v + (turns + more) * LG_THREADS) * LG_VEC;
+            lg_load_part<T>(x + at_, rest, e);
+            f(e, v + (turns + more) * LG_THREADS);
+            lg_store_part<T>(out + at_, rest, e);
+        }
+        if (more)
+            back(out, turns, f);
+        if constexpr (KEEP > 0) {
+#pragma unroll
+            for (int i = KEEP - 1; i >= 0; --i)
+                if (loose + i < turns) {
+                    float e[LG_VEC];
+                    lg_values<T>(kept[i], e);
+                    f(e, v + (loose + i) * LG_THREADS);
+                    lg_store<T>(out + (int64_t)(v + (loose + i) * LG_THREADS) * LG_VEC, e);
+                }
+        }
+        int t = loose;
+        for (; t >= AHEAD; t -= AHEAD) {
+            typename T::raw raw[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                raw[i] = lg_load<T>(at(t - 1 - i));
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                float e[LG_VEC];
+                lg_values<T>(raw[i], e);
+                f(e, v + (t - 1 - i) * LG_THREADS);
+                lg_store<T>(out + (int64_t)(v + (t - 1 - i) * LG_THREADS) * LG_VEC, e);
+            }
+        }
+        for (; t > 0; --t)
+            back(out, t - 1, f);
+    }
+    template <typename F>
+    __device__ __forceinline__ void back(typename T::bits *out, int t, F f) {
+        float e[LG_VEC];
+        lg_values<T>(lg_load<T>(at(t)), e);
+        f(e, v + t * LG_THREADS);
+        lg_store<T>(out + (int64_t)(v + t * LG_THREADS) * LG_VEC, e);
+    }
+};
+
+// The sums of the workgroup's vectors, and, with TOP, the thread's largest entry
+// and the first vector that holds it.  `map` (LG_NAMED): a byte per vector from
+// v0 on.
+template <typename T, int KIND, bool TOP, int KEEP, bool QUICK>
+__device__ __forceinline__ void lg_stream(lg_walk<T, KEEP> &walk, float c, const uint8_t *map, int v0,
+                                          lg_sums<QUICK> &s, float &best, int &where) {
+    const float slack = QUICK ? LG_SLACK : LG_SLACK / c;
+    walk.up([&](const float(&e)[LG_VEC], int at) __attribute__((always_inline)) {
         uint32_t named = 0;
         if constexpr (KIND == LG_NAMED)
-            named = map[at - r.v0];
+            named = map[at - v0];
         const float top = lg_add<KIND>(s, e, c, slack, named);
         if (TOP && top > best) {
             best = top;
             where = at;
         }
-    };
-    for (; v + (AHEAD - 1) * LG_THREADS < end; v += AHEAD * LG_THREADS) {
-        typename T::raw raw[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            raw[i] = lg_load<T>(x + (int64_t)(v + i * LG_THREADS) * LG_VEC);
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            float e[LG_VEC];
-            lg_values<T>(raw[i], e);
-            take(e, v + i * LG_THREADS);
-        }
-    }
-    for (; v < end; v += LG_THREADS) {
-        float e[LG_VEC];
-        lg_values<T>(lg_load<T>(x + (int64_t)v * LG_VEC), e);
-        take(e, v);
-    }
-    if (v == r.whole && v < r.v1) {
-        float e[LG_VEC];
-        lg_load_part<T>(x + (int64_t)v * LG_VEC, r.rest, e);
-        take(e, v);
-    }
+    });
 }
 
-// out = f(x) over a slice.  The values are read and written by the same thread,
-// so `out` may be x.
-template <typename T, typename F>
-__device__ __forceinline__ void lg_map(const typename T::bits *x, typename T::bits *out, const lg_range &r, F f) {
-    const int end = min(r.v1, r.whole);
-    int v = r.v0 + (int)threadIdx.x;
-    constexpr int AHEAD = 4;
-    for (; v + (AHEAD - 1) * LG_THREADS < end; v += AHEAD * LG_THREADS) {
-        typename T::raw raw[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            raw[i] = lg_load<T>(x + (int64_t)(v + i * LG_THREADS) * LG_VEC);
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            float e[LG_VEC];
-            lg_values<T>(raw[i], e);
-            f(e, v + i * LG_THREADS);
-            lg_store<T>(out + (int64_t)(v + i * LG_THREADS) * LG_VEC, e);
-        }
+// What the sums of a row say, whichever way they were formed.
+struct lg_row {
+    float m, S, b;      // reference; sum (LG_NAMED: of the entries not named), second sum
+    bool quick;
+    __device__ __forceinline__ float exponent(float x, float c) const {
+        return quick ? lg_exponent<true>(x, m, c) : lg_exponent<false>(x, m, c);
     }
-    for (; v < end; v += LG_THREADS) {
-        float e[LG_VEC];
-        lg_values<T>(lg_load<T>(x + (int64_t)v * LG_VEC), e);
-        f(e, v);
-        lg_store<T>(out + (int64_t)v * LG_VEC, e);
-    }
-    if (v == r.whole && v < r.v1) {
-        float e[LG_VEC];
-        lg_load_part<T>(x + (int64_t)v * LG_VEC, r.rest, e);
-        f(e, v);
-        lg_store_part<T>(out + (int64_t)v * LG_VEC, r.rest, e);
-    }
+};
+
+template <bool QUICK>
+__device__ __forceinline__ lg_row lg_row_of(const lg_sums<QUICK> &t) {
+    return {t.m, t.a, t.b, QUICK};
 }
 
 template <typename T>

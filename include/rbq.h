@@ -845,7 +845,7 @@ rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8
  * scales) and judge it by its log probabilities (perplexity).  logits is
  * device [M][vocab], a row every `row_stride` entries (>= vocab; rows may start
  * at any entry), of type RBQ_L_F16, RBQ_L_F32 or RBQ_L_BF16.  With T the
- * temperature (> 0, 1e-6 .. 1e6), p = softmax(logits / T), computed in fp32
+ * temperature (1e-3 .. 1e3), p = softmax(logits / T), computed in fp32
  * relative to the row's maximum.
  *
  * Entries of -inf are masked: p = 0.  A row of nothing else is empty: its log

@@ -133,7 +133,7 @@ def test_q4_argument_errors():
 
 
 ROW = [OK, 0, 4, 100, 100, 1.0]
-ROW_BAD = [(0, None), (1, 3), (2, -1), (3, 0), (3, -5), (4, 99), (5, 0.0), (5, -1.0), (5, float("nan")), (5, float("inf")), (5, 1e-7)]
+ROW_BAD = [(0, None), (1, 3), (2, -1), (3, 0), (3, -5), (4, 99), (5, 0.0), (5, -1.0), (5, float("nan")), (5, float("inf")), (5, 0.9e-3), (5, 1.1e3)]
 
 
 def test_logprobs_argument_errors():
