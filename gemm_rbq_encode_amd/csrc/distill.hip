@@ -30,25 +30,15 @@ struct lg_distill_args {
 
 constexpr int LG_MAP = 1 << 15;     // vectors that one map of named tokens covers
 
+// What the slots of a row say, in LDS.  One wave forms it, two slots a lane,
+// while the others read the row.
 struct lg_slots {
-    int index[RBQ_TOP_MAX];         // -1: not used
-    float x[RBQ_TOP_MAX];           // the student's logit
-    double p[RBQ_TOP_MAX];
-    double red[LG_WAVES][2];
+    int index[RBQ_TOP_MAX];     // -1: not used
+    float x[RBQ_TOP_MAX];       // the student's logit
+    double p[RBQ_TOP_MAX];      // 0: not used
+    double P, rest, own;        // sum of p, the rest, sum of p ln p over all classes
     int bad, any;
 };
-
-__device__ __forceinline__ double lg_block_sum(double v, double (*red)[2], int which) {
-    v = wave_sum_f64(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6][which] = v;
-    __syncthreads();
-    double t = 0.0;
-    for (int i = 0; i < LG_WAVES; ++i)
-        t += red[i][which];
-    return t;
-}
 
 // The workgroup's sums over a slice; the bits of the named tokens in it are set
 // in `map`, a chunk of LG_MAP vectors at a time.
@@ -67,19 +57,19 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
             for (int i = tid; i < (q.v1 - q.v0 + 3) / 4; i += LG_THREADS)
                 map[i] = 0;
             __syncthreads();
-            if (tid < slots) {
-                const int i = sl.index[tid];
+            for (int j = tid; j < slots; j += LG_THREADS) {
+                const int i = sl.index[j];
                 const int bit = i - q.v0 * LG_VEC;
                 if (i >= 0 && bit >= 0 && i / LG_VEC < q.v1)
                     atomicOr(&map[bit >> 5], 1u << (bit & 31));
             }
             __syncthreads();
-            lg_walk<T, 0> walk(x, q);
+            lg_walk<T> walk(x, q);
             lg_stream<T, KIND, false>(walk, c, (const uint8_t *)map, q.v0, s, best, where);
             __syncthreads();
         }
     } else {
-        lg_walk<T, 0> walk(x, r);
+        lg_walk<T> walk(x, r);
         lg_stream<T, KIND, false>(walk, c, nullptr, 0, s, best, where);
     }
     const lg_sums<QUICK> t = lg_join_block<KIND>(s, c, part);
@@ -93,7 +83,7 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
 template <typename T, bool QUICK>
 __device__ __forceinline__ void distill_write(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
                                               float m, float c, float w) {
-    lg_walk<T, 0> walk(x, r);
+    lg_walk<T> walk(x, r);
     walk.down(dx, [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LG_VEC; ++i)
@@ -105,6 +95,126 @@ __device__ __forceinline__ void distill_write(const typename T::bits *x, typenam
 // the slices' sums.  GRAD: the gradient of a slice is written (WHOLE, REST).
 enum { DS_WHOLE = 0, DS_SUMS = 1, DS_REST = 2 };
 
+// The slots' tokens, and the student's logits of them: x may be the gradient's
+// buffer, so the slices keep them beside their sums.
+template <typename T, int MODE>
+__device__ __forceinline__ void distill_slots(const typename T::bits *x, const lg_range &r, int row,
+                                              const lg_row_args &a, const lg_distill_args &p, float (&t)[2],
+                                              lg_slots &sl) {
+    const int lane = threadIdx.x & 63;
+    const int64_t first = (int64_t)row * p.slots;
+    int index[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = lane + 64 * q;
+        index[q] = j < p.slots ? p.index[first + j] : -1;
+        t[q] = j < p.slots ? p.t_logp[first + j] : -__builtin_inff();
+    }
+    bool bad = false, any = false;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = lane + 64 * q;
+        bad |= index[q] >= a.V;
+        if (index[q] < 0 || index[q] >= a.V || t[q] == -__builtin_inff()) {
+            index[q] = -1;
+            t[q] = -__builtin_inff();
+        }
+        any |= index[q] >= 0;
+        if (j < p.slots)
+            sl.index[j] = index[q];
+    }
+    bad = __any(bad);
+    any = __any(any);
+    if (lane == 0) {
+        sl.bad = bad;
+        sl.any = any;
+        if (bad && a.status != nullptr)
+            atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int i = index[q], j = lane + 64 * q;
+        if (i < 0)
+            continue;
+        if (MODE == DS_WHOLE)
+            sl.x[j] = T::one(x[i]);
+        else if (MODE == DS_REST)
+            sl.x[j] = a.named[first + j];
+        else if (i / LG_VEC >= r.v0 && i / LG_VEC < r.v1)
+            a.named[first + j] = T::one(x[i]);
+    }
+}
+
+// The teacher's side, from the slots' log probabilities t (-inf: not used).
+template <int KIND>
+__device__ __forceinline__ void distill_teacher(const float (&t)[2], int slots, lg_slots &sl) {
+    const int lane = threadIdx.x & 63;
+    // normalised over the slots: relative to the largest
+    const double top = KIND == LG_NAMED ? 0.0 : (double)lg_wave_max(fmaxf(t[0], t[1]));
+    double lp[2], pj[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        lp[q] = (double)t[q] - top;
+        pj[q] = t[q] == -__builtin_inff() ? 0.0 : exp(lp[q]);   // (a NaN counts)
+    }
+    double P = wave_sum_f64_dpp(pj[0] + pj[1]), rest = 0.0;
+    if (KIND != LG_NAMED) {
+        if (P != 0.0) {
+            const double by = 1.0 / P, less = log(P);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                pj[q] *= by;
+                lp[q] -= less;
+            }
+            P = P != P ? P : 1.0;
+        }
+    } else {
+        rest = 1.0 - P;
+        rest = rest > 0.0 ? rest : rest != rest ? rest : 0.0;
+    }
+    double own = wave_sum_f64_dpp((pj[0] != 0.0 ? pj[0] * lp[0] : 0.0) + (pj[1] != 0.0 ? pj[1] * lp[1] : 0.0));
+    if (KIND == LG_NAMED && rest != 0.0)
+        own += rest * log(rest);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        if (lane + 64 * q < slots)
+            sl.p[lane + 64 * q] = pj[q];
+    if (lane == 0) {
+        sl.P = P;
+        sl.rest = rest;
+        sl.own = own;
+    }
+}
+
+// A wave's part: the loss of the row, sum p ln p - sum p ln q.
+template <int KIND>
+__device__ __forceinline__ float distill_loss(const lg_row &t, double S, float cf, int slots, const lg_slots &sl) {
+    const int lane = threadIdx.x & 63;
+    const double c = cf, m = t.m;
+    double cross = 0.0;             // sum p ln e
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = lane + 64 * q;
+        const double pj = j < slots ? sl.p[j] : 0.0;
+        if (pj != 0.0) {
+            const double x = sl.x[j];
+            cross += pj * ((t.quick ? x * c - m : (x - m) * c) * 0.6931471805599453);
+        }
+    }
+    cross = wave_sum_f64_dpp(cross);
+    if (sl.bad)
+        return __builtin_nanf("");
+    if (sl.P == 0.0 && sl.rest == 0.0)
+        return 0.0f;
+    if (S == 0.0)
+        return sl.P + sl.rest != sl.P + sl.rest ? __builtin_nanf("") : __builtin_inff();
+    const double logS = log(S);
+    double loss = sl.own - cross + sl.P * logS;
+    if (KIND == LG_NAMED && sl.rest != 0.0)
+        loss -= sl.rest * (log((double)t.S) - logS);
+    return (float)loss;
+}
+
 template <typename T, int KIND, int MODE, bool GRAD>
 __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_distill_args p) {
     __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : LG_WAVES];
@@ -112,142 +222,86 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
     extern __shared__ uint32_t map[];
     const int tid = threadIdx.x;
     const int per_row = MODE == DS_REST && !GRAD ? 1 : a.slices;
-    for (int64_t u = blockIdx.x; u < (int64_t)a.M * per_row; u += gridDim.x) {
-        const int row = (int)(u / per_row), slice = (int)(u - (int64_t)row * per_row);
-        const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
-        const lg_range r = lg_slice(a.V, a.slices, slice);
-        // the slots
+    const int64_t u = a.first + blockIdx.x;
+    const int row = (int)(u / per_row), slice = (int)(u - (int64_t)row * per_row);
+    const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
+    const lg_range r = lg_slice(a.V, a.slices, slice);
+    float t_logp[2];
+    if (tid < 64)
+        distill_slots<T, MODE>(x, r, row, a, p, t_logp, sl);
+    __syncthreads();
+    if (MODE != DS_SUMS && tid < 64)
+        distill_teacher<KIND>(t_logp, p.slots, sl);
+    lg_row t;
+    if constexpr (MODE == DS_REST) {
+        for (int i = tid; i < a.slices; i += LG_THREADS)
+            part[i] = a.sums[(int64_t)row * a.slices + i];
+        __syncthreads();
+        t = lg_row_of(lg_join_list<KIND, false>(part, a.slices, a.c));
+    } else if constexpr (MODE == DS_SUMS) {
+        t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
         if (tid == 0)
-            sl.bad = sl.any = 0;
-        __syncthreads();
-        double lp = -__builtin_inf();
-        if (tid < p.slots) {
-            int i = p.index[(int64_t)row * p.slots + tid];
-            const float t = p.t_logp[(int64_t)row * p.slots + tid];
-            if (i >= a.V) {
-                sl.bad = 1;
-                i = -1;
-                if (a.status != nullptr)
-                    atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
-            } else if (i < 0 || t == -__builtin_inff()) {
-                i = -1;
-            } else {
-                lp = t;
-                sl.any = 1;
-                // (x may be the gradient's buffer: the slices keep the logits beside their sums)
-                float *kept = a.named + (int64_t)row * p.slots + tid;
-                if (MODE == DS_WHOLE)
-                    sl.x[tid] = T::one(x[i]);
-                else if (MODE == DS_REST)
-                    sl.x[tid] = *kept;
-                else if (i / LG_VEC >= r.v0 && i / LG_VEC < r.v1)
-                    *kept = T::one(x[i]);
-            }
-            sl.index[tid] = i;
-        }
-        __syncthreads();
-        // the row's sums
-        lg_row t;
-        if constexpr (MODE == DS_REST) {
-            for (int i = tid; i < a.slices; i += LG_THREADS)
-                part[i] = a.sums[(int64_t)row * a.slices + i];
+            a.sums[u] = make_float4(t.m, t.S, t.b, 0.0f);
+        return;
+    } else {
+        t = distill_sums<T, KIND, true>(x, r, sl, p.slots, a.c, map, part);
+        if (t.S != t.S) {
             __syncthreads();
-            t = lg_row_of(lg_join_list<KIND, false>(part, a.slices, a.c));
-        } else if constexpr (MODE == DS_SUMS) {
             t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
-            if (tid == 0)
-                a.sums[u] = make_float4(t.m, t.S, t.b, 0.0f);
-            __syncthreads();
-            continue;
-        } else {
-            t = distill_sums<T, KIND, true>(x, r, sl, p.slots, a.c, map, part);
-            if (t.S != t.S) {
-                __syncthreads();
-                t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
-            }
         }
-        // the teacher's side
-        double top = 0.0;
-        if (KIND != LG_NAMED) {     // normalised over the slots: relative to the largest
-            const float big = lg_wave_max((float)lp);
-            if ((tid & 63) == 0)
-                sl.red[tid >> 6][0] = big;
-            __syncthreads();
-            top = sl.red[0][0];
-            for (int i = 1; i < LG_WAVES; ++i)
-                top = fmax(top, sl.red[i][0]);
-            __syncthreads();
+    }
+    const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
+    if (tid < 64 && slice == 0 && p.loss != nullptr) {
+        const float loss = distill_loss<KIND>(t, S, a.c, p.slots, sl);
+        if (tid == 0)
+            p.loss[row] = loss;
+    }
+    if constexpr (GRAD) {
+        typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
+        const float d = p.d_loss[row];
+        if (d == 0.0f || S == 0.0 || (KIND != LG_NAMED && !sl.any && !sl.bad)) {
+            lg_zero<T>(dx, r);
+            return;
         }
-        const bool used = lp != -__builtin_inf();      // (a NaN is used)
-        double pj = used ? exp(lp - top) : 0.0;
-        double lpj = lp - top;
-        double P = lg_block_sum(pj, sl.red, 0), rest = 0.0;
-        if (KIND != LG_NAMED) {
-            if (sl.any) {
-                pj /= P;
-                lpj -= log(P);
-                P = P != P ? P : 1.0;
-            }
-        } else {
-            rest = 1.0 - P;
-            rest = rest > 0.0 ? rest : rest != rest ? rest : 0.0;
+        const double by = sl.bad ? __builtin_nan("") : (double)d * (double)a.inv_t;
+        const double all = by * (sl.P + sl.rest) / S;       // per e of a named token
+        const double away = KIND == LG_NAMED && sl.rest != 0.0 && t.S != 0.0f ? by * sl.rest / (double)t.S : 0.0;
+        // (every slot's logit has been read: dx may be x)
+        if (MODE == DS_WHOLE && t.quick)
+            distill_write<T, true>(x, dx, r, t.m, a.c, (float)(all - away));
+        else
+            distill_write<T, false>(x, dx, r, t.m, a.c, (float)(all - away));
+        __syncthreads();    // then the named tokens, a thread a slot; a token named twice gets both in each
+        for (int j = tid; j < p.slots; j += LG_THREADS) {
+            const int i = sl.index[j];
+            if (i < 0 || i / LG_VEC < r.v0 || i / LG_VEC >= r.v1)
+                continue;
+            double mine = 0.0;
+            for (int k = 0; k < p.slots; ++k)
+                if (sl.index[k] == i)
+                    mine += sl.p[k];
+            const double e = __builtin_amdgcn_exp2f(t.exponent(sl.x[j], a.c));
+            dx[i] = T::of((float)(e * all - by * mine));
         }
-        // the student's side, the loss
-        const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
-        const double logS = log(S), c = (double)a.c;
-        double term = 0.0;
-        if (used && pj != 0.0) {
-            const double xj = sl.x[tid], m = t.m, d = t.quick ? xj * c - m : (xj - m) * c;
-            term = pj * (lpj - (S == 0.0 ? -__builtin_inf() : d * 0.6931471805599453 - logS));
-        }
-        double loss = lg_block_sum(term, sl.red, 1);
-        if (KIND == LG_NAMED && rest != 0.0)
-            loss = S == 0.0 ? __builtin_inf() : loss + rest * (log(rest) - (log((double)t.S) - logS));
-        if (sl.bad)
-            loss = __builtin_nan("");
-        if (tid == 0 && slice == 0 && p.loss != nullptr)
-            p.loss[row] = (float)loss;
-        if constexpr (GRAD) {
-            typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
-            const float d = p.d_loss[row];
-            if (d == 0.0f || S == 0.0 || (KIND != LG_NAMED && !sl.any && !sl.bad)) {
-                lg_zero<T>(dx, r);
-            } else {
-                const double by = sl.bad ? __builtin_nan("") : (double)d * (double)a.inv_t;
-                const double all = by * (P + rest) / S;         // per e of a named token
-                const double away = KIND == LG_NAMED && rest != 0.0 && t.S != 0.0f ? by * rest / (double)t.S : 0.0;
-                if (used)
-                    sl.p[tid] = pj;
-                __syncthreads();    // every slot's logit has been read: dx may be x
-                if (MODE == DS_WHOLE && t.quick)
-                    distill_write<T, true>(x, dx, r, t.m, a.c, (float)(all - away));
-                else
-                    distill_write<T, false>(x, dx, r, t.m, a.c, (float)(all - away));
-                __syncthreads();    // then the named tokens, each thread a slot; a token named twice gets both in each
-                if (used && sl.index[tid] / LG_VEC >= r.v0 && sl.index[tid] / LG_VEC < r.v1) {
-                    const int i = sl.index[tid];
-                    double mine = 0.0;
-                    for (int j = 0; j < p.slots; ++j)
-                        mine += sl.index[j] == i ? sl.p[j] : 0.0;
-                    const double e = __builtin_amdgcn_exp2f(t.exponent(sl.x[tid], a.c));
-                    dx[i] = T::of((float)(e * all - by * mine));
-                }
-            }
-        }
-        __syncthreads();
     }
 }
 
 template <typename T, int KIND, bool GRAD>
 hipError_t distill_of(lg_row_args a, const lg_distill_args &p, hipStream_t st) {
-    const unsigned grid = lg_grid((int64_t)a.M * a.slices), rows = lg_grid(a.M);
+    const int64_t units = (int64_t)a.M * a.slices;
     const int vectors = (a.V + LG_VEC - 1) / LG_VEC, each = (vectors + a.slices - 1) / a.slices;
     const size_t map = KIND == LG_NAMED ? (size_t)((each < LG_MAP ? each : LG_MAP) + 3) / 4 * 4 : 0;
     if (a.slices == 1) {
-        distill_kernel<T, KIND, DS_WHOLE, GRAD><<<grid, LG_THREADS, map, st>>>(a, p);
+        lg_launches(a, units, [&](unsigned n) {
+            distill_kernel<T, KIND, DS_WHOLE, GRAD><<<n, LG_THREADS, map, st>>>(a, p);
+        });
     } else {
-        distill_kernel<T, KIND, DS_SUMS, false><<<grid, LG_THREADS, map, st>>>(a, p);
-        distill_kernel<T, KIND, DS_REST, GRAD><<<GRAD ? grid : rows, LG_THREADS, 0, st>>>(a, p);
+        lg_launches(a, units, [&](unsigned n) {
+            distill_kernel<T, KIND, DS_SUMS, false><<<n, LG_THREADS, map, st>>>(a, p);
+        });
+        lg_launches(a, GRAD ? units : a.M, [&](unsigned n) {
+            distill_kernel<T, KIND, DS_REST, GRAD><<<n, LG_THREADS, 0, st>>>(a, p);
+        });
     }
     return hipGetLastError();
 }

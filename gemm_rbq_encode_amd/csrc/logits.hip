@@ -19,58 +19,198 @@ namespace {
 
 constexpr float LN2 = 0.6931471805599453f;
 
-// The largest k entries of a slice, sorted, in lists[0 .. 64 E) (LDS; ends with
-// a barrier), for every row whatever its values at a bounded cost: each thread
-// knows its largest entry, and the k largest entries lie with the k threads
-// whose largest entries are largest (any other has k better ones before it).
-// Those threads' vectors are read once more, from the caches, by all threads,
-// and what is below the k-th of those maxima is dropped.
-template <typename T, int E>
-__device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_range &r, int k, float best, int where,
-                                          uint64_t *lists, uint64_t *waiting) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t n[E];
+// The largest k entries of a slice, sorted, for every row whatever its values at
+// a bounded cost.  Each thread knows its largest entry, and the k largest entries
+// lie with the k threads whose largest entries are largest (any other has k better
+// ones before it); among equal ones those whose entry comes first.  Those threads'
+// vectors are read once more, from the caches, by all threads, and what is below
+// the k-th of those maxima is dropped: of normally distributed entries about a
+// tenth more than k are left.  Each of them finds its place by counting the larger
+// ones.
+constexpr int LG_LEFT = 1024;       // entries left that are placed by counting
+
+template <int E>
+struct lg_pick {        // (LDS)
+    uint64_t list[64 * E];          // the result, 0 behind its end
+    uint32_t key[LG_THREADS];
+    int where[LG_THREADS], group[RBQ_TOP_MAX];
+    uint32_t least;                 // key of the k-th thread's largest entry,
+    int limit;                      // the last vector that counts where an entry equals it
+    int groups, left;
+    union {
+        uint64_t place[LG_LEFT];
+        struct {
+            uint64_t lists[LG_WAVES * 64 * E], waiting[LG_WAVES * 64 * E];
+        };
+    };
+};
+
+// Keys of one type's values, without the bits that its conversion to fp32 leaves
+// equal: the search below takes a step a bit.
+template <typename T>
+__device__ __forceinline__ uint32_t lg_short_key(float v) {
+    constexpr int SPARE = T::SPARE;
+    return v > -__builtin_inff() ? lg_ordered(v) >> SPARE : 0;
+}
+
+template <>
+struct lg_pick<0> {};
+
+// One wave finds the least key and the limit.
+__device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, int k, uint32_t &least, int &limit) {
+    constexpr int N = LG_THREADS / 64;
+    const int lane = threadIdx.x & 63;
+    uint32_t key[N], most = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        n[e] = 0;
-    n[0] = lg_key(best, where * LG_VEC + LG_VEC - 1);
-    lg_sort<E>(n);
-    lg_block_merge<E, LG_WAVES>(n, lists);
-    uint64_t least = lists[k - 1];
-    least = least == 0 ? 1 : least;
-    int groups = 0;     // threads to look at: those with an entry at all
+    for (int i = 0; i < N; ++i) {
+        key[i] = keys[i * 64 + lane];
+        most = max(most, key[i]);
+    }
+    auto count = [&](uint32_t t) __attribute__((always_inline)) {
+        int n = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        groups += __popcll(__ballot(e * 64 + lane < k && lists[e * 64 + lane] != 0));
-    const int turns = (r.v1 - r.v0 + LG_THREADS - 1) / LG_THREADS;
-    lg_top<E> top;
-    top.start(waiting + wave * 64 * E);
-    for (int q0 = wave * 64; q0 < groups * turns; q0 += LG_THREADS) {
-        const int q = q0 + lane;
-        float e[LG_VEC];
-        int v = r.v1;
-        if (q < groups * turns) {
-            const int g = q / turns;
-            v = r.v0 + (((lg_index(lists[g]) / LG_VEC) - r.v0) & (LG_THREADS - 1)) + (q - g * turns) * LG_THREADS;
+        for (int i = 0; i < N; ++i)
+            n += __popcll(__ballot(key[i] >= t));
+        return n;
+    };
+    limit = 0x7FFFFFFF;
+    uint32_t lo = 1, hi = wave_max_u32_dpp(most) + 1;
+    int above = 0;                  // keys >= hi
+    if (count(1) <= k) {            // every thread with an entry
+        least = 1;
+        return;
+    }
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = count(mid);
+        if (n == k) {
+            least = mid;
+            return;
         }
-        if (v >= r.v1) {
-#pragma unroll
-            for (int i = 0; i < LG_VEC; ++i)
-                e[i] = -__builtin_inff();
-        } else if (v < r.whole) {
-            lg_values<T>(lg_load<T>(x + (int64_t)v * LG_VEC), e);
+        if (n > k) {
+            lo = mid;
         } else {
-            lg_load_part<T>(x + (int64_t)v * LG_VEC, r.rest, e);
-        }
-#pragma unroll
-        for (int i = 0; i < LG_VEC; ++i) {
-            const uint64_t key = lg_key(e[i], v * LG_VEC + i);
-            top.offer(key, key >= least);
+            hi = mid;
+            above = n;
         }
     }
-    top.settle();
-    __syncthreads();    // the lists have been read
-    lg_block_merge<E, LG_WAVES>(top.k, lists);
+    // more than one thread has the k-th key: those of them that come first
+    least = lo;
+    int at[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        at[i] = key[i] == lo ? where[i * 64 + lane] : 0x7FFFFFFF;
+    int no = -1, yes = 0x7FFFFFFE;
+    while (yes - no > 1) {
+        const int mid = no + (yes - no) / 2;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            n += __popcll(__ballot(at[i] <= mid));
+        if (n >= k - above)
+            yes = mid;
+        else
+            no = mid;
+    }
+    limit = yes;
+}
+
+template <typename T, int E>
+__device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_range &r, int k, float best, int where,
+                                          lg_pick<E> &p) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t mine = lg_short_key<T>(best);
+    p.key[tid] = mine;
+    p.where[tid] = where;
+    if (tid == 0)
+        p.groups = p.left = 0;
+    __syncthreads();
+    if (wave == 0) {
+        uint32_t least;
+        int limit;
+        lg_find(p.key, p.where, k, least, limit);
+        if (lane == 0) {
+            p.least = least;
+            p.limit = limit;
+        }
+    }
+    __syncthreads();
+    const uint32_t least = p.least;
+    const int limit = p.limit;
+    auto counts = [&](uint32_t key, int v) __attribute__((always_inline)) {
+        return key > least || (key == least && v <= limit);
+    };
+    // a place in a list for each lane that wants one (every lane calls it)
+    auto place = [&](bool wants, int &length) __attribute__((always_inline)) -> int {
+        const uint64_t who = __ballot(wants);
+        if (who == 0)
+            return 0;
+        int first = 0;
+        if (lane == 0)
+            first = atomicAdd(&length, __popcll(who));
+        return __builtin_amdgcn_readfirstlane(first) + __popcll(who & ((1ull << lane) - 1));
+    };
+    const bool look = counts(mine, where);
+    const int g = place(look, p.groups);
+    if (look)
+        p.group[g] = tid;
+    __syncthreads();
+    const int groups = p.groups, turns = (r.v1 - r.v0 + LG_THREADS - 1) / LG_THREADS;
+    auto again = [&](auto take) __attribute__((always_inline)) {
+        for (int q0 = wave * 64; q0 < groups * turns; q0 += LG_THREADS) {
+            const int q = q0 + lane;
+            float e[LG_VEC];
+            int v = r.v1;
+            if (q < groups * turns)
+                v = r.v0 + p.group[q / turns] + q % turns * LG_THREADS;
+            if (v < min(r.v1, r.whole)) {
+                lg_values<T>(lg_load<T>(x + (int64_t)v * LG_VEC), e);
+            } else if (v < r.v1) {
+                lg_load_part<T>(x + (int64_t)v * LG_VEC, r.rest, e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < LG_VEC; ++i)
+                    e[i] = -__builtin_inff();
+            }
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < LG_VEC; ++i)
+                any |= counts(lg_short_key<T>(e[i]), v);
+            if (__ballot(any) != 0) {
+#pragma unroll
+                for (int i = 0; i < LG_VEC; ++i)
+                    take(lg_key(e[i], v * LG_VEC + i), counts(lg_short_key<T>(e[i]), v));
+            }
+        }
+    };
+    again([&](uint64_t key, bool is) __attribute__((always_inline)) {
+        const int i = place(is, p.left);
+        if (is && i < LG_LEFT)
+            p.place[i] = key;
+    });
+    __syncthreads();
+    const int left = p.left;
+    if (left <= LG_LEFT) {
+        for (int i = tid; i < left; i += LG_THREADS) {
+            const uint64_t key = p.place[i];
+            int larger = 0;
+            for (int j = 0; j < left; ++j)
+                larger += p.place[j] > key;
+            if (larger < k)
+                p.list[larger] = key;
+        }
+        for (int j = left + tid; j < k; j += LG_THREADS)
+            p.list[j] = 0;
+    } else {        // rows made for it (many entries above the k-th maximum with few threads)
+        lg_top<E> top;
+        top.start(p.waiting + wave * 64 * E);
+        again([&](uint64_t key, bool is) __attribute__((always_inline)) { top.offer(key, is); });
+        top.settle();
+        lg_block_merge<E, LG_WAVES>(top.k, p.lists);
+        for (int j = tid; j < k; j += LG_THREADS)
+            p.list[j] = p.lists[j];
+    }
+    __syncthreads();
 }
 
 struct lg_logp_args {
@@ -143,8 +283,8 @@ __device__ __forceinline__ void lg_write_top(const lg_logp_row &r, const uint64_
 }
 
 // The sums of a whole row: quickly, and once more where that was not good.
-template <typename T, bool TOP, int KEEP>
-__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T, KEEP> &walk, float c, float4 *part, float &best, int &where) {
+template <typename T, bool TOP>
+__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T> &walk, float c, float4 *part, float &best, int &where) {
     {
         lg_sums<true> s;
         lg_stream<T, LG_ENTROPY, TOP>(walk, c, nullptr, 0, s, best, where);
@@ -164,44 +304,41 @@ __device__ __forceinline__ lg_row lg_whole_row(lg_walk<T, KEEP> &walk, float c, 
 // entries.  E = 0: none.
 template <typename T, int E, bool SLICED>
 __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_logp_args p) {
-    constexpr int N = LG_WAVES * 64 * (E > 0 ? E : 1);
     __shared__ float4 part[LG_WAVES];
-    __shared__ uint64_t lists[E > 0 ? N : 1], waiting[E > 0 ? N : 1];
-    for (int64_t u = blockIdx.x; u < (int64_t)a.M * a.slices; u += gridDim.x) {
-        const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
-        const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
-        const lg_range r = lg_slice(a.V, a.slices, slice);
-        const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
-        float best = -__builtin_inff();
-        int where = 0;
-        lg_walk<T, 0> walk(x, r);
-        lg_row sums;
-        if constexpr (SLICED) {
-            lg_sums<false> s;
-            lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, 0, s, best, where);
-            sums = lg_row_of(lg_join_block<LG_ENTROPY>(s, a.c, part));
-        } else {
-            sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where);
+    __shared__ lg_pick<E> pick;
+    const int64_t u = a.first + blockIdx.x;
+    const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
+    const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
+    const lg_range r = lg_slice(a.V, a.slices, slice);
+    const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
+    float best = -__builtin_inff();
+    int where = 0;
+    lg_walk<T> walk(x, r);
+    lg_row sums;
+    if constexpr (SLICED) {
+        lg_sums<false> s;
+        lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, 0, s, best, where);
+        sums = lg_row_of(lg_join_block<LG_ENTROPY>(s, a.c, part));
+    } else {
+        sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where);
+    }
+    if constexpr (E > 0)
+        lg_select<T, E>(x, r, p.top, best, where, pick);
+    if constexpr (SLICED) {
+        if (threadIdx.x == 0) {
+            const bool here = lg_inside(target, a.V) && target >= (int64_t)r.v0 * LG_VEC &&
+                              target < (int64_t)r.v1 * LG_VEC;
+            a.sums[u] = make_float4(sums.m, sums.S, sums.b, here ? T::one(x[target]) : 0.0f);
         }
         if constexpr (E > 0)
-            lg_select<T, E>(x, r, p.top, best, where, lists, waiting);
-        if constexpr (SLICED) {
-            if (threadIdx.x == 0) {
-                const bool here = lg_inside(target, a.V) && target >= (int64_t)r.v0 * LG_VEC &&
-                                  target < (int64_t)r.v1 * LG_VEC;
-                a.sums[u] = make_float4(sums.m, sums.S, sums.b, here ? T::one(x[target]) : 0.0f);
-            }
-            if constexpr (E > 0)
-                for (int j = threadIdx.x; j < p.top; j += LG_THREADS)
-                    a.keys[u * p.top + j] = lists[j];
-        } else {
-            const lg_logp_row w(sums);
-            if (threadIdx.x == 0)
-                lg_write_logp(w, lg_inside(target, a.V) ? T::one(x[target]) : 0.0f, target, row, a, p);
-            if constexpr (E > 0)
-                lg_write_top(w, lists, row, a.c, a.inv_t, p);
-        }
-        __syncthreads();    // before the next unit writes LDS
+            for (int j = threadIdx.x; j < p.top; j += LG_THREADS)
+                a.keys[u * p.top + j] = pick.list[j];
+    } else {
+        const lg_logp_row w(sums);
+        if (threadIdx.x == 0)
+            lg_write_logp(w, lg_inside(target, a.V) ? T::one(x[target]) : 0.0f, target, row, a, p);
+        if constexpr (E > 0)
+            lg_write_top(w, pick.list, row, a.c, a.inv_t, p);
     }
 }
 
@@ -212,38 +349,36 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a
     __shared__ float4 part[LG_SLICES_MAX];
     __shared__ uint64_t lists[E > 0 ? N : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int row = blockIdx.x; row < a.M; row += gridDim.x) {
-        for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
-            part[i] = a.sums[(int64_t)row * a.slices + i];
-        if constexpr (E > 0) {
-            uint64_t best[E], next[E];
+    const int row = (int)(a.first + blockIdx.x);
+    for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
+        part[i] = a.sums[(int64_t)row * a.slices + i];
+    if constexpr (E > 0) {
+        uint64_t best[E], next[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                best[e] = 0;
-            for (int i = wave; i < a.slices; i += LG_WAVES) {
-                const uint64_t *list = a.keys + ((int64_t)row * a.slices + i) * p.top;
-                lg_wave_sync();
+        for (int e = 0; e < E; ++e)
+            best[e] = 0;
+        for (int i = wave; i < a.slices; i += LG_WAVES) {
+            const uint64_t *list = a.keys + ((int64_t)row * a.slices + i) * p.top;
+            lg_wave_sync();
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    next[e] = e * 64 + lane < p.top ? list[e * 64 + lane] : 0;
-                    lists[wave * 64 * E + e * 64 + lane] = next[e];
-                }
-                lg_wave_sync();
-                lg_merge<E>(best, lists + wave * 64 * E);
+            for (int e = 0; e < E; ++e) {
+                next[e] = e * 64 + lane < p.top ? list[e * 64 + lane] : 0;
+                lists[wave * 64 * E + e * 64 + lane] = next[e];
             }
-            __syncthreads();
-            lg_block_merge<E, LG_WAVES>(best, lists);
+            lg_wave_sync();
+            lg_merge<E>(best, lists + wave * 64 * E);
         }
         __syncthreads();
-        const lg_logp_row w(lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c)));
-        if (threadIdx.x == 0) {
-            const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
-            lg_write_logp(w, lg_kept(part, target, a), target, row, a, p);
-        }
-        if constexpr (E > 0)
-            lg_write_top(w, lists, row, a.c, a.inv_t, p);
-        __syncthreads();
+        lg_block_merge<E, LG_WAVES>(best, lists);
     }
+    __syncthreads();
+    const lg_logp_row w(lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c)));
+    if (threadIdx.x == 0) {
+        const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
+        lg_write_logp(w, lg_kept(part, target, a), target, row, a, p);
+    }
+    if constexpr (E > 0)
+        lg_write_top(w, lists, row, a.c, a.inv_t, p);
 }
 
 // The gradient of sum_m a_m logp_m + b_m H_m:
@@ -251,8 +386,8 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a
 // with p_v = e_v / S and ln p_v = ln 2 (d_v - log2 S), so that the part without
 // the target is e_v (w0 + w1 d_v).  Where rows are whole the sums are formed here,
 // and the second pass over the row finds it in the caches.
-template <typename T, bool QUICK, bool ENTROPY, int KEEP>
-__device__ __forceinline__ void lg_logp_grad(lg_walk<T, KEEP> &walk, typename T::bits *dx, float m, float c, float w0,
+template <typename T, bool QUICK, bool ENTROPY>
+__device__ __forceinline__ void lg_logp_grad(lg_walk<T> &walk, typename T::bits *dx, float m, float c, float w0,
                                              float w1, int at, int in, float own) {
     walk.down(dx, [&](float(&e)[LG_VEC], int v) __attribute__((always_inline)) {
 #pragma unroll
@@ -269,69 +404,68 @@ __device__ __forceinline__ void lg_logp_grad(lg_walk<T, KEEP> &walk, typename T:
     });
 }
 
-template <typename T, int KEEP, bool SLICED, bool ENTROPY>
+template <typename T, bool SLICED, bool ENTROPY>
 __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
     __shared__ float4 part[LG_SLICES_MAX];
-    for (int64_t u = blockIdx.x; u < (int64_t)a.M * a.slices; u += gridDim.x) {
-        const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
-        const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
-        typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
-        const lg_range r = lg_slice(a.V, a.slices, slice);
-        const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
-        const float wa = p.d_logp == nullptr || target < 0 ? 0.0f : p.d_logp[row];
-        const float wb = ENTROPY ? p.d_entropy[row] : 0.0f;
-        const bool none = wa == 0.0f && wb == 0.0f;
-        if (none && p.logp == nullptr && p.entropy == nullptr) {
-            lg_zero<T>(dx, r);
-            continue;
-        }
-        lg_walk<T, KEEP> walk(x, r);
-        lg_row sums;
-        if constexpr (SLICED) {
-            for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
-                part[i] = a.sums[(int64_t)row * a.slices + i];
-            __syncthreads();
-            sums = lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c));
-        } else {
-            float best;
-            int where;
-            sums = lg_whole_row<T, false>(walk, a.c, part, best, where);
-        }
-        const lg_logp_row w(sums);
-        if (slice == 0 && threadIdx.x == 0)
-            lg_write_logp(w,
-                          SLICED                      ? lg_kept(part, target, a)
-                          : lg_inside(target, a.V) ? T::one(x[target])
-                                                     : 0.0f,
-                          target, row, a, p);
-        if (none || w.empty) {
-            lg_zero<T>(dx, r);
-        } else {
-            const float scale = a.inv_t / w.S;
-            const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
-            const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
-            const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
-            const float own = wa * a.inv_t;
-            __syncthreads();    // the target's entry has been read: dx may be x
-            if (!SLICED && w.quick)
-                lg_logp_grad<T, true, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
-            else
-                lg_logp_grad<T, false, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
-        }
-        __syncthreads();
+    const int64_t u = a.first + blockIdx.x;
+    const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
+    const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
+    typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
+    const lg_range r = lg_slice(a.V, a.slices, slice);
+    const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
+    const float wa = p.d_logp == nullptr || target < 0 ? 0.0f : p.d_logp[row];
+    const float wb = ENTROPY ? p.d_entropy[row] : 0.0f;
+    const bool none = wa == 0.0f && wb == 0.0f;
+    if (none && p.logp == nullptr && p.entropy == nullptr) {
+        lg_zero<T>(dx, r);
+        return;
     }
+    lg_walk<T> walk(x, r);
+    lg_row sums;
+    if constexpr (SLICED) {
+        for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
+            part[i] = a.sums[(int64_t)row * a.slices + i];
+        __syncthreads();
+        sums = lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c));
+    } else {
+        float best;
+        int where;
+        sums = lg_whole_row<T, false>(walk, a.c, part, best, where);
+    }
+    const lg_logp_row w(sums);
+    if (slice == 0 && threadIdx.x == 0)
+        lg_write_logp(w,
+                      SLICED                      ? lg_kept(part, target, a)
+                      : lg_inside(target, a.V) ? T::one(x[target])
+                                                 : 0.0f,
+                      target, row, a, p);
+    if (none || w.empty) {
+        lg_zero<T>(dx, r);
+    } else {
+        const float scale = a.inv_t / w.S;
+        const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
+        const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
+        const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
+        const float own = wa * a.inv_t;
+        __syncthreads();    // the target's entry has been read: dx may be x
+        if (!SLICED && w.quick)
+            lg_logp_grad<T, true, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
+        else
+            lg_logp_grad<T, false, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
+    }
+    __syncthreads();
 }
 
 template <typename T>
 hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
-    const unsigned grid = lg_grid((int64_t)a.M * a.slices), rows = lg_grid(a.M);
+    const int64_t units = (int64_t)a.M * a.slices;
     auto run = [&](auto e) {
         constexpr int E = decltype(e)::value;
         if (a.slices > 1) {
-            logprobs_kernel<T, E, true><<<grid, LG_THREADS, 0, st>>>(a, p);
-            logprobs_join_kernel<E><<<rows, LG_THREADS, 0, st>>>(a, p);
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, true><<<n, LG_THREADS, 0, st>>>(a, p); });
+            lg_launches(a, a.M, [&](unsigned n) { logprobs_join_kernel<E><<<n, LG_THREADS, 0, st>>>(a, p); });
         } else {
-            logprobs_kernel<T, E, false><<<grid, LG_THREADS, 0, st>>>(a, p);
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, false><<<n, LG_THREADS, 0, st>>>(a, p); });
         }
     };
     if (p.top == 0)
@@ -343,22 +477,21 @@ hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool ENTROPY>
 hipError_t logprobs_grad_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
-    const unsigned grid = lg_grid((int64_t)a.M * a.slices);
-    const bool entropy = p.d_entropy != nullptr;
+    const int64_t units = (int64_t)a.M * a.slices;
     if (a.slices > 1) {
-        logprobs_kernel<T, 0, true><<<grid, LG_THREADS, 0, st>>>(a, p);
-        if (entropy)
-            logprobs_grad_kernel<T, 0, true, true><<<grid, LG_THREADS, 0, st>>>(a, p);
-        else
-            logprobs_grad_kernel<T, 0, true, false><<<grid, LG_THREADS, 0, st>>>(a, p);
-    } else if (entropy) {
-        logprobs_grad_kernel<T, LG_KEEP, false, true><<<grid, LG_THREADS, 0, st>>>(a, p);
+        lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, 0, true><<<n, LG_THREADS, 0, st>>>(a, p); });
+        lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, true, ENTROPY><<<n, LG_THREADS, 0, st>>>(a, p); });
     } else {
-        logprobs_grad_kernel<T, LG_KEEP, false, false><<<grid, LG_THREADS, 0, st>>>(a, p);
+        lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, false, ENTROPY><<<n, LG_THREADS, 0, st>>>(a, p); });
     }
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t logprobs_grad_any(const lg_row_args &a, const lg_logp_args &p, hipStream_t st) {
+    return p.d_entropy != nullptr ? logprobs_grad_of<T, true>(a, p, st) : logprobs_grad_of<T, false>(a, p, st);
 }
 
 }  // namespace
@@ -395,9 +528,9 @@ hipError_t launch_token_logprobs_backward(const void *x, uint32_t type, int M, i
     p.dx = dx;
     p.d_stride = d_stride;
     cut_rows(a, 0, 0, workspace, bytes);
-    return type == RBQ_L_F16   ? logprobs_grad_of<lg_f16>(a, p, st)
-           : type == RBQ_L_F32 ? logprobs_grad_of<lg_f32>(a, p, st)
-                               : logprobs_grad_of<lg_bf16>(a, p, st);
+    return type == RBQ_L_F16   ? logprobs_grad_any<lg_f16>(a, p, st)
+           : type == RBQ_L_F32 ? logprobs_grad_any<lg_f32>(a, p, st)
+                               : logprobs_grad_any<lg_bf16>(a, p, st);
 }
 
 }  // namespace rbq

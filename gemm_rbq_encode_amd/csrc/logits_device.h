@@ -20,6 +20,7 @@ constexpr float LG_FAR = -1.0e4f;               // exponents below this are 0 in
 typedef uint32_t lg_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 
 struct lg_f16 {
+    static constexpr int SPARE = 13;     // low bits that are equal in all of its values as fp32
     typedef uint16_t bits;
     struct raw {
         lg_u32x4 a;
@@ -28,6 +29,7 @@ struct lg_f16 {
     static __device__ __forceinline__ uint16_t of(float v) { return f2h(v); }
 };
 struct lg_bf16 {
+    static constexpr int SPARE = 16;     // low bits that are equal in all of its values as fp32
     typedef uint16_t bits;
     struct raw {
         lg_u32x4 a;
@@ -36,6 +38,7 @@ struct lg_bf16 {
     static __device__ __forceinline__ uint16_t of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
 struct lg_f32 {
+    static constexpr int SPARE = 0;     // low bits that are equal in all of its values as fp32
     typedef uint32_t bits;
     struct raw {
         lg_u32x4 a, b;
@@ -100,25 +103,15 @@ __device__ __forceinline__ void lg_store_part(typename T::bits *p, int n, const 
             p[i] = T::of(x[i]);
 }
 
-// ---- lanes --------------------------------------------------------------------
-//
-// Sums and maxima over a wave by DPP: inside quads, mirrored halves and rows of
-// 16, then row 15 -> next row and lane 31 -> upper half; lane 63 has the whole.
+// Maximum over a wave by DPP: inside quads, mirrored halves and rows of 16, then
+// lane 15 of a row to the next one and lane 31 to the upper half; lane 63 has the
+// whole.
 
 #define LG_DPP(old, v, ctrl, rows) \
     __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v), ctrl, rows, 0xF, false))
 
 __device__ __forceinline__ float lg_lane63(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
-}
-__device__ __forceinline__ float lg_wave_sum(float v) {
-    v += LG_DPP(0.0f, v, 0xB1, 0xF);
-    v += LG_DPP(0.0f, v, 0x4E, 0xF);
-    v += LG_DPP(0.0f, v, 0x141, 0xF);
-    v += LG_DPP(0.0f, v, 0x140, 0xF);
-    v += LG_DPP(0.0f, v, RBQ_DPP_ROW_BCAST15, 0xA);
-    v += LG_DPP(0.0f, v, RBQ_DPP_ROW_BCAST31, 0xC);
-    return lg_lane63(v);
 }
 __device__ __forceinline__ float lg_wave_max(float v) {
     v = fmaxf(v, LG_DPP(v, v, 0xB1, 0xF));
@@ -216,9 +209,9 @@ __device__ __forceinline__ float lg_add(lg_sums<QUICK> &s, const float (&x)[LG_V
 template <int KIND, bool QUICK>
 __device__ __forceinline__ lg_sums<QUICK> lg_join_wave(lg_sums<QUICK> s, float c) {
     lg_move<KIND>(s, lg_wave_max(s.m), c);
-    s.a = lg_wave_sum(s.a);
+    s.a = wave_sum_f32_dpp(s.a);
     if constexpr (KIND != LG_PLAIN)
-        s.b = lg_wave_sum(s.b);
+        s.b = wave_sum_f32_dpp(s.b);
     return s;
 }
 
@@ -395,6 +388,7 @@ struct lg_top {
 
 struct lg_row_args {
     const void *x;
+    int64_t first;      // the launch's first row or slice
     int64_t stride;
     int M, V, slices;
     float c, inv_t;     // log2(e) / T, 1 / T
@@ -426,21 +420,18 @@ __device__ __forceinline__ lg_range lg_slice(int V, int slices, int s) {
 }
 
 // A thread's vectors of a slice: those of `turns` whole turns of the workgroup,
-// one more where `more`, and the row's last one, part empty, where `part`.  The
-// last KEEP of the whole turns can stay in registers between two passes.
-template <typename T, int KEEP>
+// one more where `more`, and the row's last one, part empty, where `part`.
+template <typename T>
 struct lg_walk {
     static constexpr int AHEAD = 4;
     const typename T::bits *x;
-    int v, turns, loose, rest;      // first vector; loose: turns that are not kept
+    int v, turns, rest;     // v: the first vector
     bool more, part;
-    typename T::raw kept[KEEP > 0 ? KEEP : 1];
 
     __device__ __forceinline__ lg_walk(const typename T::bits *row, const lg_range &r) : x(row) {
         const int end = min(r.v1, r.whole);
         v = r.v0 + (int)threadIdx.x;
         turns = max(0, end - r.v0) / LG_THREADS;
-        loose = max(0, turns - KEEP);
         const int last = v + turns * LG_THREADS;
         more = last < end;
         part = (more ? last + LG_THREADS : last) == r.whole && r.v1 > r.whole;
@@ -453,7 +444,7 @@ struct lg_walk {
     template <typename F>
     __device__ __forceinline__ void up(F f) {
         int t = 0;
-        for (; t + AHEAD <= loose; t += AHEAD) {
+        for (; t + AHEAD <= turns; t += AHEAD) {
             typename T::raw raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
@@ -465,21 +456,8 @@ struct lg_walk {
                 f(e, v + (t + i) * LG_THREADS);
             }
         }
-        for (; t < loose; ++t)
+        for (; t < turns; ++t)
             one(t, f);
-        if constexpr (KEEP > 0) {
-#pragma unroll
-            for (int i = 0; i < KEEP; ++i)
-                if (loose + i < turns)
-                    kept[i] = lg_load<T>(at(loose + i));
-#pragma unroll
-            for (int i = 0; i < KEEP; ++i)
-                if (loose + i < turns) {
-                    float e[LG_VEC];
-                    lg_values<T>(kept[i], e);
-                    f(e, v + (loose + i) * LG_THREADS);
-                }
-        }
         if (more)
             one(turns, f);
         if (part) {
@@ -508,17 +486,7 @@ struct lg_walk {
         }
         if (more)
             back(out, turns, f);
-        if constexpr (KEEP > 0) {
-#pragma unroll
-            for (int i = KEEP - 1; i >= 0; --i)
-                if (loose + i < turns) {
-                    float e[LG_VEC];
-                    lg_values<T>(kept[i], e);
-                    f(e, v + (loose + i) * LG_THREADS);
-                    lg_store<T>(out + (int64_t)(v + (loose + i) * LG_THREADS) * LG_VEC, e);
-                }
-        }
-        int t = loose;
+        int t = turns;
         for (; t >= AHEAD; t -= AHEAD) {
             typename T::raw raw[AHEAD];
 #pragma unroll
@@ -547,8 +515,8 @@ struct lg_walk {
 // The sums of the workgroup's vectors, and, with TOP, the thread's largest entry
 // and the first vector that holds it.  `map` (LG_NAMED): a byte per vector from
 // v0 on.
-template <typename T, int KIND, bool TOP, int KEEP, bool QUICK>
-__device__ __forceinline__ void lg_stream(lg_walk<T, KEEP> &walk, float c, const uint8_t *map, int v0,
+template <typename T, int KIND, bool TOP, bool QUICK>
+__device__ __forceinline__ void lg_stream(lg_walk<T> &walk, float c, const uint8_t *map, int v0,
                                           lg_sums<QUICK> &s, float &best, int &where) {
     const float slack = QUICK ? LG_SLACK : LG_SLACK / c;
     walk.up([&](const float(&e)[LG_VEC], int at) __attribute__((always_inline)) {
@@ -588,8 +556,14 @@ __device__ __forceinline__ void lg_zero(typename T::bits *out, const lg_range &r
     }
 }
 
-// One workgroup a unit, bounded: the kernels loop.
-inline unsigned lg_grid(int64_t units) { return (unsigned)(units < (1 << 20) ? units : (1 << 20)); }
+// One workgroup a unit.  A launch has less than 2^32 threads: more units take
+// several.
+template <typename F>
+inline void lg_launches(lg_row_args &a, int64_t units, F launch) {
+    constexpr int64_t MOST = 1 << 22;
+    for (a.first = 0; a.first < units; a.first += MOST)
+        launch((unsigned)(units - a.first < MOST ? units - a.first : MOST));
+}
 
 inline lg_row_args row_args(const void *x, int M, int V, int64_t stride, float temperature, int32_t *status) {
     lg_row_args a = {};

@@ -10,7 +10,6 @@ namespace rbq {
 
 constexpr int LG_THREADS = 512;      // threads of a workgroup on logits
 constexpr int LG_VEC = 8;            // consecutive logits a thread takes at a time
-constexpr int LG_KEEP = 4;           // vectors of a row that a thread keeps between two passes
 constexpr int LG_SLICES_MAX = 256;   // slices of a row
 
 // Slices of a row: enough that M rows make about four workgroups per compute
