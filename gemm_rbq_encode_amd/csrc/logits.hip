@@ -22,11 +22,15 @@ constexpr float LN2 = 0.6931471805599453f;
 // The largest k entries of a slice, sorted, for every row whatever its values at
 // a bounded cost.  Each thread knows its largest entry, and the k largest entries
 // lie with the k threads whose largest entries are largest (any other has k better
-// ones before it); among equal ones those whose entry comes first.  Those threads'
-// vectors are read once more, from the caches, by all threads, and what is below
+// ones before it); among equal ones those whose entry comes first.  What is below
 // the k-th of those maxima is dropped: of normally distributed entries about a
 // tenth more than k are left.  Each of them finds its place by counting the larger
 // ones.
+// The vectors that hold them are known by their own largest entries, kept in LDS
+// (2 bytes for 16 or 32 of the row), and only they are read again.  Where rows are
+// too long for that, or too many vectors come into question (equal entries), all
+// vectors of those k threads are read again: 16 bytes of a line each, which for 64
+// threads costs as much as the whole row.
 constexpr int LG_LEFT = 1024;       // entries left that are placed by counting
 
 template <int E>
@@ -36,7 +40,8 @@ struct lg_pick {        // (LDS)
     int where[LG_THREADS], group[RBQ_TOP_MAX];
     uint32_t least;                 // key of the k-th thread's largest entry,
     int limit;                      // the last vector that counts where an entry equals it
-    int groups, left;
+    int groups, left, vectors;
+    int vector[LG_LEFT];            // vectors to read again
     union {
         uint64_t place[LG_LEFT];
         struct {
@@ -60,10 +65,13 @@ struct lg_pick<0> {};
 __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, int k, uint32_t &least, int &limit) {
     constexpr int N = LG_THREADS / 64;
     const int lane = threadIdx.x & 63;
-    uint32_t key[N], most = 0;
+    // (a lane's two largest: 64 lanes have k entries no less than the least of the
+    // lanes' largest, or second largest, which is where the search starts)
+    uint32_t key[N], most = 0, second = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         key[i] = keys[i * 64 + lane];
+        second = max(second, min(most, key[i]));
         most = max(most, key[i]);
     }
     auto count = [&](uint32_t t) __attribute__((always_inline)) {
@@ -74,10 +82,10 @@ __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, 
         return n;
     };
     limit = 0x7FFFFFFF;
-    uint32_t lo = 1, hi = wave_max_u32_dpp(most) + 1;
+    uint32_t lo = max(1u, ~wave_max_u32_dpp(~(k <= 64 ? most : second))), hi = wave_max_u32_dpp(most) + 1;
     int above = 0;                  // keys >= hi
-    if (count(1) <= k) {            // every thread with an entry
-        least = 1;
+    if (count(lo) <= k) {           // just k, or every thread with an entry
+        least = lo;
         return;
     }
     while (hi - lo > 1) {
@@ -117,13 +125,13 @@ __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, 
 
 template <typename T, int E>
 __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_range &r, int k, float best, int where,
-                                          lg_pick<E> &p) {
+                                          const uint16_t *tops, lg_pick<E> &p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t mine = lg_short_key<T>(best);
     p.key[tid] = mine;
     p.where[tid] = where;
     if (tid == 0)
-        p.groups = p.left = 0;
+        p.groups = p.left = p.vectors = 0;
     __syncthreads();
     if (wave == 0) {
         uint32_t least;
@@ -140,62 +148,97 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
     auto counts = [&](uint32_t key, int v) __attribute__((always_inline)) {
         return key > least || (key == least && v <= limit);
     };
-    // a place in a list for each lane that wants one (every lane calls it)
-    auto place = [&](bool wants, int &length) __attribute__((always_inline)) -> int {
-        const uint64_t who = __ballot(wants);
-        if (who == 0)
-            return 0;
-        int first = 0;
-        if (lane == 0)
-            first = atomicAdd(&length, __popcll(who));
-        return __builtin_amdgcn_readfirstlane(first) + __popcll(who & ((1ull << lane) - 1));
+    const int n = r.v1 - r.v0, end = min(r.v1, r.whole);
+    // the entries of vector v that count (every lane of a wave takes part)
+    auto offer = [&](int v, const float(&e)[LG_VEC], auto take) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < LG_VEC; ++j)
+            take(lg_key(e[j], v * LG_VEC + j), counts(lg_short_key<T>(e[j]), v));
     };
+    auto keep = [&](uint64_t key, bool is) __attribute__((always_inline)) {
+        if (is) {
+            const int i = atomicAdd(&p.left, 1);
+            if (i < LG_LEFT)
+                p.place[i] = key;
+        }
+    };
+    if (tops != nullptr) {
+        const uint32_t bound = (least << T::SPARE) >> 16;
+        for (int i = tid * 8; i < n; i += LG_THREADS * 8) {
+            const uint4 w = *(const uint4 *)(tops + i);
+            const uint32_t h[8] = {w.x & 0xFFFF, w.x >> 16, w.y & 0xFFFF, w.y >> 16,
+                                   w.z & 0xFFFF, w.z >> 16, w.w & 0xFFFF, w.w >> 16};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (h[j] >= bound && i + j < n) {
+                    const int at = atomicAdd(&p.vectors, 1);
+                    if (at < LG_LEFT)
+                        p.vector[at] = r.v0 + i + j;
+                }
+        }
+    }
     const bool look = counts(mine, where);
-    const int g = place(look, p.groups);
     if (look)
-        p.group[g] = tid;
+        p.group[atomicAdd(&p.groups, 1)] = tid;
     __syncthreads();
-    const int groups = p.groups, turns = (r.v1 - r.v0 + LG_THREADS - 1) / LG_THREADS;
-    auto again = [&](auto take) __attribute__((always_inline)) {
-        for (int q0 = wave * 64; q0 < groups * turns; q0 += LG_THREADS) {
-            const int q = q0 + lane;
+    const int vectors = p.vectors;
+    const bool known = tops != nullptr && vectors <= LG_LEFT;
+    if (known) {
+        for (int i = tid; i < vectors; i += LG_THREADS) {
+            const int v = p.vector[i];
             float e[LG_VEC];
-            int v = r.v1;
-            if (q < groups * turns)
-                v = r.v0 + p.group[q / turns] + q % turns * LG_THREADS;
-            if (v < min(r.v1, r.whole)) {
+            if (v < end)
                 lg_values<T>(lg_load<T>(x + (int64_t)v * LG_VEC), e);
-            } else if (v < r.v1) {
+            else
                 lg_load_part<T>(x + (int64_t)v * LG_VEC, r.rest, e);
-            } else {
+            offer(v, e, keep);
+        }
+    }
+    const int groups = p.groups, turns = (n + LG_THREADS - 1) / LG_THREADS;
+    // take(key, whether it counts) of those threads' entries; every lane of a wave
+    // takes part each time
+    constexpr int AHEAD = 4;
+    auto again = [&](auto take) __attribute__((always_inline)) {
+        const int items = groups * turns;
+        for (int q0 = wave * 64; q0 < items; q0 += AHEAD * LG_THREADS) {
+            typename T::raw raw[AHEAD];
+            int v[AHEAD];
 #pragma unroll
-                for (int i = 0; i < LG_VEC; ++i)
-                    e[i] = -__builtin_inff();
+            for (int i = 0; i < AHEAD; ++i) {
+                const int q = q0 + i * LG_THREADS + lane;
+                v[i] = q < items ? r.v0 + p.group[q / turns] + q % turns * LG_THREADS : r.v1;
+                if (v[i] < end)
+                    raw[i] = lg_load<T>(x + (int64_t)v[i] * LG_VEC);
             }
-            bool any = false;
 #pragma unroll
-            for (int i = 0; i < LG_VEC; ++i)
-                any |= counts(lg_short_key<T>(e[i]), v);
-            if (__ballot(any) != 0) {
-#pragma unroll
-                for (int i = 0; i < LG_VEC; ++i)
-                    take(lg_key(e[i], v * LG_VEC + i), counts(lg_short_key<T>(e[i]), v));
+            for (int i = 0; i < AHEAD; ++i) {
+                float e[LG_VEC];
+                if (v[i] < end) {
+                    lg_values<T>(raw[i], e);
+                } else {
+                    const int n = v[i] < r.v1 ? r.rest : 0;
+                    lg_load_part<T>(x + (int64_t)v[i] * LG_VEC, n, e);
+                }
+                offer(v[i], e, take);
             }
         }
     };
-    again([&](uint64_t key, bool is) __attribute__((always_inline)) {
-        const int i = place(is, p.left);
-        if (is && i < LG_LEFT)
-            p.place[i] = key;
-    });
+    if (!known)
+        again(keep);
     __syncthreads();
     const int left = p.left;
     if (left <= LG_LEFT) {
+        // (behind the end: keys of no entry, up to whole eights)
+        if (tid < -left % 8 + 8 && left + tid < LG_LEFT)
+            p.place[left + tid] = 0;
+        __syncthreads();
         for (int i = tid; i < left; i += LG_THREADS) {
             const uint64_t key = p.place[i];
             int larger = 0;
-            for (int j = 0; j < left; ++j)
-                larger += p.place[j] > key;
+            for (int j = 0; j < left; j += 8)
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    larger += p.place[j + h] > key;
             if (larger < k)
                 p.list[larger] = key;
         }
@@ -284,10 +327,11 @@ __device__ __forceinline__ void lg_write_top(const lg_logp_row &r, const uint64_
 
 // The sums of a whole row: quickly, and once more where that was not good.
 template <typename T, bool TOP>
-__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T> &walk, float c, float4 *part, float &best, int &where) {
+__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T> &walk, float c, float4 *part, float &best, int &where,
+                                               uint16_t *tops) {
     {
         lg_sums<true> s;
-        lg_stream<T, LG_ENTROPY, TOP>(walk, c, nullptr, 0, s, best, where);
+        lg_stream<T, LG_ENTROPY, TOP>(walk, c, nullptr, 0, s, best, where, tops);
         const lg_sums<true> t = lg_join_block<LG_ENTROPY>(s, c, part);
         if (lg_good(t))
             return lg_row_of(t);
@@ -306,6 +350,8 @@ template <typename T, int E, bool SLICED>
 __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_logp_args p) {
     __shared__ float4 part[LG_WAVES];
     __shared__ lg_pick<E> pick;
+    extern __shared__ __align__(16) uint16_t vector_tops[];
+    uint16_t *tops = E > 0 && lg_each(a.V, a.slices) <= LG_TOPS ? vector_tops : nullptr;
     const int64_t u = a.first + blockIdx.x;
     const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
     const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
@@ -317,13 +363,13 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_
     lg_row sums;
     if constexpr (SLICED) {
         lg_sums<false> s;
-        lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, 0, s, best, where);
+        lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, r.v0, s, best, where, tops);
         sums = lg_row_of(lg_join_block<LG_ENTROPY>(s, a.c, part));
     } else {
-        sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where);
+        sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where, tops);
     }
     if constexpr (E > 0)
-        lg_select<T, E>(x, r, p.top, best, where, pick);
+        lg_select<T, E>(x, r, p.top, best, where, tops, pick);
     if constexpr (SLICED) {
         if (threadIdx.x == 0) {
             const bool here = lg_inside(target, a.V) && target >= (int64_t)r.v0 * LG_VEC &&
@@ -430,7 +476,7 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a
     } else {
         float best;
         int where;
-        sums = lg_whole_row<T, false>(walk, a.c, part, best, where);
+        sums = lg_whole_row<T, false>(walk, a.c, part, best, where, nullptr);
     }
     const lg_logp_row w(sums);
     if (slice == 0 && threadIdx.x == 0)
@@ -461,11 +507,13 @@ hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     const int64_t units = (int64_t)a.M * a.slices;
     auto run = [&](auto e) {
         constexpr int E = decltype(e)::value;
+        const int each = lg_each(a.V, a.slices);
+        const size_t tops = E > 0 && each <= LG_TOPS ? ((size_t)each * 2 + 15) / 16 * 16 : 0;
         if (a.slices > 1) {
-            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, true><<<n, LG_THREADS, 0, st>>>(a, p); });
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, true><<<n, LG_THREADS, tops, st>>>(a, p); });
             lg_launches(a, a.M, [&](unsigned n) { logprobs_join_kernel<E><<<n, LG_THREADS, 0, st>>>(a, p); });
         } else {
-            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, false><<<n, LG_THREADS, 0, st>>>(a, p); });
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, false><<<n, LG_THREADS, tops, st>>>(a, p); });
         }
     };
     if (p.top == 0)

@@ -405,7 +405,7 @@ struct lg_range {
 };
 
 // Vectors of a slice (the last ones may have fewer).
-__device__ __forceinline__ int lg_each(int V, int slices) {
+__host__ __device__ __forceinline__ int lg_each(int V, int slices) {
     return ((V + LG_VEC - 1) / LG_VEC + slices - 1) / slices;
 }
 
@@ -512,21 +512,26 @@ struct lg_walk {
     }
 };
 
-// The sums of the workgroup's vectors, and, with TOP, the thread's largest entry
-// and the first vector that holds it.  `map` (LG_NAMED): a byte per vector from
-// v0 on.
+// The sums of the workgroup's vectors of a slice from v0 on, and, with TOP, the
+// thread's largest entry and the first vector that holds it, and in `tops` (where
+// given) the upper halves of the vectors' largest entries' keys.  `map` (LG_NAMED):
+// a byte per vector.
 template <typename T, int KIND, bool TOP, bool QUICK>
 __device__ __forceinline__ void lg_stream(lg_walk<T> &walk, float c, const uint8_t *map, int v0,
-                                          lg_sums<QUICK> &s, float &best, int &where) {
+                                          lg_sums<QUICK> &s, float &best, int &where, uint16_t *tops = nullptr) {
     const float slack = QUICK ? LG_SLACK : LG_SLACK / c;
     walk.up([&](const float(&e)[LG_VEC], int at) __attribute__((always_inline)) {
         uint32_t named = 0;
         if constexpr (KIND == LG_NAMED)
             named = map[at - v0];
         const float top = lg_add<KIND>(s, e, c, slack, named);
-        if (TOP && top > best) {
-            best = top;
-            where = at;
+        if (TOP) {
+            if (tops != nullptr)
+                tops[at - v0] = (uint16_t)(lg_ordered(top) >> 16);
+            if (top > best) {
+                best = top;
+                where = at;
+            }
         }
     });
 }

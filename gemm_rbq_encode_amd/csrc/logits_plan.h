@@ -12,6 +12,8 @@ constexpr int LG_THREADS = 512;      // threads of a workgroup on logits
 constexpr int LG_VEC = 8;            // consecutive logits a thread takes at a time
 constexpr int LG_SLICES_MAX = 256;   // slices of a row
 
+constexpr int LG_TOPS = 1 << 14;     // vectors of a slice whose maxima LDS holds
+
 // Slices of a row: enough that M rows make about four workgroups per compute
 // unit, each thread with one vector at least.
 inline int logits_slices(int M, int vocab) {
