@@ -42,7 +42,7 @@ struct lg_slots {
 
 // The workgroup's sums over a slice; the bits of the named tokens in it are set
 // in `map`, a chunk of LG_MAP vectors at a time.
-template <typename T, int KIND, bool QUICK>
+template <typename T, int KIND, bool QUICK, int TH>
 __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const lg_range &r, const lg_slots &sl,
                                                int slots, float c, uint32_t *map, float4 *part) {
     const int tid = threadIdx.x;
@@ -54,25 +54,25 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
             lg_range q = r;
             q.v0 = v0;
             q.v1 = min(r.v1, v0 + LG_MAP);
-            for (int i = tid; i < (q.v1 - q.v0 + 3) / 4; i += LG_THREADS)
+            for (int i = tid; i < (q.v1 - q.v0 + 3) / 4; i += TH)
                 map[i] = 0;
             __syncthreads();
-            for (int j = tid; j < slots; j += LG_THREADS) {
+            for (int j = tid; j < slots; j += TH) {
                 const int i = sl.index[j];
                 const int bit = i - q.v0 * LG_VEC;
                 if (i >= 0 && bit >= 0 && i / LG_VEC < q.v1)
                     atomicOr(&map[bit >> 5], 1u << (bit & 31));
             }
             __syncthreads();
-            lg_walk<T> walk(x, q);
+            lg_walk<T, TH> walk(x, q);
             lg_stream<T, KIND, false>(walk, c, (const uint8_t *)map, q.v0, s, best, where);
             __syncthreads();
         }
     } else {
-        lg_walk<T> walk(x, r);
+        lg_walk<T, TH> walk(x, r);
         lg_stream<T, KIND, false>(walk, c, nullptr, 0, s, best, where);
     }
-    const lg_sums<QUICK> t = lg_join_block<KIND>(s, c, part);
+    const lg_sums<QUICK> t = lg_join_block<KIND, TH>(s, c, part);
     if constexpr (QUICK)
         if (!lg_good(t))
             return {t.m, __builtin_nanf(""), 0.0f, true};
@@ -80,10 +80,10 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
 }
 
 // dx = e w of a slice.
-template <typename T, bool QUICK>
+template <typename T, bool QUICK, int TH>
 __device__ __forceinline__ void distill_write(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
                                               float m, float c, float w) {
-    lg_walk<T> walk(x, r);
+    lg_walk<T, TH> walk(x, r);
     walk.down(dx, [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LG_VEC; ++i)
@@ -215,9 +215,9 @@ __device__ __forceinline__ float distill_loss(const lg_row &t, double S, float c
     return (float)loss;
 }
 
-template <typename T, int KIND, int MODE, bool GRAD>
-__global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_distill_args p) {
-    __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : LG_WAVES];
+template <typename T, int KIND, int MODE, bool GRAD, int TH>
+__global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_args p) {
+    __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : TH / 64];
     __shared__ lg_slots sl;
     extern __shared__ uint32_t map[];
     const int tid = threadIdx.x;
@@ -234,20 +234,20 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
         distill_teacher<KIND>(t_logp, p.slots, sl);
     lg_row t;
     if constexpr (MODE == DS_REST) {
-        for (int i = tid; i < a.slices; i += LG_THREADS)
+        for (int i = tid; i < a.slices; i += TH)
             part[i] = a.sums[(int64_t)row * a.slices + i];
         __syncthreads();
         t = lg_row_of(lg_join_list<KIND, false>(part, a.slices, a.c));
     } else if constexpr (MODE == DS_SUMS) {
-        t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
+        t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part);
         if (tid == 0)
             a.sums[u] = make_float4(t.m, t.S, t.b, 0.0f);
         return;
     } else {
-        t = distill_sums<T, KIND, true>(x, r, sl, p.slots, a.c, map, part);
+        t = distill_sums<T, KIND, true, TH>(x, r, sl, p.slots, a.c, map, part);
         if (t.S != t.S) {
             __syncthreads();
-            t = distill_sums<T, KIND, false>(x, r, sl, p.slots, a.c, map, part);
+            t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part);
         }
     }
     const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
         typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
         const float d = p.d_loss[row];
         if (d == 0.0f || S == 0.0 || (KIND != LG_NAMED && !sl.any && !sl.bad)) {
-            lg_zero<T>(dx, r);
+            lg_zero<T, TH>(dx, r);
             return;
         }
         const double by = sl.bad ? __builtin_nan("") : (double)d * (double)a.inv_t;
@@ -268,11 +268,11 @@ __global__ __launch_bounds__(LG_THREADS) void distill_kernel(lg_row_args a, lg_d
         const double away = KIND == LG_NAMED && sl.rest != 0.0 && t.S != 0.0f ? by * sl.rest / (double)t.S : 0.0;
         // (every slot's logit has been read: dx may be x)
         if (MODE == DS_WHOLE && t.quick)
-            distill_write<T, true>(x, dx, r, t.m, a.c, (float)(all - away));
+            distill_write<T, true, TH>(x, dx, r, t.m, a.c, (float)(all - away));
         else
-            distill_write<T, false>(x, dx, r, t.m, a.c, (float)(all - away));
+            distill_write<T, false, TH>(x, dx, r, t.m, a.c, (float)(all - away));
         __syncthreads();    // then the named tokens, a thread a slot; a token named twice gets both in each
-        for (int j = tid; j < p.slots; j += LG_THREADS) {
+        for (int j = tid; j < p.slots; j += TH) {
             const int i = sl.index[j];
             if (i < 0 || i / LG_VEC < r.v0 || i / LG_VEC >= r.v1)
                 continue;
@@ -291,18 +291,28 @@ hipError_t distill_of(lg_row_args a, const lg_distill_args &p, hipStream_t st) {
     const int64_t units = (int64_t)a.M * a.slices;
     const int vectors = (a.V + LG_VEC - 1) / LG_VEC, each = (vectors + a.slices - 1) / a.slices;
     const size_t map = KIND == LG_NAMED ? (size_t)((each < LG_MAP ? each : LG_MAP) + 3) / 4 * 4 : 0;
-    if (a.slices == 1) {
-        lg_launches(a, units, [&](unsigned n) {
-            distill_kernel<T, KIND, DS_WHOLE, GRAD><<<n, LG_THREADS, map, st>>>(a, p);
-        });
-    } else {
-        lg_launches(a, units, [&](unsigned n) {
-            distill_kernel<T, KIND, DS_SUMS, false><<<n, LG_THREADS, map, st>>>(a, p);
-        });
-        lg_launches(a, GRAD ? units : a.M, [&](unsigned n) {
-            distill_kernel<T, KIND, DS_REST, GRAD><<<n, LG_THREADS, 0, st>>>(a, p);
-        });
-    }
+    auto run = [&](auto th) {
+        constexpr int TH = decltype(th)::value;
+        if (a.slices == 1) {
+            lg_launches(a, units, [&](unsigned n) {
+                distill_kernel<T, KIND, DS_WHOLE, GRAD, TH><<<n, TH, map, st>>>(a, p);
+            });
+        } else {
+            lg_launches(a, units, [&](unsigned n) {
+                distill_kernel<T, KIND, DS_SUMS, false, TH><<<n, TH, map, st>>>(a, p);
+            });
+            lg_launches(a, GRAD ? units : a.M, [&](unsigned n) {
+                distill_kernel<T, KIND, DS_REST, GRAD, TH><<<n, TH, 0, st>>>(a, p);
+            });
+        }
+    };
+    const int threads = logits_threads(each, 0);
+    if (threads == 512)
+        run(std::integral_constant<int, 512>{});
+    else if (threads == 256)
+        run(std::integral_constant<int, 256>{});
+    else
+        run(std::integral_constant<int, 128>{});
     return hipGetLastError();
 }
 

@@ -31,21 +31,23 @@ constexpr float LN2 = 0.6931471805599453f;
 // too long for that, or too many vectors come into question (equal entries), all
 // vectors of those k threads are read again: 16 bytes of a line each, which for 64
 // threads costs as much as the whole row.
-constexpr int LG_LEFT = 1024;       // entries left that are placed by counting
+constexpr int LG_LEFT = 1024;       // most entries left that are placed so,
+constexpr int LG_COUNTED = 256;     // and most that are counted before the k-th is looked for
 
-template <int E>
+template <int E, int TH>
 struct lg_pick {        // (LDS)
     uint64_t list[64 * E];          // the result, 0 behind its end
-    uint32_t key[LG_THREADS];
-    int where[LG_THREADS], group[RBQ_TOP_MAX];
+    uint32_t key[TH];
+    int where[TH], group[RBQ_TOP_MAX];
     uint32_t least;                 // key of the k-th thread's largest entry,
     int limit;                      // the last vector that counts where an entry equals it
     int groups, left, vectors;
+    uint64_t first;
     int vector[LG_LEFT];            // vectors to read again
     union {
         uint64_t place[LG_LEFT];
         struct {
-            uint64_t lists[LG_WAVES * 64 * E], waiting[LG_WAVES * 64 * E];
+            uint64_t lists[(TH / 64) * 64 * E], waiting[(TH / 64) * 64 * E];
         };
     };
 };
@@ -58,22 +60,14 @@ __device__ __forceinline__ uint32_t lg_short_key(float v) {
     return v > -__builtin_inff() ? lg_ordered(v) >> SPARE : 0;
 }
 
-template <>
-struct lg_pick<0> {};
+template <int TH>
+struct lg_pick<0, TH> {};
 
-// One wave finds the least key and the limit.
-__device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, int k, uint32_t &least, int &limit) {
-    constexpr int N = LG_THREADS / 64;
-    const int lane = threadIdx.x & 63;
-    // (a lane's two largest: 64 lanes have k entries no less than the least of the
-    // lanes' largest, or second largest, which is where the search starts)
-    uint32_t key[N], most = 0, second = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        key[i] = keys[i * 64 + lane];
-        second = max(second, min(most, key[i]));
-        most = max(most, key[i]);
-    }
+// Of 64 N keys (0: none), N a lane, one wave finds the k-th largest and, where
+// several equal it, the last place (at(i) of a lane's key i, all different) that
+// still belongs to the k largest.
+template <int N, typename AT>
+__device__ __forceinline__ void lg_find(const uint32_t (&key)[N], AT at, int k, uint32_t &least, int &limit) {
     auto count = [&](uint32_t t) __attribute__((always_inline)) {
         int n = 0;
 #pragma unroll
@@ -81,10 +75,18 @@ __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, 
             n += __popcll(__ballot(key[i] >= t));
         return n;
     };
+    // (a lane's two largest: 64 lanes have k keys no less than the least of the
+    // lanes' largest, or second largest, which is where the search starts)
+    uint32_t most = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        second = max(second, min(most, key[i]));
+        most = max(most, key[i]);
+    }
     limit = 0x7FFFFFFF;
     uint32_t lo = max(1u, ~wave_max_u32_dpp(~(k <= 64 ? most : second))), hi = wave_max_u32_dpp(most) + 1;
     int above = 0;                  // keys >= hi
-    if (count(lo) <= k) {           // just k, or every thread with an entry
+    if (count(lo) <= k) {           // just k, or all there are
         least = lo;
         return;
     }
@@ -102,19 +104,23 @@ __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, 
             above = n;
         }
     }
-    // more than one thread has the k-th key: those of them that come first
+    // more than one has the k-th key: those of them that come first
     least = lo;
-    int at[N];
+    int place[N];
+    uint32_t far = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        at[i] = key[i] == lo ? where[i * 64 + lane] : 0x7FFFFFFF;
-    int no = -1, yes = 0x7FFFFFFE;
+    for (int i = 0; i < N; ++i) {
+        const bool is = key[i] == lo;
+        place[i] = is ? at(i) : 0x7FFFFFFF;
+        far = max(far, is ? (uint32_t)place[i] : 0u);
+    }
+    int no = -1, yes = (int)wave_max_u32_dpp(far);
     while (yes - no > 1) {
         const int mid = no + (yes - no) / 2;
         int n = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            n += __popcll(__ballot(at[i] <= mid));
+            n += __popcll(__ballot(place[i] <= mid));
         if (n >= k - above)
             yes = mid;
         else
@@ -123,9 +129,9 @@ __device__ __forceinline__ void lg_find(const uint32_t *keys, const int *where, 
     limit = yes;
 }
 
-template <typename T, int E>
+template <typename T, int E, int TH>
 __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_range &r, int k, float best, int where,
-                                          const uint16_t *tops, lg_pick<E> &p) {
+                                          const uint16_t *tops, lg_pick<E, TH> &p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t mine = lg_short_key<T>(best);
     p.key[tid] = mine;
@@ -134,9 +140,12 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
         p.groups = p.left = p.vectors = 0;
     __syncthreads();
     if (wave == 0) {
-        uint32_t least;
+        uint32_t key[TH / 64], least;
         int limit;
-        lg_find(p.key, p.where, k, least, limit);
+#pragma unroll
+        for (int i = 0; i < TH / 64; ++i)
+            key[i] = p.key[i * 64 + lane];
+        lg_find(key, [&](int i) __attribute__((always_inline)) { return p.where[i * 64 + lane]; }, k, least, limit);
         if (lane == 0) {
             p.least = least;
             p.limit = limit;
@@ -164,7 +173,7 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
     };
     if (tops != nullptr) {
         const uint32_t bound = (least << T::SPARE) >> 16;
-        for (int i = tid * 8; i < n; i += LG_THREADS * 8) {
+        for (int i = tid * 8; i < n; i += TH * 8) {
             const uint4 w = *(const uint4 *)(tops + i);
             const uint32_t h[8] = {w.x & 0xFFFF, w.x >> 16, w.y & 0xFFFF, w.y >> 16,
                                    w.z & 0xFFFF, w.z >> 16, w.w & 0xFFFF, w.w >> 16};
@@ -184,7 +193,7 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
     const int vectors = p.vectors;
     const bool known = tops != nullptr && vectors <= LG_LEFT;
     if (known) {
-        for (int i = tid; i < vectors; i += LG_THREADS) {
+        for (int i = tid; i < vectors; i += TH) {
             const int v = p.vector[i];
             float e[LG_VEC];
             if (v < end)
@@ -194,19 +203,19 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
             offer(v, e, keep);
         }
     }
-    const int groups = p.groups, turns = (n + LG_THREADS - 1) / LG_THREADS;
+    const int groups = p.groups, turns = (n + TH - 1) / TH;
     // take(key, whether it counts) of those threads' entries; every lane of a wave
     // takes part each time
     constexpr int AHEAD = 4;
     auto again = [&](auto take) __attribute__((always_inline)) {
         const int items = groups * turns;
-        for (int q0 = wave * 64; q0 < items; q0 += AHEAD * LG_THREADS) {
+        for (int q0 = wave * 64; q0 < items; q0 += AHEAD * TH) {
             typename T::raw raw[AHEAD];
             int v[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                const int q = q0 + i * LG_THREADS + lane;
-                v[i] = q < items ? r.v0 + p.group[q / turns] + q % turns * LG_THREADS : r.v1;
+                const int q = q0 + i * TH + lane;
+                v[i] = q < items ? r.v0 + p.group[q / turns] + q % turns * TH : r.v1;
                 if (v[i] < end)
                     raw[i] = lg_load<T>(x + (int64_t)v[i] * LG_VEC);
             }
@@ -228,29 +237,65 @@ __device__ __forceinline__ void lg_select(const typename T::bits *x, const lg_ra
     __syncthreads();
     const int left = p.left;
     if (left <= LG_LEFT) {
+        int ranked = left;
+        uint64_t first = 1;     // the least key that counts
+        if (left > LG_COUNTED) {
+            // too many to count: the k-th largest is looked for first
+            if (wave == 0) {
+                uint32_t key[LG_LEFT / 64], kth;
+                int last;
+#pragma unroll
+                for (int i = 0; i < LG_LEFT / 64; ++i)
+                    key[i] = i * 64 + lane < left ? (uint32_t)(p.place[i * 64 + lane] >> 32) : 0;
+                lg_find(key, [&](int i) __attribute__((always_inline)) { return lg_index(p.place[i * 64 + lane]); }, k, kth, last);
+                if (lane == 0)
+                    p.first = (uint64_t)kth << 32 | (uint32_t)~last;
+            }
+            __syncthreads();
+            first = p.first;
+        }
         // (behind the end: keys of no entry, up to whole eights)
         if (tid < -left % 8 + 8 && left + tid < LG_LEFT)
             p.place[left + tid] = 0;
         __syncthreads();
-        for (int i = tid; i < left; i += LG_THREADS) {
+        if (left > LG_COUNTED) {
+            // those that count, moved together
+            uint64_t mine[LG_LEFT / TH];
+#pragma unroll
+            for (int i = 0; i < LG_LEFT / TH; ++i)
+                mine[i] = i * TH + tid < left ? p.place[i * TH + tid] : 0;
+            if (tid == 0)
+                p.left = 0;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < LG_LEFT / TH; ++i)
+                if (mine[i] >= first)
+                    p.place[atomicAdd(&p.left, 1)] = mine[i];
+            __syncthreads();
+            ranked = p.left;
+            if (tid < -ranked % 8 + 8)
+                p.place[ranked + tid] = 0;
+            __syncthreads();
+        }
+        for (int i = tid; i < ranked; i += TH) {
             const uint64_t key = p.place[i];
             int larger = 0;
-            for (int j = 0; j < left; j += 8)
+            for (int j = 0; j < ranked; j += 8)
 #pragma unroll
                 for (int h = 0; h < 8; ++h)
                     larger += p.place[j + h] > key;
             if (larger < k)
                 p.list[larger] = key;
         }
-        for (int j = left + tid; j < k; j += LG_THREADS)
+        for (int j = left + tid; j < k; j += TH)
             p.list[j] = 0;
     } else {        // rows made for it (many entries above the k-th maximum with few threads)
         lg_top<E> top;
         top.start(p.waiting + wave * 64 * E);
         again([&](uint64_t key, bool is) __attribute__((always_inline)) { top.offer(key, is); });
         top.settle();
-        lg_block_merge<E, LG_WAVES>(top.k, p.lists);
-        for (int j = tid; j < k; j += LG_THREADS)
+        lg_block_merge<E, TH / 64>(top.k, p.lists);
+        for (int j = tid; j < k; j += TH)
             p.list[j] = p.lists[j];
     }
     __syncthreads();
@@ -326,13 +371,13 @@ __device__ __forceinline__ void lg_write_top(const lg_logp_row &r, const uint64_
 }
 
 // The sums of a whole row: quickly, and once more where that was not good.
-template <typename T, bool TOP>
-__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T> &walk, float c, float4 *part, float &best, int &where,
+template <typename T, bool TOP, int TH>
+__device__ __forceinline__ lg_row lg_whole_row(lg_walk<T, TH> &walk, float c, float4 *part, float &best, int &where,
                                                uint16_t *tops) {
     {
         lg_sums<true> s;
         lg_stream<T, LG_ENTROPY, TOP>(walk, c, nullptr, 0, s, best, where, tops);
-        const lg_sums<true> t = lg_join_block<LG_ENTROPY>(s, c, part);
+        const lg_sums<true> t = lg_join_block<LG_ENTROPY, TH>(s, c, part);
         if (lg_good(t))
             return lg_row_of(t);
     }
@@ -341,15 +386,15 @@ __device__ __forceinline__ lg_row lg_whole_row(lg_walk<T> &walk, float c, float4
     float b2;
     int w2;
     lg_stream<T, LG_ENTROPY, false>(walk, c, nullptr, 0, s, b2, w2);
-    return lg_row_of(lg_join_block<LG_ENTROPY>(s, c, part));
+    return lg_row_of(lg_join_block<LG_ENTROPY, TH>(s, c, part));
 }
 
 // The sums of a slice per workgroup (SLICED), or a whole row, and its largest
 // entries.  E = 0: none.
-template <typename T, int E, bool SLICED>
-__global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_logp_args p) {
-    __shared__ float4 part[LG_WAVES];
-    __shared__ lg_pick<E> pick;
+template <typename T, int E, int TH, bool SLICED>
+__global__ __launch_bounds__(TH) void logprobs_kernel(lg_row_args a, lg_logp_args p) {
+    __shared__ float4 part[(TH / 64)];
+    __shared__ lg_pick<E, TH> pick;
     extern __shared__ __align__(16) uint16_t vector_tops[];
     uint16_t *tops = E > 0 && lg_each(a.V, a.slices) <= LG_TOPS ? vector_tops : nullptr;
     const int64_t u = a.first + blockIdx.x;
@@ -359,17 +404,17 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_
     const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
     float best = -__builtin_inff();
     int where = 0;
-    lg_walk<T> walk(x, r);
+    lg_walk<T, TH> walk(x, r);
     lg_row sums;
     if constexpr (SLICED) {
         lg_sums<false> s;
         lg_stream<T, LG_ENTROPY, (E > 0)>(walk, a.c, nullptr, r.v0, s, best, where, tops);
-        sums = lg_row_of(lg_join_block<LG_ENTROPY>(s, a.c, part));
+        sums = lg_row_of(lg_join_block<LG_ENTROPY, TH>(s, a.c, part));
     } else {
         sums = lg_whole_row<T, (E > 0)>(walk, a.c, part, best, where, tops);
     }
     if constexpr (E > 0)
-        lg_select<T, E>(x, r, p.top, best, where, tops, pick);
+        lg_select<T, E, TH>(x, r, p.top, best, where, tops, pick);
     if constexpr (SLICED) {
         if (threadIdx.x == 0) {
             const bool here = lg_inside(target, a.V) && target >= (int64_t)r.v0 * LG_VEC &&
@@ -377,7 +422,7 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_
             a.sums[u] = make_float4(sums.m, sums.S, sums.b, here ? T::one(x[target]) : 0.0f);
         }
         if constexpr (E > 0)
-            for (int j = threadIdx.x; j < p.top; j += LG_THREADS)
+            for (int j = threadIdx.x; j < p.top; j += TH)
                 a.keys[u * p.top + j] = pick.list[j];
     } else {
         const lg_logp_row w(sums);
@@ -389,21 +434,23 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_kernel(lg_row_args a, lg_
 }
 
 // The slices of a row joined.
+constexpr int LG_JOIN = 512;
+
 template <int E>
-__global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a, lg_logp_args p) {
-    constexpr int N = LG_WAVES * 64 * (E > 0 ? E : 1);
+__global__ __launch_bounds__(LG_JOIN) void logprobs_join_kernel(lg_row_args a, lg_logp_args p) {
+    constexpr int N = (LG_JOIN / 64) * 64 * (E > 0 ? E : 1);
     __shared__ float4 part[LG_SLICES_MAX];
     __shared__ uint64_t lists[E > 0 ? N : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = (int)(a.first + blockIdx.x);
-    for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
+    for (int i = threadIdx.x; i < a.slices; i += LG_JOIN)
         part[i] = a.sums[(int64_t)row * a.slices + i];
     if constexpr (E > 0) {
         uint64_t best[E], next[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
             best[e] = 0;
-        for (int i = wave; i < a.slices; i += LG_WAVES) {
+        for (int i = wave; i < a.slices; i += (LG_JOIN / 64)) {
             const uint64_t *list = a.keys + ((int64_t)row * a.slices + i) * p.top;
             lg_wave_sync();
 #pragma unroll
@@ -415,7 +462,7 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a
             lg_merge<E>(best, lists + wave * 64 * E);
         }
         __syncthreads();
-        lg_block_merge<E, LG_WAVES>(best, lists);
+        lg_block_merge<E, LG_JOIN / 64>(best, lists);
     }
     __syncthreads();
     const lg_logp_row w(lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c)));
@@ -432,8 +479,8 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_join_kernel(lg_row_args a
 // with p_v = e_v / S and ln p_v = ln 2 (d_v - log2 S), so that the part without
 // the target is e_v (w0 + w1 d_v).  Where rows are whole the sums are formed here,
 // and the second pass over the row finds it in the caches.
-template <typename T, bool QUICK, bool ENTROPY>
-__device__ __forceinline__ void lg_logp_grad(lg_walk<T> &walk, typename T::bits *dx, float m, float c, float w0,
+template <typename T, bool QUICK, bool ENTROPY, int TH>
+__device__ __forceinline__ void lg_logp_grad(lg_walk<T, TH> &walk, typename T::bits *dx, float m, float c, float w0,
                                              float w1, int at, int in, float own) {
     walk.down(dx, [&](float(&e)[LG_VEC], int v) __attribute__((always_inline)) {
 #pragma unroll
@@ -450,8 +497,8 @@ __device__ __forceinline__ void lg_logp_grad(lg_walk<T> &walk, typename T::bits 
     });
 }
 
-template <typename T, bool SLICED, bool ENTROPY>
-__global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
+template <typename T, int TH, bool SLICED, bool ENTROPY>
+__global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
     __shared__ float4 part[LG_SLICES_MAX];
     const int64_t u = a.first + blockIdx.x;
     const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
@@ -463,13 +510,13 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a
     const float wb = ENTROPY ? p.d_entropy[row] : 0.0f;
     const bool none = wa == 0.0f && wb == 0.0f;
     if (none && p.logp == nullptr && p.entropy == nullptr) {
-        lg_zero<T>(dx, r);
+        lg_zero<T, TH>(dx, r);
         return;
     }
-    lg_walk<T> walk(x, r);
+    lg_walk<T, TH> walk(x, r);
     lg_row sums;
     if constexpr (SLICED) {
-        for (int i = threadIdx.x; i < a.slices; i += LG_THREADS)
+        for (int i = threadIdx.x; i < a.slices; i += TH)
             part[i] = a.sums[(int64_t)row * a.slices + i];
         __syncthreads();
         sums = lg_row_of(lg_join_list<LG_ENTROPY, false>(part, a.slices, a.c));
@@ -486,7 +533,7 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a
                                                  : 0.0f,
                       target, row, a, p);
     if (none || w.empty) {
-        lg_zero<T>(dx, r);
+        lg_zero<T, TH>(dx, r);
     } else {
         const float scale = a.inv_t / w.S;
         const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
@@ -502,38 +549,55 @@ __global__ __launch_bounds__(LG_THREADS) void logprobs_grad_kernel(lg_row_args a
     __syncthreads();
 }
 
+// f(threads of a workgroup) for a slice of `each` vectors and k alternatives.
+template <typename F>
+void with_threads(int each, int k, F f) {
+    const int n = logits_threads(each, k);
+    if (n == 512)
+        f(std::integral_constant<int, 512>{});
+    else if (n == 256)
+        f(std::integral_constant<int, 256>{});
+    else
+        f(std::integral_constant<int, 128>{});
+}
+
 template <typename T>
 hipError_t logprobs_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     const int64_t units = (int64_t)a.M * a.slices;
-    auto run = [&](auto e) {
-        constexpr int E = decltype(e)::value;
-        const int each = lg_each(a.V, a.slices);
+    const int each = lg_each(a.V, a.slices);
+    auto run = [&](auto e, auto th) {
+        constexpr int E = decltype(e)::value, TH = decltype(th)::value;
         const size_t tops = E > 0 && each <= LG_TOPS ? ((size_t)each * 2 + 15) / 16 * 16 : 0;
         if (a.slices > 1) {
-            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, true><<<n, LG_THREADS, tops, st>>>(a, p); });
-            lg_launches(a, a.M, [&](unsigned n) { logprobs_join_kernel<E><<<n, LG_THREADS, 0, st>>>(a, p); });
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, TH, true><<<n, TH, tops, st>>>(a, p); });
+            lg_launches(a, a.M, [&](unsigned n) { logprobs_join_kernel<E><<<n, LG_JOIN, 0, st>>>(a, p); });
         } else {
-            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, false><<<n, LG_THREADS, tops, st>>>(a, p); });
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, E, TH, false><<<n, TH, tops, st>>>(a, p); });
         }
     };
-    if (p.top == 0)
-        run(std::integral_constant<int, 0>{});
-    else if (p.top <= 64)
-        run(std::integral_constant<int, 1>{});
-    else
-        run(std::integral_constant<int, 2>{});
+    with_threads(each, p.top, [&](auto th) {
+        if (p.top == 0)
+            run(std::integral_constant<int, 0>{}, th);
+        else if (p.top <= 64)
+            run(std::integral_constant<int, 1>{}, th);
+        else if constexpr (decltype(th)::value > 128)
+            run(std::integral_constant<int, 2>{}, th);
+    });
     return hipGetLastError();
 }
 
 template <typename T, bool ENTROPY>
 hipError_t logprobs_grad_of(lg_row_args a, const lg_logp_args &p, hipStream_t st) {
     const int64_t units = (int64_t)a.M * a.slices;
-    if (a.slices > 1) {
-        lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, 0, true><<<n, LG_THREADS, 0, st>>>(a, p); });
-        lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, true, ENTROPY><<<n, LG_THREADS, 0, st>>>(a, p); });
-    } else {
-        lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, false, ENTROPY><<<n, LG_THREADS, 0, st>>>(a, p); });
-    }
+    with_threads(lg_each(a.V, a.slices), 0, [&](auto th) {
+        constexpr int TH = decltype(th)::value;
+        if (a.slices > 1) {
+            lg_launches(a, units, [&](unsigned n) { logprobs_kernel<T, 0, TH, true><<<n, TH, 0, st>>>(a, p); });
+            lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, TH, true, ENTROPY><<<n, TH, 0, st>>>(a, p); });
+        } else {
+            lg_launches(a, units, [&](unsigned n) { logprobs_grad_kernel<T, TH, false, ENTROPY><<<n, TH, 0, st>>>(a, p); });
+        }
+    });
     return hipGetLastError();
 }
 

@@ -8,7 +8,6 @@
 
 namespace rbq {
 
-constexpr int LG_WAVES = LG_THREADS / RBQ_WAVE;
 constexpr float LG_LOWEST = -3.402823466e38f;   // the lowest finite float
 constexpr float LG_FAR = -1.0e4f;               // exponents below this are 0 in any case
 
@@ -232,13 +231,13 @@ __device__ __forceinline__ lg_sums<QUICK> lg_join_list(const float4 *v, int n, f
 }
 
 // All threads' sums (in every thread); `part` holds one float4 per wave.
-template <int KIND, bool QUICK>
+template <int KIND, int TH, bool QUICK>
 __device__ __forceinline__ lg_sums<QUICK> lg_join_block(const lg_sums<QUICK> &s, float c, float4 *part) {
     const lg_sums<QUICK> w = lg_join_wave<KIND>(s, c);
     if ((threadIdx.x & 63) == 0)
         part[threadIdx.x >> 6] = make_float4(w.m, w.a, w.b, 0.0f);
     __syncthreads();
-    return lg_join_list<KIND, QUICK>(part, LG_WAVES, c);
+    return lg_join_list<KIND, QUICK>(part, TH / 64, c);
 }
 
 // ---- the largest entries ----------------------------------------------------------
@@ -421,7 +420,7 @@ __device__ __forceinline__ lg_range lg_slice(int V, int slices, int s) {
 
 // A thread's vectors of a slice: those of `turns` whole turns of the workgroup,
 // one more where `more`, and the row's last one, part empty, where `part`.
-template <typename T>
+template <typename T, int TH>
 struct lg_walk {
     static constexpr int AHEAD = 4;
     const typename T::bits *x;
@@ -431,14 +430,14 @@ struct lg_walk {
     __device__ __forceinline__ lg_walk(const typename T::bits *row, const lg_range &r) : x(row) {
         const int end = min(r.v1, r.whole);
         v = r.v0 + (int)threadIdx.x;
-        turns = max(0, end - r.v0) / LG_THREADS;
-        const int last = v + turns * LG_THREADS;
+        turns = max(0, end - r.v0) / TH;
+        const int last = v + turns * TH;
         more = last < end;
-        part = (more ? last + LG_THREADS : last) == r.whole && r.v1 > r.whole;
+        part = (more ? last + TH : last) == r.whole && r.v1 > r.whole;
         rest = r.rest;
     }
     __device__ __forceinline__ const typename T::bits *at(int turn) const {
-        return x + (int64_t)(v + turn * LG_THREADS) * LG_VEC;
+        return x + (int64_t)(v + turn * TH) * LG_VEC;
     }
     // f(values, vector) of all, upwards
     template <typename F>
@@ -453,7 +452,7 @@ struct lg_walk {
             for (int i = 0; i < AHEAD; ++i) {
                 float e[LG_VEC];
                 lg_values<T>(raw[i], e);
-                f(e, v + (t + i) * LG_THREADS);
+                f(e, v + (t + i) * TH);
             }
         }
         for (; t < turns; ++t)
@@ -463,14 +462,14 @@ struct lg_walk {
         if (part) {
             float e[LG_VEC];
             lg_load_part<T>(at(turns + more), rest, e);
-            f(e, v + (turns + more) * LG_THREADS);
+            f(e, v + (turns + more) * TH);
         }
     }
     template <typename F>
     __device__ __forceinline__ void one(int t, F f) {
         float e[LG_VEC];
         lg_values<T>(lg_load<T>(at(t)), e);
-        f(e, v + t * LG_THREADS);
+        f(e, v + t * TH);
     }
     // out = f(values, vector) of all, downwards: what was read last is still in
     // the caches.  A thread writes what it has read itself, so `out` may be x.
@@ -479,9 +478,9 @@ struct lg_walk {
     __device__ __forceinline__ void down(typename T::bits *out, F f) {
         if (part) {
             float e[LG_VEC];
-            const int64_t at_ = (int64_t)(v + (turns + more) * LG_THREADS) * LG_VEC;
+            const int64_t at_ = (int64_t)(v + (turns + more) * TH) * LG_VEC;
             lg_load_part<T>(x + at_, rest, e);
-            f(e, v + (turns + more) * LG_THREADS);
+            f(e, v + (turns + more) * TH);
             lg_store_part<T>(out + at_, rest, e);
         }
         if (more)
@@ -496,8 +495,8 @@ struct lg_walk {
             for (int i = 0; i < AHEAD; ++i) {
                 float e[LG_VEC];
                 lg_values<T>(raw[i], e);
-                f(e, v + (t - 1 - i) * LG_THREADS);
-                lg_store<T>(out + (int64_t)(v + (t - 1 - i) * LG_THREADS) * LG_VEC, e);
+                f(e, v + (t - 1 - i) * TH);
+                lg_store<T>(out + (int64_t)(v + (t - 1 - i) * TH) * LG_VEC, e);
             }
         }
         for (; t > 0; --t)
@@ -507,8 +506,8 @@ struct lg_walk {
     __device__ __forceinline__ void back(typename T::bits *out, int t, F f) {
         float e[LG_VEC];
         lg_values<T>(lg_load<T>(at(t)), e);
-        f(e, v + t * LG_THREADS);
-        lg_store<T>(out + (int64_t)(v + t * LG_THREADS) * LG_VEC, e);
+        f(e, v + t * TH);
+        lg_store<T>(out + (int64_t)(v + t * TH) * LG_VEC, e);
     }
 };
 
@@ -516,8 +515,8 @@ struct lg_walk {
 // thread's largest entry and the first vector that holds it, and in `tops` (where
 // given) the upper halves of the vectors' largest entries' keys.  `map` (LG_NAMED):
 // a byte per vector.
-template <typename T, int KIND, bool TOP, bool QUICK>
-__device__ __forceinline__ void lg_stream(lg_walk<T> &walk, float c, const uint8_t *map, int v0,
+template <typename T, int KIND, bool TOP, int TH, bool QUICK>
+__device__ __forceinline__ void lg_stream(lg_walk<T, TH> &walk, float c, const uint8_t *map, int v0,
                                           lg_sums<QUICK> &s, float &best, int &where, uint16_t *tops = nullptr) {
     const float slack = QUICK ? LG_SLACK : LG_SLACK / c;
     walk.up([&](const float(&e)[LG_VEC], int at) __attribute__((always_inline)) {
@@ -550,10 +549,10 @@ __device__ __forceinline__ lg_row lg_row_of(const lg_sums<QUICK> &t) {
     return {t.m, t.a, t.b, QUICK};
 }
 
-template <typename T>
+template <typename T, int TH>
 __device__ __forceinline__ void lg_zero(typename T::bits *out, const lg_range &r) {
     const float zero[LG_VEC] = {};
-    for (int v = r.v0 + (int)threadIdx.x; v < r.v1; v += LG_THREADS) {
+    for (int v = r.v0 + (int)threadIdx.x; v < r.v1; v += TH) {
         if (v < r.whole)
             lg_store<T>(out + (int64_t)v * LG_VEC, zero);
         else

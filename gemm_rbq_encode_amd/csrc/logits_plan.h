@@ -8,7 +8,7 @@
 
 namespace rbq {
 
-constexpr int LG_THREADS = 512;      // threads of a workgroup on logits
+constexpr int LG_THREADS = 512;      // threads of a workgroup on a long row
 constexpr int LG_VEC = 8;            // consecutive logits a thread takes at a time
 constexpr int LG_SLICES_MAX = 256;   // slices of a row
 
@@ -21,6 +21,21 @@ inline int logits_slices(int M, int vocab) {
     const int64_t want = std::min<int64_t>((1024 + (int64_t)M - 1) / M, LG_SLICES_MAX);
     const int64_t most = (vectors + LG_THREADS - 1) / LG_THREADS;
     return (int)std::max<int64_t>(1, std::min(want, most));
+}
+
+// Threads of a workgroup on slices of `each` vectors, with k alternatives.  More
+// wait longer for each other at every step of a short row, and share the steps of
+// a long one.  us with 512, 256 and 128 threads, 64 million fp16 logits in rows of
+//                       1000            4000           16000           32000          128256 (2048 rows)
+//   sums alone      176  103   66    66   42   35    34   31   32    29   30   29     96   97
+//   gradient        234  135   86    85   63   58    57   62   67    61   65   64    247  254
+//   distillation    543  287  216   171  114  100    89   78   83    74   78   80    257  278
+//   64 alternatives 750  346  229   208  109   91    76   51   53    54   44   51    118  135
+// More than 64 alternatives need more threads than they are.
+inline int logits_threads(int each, int k) {
+    if (k > 0)
+        return each > 12000 ? 512 : each > 1200 || k > 64 ? 256 : 128;
+    return each > 1800 ? 512 : each > 900 ? 256 : 128;
 }
 
 // Bytes of the partial results of all slices, 0 where a row is one slice: per

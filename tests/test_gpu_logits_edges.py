@@ -141,21 +141,41 @@ def test_gradient_in_the_logits_place(M):
         assert all(torch.equal(p, q) for p, q in zip(ref, got))
 
 
-def test_without_a_workspace():
-    """Rows not cut: the same values within the bounds."""
-    M, V = 3, 40001
+@pytest.mark.parametrize("V", [900, 9000, 20007, 40001, 100003])
+def test_without_a_workspace(V):
+    """Rows not cut, by workgroups of every size: the same values within the bounds."""
+    M = 3
     x = rows(M, V, 12, torch.float16)
     none = torch.empty(0, dtype=torch.uint8, device=dev())
-    targets = torch.tensor([5, 40000, 17], device=dev())
+    targets = torch.tensor([5, V - 1, 17], device=dev())
     r = oracle.Rows(np64(x), 1.0)
-    b = Bound(r, V)
-    b.dS *= 20                               # a thread adds all of its row's terms
-    logp, H, top, idx = rbq.token_logprobs(x, targets, top=65, workspace=none)
-    near(H, r.H, b.H * 20, "entropy")
-    near(logp, r.lp[np.arange(3), targets.cpu().numpy()], 20 * b.lp[np.arange(3), targets.cpu().numpy()], "logp")
-    assert np.array_equal(idx.cpu().numpy(), oracle.top(np64(x), 65))
-    idx, v = teacher(M, V, 64, 4, 1.0)
-    check_distill(rows(M, V, 13, torch.float32, masked=False), idx, v, np.ones(M, np.float32), 1.0, True, workspace=none)
+    b = Bound(r, 8 * V)                      # (a thread adds up to eight times the terms that one of 512 slices' does)
+    at = (np.arange(3), targets.cpu().numpy())
+    for k in (3, 64, 65):
+        logp, H, top, idx = rbq.token_logprobs(x, targets, top=k, workspace=none)
+        near(H, r.H, b.H, "entropy")
+        near(logp, r.lp[at], b.lp[at], "logp")
+        assert np.array_equal(idx.cpu().numpy(), oracle.top(np64(x), k))
+    d = torch.rand(M, device=dev())
+    dx, logp, _ = rbq.token_logprobs_backward(x, targets, d, d, workspace=none)
+    g = oracle.logprobs_grad(r, at[1], d.cpu().double().numpy(), d.cpu().double().numpy())
+    lp = np.where(r.p > 0, np.abs(r.lp), 0.0)
+    tol = r.p * b.rel + 2.0 ** -20 * (g != 0) + r.p * ((lp + r.H[:, None]) * (b.rel + 2.0 ** -20) + b.lp + b.H[:, None])
+    near(dx, g, tol + 2.0 ** -11 * (np.abs(g) + tol) + 2.0 ** -25, "gradient")
+    for tail in (False, True):
+        idx, v = teacher(M, V, 64, 4, 1.0)
+        check_distill(rows(M, V, 13, torch.float32, masked=False), idx, v, np.ones(M, np.float32), 1.0, tail,
+                      workspace=none)
+
+
+@pytest.mark.parametrize("M,V", [(2, 1000), (1030, 1000), (1030, 130), (2, 128), (1030, 4003)])
+def test_more_alternatives_than_threads_have(M, V):
+    """As many alternatives as vectors, or nearly: every entry comes into question."""
+    for seed in (0, 1):
+        x = rows(M, V, seed, torch.float32) if seed else t(np.random.default_rng(2).integers(0, 40, (M, V)), torch.bfloat16)
+        for k in (60, 100, 128):
+            *_, idx = rbq.token_logprobs(x, top=k)
+            assert np.array_equal(idx[:6].cpu().numpy(), oracle.top(np64(x[:6]), k)), k
 
 
 def test_a_workspace_of_any_contents():
