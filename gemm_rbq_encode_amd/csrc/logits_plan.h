@@ -14,10 +14,23 @@ constexpr int LG_SLICES_MAX = 256;   // slices of a row
 
 constexpr int LG_TOPS = 1 << 14;     // vectors of a slice whose maxima LDS holds
 
-// Slices of a row: enough that M rows make about four workgroups per compute
-// unit, each thread with one vector at least.
+// Slices of a row.  Cutting takes a second launch and a second start of every
+// workgroup, so only a few long rows are cut, each thread with one vector at least.
+// us whole / cut, fp16:
+//              sums alone    20 alternatives    gradient      distillation and gradient
+//   1 x  32000   5.2   5.7      11.1  12.9       7.8   7.6       11.1  11.2
+//  64 x  32000   6.4   7.7      13.6  15.4       9.2   9.8       12.9  13.9
+//   1 x  64000   7.3   5.7      14.8  13.4      11.7   7.6       15.1  10.9
+//  64 x  64000   9.0   8.1      18.0  16.7      13.5  10.4       17.1  14.3
+// 256 x  64000  11.0  13.7      20.3  22.2      17.7  21.6       21.9  26.5
+//   1 x 128256  11.9   5.7      19.0  14.8      19.9   7.9       23.5  11.3
+//  64 x 128256  13.9   9.5      22.8  18.8      21.5  13.4       25.6  17.4
+// 128 x 128256  15.2  13.6      24.1  22.2      24.1  21.5       28.4  25.8
+// 256 x 128256  17.3  19.4      26.0  28.6      33.5  38.3       37.0  43.9
 inline int logits_slices(int M, int vocab) {
     const int64_t vectors = ((int64_t)vocab + LG_VEC - 1) / LG_VEC;
+    if (vectors < 6000 || M > vectors / 100)
+        return 1;
     const int64_t want = std::min<int64_t>((1024 + (int64_t)M - 1) / M, LG_SLICES_MAX);
     const int64_t most = (vectors + LG_THREADS - 1) / LG_THREADS;
     return (int)std::max<int64_t>(1, std::min(want, most));

@@ -103,82 +103,179 @@ __global__ __launch_bounds__(Q4E_THREADS) void encode_q4_kernel(const float *__r
 }
 
 // ---------------------------------------------------------------------------
-// few tokens: a workgroup takes 16 rows and up to 16 MT tokens, its waves split
-// the columns in chunks of 512.  A lane holds one row's 32 columns of a group in
-// one 16-byte load, which four matrix instructions take apart; a group's sums
-// are scaled and added in fp32.
+// few tokens: a workgroup takes 16 NT rows and 16 MT tokens; each of its waves takes
+// one group at a time, the next two on their way, and goes through the row tiles
+// with the tokens' operands of that group.  A lane holds one row's 32 columns of a
+// group in one 16-byte load, which four matrix instructions take apart; a group's
+// sums are scaled and added in fp32, the waves' sums in their order.  The rows'
+// scales and zero points pass through LDS (STAGED) where they fit: read by the lanes
+// that use them, 2 bytes of 16 lines each, they took as long as half of the codes
+// (11008 x 4096, one token: 9.9 us with, 7.7 without their loads).
+//
+// Up to 4 tokens (FEW) a group of them is one load, and the four operands of 8
+// columns that a lane would hold for its token are held by four lanes: row 4 m + q of
+// the matrix instruction is part q of token m.  Of its product with part q' of the
+// codes row 4 m + q' counts, which is result q' of lanes 16 m .. 16 m + 15, so the
+// sum over q' needs four instructions, as before, and three additions.
+constexpr int Q4_WAVES = 8;
 
-constexpr int Q4_WAVES = 8, Q4_AHEAD = 4;
+typedef uint32_t q4_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
-template <int MT, bool ZEROS, bool WIDE>
+// n bytes to LDS (any alignment in memory, 16 bytes' in LDS).
+__device__ __forceinline__ void q4_stage(const void *from, uint8_t *to, int n) {
+    const uint8_t *p = (const uint8_t *)from;
+    for (int i = threadIdx.x * 16; i + 16 <= n; i += Q4_WAVES * 64 * 16)
+        *(uint4 *)(to + i) = __builtin_bit_cast(uint4, *(const q4_bytes16 *)(p + i));
+    const int rest = n & 15;
+    if ((int)threadIdx.x < rest)
+        to[n - rest + threadIdx.x] = p[n - rest + threadIdx.x];
+}
+
+template <int MT, int NT, bool FEW, bool STAGED, bool ZEROS, bool WIDE>
 __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_t *__restrict__ codes,
                                                                     const uint16_t *__restrict__ scales,
                                                                     const uint8_t *__restrict__ zeros, int out, int in,
                                                                     int T, const uint16_t *__restrict__ X, int M,
                                                                     void *__restrict__ Y) {
-    __shared__ q4_f32x4 part[Q4_WAVES][MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * MT);
-    const int row = min(r0 + (lane & 15), out - 1), kb = lane >> 4;
-    const uint8_t *w = codes + (int64_t)row * (in / 2) + kb * 16;
-    const uint16_t *s = scales + (int64_t)row * T;
-    const uint8_t *z = ZEROS ? zeros + (int64_t)row * T : nullptr;
-    const uint16_t *x[MT];
+    constexpr int W = Q4_WAVES, PARTS = FEW ? 1 : 4;
+    // (the waves' tokens, then their sums)
+    constexpr int SUMS = W * MT * NT * PARTS * 64 * (int)sizeof(float), TOKENS = FEW ? 0 : W * 4096;
+    __shared__ __align__(16) uint8_t shared[SUMS > TOKENS ? SUMS : TOKENS];
+    auto part = (float(*)[MT][NT][PARTS][64])shared;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, kb = lane >> 4;
+    const int64_t r0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int tokens = (int)min((int64_t)(16 * MT), M - m0);
+    X += m0 * in;
+    // (rows past the end repeat the last one; 32-bit offsets from the first row)
+    const int last = (int)min((int64_t)16 * NT - 1, (int64_t)out - 1 - r0);
+    const uint16_t *ls = STAGED ? (const uint16_t *)lds : scales + r0 * T;
+    const uint8_t *lz = STAGED ? lds + q4_staged_scales(16 * NT, T) : zeros + (ZEROS ? r0 * T : 0);
+    const uint8_t *wbase = codes + r0 * (in / 2);
+    uint32_t woff[NT], at_scale[NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-        x[i] = X + (int64_t)min(m0 + 16 * i + (lane & 15), M - 1) * in + kb * 32;
+    for (int i = 0; i < NT; ++i) {
+        const int row = min(16 * i + li, last);
+        woff[i] = (uint32_t)row * (uint32_t)(in / 2);
+        at_scale[i] = (uint32_t)row * (uint32_t)T;
+    }
+    constexpr int XL = FEW ? 1 : 4 * MT;
+    // 16 lanes load a token's 128 columns: FEW, in the operand's order already; else
+    // tokens 4 q + kb, side by side, and through LDS to the order
+    const int xm = FEW ? li >> 2 : kb, xc = FEW ? kb * 32 + (li & 3) * 8 : li * 8;
+    // groups in flight; two take turns
+    struct {
+        uint4 w[NT], x[XL];
+    } load[2];
+    auto request = [&](int t, int b) __attribute__((always_inline)) {
+        if (t >= T)
+            return;
+        // (past a row's end: any codes, the tokens are 0 there)
+        const uint32_t at = (uint32_t)min(t * 64 + kb * 16, in / 2 - 16);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            load[b].w[i] = *(const uint4 *)(wbase + (woff[i] + at));
+        const int column = t * 128 + xc;
+#pragma unroll
+        for (int q = 0; q < XL; ++q) {
+            load[b].x[q] = make_uint4(0, 0, 0, 0);
+            if (xm + 4 * q < tokens && column < in)
+                load[b].x[q] = *(const uint4 *)(X + (int64_t)(xm + 4 * q) * in + column);
+        }
+    };
     const q4_bits bits;
-    q4_f32x4 acc[MT] = {};
-    for (int t0 = wave * Q4_AHEAD; t0 < T; t0 += Q4_WAVES * Q4_AHEAD) {
-        uint4 raw[Q4_AHEAD];
-        float sc[Q4_AHEAD];
-        int zp[Q4_AHEAD];
+    float acc[MT][NT][PARTS] = {};
+    auto compute = [&](int t, int b) __attribute__((always_inline)) {
+        if (t >= T)
+            return;
+        q4_f16x8 w[NT][4];
+        float by[NT];
 #pragma unroll
-        for (int i = 0; i < Q4_AHEAD; ++i) {
-            const int t = t0 + i;
-            const bool here = t < T && t * 128 + kb * 32 < in;
-            raw[i] = here ? *(const uint4 *)(w + (int64_t)t * 64) : make_uint4(0, 0, 0, 0);
-            sc[i] = t < T ? h2f(s[t]) : 0.0f;
-            zp[i] = ZEROS ? (t < T ? z[t] : 0) : 8;
+        for (int i = 0; i < NT; ++i) {
+            q4_unpack(bits, load[b].w[i], ZEROS ? lz[at_scale[i] + t] : 8, w[i]);
+            by[i] = h2f(ls[at_scale[i] + t]);
         }
 #pragma unroll
-        for (int i = 0; i < Q4_AHEAD; ++i) {
-            const int t = t0 + i;
-            if (t >= T)
-                break;
-            const bool here = t * 128 + kb * 32 < in;
-            q4_f16x8 b[4];
-            q4_unpack(bits, raw[i], zp[i], b);
+        for (int n = 0; n < MT; ++n) {
+            q4_f16x8 a[4];
+            if constexpr (FEW) {
+                a[0] = q4_order(load[b].x[0]);
+            } else {
+                // (a wave's own 4 KB, in its order: no barrier; the 16-byte pieces of a
+                // token change places by its number, which spreads them over the banks)
+                uint4 *mine = (uint4 *)(shared + wave * 4096);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                q4_f32x4 g = {};
+                for (int q = 0; q < 4; ++q)
+                    mine[(4 * q + kb) * 16 + (li ^ (4 * q + kb))] = load[b].x[4 * n + q];
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = here ? *(const uint4 *)(x[mt] + (int64_t)t * 128 + j * 8) : make_uint4(0, 0, 0, 0);
-                    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(q4_order(v), b[j], g, 0, 0, 0);
+                for (int q = 0; q < 4; ++q)
+                    a[q] = q4_order(mine[li * 16 + ((kb * 4 + q) ^ li)]);
+                __builtin_amdgcn_wave_barrier();
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const q4_f32x4 none = {};
+                if constexpr (FEW) {
+                    float g = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const q4_f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], w[i][q], none, 0, 0, 0);
+                        g = q == 0 ? d[0] : g + d[q];
+                    }
+                    acc[n][i][0] = __builtin_fmaf(g, by[i], acc[n][i][0]);
+                } else {
+                    q4_f32x4 g = none;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], w[i][q], g, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[n][i][k] = __builtin_fmaf(g[k], by[i], acc[n][i][k]);
                 }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc[mt][k] = __builtin_fmaf(g[k], sc[i], acc[mt][k]);
             }
         }
+    };
+    int t = wave;
+    request(t, 0);
+    if (STAGED) {
+        q4_stage(scales + r0 * T, lds, (last + 1) * T * 2);
+        if (ZEROS)
+            q4_stage(zeros + r0 * T, lds + q4_staged_scales(16 * NT, T), (last + 1) * T);
     }
+    request(t + W, 1);
+    if (STAGED)
+        __syncthreads();
+    for (; t < T; t += 2 * W) {
+        compute(t, 0);
+        request(t + 2 * W, 0);
+        compute(t + W, 1);
+        request(t + 3 * W, 1);
+    }
+    if (!FEW)
+        __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        part[wave][mt][lane] = acc[mt];
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+                part[wave][n][i][k][lane] = acc[n][i][k];
     __syncthreads();
-    for (int q = threadIdx.x; q < MT * 256; q += Q4_WAVES * 64) {
-        const int mt = q >> 8, k = q >> 6 & 3, l = q & 63;
+    for (int q = threadIdx.x; q < tokens * 16 * NT; q += W * 64) {
+        // (16 NT rows of a token side by side)
+        const int r = q % (16 * NT), token = q / (16 * NT), m = token & 15;
+        const int l = (FEW ? m : m >> 2) * 16 + (r & 15), k = FEW ? 0 : m & 3;
         float y = 0.0f;
 #pragma unroll
-        for (int i = 0; i < Q4_WAVES; ++i)
-            y += part[i][mt][l][k];
-        const int m = m0 + 16 * mt + (l >> 4) * 4 + k, r = r0 + (l & 15);
-        if (m < M && r < out) {
+        for (int i = 0; i < W; ++i)
+            y += part[i][token >> 4][r >> 4][k][l];
+        if (r0 + r < out) {
+            const int64_t at = (m0 + token) * out + r0 + r;
             if (WIDE)
-                ((float *)Y)[(int64_t)m * out + r] = y;
+                ((float *)Y)[at] = y;
             else
-                ((uint16_t *)Y)[(int64_t)m * out + r] = f2h(y);
+                ((uint16_t *)Y)[at] = f2h(y);
         }
     }
 }
@@ -204,25 +301,43 @@ hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const ui
     if (q4_tiled(out, in, M))
         return launch_gemm_q4_tile(codes, scales, zeros, out, in, X, M, Y, y_f32, workspace, ws_bytes, st);
     const int T = (in + 127) / 128;
-    auto run = [&](auto mt, auto wide, auto zero) {
-        constexpr int MT = decltype(mt)::value;
-        const dim3 grid((unsigned)((out + 15) / 16), (unsigned)((M + 16 * MT - 1) / (16 * MT)));
-        gemm_q4_few_kernel<MT, decltype(zero)::value, decltype(wide)::value>
-            <<<grid, Q4_WAVES * 64, 0, st>>>(codes, scales, zeros, out, in, T, X, M, Y);
+    using std::bool_constant;
+    auto run = [&](auto mt, auto nt, auto few, auto staged, auto zero, auto wide) {
+        constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value;
+        constexpr bool STAGED = decltype(staged)::value, ZEROS = decltype(zero)::value;
+        const int64_t across = ((int64_t)out + 16 * NT - 1) / (16 * NT);
+        const size_t lds = STAGED ? q4_staged_scales(16 * NT, T) + (ZEROS ? (size_t)(16 * NT) * T : 0) : 0;
+        // (a grid's second axis ends at 65535)
+        constexpr int64_t TOKENS = 65535 * 16 * MT;
+        for (int64_t m = 0; m < M; m += TOKENS) {
+            const int n = (int)std::min<int64_t>(M - m, TOKENS);
+            const dim3 grid((unsigned)across, (unsigned)((n + 16 * MT - 1) / (16 * MT)));
+            gemm_q4_few_kernel<MT, NT, decltype(few)::value, STAGED, ZEROS, decltype(wide)::value>
+                <<<grid, Q4_WAVES * 64, lds, st>>>(codes, scales, zeros, out, in, T, X + m * in, n,
+                                                   (uint8_t *)Y + m * out * (decltype(wide)::value ? 4 : 2));
+        }
     };
-    auto typed = [&](auto mt) {
-        using std::bool_constant;
-        if (y_f32)
-            zeros != nullptr ? run(mt, bool_constant<true>{}, bool_constant<true>{})
-                             : run(mt, bool_constant<true>{}, bool_constant<false>{});
-        else
-            zeros != nullptr ? run(mt, bool_constant<false>{}, bool_constant<true>{})
-                             : run(mt, bool_constant<false>{}, bool_constant<false>{});
+    auto typed = [&](auto mt, auto nt, auto few, auto staged) {
+        auto zeroed = [&](auto zero) {
+            y_f32 ? run(mt, nt, few, staged, zero, bool_constant<true>{})
+                  : run(mt, nt, few, staged, zero, bool_constant<false>{});
+        };
+        zeros != nullptr ? zeroed(bool_constant<true>{}) : zeroed(bool_constant<false>{});
     };
-    if (M <= 16)
-        typed(std::integral_constant<int, 1>{});
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> two;
+    constexpr std::integral_constant<int, 3> three;
+    constexpr bool_constant<true> yes;
+    constexpr bool_constant<false> no;
+    const q4_few_plan p = plan_q4_few(out, in, M);
+    if (p.four)
+        p.staged ? typed(one, one, yes, yes) : typed(one, one, yes, no);
+    else if (!p.staged)
+        p.token_tiles == 1 ? typed(one, one, no, no) : typed(two, one, no, no);
+    else if (p.token_tiles == 1)
+        p.row_tiles == 1 ? typed(one, one, no, yes) : p.row_tiles == 2 ? typed(one, two, no, yes) : typed(one, three, no, yes);
     else
-        typed(std::integral_constant<int, 4>{});
+        p.row_tiles == 1 ? typed(two, one, no, yes) : typed(two, two, no, yes);
     return hipGetLastError();
 }
 

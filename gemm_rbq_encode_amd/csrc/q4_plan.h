@@ -3,16 +3,44 @@
 #pragma once
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 namespace rbq {
 
-// Up to this many tokens: the few-token kernel (q4.hip); more: the tiled ones.
-constexpr int Q4_FEW = 64;
+// The few-token kernel (q4.hip) up to 32 tokens, and above as long as it has little
+// to do: it took 13.9 us for 64 tokens of 4096 x 4096, 25 of 11008 x 4096, 109 of
+// 28672 x 8192, the tiled one 26, 30 and 88 (65 tokens).
+inline bool q4_few(int out, int in, int M) {
+    return M <= 32 || (double)M * out * in <= 3e9;
+}
+
+// Groups of a row whose scales and zero points the few-token kernel takes into LDS:
+// 48 rows' 3 bytes a group, beside the 32 KB of its tokens, in 64 KB.
+constexpr int Q4_STAGED_GROUPS = 224;
+
+// Bytes of the scales of some rows there.
+constexpr size_t q4_staged_scales(int rows, int T) {
+    return ((size_t)rows * T * 2 + 15) / 16 * 16;
+}
+
+struct q4_few_plan {
+    bool four;          // up to 4 tokens
+    bool staged;        // scales through LDS
+    int token_tiles, row_tiles;
+};
+
+inline q4_few_plan plan_q4_few(int out, int in, int M) {
+    q4_few_plan p = {M <= 4, (in + 127) / 128 <= Q4_STAGED_GROUPS, M <= 16 ? 1 : 2, 1};
+    const int64_t tiles = ((int64_t)out + 15) / 16;
+    if (p.staged && !p.four)
+        p.row_tiles = tiles <= 256 ? 1 : p.token_tiles == 1 && tiles > 512 && tiles <= 768 ? 3 : 2;
+    return p;
+}
 
 // Offsets inside a tile are 32-bit and the tiles are numbered in 31 bits.
 inline bool q4_tiled(int out, int in, int M) {
-    return M > Q4_FEW && in <= (1 << 23) && ((int64_t)out / 128 + 1) * ((int64_t)M / 64 + 1) < (1 << 24);
+    return !q4_few(out, in, M) && in <= (1 << 23) && ((int64_t)out / 128 + 1) * ((int64_t)M / 64 + 1) < (1 << 24);
 }
 
 // Kinds of tiles (rows x tokens): 512 x 64, 256 x 64.
