@@ -29,23 +29,33 @@ __device__ __forceinline__ Y q4_to(float v) {
         return (Y)v;
 }
 
-// Tiles of 64 WM rows by 64 WN tokens, a wave 64 x 64 of them; a group of 128
-// columns a stage.  The tokens of a stage go through registers, where they are
-// put into the operands' order, to one of two buffers in LDS (256 bytes a token,
-// the 16-byte piece q of token m at q ^ (m & 15), so that 16 tokens' reads of one
-// piece and 16 pieces' writes of one token hit every bank once).  The codes of a
-// wave's rows go straight to its registers, 16 bytes a lane and row tile, and are
-// unpacked there for 64 tokens each.  Both are requested a stage ahead.
-template <int WM, int WN, bool ZEROS, typename Y>
-__global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
+// Tiles of 256 rows by 64 tokens, a wave 64 rows of them; a group of 128 columns a
+// stage.  The tokens of a stage go through registers, where they are put into the
+// operands' order, to one of two buffers in LDS (256 bytes a token, placed so that 16
+// tokens' reads of one piece and 16 pieces' writes of one token hit every bank once).
+// The codes of a wave's rows go straight to its registers, 16 bytes a lane and row
+// tile, and are unpacked there for 64 tokens each.  Both are requested a stage ahead.
+// The scales and zero points of Q4_AHEAD groups at a time go through LDS, a row a
+// thread: loaded where they are used, 2 bytes from each of 16 rows, they took 39 of
+// 277 us (2048 tokens, 14336 x 4096).
+constexpr int Q4_AHEAD = 8;
+
+typedef uint32_t q4_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t q4_u32x2 __attribute__((ext_vector_type(2), aligned(1)));
+
+template <bool ZEROS, typename Y>
+__global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros, int out,
     int in, int T, const uint16_t *__restrict__ X, int M, Y *__restrict__ y, float *__restrict__ parts, int tiles_m,
     int tiles_r, int slices) {
-    constexpr int TM = 4, TN = 4, THREADS = WM * WN * 64, RT = WM * 64, CT = WN * 64;
+    constexpr int TM = 4, TN = 4, THREADS = 256, RT = Q4_ROWS, CT = Q4_TOKENS;
+    static_assert(RT == THREADS && RT == TM * 64 && CT == TN * 16);
     constexpr int PIECES = CT * 16 / THREADS;       // 16-byte pieces of X a thread stages
     __shared__ __align__(16) uint8_t lds[2][CT * 256];
+    __shared__ __align__(16) uint16_t lscales[2][RT][Q4_AHEAD];
+    __shared__ __align__(8) uint8_t lzeros[ZEROS ? 2 : 1][RT][Q4_AHEAD];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WM, wc = wave / WM;
+    const int wr = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // tiles in bands of 8 token tiles, tokens fastest: the workgroups of an XCD
     // share tokens and rows
@@ -64,10 +74,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
     // share are scalar.
     const uint32_t rows = (uint32_t)min((int64_t)RT, (int64_t)out - r0), toks = (uint32_t)min((int64_t)CT, (int64_t)M - m0);
     const auto wbuf = q4_buffer(codes + r0 * (in / 2), rows * (uint32_t)(in / 2));
-    const auto sbuf = q4_buffer(scales + r0 * T, rows * (uint32_t)T * 2u);
-    const auto zbuf = q4_buffer(ZEROS ? zeros + r0 * T : codes, rows * (uint32_t)T);
     const auto xbuf = q4_buffer(X + m0 * in, toks * (uint32_t)in * 2u);
-    const uint32_t woff = (uint32_t)li * (uint32_t)(in / 2) + g * 16, soff = (uint32_t)li * (uint32_t)T;
+    const uint32_t woff = (uint32_t)li * (uint32_t)(in / 2) + g * 16;
     const uint32_t xoff = (uint32_t)(tid >> 4) * (uint32_t)in * 2u + (tid & 15) * 16;
     // (a thread's tokens are THREADS / 16 apart, a multiple of 16)
     const uint32_t xat = (uint32_t)((tid >> 4) * 256 + (q4_place(tid & 15, tid >> 4 & 15) * 16));
@@ -79,16 +87,37 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
     // row tile uses them.
     const q4_bits bits;
     uint4 wraw[TM], xraw[PIECES];
-    uint32_t sraw[TM], zraw[TM];
+    uint32_t sraw, zraw;
     float s[2];
     q4_f16x8 a[TN][4], b[2][4];
     q4_f32x4 acc[TM][TN] = {}, p[2][TN] = {};
     auto request_w = [&](int t, int i) __attribute__((always_inline)) {
         const uint32_t row = (uint32_t)(wr * 64 + i * 16);
         wraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff, row * (uint32_t)(in / 2) + t * 64, 0));
-        sraw[i] = __builtin_amdgcn_raw_buffer_load_b16(sbuf, soff * 2u, (row * (uint32_t)T + t) * 2u, 0);
+    };
+    // Q4_AHEAD groups of the thread's row (past the row's end: anything, not used;
+    // past the array's end none)
+    const int64_t srow = (r0 + min(tid, (int)rows - 1)) * T, send = (int64_t)out * T;
+    auto stage_s = [&](int t, int buffer) __attribute__((always_inline)) {
+        const int64_t at = srow + t;
+        if (at + Q4_AHEAD <= send) {
+            *(uint4 *)lscales[buffer][tid] = __builtin_bit_cast(uint4, *(const q4_u32x4 *)(scales + at));
+            if (ZEROS)
+                *(uint2 *)lzeros[buffer][tid] = __builtin_bit_cast(uint2, *(const q4_u32x2 *)(zeros + at));
+        } else {
+            for (int e = 0; e < Q4_AHEAD; ++e)
+                if (at + e < send) {
+                    lscales[buffer][tid][e] = scales[at + e];
+                    if (ZEROS)
+                        lzeros[buffer][tid][e] = zeros[at + e];
+                }
+        }
+    };
+    auto read_s = [&](int t, int i) __attribute__((always_inline)) {
+        const int row = wr * 64 + i * 16 + li, at = (t - t0) % Q4_AHEAD, buffer = (t - t0) / Q4_AHEAD & 1;
+        sraw = lscales[buffer][row][at];
         if (ZEROS)
-            zraw[i] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, soff, row * (uint32_t)T + t, 0);
+            zraw = lzeros[buffer][row][at];
     };
     auto request_x = [&](int t) __attribute__((always_inline)) {
         const uint32_t at = t * 128 + (tid & 15) * 8 < in ? xoff : 0x80000000u;     // (past a row's end: 0)
@@ -102,12 +131,12 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
             *(q4_f16x8 *)(lds[buffer] + xat + i * (THREADS / 16) * 256) = q4_order(xraw[i]);
     };
     auto read = [&](int buffer, int n, int j) __attribute__((always_inline)) {
-        a[n][j] = *(const q4_f16x8 *)(lds[buffer] + (wc * 64 + li) * 256 + n * 16 * 256 + q4_place(4 * g + j, li) * 16);
+        a[n][j] = *(const q4_f16x8 *)(lds[buffer] + li * 256 + n * 16 * 256 + q4_place(4 * g + j, li) * 16);
     };
     auto unpack = [&](int i) __attribute__((always_inline)) {
-        s[i & 1] = h2f((uint16_t)sraw[i]);
-        asm("" : "+v"(s[i & 1]));       // (converted here, or the raw scale's register would be waited for early)
-        q4_unpack(bits, wraw[i], ZEROS ? zraw[i] : 8, b[i & 1]);
+        s[i & 1] = h2f((uint16_t)sraw);
+        asm("" : "+v"(s[i & 1]));       // (converted once, not in each fma)
+        q4_unpack(bits, wraw[i], ZEROS ? zraw : 8, b[i & 1]);
     };
     auto scale = [&](int i, float by) __attribute__((always_inline)) {
 #pragma unroll
@@ -123,6 +152,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
         for (int i = 0; i < TM; ++i)
             request_w(t0, i);
         request_x(t0);
+        stage_s(t0, 0);
         stage_x(0);
         request_x(min(t0 + 1, last));
         __syncthreads();
@@ -131,8 +161,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 read(0, n, j);
+        read_s(t0, 0);
         unpack(0);
         request_w(min(t0 + 1, last), 0);
+        read_s(t0, 1);
     }
     float before = 0.0f;        // the scale of the last row tile of the group before
     for (int t = t0; t < t1; ++t) {
@@ -142,7 +174,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
             if (i == TM - 1)
                 __syncthreads();
             const float by = i == 0 ? before : s[(i - 1) & 1];
+            // (a group's tile 1 on; its tile 0 and the next tile's scale are of the next)
             unpack((i + 1) % TM);
+            read_s(i + 2 < TM ? t : next, (i + 2) % TM);
+            if (i == 0 && (t - t0) % Q4_AHEAD == 0)
+                stage_s(t + Q4_AHEAD, ((t - t0) / Q4_AHEAD + 1) & 1);
             request_w(i + 1 < TM ? next : min(t + 2, last), (i + 1) % TM);
             if (i == TM - 2) {
                 stage_x(buffer);
@@ -176,7 +212,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
     for (int n = 0; n < TN; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int64_t m = m0 + wc * 64 + n * 16 + 4 * g + k;
+            const int64_t m = m0 + n * 16 + 4 * g + k;
             if (m >= M)
                 continue;
 #pragma unroll
@@ -192,23 +228,30 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void gemm_q4_tile_kernel(
         }
 }
 
-// Y = the slices' sums, in their order.
+// Y = the slices' sums, in their order, eight loads on their way at a time.
 template <typename Y>
 __global__ __launch_bounds__(256) void gemm_q4_sum_kernel(const float *__restrict__ parts, int64_t n, int slices,
                                                           Y *__restrict__ y) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v = parts[i];
-        for (int s = 1; s < slices; ++s)
-            v += parts[s * n + i];
+        float v = 0.0f;
+        for (int s = 0; s < slices; s += 8) {
+            float a[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                a[k] = s + k < slices ? parts[(s + k) * n + i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v += a[k];
+        }
         y[i] = q4_to<Y>(v);
     }
 }
 
-template <int WM, int WN, bool ZEROS, typename Y>
+template <bool ZEROS, typename Y>
 hipError_t launch_tile(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
                        const uint16_t *X, int M, Y *y, float *parts, int slices, hipStream_t st) {
-    const int tiles_m = (M + WN * 64 - 1) / (WN * 64), tiles_r = (out + WM * 64 - 1) / (WM * 64);
-    gemm_q4_tile_kernel<WM, WN, ZEROS, Y><<<(unsigned)(tiles_m * tiles_r * slices), WM * WN * 64, 0, st>>>(
+    const int tiles_m = (M + Q4_TOKENS - 1) / Q4_TOKENS, tiles_r = (out + Q4_ROWS - 1) / Q4_ROWS;
+    gemm_q4_tile_kernel<ZEROS, Y><<<(unsigned)(tiles_m * tiles_r * slices), 256, 0, st>>>(
         codes, scales, zeros, out, in, (in + 127) / 128, X, M, y, parts, tiles_m, tiles_r, slices);
     if (slices > 1) {
         const int64_t n = (int64_t)M * out;
@@ -219,18 +262,9 @@ hipError_t launch_tile(const uint8_t *codes, const uint16_t *scales, const uint8
 
 template <typename Y>
 hipError_t launch_typed(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
-                        const uint16_t *X, int M, Y *y, float *parts, q4_plan p, hipStream_t st) {
-    auto run = [&](auto wm, auto wn) {
-        constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
-        return zeros != nullptr
-                   ? launch_tile<WM, WN, true>(codes, scales, zeros, out, in, X, M, y, parts, p.slices, st)
-                   : launch_tile<WM, WN, false>(codes, scales, zeros, out, in, X, M, y, parts, p.slices, st);
-    };
-    constexpr std::integral_constant<int, 1> one;
-    switch (p.kind) {
-    case Q4_512: return run(std::integral_constant<int, 8>{}, one);
-    default: return run(std::integral_constant<int, 4>{}, one);
-    }
+                        const uint16_t *X, int M, Y *y, float *parts, int slices, hipStream_t st) {
+    return zeros != nullptr ? launch_tile<true>(codes, scales, zeros, out, in, X, M, y, parts, slices, st)
+                            : launch_tile<false>(codes, scales, zeros, out, in, X, M, y, parts, slices, st);
 }
 
 }  // namespace
@@ -238,19 +272,17 @@ hipError_t launch_typed(const uint8_t *codes, const uint16_t *scales, const uint
 size_t gemm_q4_workspace_bytes(int out, int in, int M) {
     if (!q4_tiled(out, in, M))
         return 0;
-    const q4_plan p = plan_q4(out, in, M);
-    return p.slices > 1 ? (size_t)p.slices * (size_t)M * (size_t)out * sizeof(float) : 0;
+    const int slices = q4_slices(out, in, M);
+    return slices > 1 ? (size_t)slices * (size_t)M * (size_t)out * sizeof(float) : 0;
 }
 
 hipError_t launch_gemm_q4_tile(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int out, int in,
                                const uint16_t *X, int M, void *y, int y_f32, void *workspace, size_t ws_bytes,
                                hipStream_t st) {
-    q4_plan p = plan_q4(out, in, M);
-    if (ws_bytes < gemm_q4_workspace_bytes(out, in, M))
-        p.slices = 1;
+    const int slices = ws_bytes < gemm_q4_workspace_bytes(out, in, M) ? 1 : q4_slices(out, in, M);
     float *parts = static_cast<float *>(workspace);
-    return y_f32 ? launch_typed(codes, scales, zeros, out, in, X, M, static_cast<float *>(y), parts, p, st)
-                 : launch_typed(codes, scales, zeros, out, in, X, M, static_cast<uint16_t *>(y), parts, p, st);
+    return y_f32 ? launch_typed(codes, scales, zeros, out, in, X, M, static_cast<float *>(y), parts, slices, st)
+                 : launch_typed(codes, scales, zeros, out, in, X, M, static_cast<uint16_t *>(y), parts, slices, st);
 }
 
 }  // namespace rbq

@@ -103,7 +103,7 @@ __global__ __launch_bounds__(Q4E_THREADS) void encode_q4_kernel(const float *__r
 }
 
 // ---------------------------------------------------------------------------
-// few tokens: a workgroup takes 16 NT rows and 16 MT tokens; each of its waves takes
+// few tokens: a workgroup takes 16 NT rows and 16 tokens; each of its waves takes
 // one group at a time, the next two on their way, and goes through the row tiles
 // with the tokens' operands of that group.  A lane holds one row's 32 columns of a
 // group in one 16-byte load, which four matrix instructions take apart; a group's
@@ -131,7 +131,7 @@ __device__ __forceinline__ void q4_stage(const void *from, uint8_t *to, int n) {
         to[n - rest + threadIdx.x] = p[n - rest + threadIdx.x];
 }
 
-template <int MT, int NT, bool FEW, bool STAGED, bool ZEROS, bool WIDE>
+template <int NT, bool FEW, bool STAGED, bool ZEROS, bool WIDE>
 __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_t *__restrict__ codes,
                                                                     const uint16_t *__restrict__ scales,
                                                                     const uint8_t *__restrict__ zeros, int out, int in,
@@ -139,13 +139,13 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
                                                                     void *__restrict__ Y) {
     constexpr int W = Q4_WAVES, PARTS = FEW ? 1 : 4;
     // (the waves' tokens, then their sums)
-    constexpr int SUMS = W * MT * NT * PARTS * 64 * (int)sizeof(float), TOKENS = FEW ? 0 : W * 4096;
+    constexpr int SUMS = W * NT * PARTS * 64 * (int)sizeof(float), TOKENS = FEW ? 0 : W * 4096;
     __shared__ __align__(16) uint8_t shared[SUMS > TOKENS ? SUMS : TOKENS];
-    auto part = (float(*)[MT][NT][PARTS][64])shared;
+    auto part = (float(*)[NT][PARTS][64])shared;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, kb = lane >> 4;
-    const int64_t r0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
-    const int tokens = (int)min((int64_t)(16 * MT), M - m0);
+    const int64_t r0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * 16;
+    const int tokens = (int)min((int64_t)16, M - m0);
     X += m0 * in;
     // (rows past the end repeat the last one; 32-bit offsets from the first row)
     const int last = (int)min((int64_t)16 * NT - 1, (int64_t)out - 1 - r0);
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
         woff[i] = (uint32_t)row * (uint32_t)(in / 2);
         at_scale[i] = (uint32_t)row * (uint32_t)T;
     }
-    constexpr int XL = FEW ? 1 : 4 * MT;
+    constexpr int XL = FEW ? 1 : 4;
     // 16 lanes load a token's 128 columns: FEW, in the operand's order already; else
     // tokens 4 q + kb, side by side, and through LDS to the order
     const int xm = FEW ? li >> 2 : kb, xc = FEW ? kb * 32 + (li & 3) * 8 : li * 8;
@@ -184,55 +184,48 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
         }
     };
     const q4_bits bits;
-    float acc[MT][NT][PARTS] = {};
+    float acc[NT][PARTS] = {};
     auto compute = [&](int t, int b) __attribute__((always_inline)) {
         if (t >= T)
             return;
-        q4_f16x8 w[NT][4];
-        float by[NT];
+        q4_f16x8 a[4];
+        if constexpr (FEW) {
+            a[0] = q4_order(load[b].x[0]);
+        } else {
+            // (a wave's own 4 KB, in its order: no barrier; the 16-byte pieces of a
+            // token change places by its number, which spreads them over the banks)
+            uint4 *mine = (uint4 *)(shared + wave * 4096);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            q4_unpack(bits, load[b].w[i], ZEROS ? lz[at_scale[i] + t] : 8, w[i]);
-            by[i] = h2f(ls[at_scale[i] + t]);
+            for (int q = 0; q < 4; ++q)
+                mine[(4 * q + kb) * 16 + (li ^ (4 * q + kb))] = load[b].x[q];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                a[q] = q4_order(mine[li * 16 + ((kb * 4 + q) ^ li)]);
+            __builtin_amdgcn_wave_barrier();
         }
 #pragma unroll
-        for (int n = 0; n < MT; ++n) {
-            q4_f16x8 a[4];
+        for (int i = 0; i < NT; ++i) {
+            q4_f16x8 w[4];
+            q4_unpack(bits, load[b].w[i], ZEROS ? lz[at_scale[i] + t] : 8, w);
+            const float by = h2f(ls[at_scale[i] + t]);
+            const q4_f32x4 none = {};
             if constexpr (FEW) {
-                a[0] = q4_order(load[b].x[0]);
-            } else {
-                // (a wave's own 4 KB, in its order: no barrier; the 16-byte pieces of a
-                // token change places by its number, which spreads them over the banks)
-                uint4 *mine = (uint4 *)(shared + wave * 4096);
+                float g = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mine[(4 * q + kb) * 16 + (li ^ (4 * q + kb))] = load[b].x[4 * n + q];
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    a[q] = q4_order(mine[li * 16 + ((kb * 4 + q) ^ li)]);
-                __builtin_amdgcn_wave_barrier();
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const q4_f32x4 none = {};
-                if constexpr (FEW) {
-                    float g = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const q4_f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], w[i][q], none, 0, 0, 0);
-                        g = q == 0 ? d[0] : g + d[q];
-                    }
-                    acc[n][i][0] = __builtin_fmaf(g, by[i], acc[n][i][0]);
-                } else {
-                    q4_f32x4 g = none;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], w[i][q], g, 0, 0, 0);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[n][i][k] = __builtin_fmaf(g[k], by[i], acc[n][i][k]);
+                for (int q = 0; q < 4; ++q) {
+                    const q4_f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], w[q], none, 0, 0, 0);
+                    g = q == 0 ? d[0] : g + d[q];
                 }
+                acc[i][0] = __builtin_fmaf(g, by, acc[i][0]);
+            } else {
+                q4_f32x4 g = none;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], w[q], g, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc[i][k] = __builtin_fmaf(g[k], by, acc[i][k]);
             }
         }
     };
@@ -255,21 +248,19 @@ __global__ __launch_bounds__(Q4_WAVES * 64) void gemm_q4_few_kernel(const uint8_
     if (!FEW)
         __syncthreads();
 #pragma unroll
-    for (int n = 0; n < MT; ++n)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int k = 0; k < PARTS; ++k)
-                part[wave][n][i][k][lane] = acc[n][i][k];
+        for (int k = 0; k < PARTS; ++k)
+            part[wave][i][k][lane] = acc[i][k];
     __syncthreads();
     for (int q = threadIdx.x; q < tokens * 16 * NT; q += W * 64) {
         // (16 NT rows of a token side by side)
-        const int r = q % (16 * NT), token = q / (16 * NT), m = token & 15;
-        const int l = (FEW ? m : m >> 2) * 16 + (r & 15), k = FEW ? 0 : m & 3;
+        const int r = q % (16 * NT), token = q / (16 * NT);
+        const int l = (FEW ? token : token >> 2) * 16 + (r & 15), k = FEW ? 0 : token & 3;
         float y = 0.0f;
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            y += part[i][token >> 4][r >> 4][k][l];
+            y += part[i][r >> 4][k][l];
         if (r0 + r < out) {
             const int64_t at = (m0 + token) * out + r0 + r;
             if (WIDE)
@@ -302,25 +293,24 @@ hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const ui
         return launch_gemm_q4_tile(codes, scales, zeros, out, in, X, M, Y, y_f32, workspace, ws_bytes, st);
     const int T = (in + 127) / 128;
     using std::bool_constant;
-    auto run = [&](auto mt, auto nt, auto few, auto staged, auto zero, auto wide) {
-        constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value;
+    auto run = [&](auto nt, auto few, auto staged, auto zero, auto wide) {
+        constexpr int NT = decltype(nt)::value;
         constexpr bool STAGED = decltype(staged)::value, ZEROS = decltype(zero)::value;
         const int64_t across = ((int64_t)out + 16 * NT - 1) / (16 * NT);
         const size_t lds = STAGED ? q4_staged_scales(16 * NT, T) + (ZEROS ? (size_t)(16 * NT) * T : 0) : 0;
         // (a grid's second axis ends at 65535)
-        constexpr int64_t TOKENS = 65535 * 16 * MT;
+        constexpr int64_t TOKENS = 65535 * 16;
         for (int64_t m = 0; m < M; m += TOKENS) {
             const int n = (int)std::min<int64_t>(M - m, TOKENS);
-            const dim3 grid((unsigned)across, (unsigned)((n + 16 * MT - 1) / (16 * MT)));
-            gemm_q4_few_kernel<MT, NT, decltype(few)::value, STAGED, ZEROS, decltype(wide)::value>
+            const dim3 grid((unsigned)across, (unsigned)((n + 15) / 16));
+            gemm_q4_few_kernel<NT, decltype(few)::value, STAGED, ZEROS, decltype(wide)::value>
                 <<<grid, Q4_WAVES * 64, lds, st>>>(codes, scales, zeros, out, in, T, X + m * in, n,
                                                    (uint8_t *)Y + m * out * (decltype(wide)::value ? 4 : 2));
         }
     };
-    auto typed = [&](auto mt, auto nt, auto few, auto staged) {
+    auto typed = [&](auto nt, auto few, auto staged) {
         auto zeroed = [&](auto zero) {
-            y_f32 ? run(mt, nt, few, staged, zero, bool_constant<true>{})
-                  : run(mt, nt, few, staged, zero, bool_constant<false>{});
+            y_f32 ? run(nt, few, staged, zero, bool_constant<true>{}) : run(nt, few, staged, zero, bool_constant<false>{});
         };
         zeros != nullptr ? zeroed(bool_constant<true>{}) : zeroed(bool_constant<false>{});
     };
@@ -331,13 +321,11 @@ hipError_t launch_gemm_q4(const uint8_t *codes, const uint16_t *scales, const ui
     constexpr bool_constant<false> no;
     const q4_few_plan p = plan_q4_few(out, in, M);
     if (p.four)
-        p.staged ? typed(one, one, yes, yes) : typed(one, one, yes, no);
+        p.staged ? typed(one, yes, yes) : typed(one, yes, no);
     else if (!p.staged)
-        p.token_tiles == 1 ? typed(one, one, no, no) : typed(two, one, no, no);
-    else if (p.token_tiles == 1)
-        p.row_tiles == 1 ? typed(one, one, no, yes) : p.row_tiles == 2 ? typed(one, two, no, yes) : typed(one, three, no, yes);
+        typed(one, no, no);
     else
-        p.row_tiles == 1 ? typed(two, one, no, yes) : typed(two, two, no, yes);
+        p.row_tiles == 1 ? typed(one, no, yes) : p.row_tiles == 2 ? typed(two, no, yes) : typed(three, no, yes);
     return hipGetLastError();
 }
 

@@ -8,11 +8,15 @@
 
 namespace rbq {
 
-// The few-token kernel (q4.hip) up to 32 tokens, and above as long as it has little
-// to do: it took 13.9 us for 64 tokens of 4096 x 4096, 25 of 11008 x 4096, 109 of
-// 28672 x 8192, the tiled one 26, 30 and 88 (65 tokens).
+// The few-token kernel (q4.hip) up to 16 tokens, and above as long as it has little
+// to do.  It took, the many-token kernel (gemm_q4.hip) took, in us:
+//      32 tokens, 11008 x 4096      16.7    24
+//      64          4096 x 4096      13.5    19
+//     128          4096 x 4096      22.8    23.4
+//      64          4096 x 11008     29      23
+//      32         28672 x 8192      79      57
 inline bool q4_few(int out, int in, int M) {
-    return M <= 32 || (double)M * out * in <= 3e9;
+    return M <= 16 || (double)M * out * in <= 2e9;
 }
 
 // Groups of a row whose scales and zero points the few-token kernel takes into LDS:
@@ -27,51 +31,49 @@ constexpr size_t q4_staged_scales(int rows, int T) {
 struct q4_few_plan {
     bool four;          // up to 4 tokens
     bool staged;        // scales through LDS
-    int token_tiles, row_tiles;
+    int row_tiles;      // of a workgroup
 };
 
+// Row tiles: up to 4 tokens one (11008 x 4096: 7.3 us with one, 8.0 with two;
+// 128256 x 4096: 54 and 50).  Else more tiles use the tokens again: three if that
+// makes one round of all workgroups (16 tokens, 11008 x 4096: 11.9 us with one, 11.7
+// with two, 9.8 with three), two where there are more rounds (128256 x 4096: 110, 83,
+// 92), one where the workgroups would not fill the chip (4096 x 4096: 6.0, 6.9, 8.4).
 inline q4_few_plan plan_q4_few(int out, int in, int M) {
-    q4_few_plan p = {M <= 4, (in + 127) / 128 <= Q4_STAGED_GROUPS, M <= 16 ? 1 : 2, 1};
+    q4_few_plan p = {M <= 4, (in + 127) / 128 <= Q4_STAGED_GROUPS, 1};
     const int64_t tiles = ((int64_t)out + 15) / 16;
     if (p.staged && !p.four)
-        p.row_tiles = tiles <= 256 ? 1 : p.token_tiles == 1 && tiles > 512 && tiles <= 768 ? 3 : 2;
+        p.row_tiles = tiles <= 256 ? 1 : tiles > 512 && tiles <= 768 ? 3 : 2;
     return p;
 }
 
+// Tiles of the many-token kernel (gemm_q4.hip).
+constexpr int Q4_ROWS = 256, Q4_TOKENS = 64;
+
 // Offsets inside a tile are 32-bit and the tiles are numbered in 31 bits.
 inline bool q4_tiled(int out, int in, int M) {
-    return !q4_few(out, in, M) && in <= (1 << 23) && ((int64_t)out / 128 + 1) * ((int64_t)M / 64 + 1) < (1 << 24);
+    return !q4_few(out, in, M) && in <= (1 << 23) && ((int64_t)out / Q4_ROWS + 1) * ((int64_t)M / Q4_TOKENS + 1) < (1 << 24);
 }
 
-// Kinds of tiles (rows x tokens): 512 x 64, 256 x 64.
-enum { Q4_512 = 0, Q4_256 = 1, Q4_KINDS = 2 };
-constexpr int Q4_ROWS[Q4_KINDS] = {512, 256}, Q4_TOKENS[Q4_KINDS] = {64, 64};
-
-struct q4_plan {
-    int kind, slices;
-};
-
-inline q4_plan plan_q4(int out, int in, int M) {
+// Slices of the columns, by what was measured (S = 1 .. 16 at twelve sizes): a
+// workgroup takes 1.1 us for a group and 7 to begin and end, every 256 take that
+// long again (two on a CU take twice as long), and joining slices takes 4 us and
+// their sums' way through memory.  64 tokens of 4096 x 4096: 41.8 us with one, 28.4
+// two, 20.6 four, 19.1 eight, 22.7 sixteen; 128 of 11008 x 4096: 42.5, 33.1, 32.7,
+// 39.7, 55.
+inline int q4_slices(int out, int in, int M) {
     const int T = (in + 127) / 128;
-    q4_plan best = {Q4_512, 1};
-    float least = 0.0f;
-    static constexpr float stage[Q4_KINDS] = {1.7f, 0.9f};
-    for (int k = 0; k < Q4_KINDS; ++k) {
-        const int64_t tiles = (((int64_t)out + Q4_ROWS[k] - 1) / Q4_ROWS[k]) *
-                              (((int64_t)M + Q4_TOKENS[k] - 1) / Q4_TOKENS[k]);
-        const int64_t at_once = 256 * (k == 0 ? 1 : 2);
-        for (int S = 1; S <= 16 && 2 * S <= T + 1; ++S) {
-            const float rounds = (float)((tiles * S + at_once - 1) / at_once);
-            const int each = (T + S - 1) / S;
-            const float share = std::min(1.0f, (float)(tiles * S) / (float)at_once);
-            (void)share;
-            float cost = rounds * ((float)each * stage[k] * (k == 0 ? 1.0f : 2.0f) + 2.5f);
-            if (S > 1)
-                cost += 3.0f + (float)(S + 1) * 4.0f * (float)M * (float)out / 5.0e6f;
-            if (least == 0.0f || cost < least) {
-                least = cost;
-                best = {k, S};
-            }
+    const int64_t tiles = (((int64_t)out + Q4_ROWS - 1) / Q4_ROWS) * (((int64_t)M + Q4_TOKENS - 1) / Q4_TOKENS);
+    int best = 1;
+    double least = 0.0;
+    for (int S = 1; S <= 16 && 2 * S <= T + 1; ++S) {
+        const double rounds = (double)((tiles * S + 255) / 256);
+        double cost = rounds * ((T + S - 1) / S) * 1.1 + 7.0;
+        if (S > 1)
+            cost += 4.0 + (double)(S + 1) * 4.0 * (double)M * (double)out / 3.0e6;
+        if (S == 1 || cost < least) {
+            least = cost;
+            best = S;
         }
     }
     return best;
