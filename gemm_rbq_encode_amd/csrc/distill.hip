@@ -36,7 +36,7 @@ struct lg_slots {
     int index[RBQ_TOP_MAX];     // -1: not used
     float x[RBQ_TOP_MAX];       // the student's logit
     double p[RBQ_TOP_MAX];      // 0: not used
-    double P, rest, own;        // sum of p, the rest, sum of p ln p over all classes
+    double P, rest, own;        // sum of p, the rest, sum of p ln p over the slots
     int bad, any;
 };
 
@@ -173,8 +173,6 @@ __device__ __forceinline__ void distill_teacher(const float (&t)[2], int slots, 
         rest = rest > 0.0 ? rest : rest != rest ? rest : 0.0;
     }
     double own = wave_sum_f64_dpp((pj[0] != 0.0 ? pj[0] * lp[0] : 0.0) + (pj[1] != 0.0 ? pj[1] * lp[1] : 0.0));
-    if (KIND == LG_NAMED && rest != 0.0)
-        own += rest * log(rest);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
         if (lane + 64 * q < slots)
@@ -184,6 +182,14 @@ __device__ __forceinline__ void distill_teacher(const float (&t)[2], int slots, 
         sl.rest = rest;
         sl.own = own;
     }
+}
+
+// The teacher's rest: what rounding of its log probabilities can leave (their sum is
+// off by up to 2^-15) is none where the student has no mass on the tokens not named --
+// all tokens are named, or both mask the others.
+template <int KIND>
+__device__ __forceinline__ double distill_rest(const lg_row &t, const lg_slots &sl) {
+    return KIND != LG_NAMED || (t.S == 0.0f && sl.rest <= 0x1p-15) ? 0.0 : sl.rest;
 }
 
 // A wave's part: the loss of the row, sum p ln p - sum p ln q.
@@ -204,14 +210,15 @@ __device__ __forceinline__ float distill_loss(const lg_row &t, double S, float c
     cross = wave_sum_f64_dpp(cross);
     if (sl.bad)
         return __builtin_nanf("");
-    if (sl.P == 0.0 && sl.rest == 0.0)
+    const double rest = distill_rest<KIND>(t, sl);
+    if (sl.P == 0.0 && rest == 0.0)
         return 0.0f;
     if (S == 0.0)
-        return sl.P + sl.rest != sl.P + sl.rest ? __builtin_nanf("") : __builtin_inff();
+        return sl.P + rest != sl.P + rest ? __builtin_nanf("") : __builtin_inff();
     const double logS = log(S);
     double loss = sl.own - cross + sl.P * logS;
-    if (KIND == LG_NAMED && sl.rest != 0.0)
-        loss -= sl.rest * (log((double)t.S) - logS);
+    if (KIND == LG_NAMED && rest != 0.0)
+        loss += rest * (log(rest) - (log((double)t.S) - logS));
     return (float)loss;
 }
 
@@ -264,8 +271,9 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
             return;
         }
         const double by = sl.bad ? __builtin_nan("") : (double)d * (double)a.inv_t;
-        const double all = by * (sl.P + sl.rest) / S;       // per e of a named token
-        const double away = KIND == LG_NAMED && sl.rest != 0.0 && t.S != 0.0f ? by * sl.rest / (double)t.S : 0.0;
+        const double rest = distill_rest<KIND>(t, sl);
+        const double all = by * (sl.P + rest) / S;          // per e of a named token
+        const double away = KIND == LG_NAMED && rest != 0.0 && t.S != 0.0f ? by * rest / (double)t.S : 0.0;
         // (every slot's logit has been read: dx may be x)
         if (MODE == DS_WHOLE && t.quick)
             distill_write<T, true, TH>(x, dx, r, t.m, a.c, (float)(all - away));

@@ -78,6 +78,7 @@ def distill(r: Rows, index, t, tail: bool):
                 named[i] = True
                 want[i] += pj
             q_rest = r.p[m][~named].sum()
+            rest = 0.0 if q_rest == 0 and rest <= 2.0 ** -15 else rest
             L = sum(pj * (np.log(pj) - r.lp[m, i]) for (i, _), pj in zip(slots, p) if pj > 0)
             if rest > 0:
                 L += rest * (np.log(rest) - np.log(q_rest)) if not r.empty[m] else np.inf

@@ -5,8 +5,10 @@ The bounds.  u = 2^-23 (an operation rounds by at most half of it; the hardware'
 exp2 and log2 by up to a whole one).  An exponent (x - m) c meets three roundings
 of its size, and m lies at most 4 ln 2 / 1 (in nats) from the row's maximum, so
 with D = distance to the maximum + 3 a term of the sum is off by (3 D + 1) u, and a
-sum of n terms by n u more.  Where a thread adds n = 8 ceil(V / (8 512)) terms, its
-wave 6, the workgroup 8 and the slices up to 10 joinings (two roundings each):
+sum of n terms by n u more.  Where a thread adds n = 8 ceil(V / (8 threads)) terms (128
+threads at least on up to 1200 vectors of 8, 256 on up to 12000, else 512; a cut row
+has fewer), its wave 6, the workgroup 8 and the slices up to 10 joinings (two
+roundings each):
   dS    = u (n + 60 + 3 (mean D))               relative, of a row's sum
   logp  : dS + u (4 D_target + 4 |logp| + 4 ln S + 4)
   H     : (mean D + 2)(dS) + u (4 mean D^2 + 4 mean D + 8 ln S + 8)
@@ -50,7 +52,7 @@ def rows(M, V, seed, dtype, masked=True, scale=3.0):
 
 class Bound:
     def __init__(self, r, V):
-        n = 8 * -(-V // (8 * 512))
+        n = 8 * -(-V // (8 * (128 if V <= 9600 else 256 if V <= 96000 else 512)))
         self.D = r.far + 3.0
         mean, square = r.mean + 3.0, r.square + 6 * r.mean + 9.0
         self.dS = U * (n + 60 + 3 * mean)
@@ -74,6 +76,8 @@ def half(dtype, v):
 
 
 SHAPES = [(1, 1), (3, 2), (2, 7), (1, 8), (5, 9), (2, 513), (4, 4099), (1, 32000), (2, 50257), (40, 8195), (1030, 1001)]
+# ... and of rows cut into slices of every length, of which a few rows are compared
+CUT_SHAPES = [(3, 9601), (5, 64009), (66, 60007), (60, 150_001), (60, 400_003), (400, 320_009), (2, 1_000_003), (400, 100_003)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -183,3 +187,38 @@ def test_distill(M, V, dtype, tail):
     if M > 2:
         d[1] = 0.0
     check_distill(x, idx, v, d, T, tail)
+
+
+@pytest.mark.parametrize("M,V", CUT_SHAPES)
+def test_cuts(M, V):
+    T = 1.5
+    x = (torch.randn((M, V), device=dev(), generator=torch.Generator(dev()).manual_seed(V)) * 3).half()
+    some = sorted({0, 1, M // 2, M - 1})
+    targets = torch.arange(M, device=dev()) * 7
+    ones = torch.ones(M, device=dev())
+    r = oracle.Rows(np64(x[some]), T)
+    b = Bound(r, V)
+    at = (np.arange(len(some)), targets[some].cpu().numpy())
+    for k in (0, 20, 128):
+        logp, H, top, idx = rbq.token_logprobs(x, targets, top=k, temperature=T)
+        near(logp[some], r.lp[at], b.lp[at], "logp")
+        near(H[some], r.H, b.H, "entropy")
+        want = oracle.top(np64(x[some]), k)
+        assert np.array_equal(idx[some].cpu().numpy(), want)
+        m = np.arange(len(some))[:, None]
+        near(top[some], r.lp[m, want], b.lp[m, want], "top")
+    dx, logp, H = rbq.token_logprobs_backward(x, targets, ones, ones, temperature=T)
+    g = oracle.logprobs_grad(r, at[1], np.ones(len(some)), np.ones(len(some)))
+    lp = np.abs(r.lp)
+    tol = (r.p * (b.rel + 4 * U) + 4 * U * (g != 0) + r.p * ((lp + r.H[:, None]) * (b.rel + 8 * U) + b.lp + b.H[:, None])) / T
+    near(dx[some], g, tol + half(torch.float16, np.abs(g) + tol), "gradient")
+    near(H[some], r.H, b.H, "entropy of the backward")
+    tv, ti = top, idx
+    loss, grad, size = oracle.distill(r, idx[some].cpu().numpy(), np64(tv[some]), True)
+    L = rbq.distill_forward(x, ti, tv, temperature=T, tail=True)
+    dx, L2 = rbq.distill_backward(x, ti, tv, ones, temperature=T, tail=True)
+    tol = 4 * b.dS + U * (4 * b.D.max(1) + np.abs(loss) + 4)
+    near(L[some], loss, tol, "loss")
+    near(L2[some], loss, tol, "loss of the backward")
+    e = size * (b.rel + 2 * b.dS[:, None] + 8 * U) + 2.0 ** -40
+    near(dx[some], grad, e + half(torch.float16, np.abs(grad) + e), "gradient")

@@ -17,10 +17,9 @@ def lowest(dtype):
     return torch.finfo(dtype).min
 
 
-@pytest.mark.parametrize("M", [2, 1100], ids=["slices", "whole rows"])
+@pytest.mark.parametrize("M,V", [(2, 9001), (1100, 9001), (12, 60001)], ids=["two rows", "many rows", "slices"])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_masks_and_extremes(dtype, M):
-    V = 9001
+def test_masks_and_extremes(dtype, M, V):
     x = rows(M, V, 3, dtype)
     x[0] = -INF                              # nothing left
     if M > 2:
@@ -57,7 +56,7 @@ def test_masks_and_extremes(dtype, M):
     near(g[ok], w[ok], (tol + torch.finfo(dtype).eps / 2 * (np.abs(w) + tol) + 2.0 ** -25)[ok], "gradient")
 
 
-@pytest.mark.parametrize("V", [1000, 33000])
+@pytest.mark.parametrize("V", [1000, 33000, 70001])
 def test_ties_go_to_the_lowest_index(V):
     """Few different values: most alternatives are ties, also at the last place."""
     rng = np.random.default_rng(V)
@@ -72,15 +71,15 @@ def test_ties_go_to_the_lowest_index(V):
             assert np.array_equal(idx.cpu().numpy(), oracle.top(np64(x), k)), (M, k)
 
 
-@pytest.mark.parametrize("M", [2, 1025])
-def test_unkind_orders(M):
+@pytest.mark.parametrize("M,V", [(2, 20000), (1025, 20000), (3, 64000)])
+def test_unkind_orders(M, V):
     """Rows whose largest entries come last, first, or all from one thread's columns."""
-    V = 20000
     x = torch.arange(V, device=dev(), dtype=torch.float32).repeat(M, 1) / 1000
     x[1] = x[1].flip(0)
     if M > 2:
         x[2] = 0.0
-        x[2].view(-1, 8)[3::512] = torch.arange(40, device=dev(), dtype=torch.float32).view(5, 8) + 30
+        n = len(range(3, V // 8, 512))
+        x[2].view(-1, 8)[3::512] = torch.arange(8 * n, device=dev(), dtype=torch.float32).view(n, 8) + 30
     for k in (5, 64, 128):
         *_, idx = rbq.token_logprobs(x, top=k)
         assert np.array_equal(idx.cpu().numpy()[:4], oracle.top(np64(x[:4]), k)), k
@@ -99,7 +98,7 @@ def test_fewer_entries_than_alternatives():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,V", [(5, 5001), (1026, 777)])
+@pytest.mark.parametrize("M,V", [(5, 5001), (1026, 777), (5, 60001)])
 def test_rows_that_lie_apart(M, V, dtype):
     """Logits that are columns of a wider tensor, starting at an odd entry; what lies between gradients stays."""
     wide = rows(M, V + 13, 9, dtype)
@@ -122,9 +121,8 @@ def test_rows_that_lie_apart(M, V, dtype):
     assert bool((out[:, :3] == 7).all()) and bool((out[:, 3 + V:] == 7).all())
 
 
-@pytest.mark.parametrize("M", [3, 1040])
-def test_gradient_in_the_logits_place(M):
-    V = 8999
+@pytest.mark.parametrize("M,V", [(3, 8999), (1040, 8999), (3, 60007)])
+def test_gradient_in_the_logits_place(M, V):
     x = rows(M, V, 11, torch.float16, masked=False)
     targets = torch.randint(0, V, (M,), device=dev())
     d = torch.rand(M, device=dev()) + 0.5
@@ -179,7 +177,7 @@ def test_more_alternatives_than_threads_have(M, V):
 
 
 def test_a_workspace_of_any_contents():
-    M, V = 4, 30000
+    M, V = 4, 60000
     x = rows(M, V, 14, torch.float32, masked=False)
     targets = torch.randint(0, V, (M,), device=dev())
     need = int(rbq.lib().rbq_token_logprobs_workspace_bytes(M, V, 128))
@@ -198,8 +196,7 @@ def test_a_workspace_of_any_contents():
 
 
 def test_broken_tokens():
-    for M in (4, 1030):
-        V = 6000
+    for M, V in ((4, 6000), (1030, 6000), (4, 64000)):
         x = rows(M, V, 15, torch.float16, masked=False)
         targets = torch.full((M,), 3, dtype=torch.int64, device=dev())
         targets[1], targets[2] = V, 2 ** 40
@@ -228,9 +225,8 @@ def test_broken_tokens():
 
 
 @pytest.mark.parametrize("tail", [False, True])
-@pytest.mark.parametrize("M", [6, 1030])
-def test_distillation_edges(M, tail):
-    V = 7000
+@pytest.mark.parametrize("M,V", [(6, 7000), (1030, 7000), (6, 60001)])
+def test_distillation_edges(M, V, tail):
     x = rows(M, V, 16, torch.float32, masked=False)
     idx, v = teacher(M, V, 8, 17, 1.0)
     idx[0], v[0] = -1, 0.0                   # no slots
@@ -298,9 +294,9 @@ def test_gradients_against_differences():
                 assert abs(diff - g[m, j].item()) <= 4 * h * h + 2.0 ** -12, (which, m, j)
 
 
-def test_streams_and_replayed_graphs():
+@pytest.mark.parametrize("M,V", [(3, 20001), (3, 60001)])
+def test_streams_and_replayed_graphs(M, V):
     """Two graphs that share a workspace, replayed in turn with other work between, and a side stream."""
-    M, V = 3, 20001
     xs = [rows(M, V, s, torch.float16, masked=False) for s in (31, 32)]
     targets = torch.randint(0, V, (M,), device=dev())
     d = torch.ones(M, device=dev())
@@ -400,3 +396,89 @@ def test_a_run_of_all(seed=50):
     size = y.grad.abs()
     assert bool(((dY.double() - y.grad).abs() <= 2.0 ** -11 * size + 2.0 ** -25 + 2.0 ** -14 * d[0] * lq.exp()).all())
     assert torch.allclose(dW, dY.float().t().contiguous() @ X.float(), rtol=1e-3, atol=1e-4)
+
+
+@pytest.mark.parametrize("V", [500, 60001])
+def test_refusals(V):
+    """Types, sizes, strides and gradients that lie over what is read."""
+    x = rows(4, V, 60, torch.float16)
+    f, i = torch.zeros(4, device=dev()), torch.zeros(4, dtype=torch.int64, device=dev())
+    ti, tv = torch.zeros((4, 3), dtype=torch.int32, device=dev()), torch.zeros((4, 3), device=dev())
+    wrong = (TypeError, ValueError)
+    for bad in (x.double(), x.int(), x[0], x.t(), x[:, ::2], x[:1].expand(4, V), x[:, :0], x.cpu()):
+        for call in (lambda: rbq.token_logprobs(bad), lambda: rbq.token_logprobs_backward(bad, i, f),
+                     lambda: rbq.distill_forward(bad, ti, tv), lambda: rbq.distill_backward(bad, ti, tv, f)):
+            with pytest.raises(wrong):
+                call()
+    for call in (lambda: rbq.token_logprobs(x, i.int()), lambda: rbq.token_logprobs(x, i[:3]),
+                 lambda: rbq.token_logprobs(x, top=129), lambda: rbq.token_logprobs(x, top=-1),
+                 lambda: rbq.token_logprobs_backward(x, i, f.double()), lambda: rbq.token_logprobs_backward(x, i, f[:2]),
+                 lambda: rbq.token_logprobs_backward(x, i, f, f.half()),
+                 lambda: rbq.token_logprobs_backward(x, i, f, d_logits=x.float()),
+                 lambda: rbq.token_logprobs_backward(x, i, f, d_logits=torch.empty_like(x)[:, :-1]),
+                 lambda: rbq.distill_forward(x, ti.long(), tv), lambda: rbq.distill_forward(x, ti, tv.half()),
+                 lambda: rbq.distill_forward(x, ti[:3], tv[:3]), lambda: rbq.distill_forward(x, ti, tv[:, :2]),
+                 lambda: rbq.distill_forward(x, torch.zeros((4, 129), dtype=torch.int32, device=dev()),
+                                             torch.zeros((4, 129), device=dev())),
+                 lambda: rbq.distill_backward(x, ti, tv, f[:1])):
+        with pytest.raises(wrong):
+            call()
+    for T in (0.0, -1.0, float("nan"), float("inf"), 1e-4, 1e4):
+        with pytest.raises(rbq.RbqError):
+            rbq.token_logprobs(x, temperature=T)
+        with pytest.raises(rbq.RbqError):
+            rbq.distill_forward(x, ti, tv, temperature=T)
+    # a gradient half over the logits: another row's place, or another stride
+    wide = torch.zeros(6, V, dtype=torch.float16, device=dev())
+    with pytest.raises(rbq.RbqError):
+        rbq.token_logprobs_backward(wide[:4], i, f, d_logits=wide[1:5])
+    with pytest.raises(rbq.RbqError):
+        rbq.distill_backward(wide[:4], ti, tv, f, d_logits=wide[2:6])
+    # a gradient that is asked of a target needs targets
+    with pytest.raises(rbq.RbqError):
+        rbq.token_logprobs_backward(x, None, f)
+    torch.cuda.synchronize()
+
+
+def test_no_rows_and_one_entry():
+    """No rows at all; a vocabulary of one, whose only token is certain."""
+    e = torch.empty((0, 70), dtype=torch.bfloat16, device=dev())
+    none = torch.empty(0, device=dev())
+    logp, H, top, idx = rbq.token_logprobs(e, torch.empty(0, dtype=torch.int64, device=dev()), top=5)
+    assert logp.shape == H.shape == (0,) and top.shape == idx.shape == (0, 5)
+    assert rbq.distill_backward(e, idx, top, none)[0].shape == (0, 70)
+    x = torch.tensor([[3.0], [-INF], [-7.0]], device=dev())
+    i = torch.zeros(3, dtype=torch.int64, device=dev())
+    logp, H, top, idx = rbq.token_logprobs(x, i, top=2)
+    # (the bounds of tests/test_gpu_logits.py with n = 8, D = 3, nothing else: all of 4 (n + 60 + 3 D) + 4 D + 8 steps)
+    tol = (4 * (8 + 60 + 9) + 4 * 3 + 8) * 2.0 ** -23
+    near(logp[[0, 2]], np.zeros(2), tol, "logp")
+    near(H[[0, 2]], np.zeros(2), tol, "entropy")
+    assert idx[[0, 2]].tolist() == [[0, -1]] * 2 and idx[1].tolist() == [-1, -1]
+    one = torch.ones(3, device=dev())
+    d, *_ = rbq.token_logprobs_backward(x, i, one, one)
+    near(d[[0, 2]], np.zeros((2, 1)), 2 * tol, "gradient")
+    assert not d[1].any()
+    d, loss = rbq.distill_backward(x[:1], idx[:1], top[:1], one[:1], tail=True)
+    near(d, np.zeros((1, 1)), 2 * tol, "gradient")
+    near(loss, np.zeros(1), 2 * tol, "loss")
+
+
+@pytest.mark.parametrize("M,V", [(2, 100), (1030, 5000), (2, 60001)])
+def test_a_rest_that_is_none(M, V):
+    """Teacher and student mask the same tokens, or all are named: what the teacher's rounded log probabilities leave
+    beside the named ones is no class of its own."""
+    x, y = (rows(M, V, s, torch.float32, masked=False) for s in (70, 71))
+    for mask in (-INF, lowest(torch.float32)):
+        if V > 128:
+            x[:, 100:] = mask
+            y[:, 100:] = mask
+        *_, v, idx = rbq.token_logprobs(y, top=128)
+        dx, loss = rbq.distill_backward(x, idx, v, torch.ones(M, device=dev()), tail=True)
+        assert torch.isfinite(loss).all() and torch.isfinite(dx).all()
+        # of 100 tokens, all named: the full divergence
+        lp, lq = (torch.log_softmax(z[:, :100].double(), 1) for z in (y, x))
+        want = (lp.exp() * (lp - lq)).sum(1)
+        # each side's sum off by dS = 2^-23 (n + 60 + 3 D), D and a term's distance up to 64 here, p by as much
+        tol = 2.0 ** -23 * (8 * 64 + 60 + 3 * 64) * (2 + want)
+        assert bool(((loss.double() - want).abs() <= tol).all())
