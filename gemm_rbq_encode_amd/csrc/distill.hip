@@ -95,11 +95,8 @@ __device__ __forceinline__ void distill_write(const typename T::bits *x, typenam
 // the slices' sums.  GRAD: the gradient of a slice is written (WHOLE, REST).
 enum { DS_WHOLE = 0, DS_SUMS = 1, DS_REST = 2 };
 
-// The slots' tokens, and the student's logits of them: x may be the gradient's
-// buffer, so the slices keep them beside their sums.
-template <typename T, int MODE>
-__device__ __forceinline__ void distill_slots(const typename T::bits *x, const lg_range &r, int row,
-                                              const lg_row_args &a, const lg_distill_args &p, float (&t)[2],
+// The slots' tokens.
+__device__ __forceinline__ void distill_slots(int row, const lg_row_args &a, const lg_distill_args &p, float (&t)[2],
                                               lg_slots &sl) {
     const int lane = threadIdx.x & 63;
     const int64_t first = (int64_t)row * p.slots;
@@ -120,8 +117,7 @@ __device__ __forceinline__ void distill_slots(const typename T::bits *x, const l
             t[q] = -__builtin_inff();
         }
         any |= index[q] >= 0;
-        if (j < p.slots)
-            sl.index[j] = index[q];
+        sl.index[j] = index[q];
     }
     bad = __any(bad);
     any = __any(any);
@@ -131,9 +127,19 @@ __device__ __forceinline__ void distill_slots(const typename T::bits *x, const l
         if (bad && a.status != nullptr)
             atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
     }
+}
+
+// The student's logits of the slots' tokens: x may be the gradient's buffer, so the
+// slices keep them beside their sums.  A wave's part, behind the barrier that the
+// others wait at for the tokens alone.
+template <typename T, int MODE>
+__device__ __forceinline__ void distill_logits(const typename T::bits *x, const lg_range &r, int row,
+                                               const lg_row_args &a, const lg_distill_args &p, lg_slots &sl) {
+    const int lane = threadIdx.x & 63;
+    const int64_t first = (int64_t)row * p.slots;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int i = index[q], j = lane + 64 * q;
+        const int j = lane + 64 * q, i = sl.index[j];
         if (i < 0)
             continue;
         if (MODE == DS_WHOLE)
@@ -242,10 +248,13 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
     const lg_range r = lg_slice(a.V, a.slices, slice);
     float t_logp[2];
     if (tid < 64)
-        distill_slots<T, MODE>(x, r, row, a, p, t_logp, sl);
+        distill_slots(row, a, p, t_logp, sl);
     __syncthreads();
-    if (MODE != DS_SUMS && tid < 64)
-        distill_teacher<KIND>(t_logp, p.slots, sl);
+    if (tid < 64) {
+        distill_logits<T, MODE>(x, r, row, a, p, sl);
+        if (MODE != DS_SUMS)
+            distill_teacher<KIND>(t_logp, p.slots, sl);
+    }
     lg_row t;
     if constexpr (MODE == DS_REST) {
         for (int i = tid; i < a.slices; i += TH)
@@ -292,9 +301,18 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
             if (i < 0 || i / LG_VEC < r.v0 || i / LG_VEC >= r.v1)
                 continue;
             double mine = 0.0;
-            for (int k = 0; k < p.slots; ++k)
-                if (sl.index[k] == i)
-                    mine += sl.p[k];
+            for (int k = 0; k < p.slots; k += 8) {      // (8 reads on their way at a time; slots behind the last: -1)
+                int same[8];
+                double pk[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    same[q] = sl.index[k + q];
+                    pk[q] = sl.p[k + q];
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    mine += same[q] == i ? pk[q] : 0.0;
+            }
             const double e = __builtin_amdgcn_exp2f(t.exponent(sl.x[j], a.c));
             dx[i] = T::of((float)(e * all - by * mine));
         }
