@@ -44,7 +44,8 @@ struct lg_slots {
 // in `map`, a chunk of LG_MAP vectors at a time.
 template <typename T, int KIND, bool QUICK, int TH>
 __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const lg_range &r, const lg_slots &sl,
-                                               int slots, float c, uint32_t *map, float4 *part) {
+                                               int slots, float c, uint32_t *map, float4 *part,
+                                               void *held) {
     const int tid = threadIdx.x;
     lg_sums<QUICK> s;
     float best;
@@ -64,12 +65,12 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
                     atomicOr(&map[bit >> 5], 1u << (bit & 31));
             }
             __syncthreads();
-            lg_walk<T, TH> walk(x, q);
+            lg_walk<T, TH> walk(x, q, held);
             lg_stream<T, KIND, false>(walk, c, (const uint8_t *)map, q.v0, s, best, where);
             __syncthreads();
         }
     } else {
-        lg_walk<T, TH> walk(x, r);
+        lg_walk<T, TH> walk(x, r, held);
         lg_stream<T, KIND, false>(walk, c, nullptr, 0, s, best, where);
     }
     const lg_sums<QUICK> t = lg_join_block<KIND, TH>(s, c, part);
@@ -82,8 +83,8 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
 // dx = e w of a slice.
 template <typename T, bool QUICK, int TH>
 __device__ __forceinline__ void distill_write(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
-                                              float m, float c, float w) {
-    lg_walk<T, TH> walk(x, r);
+                                              float m, float c, float w, void *held) {
+    lg_walk<T, TH> walk(x, r, held);
     walk.down(dx, [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LG_VEC; ++i)
@@ -239,6 +240,7 @@ template <typename T, int KIND, int MODE, bool GRAD, int TH>
 __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_args p) {
     __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : TH / 64];
     __shared__ lg_slots sl;
+    __shared__ uint4 held_[GRAD && MODE == DS_WHOLE ? lg_walk<T, TH>::HELD_BYTES / 16 : 1];
     extern __shared__ uint32_t map[];
     const int tid = threadIdx.x;
     const int per_row = MODE == DS_REST && !GRAD ? 1 : a.slices;
@@ -246,6 +248,8 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
     const int row = (int)(u / per_row), slice = (int)(u - (int64_t)row * per_row);
     const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
     const lg_range r = lg_slice(a.V, a.slices, slice);
+    // (a row in several maps is not held: its walks up end elsewhere)
+    uint4 *const held = GRAD && MODE == DS_WHOLE && (KIND != LG_NAMED || r.v1 <= LG_MAP) ? held_ : nullptr;
     float t_logp[2];
     if (tid < 64)
         distill_slots(row, a, p, t_logp, sl);
@@ -262,15 +266,15 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
         __syncthreads();
         t = lg_row_of(lg_join_list<KIND, false>(part, a.slices, a.c));
     } else if constexpr (MODE == DS_SUMS) {
-        t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part);
+        t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part, held);
         if (tid == 0)
             a.sums[u] = make_float4(t.m, t.S, t.b, 0.0f);
         return;
     } else {
-        t = distill_sums<T, KIND, true, TH>(x, r, sl, p.slots, a.c, map, part);
+        t = distill_sums<T, KIND, true, TH>(x, r, sl, p.slots, a.c, map, part, held);
         if (t.S != t.S) {
             __syncthreads();
-            t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part);
+            t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part, held);
         }
     }
     const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
@@ -292,9 +296,9 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
         const double away = KIND == LG_NAMED && rest != 0.0 && t.S != 0.0f ? by * rest / (double)t.S : 0.0;
         // (every slot's logit has been read: dx may be x)
         if (MODE == DS_WHOLE && t.quick)
-            distill_write<T, true, TH>(x, dx, r, t.m, a.c, (float)(all - away));
+            distill_write<T, true, TH>(x, dx, r, t.m, a.c, (float)(all - away), held);
         else
-            distill_write<T, false, TH>(x, dx, r, t.m, a.c, (float)(all - away));
+            distill_write<T, false, TH>(x, dx, r, t.m, a.c, (float)(all - away), held);
         __syncthreads();    // then the named tokens, a thread a slot; a token named twice gets both in each
         for (int j = tid; j < p.slots; j += TH) {
             const int i = sl.index[j];

@@ -506,7 +506,7 @@ __device__ __forceinline__ void lg_logp_grad(lg_walk<T, TH> &walk, typename T::b
 // 50257 bf16 with the entropy's part 21.6 (3.1: 333 workgroups on 256 CUs).
 template <typename T, int TH, bool SLICED, bool ENTROPY>
 __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
-    __shared__ float4 part[LG_SLICES_MAX];
+    __shared__ float4 part[SLICED ? LG_SLICES_MAX : TH / 64];
     const int64_t u = a.first + blockIdx.x;
     const int row = (int)(u / a.slices), slice = (int)(u - (int64_t)row * a.slices);
     const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
@@ -520,7 +520,8 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
         lg_zero<T, TH>(dx, r);
         return;
     }
-    lg_walk<T, TH> walk(x, r);
+    __shared__ uint4 held[SLICED ? 1 : lg_walk<T, TH>::HELD_BYTES / 16];
+    lg_walk<T, TH> walk(x, r, SLICED ? nullptr : held);
     lg_row sums;
     if constexpr (SLICED) {
         for (int i = threadIdx.x; i < a.slices; i += TH)

@@ -55,6 +55,16 @@ __device__ __forceinline__ typename T::raw lg_load(const typename T::bits *p) {
     return r;
 }
 
+// ... past the caches
+template <typename T>
+__device__ __forceinline__ typename T::raw lg_load_past(const typename T::bits *p) {
+    typename T::raw r;
+    r.a = __builtin_nontemporal_load((const lg_u32x4 *)p);
+    if constexpr (sizeof(typename T::bits) == 4)
+        r.b = __builtin_nontemporal_load((const lg_u32x4 *)(p + 4));
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void lg_values(const typename T::raw &r, float (&x)[LG_VEC]) {
 #pragma unroll
@@ -420,14 +430,21 @@ __device__ __forceinline__ lg_range lg_slice(int V, int slices, int s) {
 
 // A thread's vectors of a slice: those of `turns` whole turns of the workgroup,
 // one more where `more`, and the row's last one, part empty, where `part`.
+//
+// A walk up that another one down follows keeps the last HELD turns in LDS (64 bytes
+// a thread: the rest of 160 KB when a CU is full of threads), read past the caches,
+// which keep the others: a CU's share of the second-level cache is 128 KB.
 template <typename T, int TH>
 struct lg_walk {
     static constexpr int AHEAD = 4;
+    static constexpr int HELD = 64 / (int)sizeof(typename T::raw);
+    static constexpr int HELD_BYTES = TH * 64;
     const typename T::bits *x;
     int v, turns, rest;     // v: the first vector
     bool more, part;
+    uint4 *hold;            // (LDS) or none
 
-    __device__ __forceinline__ lg_walk(const typename T::bits *row, const lg_range &r) : x(row) {
+    __device__ __forceinline__ lg_walk(const typename T::bits *row, const lg_range &r, void *held = nullptr) : x(row) {
         const int end = min(r.v1, r.whole);
         v = r.v0 + (int)threadIdx.x;
         turns = max(0, end - r.v0) / TH;
@@ -435,6 +452,7 @@ struct lg_walk {
         more = last < end;
         part = (more ? last + TH : last) == r.whole && r.v1 > r.whole;
         rest = r.rest;
+        hold = turns >= HELD ? (uint4 *)held : nullptr;
     }
     __device__ __forceinline__ const typename T::bits *at(int turn) const {
         return x + (int64_t)(v + turn * TH) * LG_VEC;
@@ -443,7 +461,8 @@ struct lg_walk {
     template <typename F>
     __device__ __forceinline__ void up(F f) {
         int t = 0;
-        for (; t + AHEAD <= turns; t += AHEAD) {
+        const int cached = hold != nullptr ? turns - HELD : turns;
+        for (; t + AHEAD <= cached; t += AHEAD) {
             typename T::raw raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
@@ -455,8 +474,23 @@ struct lg_walk {
                 f(e, v + (t + i) * TH);
             }
         }
-        for (; t < turns; ++t)
+        for (; t < cached; ++t)
             one(t, f);
+        if (hold != nullptr) {
+            typename T::raw raw[HELD];
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                raw[i] = lg_load_past<T>(at(t + i));
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                hold[i * TH + threadIdx.x] = __builtin_bit_cast(uint4, raw[i].a);
+                if constexpr (sizeof(typename T::bits) == 4)
+                    hold[(HELD + i) * TH + threadIdx.x] = __builtin_bit_cast(uint4, raw[i].b);
+                float e[LG_VEC];
+                lg_values<T>(raw[i], e);
+                f(e, v + (t + i) * TH);
+            }
+        }
         if (more)
             one(turns, f);
         if (part) {
@@ -486,6 +520,20 @@ struct lg_walk {
         if (more)
             back(out, turns, f);
         int t = turns;
+        if (hold != nullptr) {
+#pragma unroll
+            for (int i = HELD - 1; i >= 0; --i) {
+                --t;
+                typename T::raw raw;
+                raw.a = __builtin_bit_cast(lg_u32x4, hold[i * TH + threadIdx.x]);
+                if constexpr (sizeof(typename T::bits) == 4)
+                    raw.b = __builtin_bit_cast(lg_u32x4, hold[(HELD + i) * TH + threadIdx.x]);
+                float e[LG_VEC];
+                lg_values<T>(raw, e);
+                f(e, v + t * TH);
+                lg_store<T>(out + (int64_t)(v + t * TH) * LG_VEC, e);
+            }
+        }
         for (; t >= AHEAD; t -= AHEAD) {
             typename T::raw raw[AHEAD];
 #pragma unroll
