@@ -233,9 +233,9 @@ __device__ __forceinline__ float distill_loss(const lg_row &t, double S, float c
 // by wave 0 while the others read logits.  The named tokens are marked in a map of bits
 // in LDS, and their exponentials left out of the sum of the rest as it is formed: 1 -
 // sum q would cancel.  Bound by the read and the write of the gradient: a step of 2048 x
-// 128256 fp16 with 64 slots and the tail 254 us (4.1 TB/s of both, a copy 5.2), the loss
-// alone 98 (5.4 TB/s); 64 x 128256 fp32 13.5, of it 9.1 the slices' sums and 4.4 the
-// second launch; 77 x 32001 bf16 12.6 on the device.
+// 128256 fp16 with 64 slots and the tail 240 to 247 us (4.3 TB/s of both, a copy 5.2),
+// the loss alone 98 (5.4 TB/s); 64 x 128256 fp32 13.5, of it 9.1 the slices' sums and
+// 4.4 the second launch; 77 x 32001 bf16 12 on the device.
 template <typename T, int KIND, int MODE, bool GRAD, int TH>
 __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_args p) {
     __shared__ float4 part[MODE == DS_REST ? LG_SLICES_MAX : TH / 64];

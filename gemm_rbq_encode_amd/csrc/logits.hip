@@ -501,9 +501,9 @@ __device__ __forceinline__ void lg_logp_grad(lg_walk<T, TH> &walk, typename T::b
 }
 
 // The row's sums, then a second walk from its end, whose last vectors are still in the
-// cache, that writes the gradient past it.  Bound by the read and the write: 2048 x
-// 32000 fp16 57 us (4.6 TB/s of both, a copy 5.2), 2048 x 128256 234 (4.5), 333 x
-// 50257 bf16 with the entropy's part 21.6 (3.1: 333 workgroups on 256 CUs).
+// cache or in LDS, that writes the gradient past it.  Bound by the read and the write:
+// 2048 x 32000 fp16 52 to 55 us (5.0 TB/s of both, a copy 5.2), 2048 x 128256 237 (4.4),
+// 333 x 50257 bf16 with the entropy's part 21.6 (3.1: 333 workgroups on 256 CUs).
 template <typename T, int TH, bool SLICED, bool ENTROPY>
 __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_logp_args p) {
     __shared__ float4 part[SLICED ? LG_SLICES_MAX : TH / 64];
@@ -521,7 +521,9 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
         return;
     }
     __shared__ uint4 held[SLICED ? 1 : lg_walk<T, TH>::HELD_BYTES / 16];
-    lg_walk<T, TH> walk(x, r, SLICED ? nullptr : held);
+    // (few rows stay in the caches: 333 x 50257 bf16 21.6 us without, 24.1 held; 512 x
+    // 32000 fp16 16.6 and 16.3)
+    lg_walk<T, TH> walk(x, r, SLICED || a.M < 512 ? nullptr : held);
     lg_row sums;
     if constexpr (SLICED) {
         for (int i = threadIdx.x; i < a.slices; i += TH)

@@ -16,7 +16,8 @@ constexpr int LG_TOPS = 1 << 14;     // vectors of a slice whose maxima LDS hold
 
 // Slices of a row.  Cutting takes a second launch and a second start of every
 // workgroup, so only a few long rows are cut, each thread with one vector at least.
-// us whole / cut, fp16:
+// us whole / cut, fp16 (before rows were held in LDS and the named tokens' shares read
+// eight at a time, which takes 4 us off a distillation step on either side):
 //              sums alone    20 alternatives    gradient      distillation and gradient
 //   1 x  32000   5.2   5.7      11.1  12.9       7.8   7.6       11.1  11.2
 //  64 x  32000   6.4   7.7      13.6  15.4       9.2   9.8       12.9  13.9
@@ -43,6 +44,8 @@ inline int logits_slices(int M, int vocab) {
 //   sums alone      176  103   66    66   42   35    34   31   32    29   30   29     96   97
 //   gradient        234  135   86    85   63   58    57   62   67    61   65   64    247  254
 //   distillation    543  287  216   171  114  100    89   78   83    74   78   80    257  278
+// (with parts of the rows held in LDS since: gradient 86, 52, 55 with 128, 256 and 512
+// threads on rows of 1000, 4000 and 32000, distillation 88 and 63 on 4000 and 32000)
 //   64 alternatives 750  346  229   208  109   91    76   51   53    54   44   51    118  135
 // More than 64 alternatives need more threads than they are.
 inline int logits_threads(int each, int k) {
