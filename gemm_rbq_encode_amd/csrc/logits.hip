@@ -542,6 +542,7 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
                       : lg_inside(target, a.V) ? T::one(x[target])
                                                  : 0.0f,
                       target, row, a, p);
+    __syncthreads();    // the target's entry has been read: dx may be x, of rows without weight too
     if (none || w.empty) {
         lg_zero<T, TH>(dx, r);
     } else {
@@ -550,13 +551,11 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
         const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
         const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
         const float own = wa * a.inv_t;
-        __syncthreads();    // the target's entry has been read: dx may be x
         if (!SLICED && w.quick)
             lg_logp_grad<T, true, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
         else
             lg_logp_grad<T, false, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);
     }
-    __syncthreads();
 }
 
 // f(threads of a workgroup) for a slice of `each` vectors and k alternatives.
