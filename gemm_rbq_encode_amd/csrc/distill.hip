@@ -286,7 +286,7 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
     if constexpr (GRAD) {
         typename T::bits *dx = (typename T::bits *)p.dx + row * p.d_stride;
         const float d = p.d_loss[row];
-        if (d == 0.0f || S == 0.0 || (KIND != LG_NAMED && !sl.any && !sl.bad)) {
+        if (d == 0.0f || (!sl.bad && (S == 0.0 || (KIND != LG_NAMED && !sl.any)))) {
             lg_zero<T, TH>(dx, r);
             return;
         }

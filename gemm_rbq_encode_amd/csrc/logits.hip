@@ -543,13 +543,14 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
                                                  : 0.0f,
                       target, row, a, p);
     __syncthreads();    // the target's entry has been read: dx may be x, of rows without weight too
-    if (none || w.empty) {
+    // (the entropy's part does not depend on the token)
+    const bool bad = target >= a.V && wa != 0.0f;
+    if (none || (w.empty && !bad)) {
         lg_zero<T, TH>(dx, r);
     } else {
         const float scale = a.inv_t / w.S;
-        const float bad = target >= a.V ? __builtin_nanf("") : 0.0f;
-        const float w0 = -scale * (wa + wb * (w.H - LN2 * w.logS)) + bad, w1 = -scale * wb * LN2;
-        const int at = target < 0 ? -1 : (int)(target / LG_VEC), in = (int)(target % LG_VEC);
+        const float w0 = bad ? __builtin_nanf("") : -scale * (wa + wb * (w.H - LN2 * w.logS)), w1 = -scale * wb * LN2;
+        const int at = lg_inside(target, a.V) ? (int)target / LG_VEC : -1, in = (int)target % LG_VEC;
         const float own = wa * a.inv_t;
         if (!SLICED && w.quick)
             lg_logp_grad<T, true, ENTROPY>(walk, dx, w.m, a.c, w0, w1, at, in, own);

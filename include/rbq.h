@@ -852,7 +852,8 @@ rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8
  * probabilities are -inf, its entropy 0, its gradients 0.  A row with a NaN or
  * +inf entry has NaN outputs and gradients, and alternatives of index -1.  A
  * token number of `vocab` or more sets RBQ_STATUS_BAD_TOKEN in status_dev, and
- * that row's outputs and gradients that depend on it are NaN.
+ * that row's outputs and gradients that depend on it are NaN, an empty row's
+ * among them.  (What has a weight of 0 depends on no token.)
  *
  * workspace: 16-byte aligned device memory of the query's size, any contents.
  * With few rows, each is cut into slices over workgroups whose partial results
