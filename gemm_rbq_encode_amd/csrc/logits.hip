@@ -335,12 +335,15 @@ struct lg_logp_row : lg_row {
 __device__ __forceinline__ float lg_target(const lg_logp_row &r, float v, int64_t target, const lg_row_args &a) {
     if (target < 0)
         return 0.0f;
-    if (target >= a.V) {
-        if (a.status != nullptr)
-            atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
+    if (target >= a.V)
         return __builtin_nanf("");
-    }
     return r.empty ? -__builtin_inff() : r.logp(v, a.c, a.inv_t);
+}
+
+// A row's token beyond the vocabulary is reported whatever is asked of the row.
+__device__ __forceinline__ void lg_report(int64_t target, const lg_row_args &a) {
+    if (target >= a.V && a.status != nullptr)
+        atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
 }
 
 // What thread 0 writes of a row.  The target's logit is found in the row, or,
@@ -405,6 +408,8 @@ __global__ __launch_bounds__(TH) void logprobs_kernel(lg_row_args a, lg_logp_arg
     const typename T::bits *x = (const typename T::bits *)a.x + row * a.stride;
     const lg_range r = lg_slice(a.V, a.slices, slice);
     const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
+    if (slice == 0 && threadIdx.x == 0)
+        lg_report(target, a);
     float best = -__builtin_inff();
     int where = 0;
     lg_walk<T, TH> walk(x, r);
@@ -515,6 +520,8 @@ __global__ __launch_bounds__(TH) void logprobs_grad_kernel(lg_row_args a, lg_log
     const int64_t target = p.targets == nullptr ? -1 : p.targets[row];
     const float wa = p.d_logp == nullptr || target < 0 ? 0.0f : p.d_logp[row];
     const float wb = ENTROPY ? p.d_entropy[row] : 0.0f;
+    if (!SLICED && threadIdx.x == 0)
+        lg_report(target, a);       // (cut rows: with their sums)
     const bool none = wa == 0.0f && wb == 0.0f;
     if (none && p.logp == nullptr && p.entropy == nullptr) {
         lg_zero<T, TH>(dx, r);

@@ -1,4 +1,5 @@
-"""Token numbers beyond the vocabulary: NaN exactly in what depends on them."""
+"""Token numbers beyond the vocabulary: reported whatever is asked of their rows, and
+NaN exactly in what depends on them."""
 import pytest
 import torch
 
@@ -54,3 +55,27 @@ def test_empty_rows_with_a_bad_token(M, V):
         dx, loss = rbq.distill_backward(x, t(idx, torch.int32), t(v, torch.float32), a, tail=tail)
         assert torch.isnan(loss[1:3]).all() and loss[3] == INF
         assert torch.isnan(dx[1]).all() and not dx[2:4].any() and torch.isfinite(dx[0]).all()
+
+
+@pytest.mark.parametrize("M,V", SIZES)
+def test_tokens_are_reported_where_no_log_probability_is_asked_for(M, V):
+    """The C calls with logp NULL, rows without weight among them."""
+    x = rows(M, V, M + V, torch.float16, masked=False)
+    dx = torch.empty_like(x)
+    H, zero, one = torch.empty(M, device=dev()), torch.zeros(M, device=dev()), torch.ones(M, device=dev())
+    L, none = rbq.lib(), torch.full((M,), -1, dtype=torch.int64, device=dev())
+    need = int(L.rbq_token_logprobs_workspace_bytes(M, V, 0))
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev())
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    for targets, want in ((bad_targets(M, V), rbq.RBQ_STATUS_BAD_TOKEN), (none, 0)):
+        for n in (0, need):
+            row = [x.data_ptr(), rbq.RBQ_L_F16, M, V, V, 1.0, targets.data_ptr()]
+            room = [ws.data_ptr(), n]
+            for call, more in ((L.rbq_token_logprobs, [None, H.data_ptr(), 0, None, None]),
+                               (L.rbq_token_logprobs_backward, [zero.data_ptr(), None, dx.data_ptr(), V, None, None]),
+                               (L.rbq_token_logprobs_backward, [zero.data_ptr(), zero.data_ptr(), dx.data_ptr(), V, None, None]),
+                               (L.rbq_token_logprobs_backward, [None, one.data_ptr(), dx.data_ptr(), V, None, H.data_ptr()])):
+                st = torch.zeros(1, dtype=torch.int32, device=dev())
+                assert call(*row, *more, *room, st.data_ptr(), stream) == rbq.RBQ_OK
+                assert int(st.item()) == want
