@@ -108,11 +108,12 @@ __device__ __forceinline__ void distill_slots(int row, const lg_row_args &a, con
         index[q] = j < p.slots ? p.index[first + j] : -1;
         t[q] = j < p.slots ? p.t_logp[first + j] : -__builtin_inff();
     }
-    bool bad = false, any = false;
+    bool bad = false, any = false, beyond = false;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int j = lane + 64 * q;
-        bad |= index[q] >= a.V;
+        beyond |= index[q] >= a.V;
+        bad |= index[q] >= a.V && t[q] != -__builtin_inff();    // (else not used)
         if (index[q] < 0 || index[q] >= a.V || t[q] == -__builtin_inff()) {
             index[q] = -1;
             t[q] = -__builtin_inff();
@@ -122,10 +123,11 @@ __device__ __forceinline__ void distill_slots(int row, const lg_row_args &a, con
     }
     bad = __any(bad);
     any = __any(any);
+    beyond = __any(beyond);
     if (lane == 0) {
         sl.bad = bad;
         sl.any = any;
-        if (bad && a.status != nullptr)
+        if (beyond && a.status != nullptr)
             atomicOr(a.status, RBQ_STATUS_BAD_TOKEN);
     }
 }

@@ -853,8 +853,8 @@ rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8
  * +inf entry has NaN outputs and gradients, and alternatives of index -1.  A
  * token number of `vocab` or more sets RBQ_STATUS_BAD_TOKEN in status_dev, and
  * that row's outputs and gradients that depend on it are NaN, an empty row's
- * among them.  (A log probability that is not asked for and a weight of 0 depend
- * on no token.)
+ * among them.  (A log probability that is not asked for, a weight of 0 and a
+ * slot that is not used depend on no token.)
  *
  * workspace: 16-byte aligned device memory of the query's size, any contents.
  * With few rows, each is cut into slices over workgroups whose partial results

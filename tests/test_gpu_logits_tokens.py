@@ -58,6 +58,23 @@ def test_empty_rows_with_a_bad_token(M, V):
 
 
 @pytest.mark.parametrize("M,V", SIZES)
+def test_slots_that_are_not_used_name_no_token(M, V):
+    x = rows(M, V, M + V, torch.float16, masked=False)
+    idx, v = teacher(M, V, 6, 4, 1.0)
+    v[:, 4] = -INF
+    bad = idx.copy()
+    bad[::2, 4] = 2 ** 31 - 1
+    d = torch.ones(M, device=dev())
+    for tail in (False, True):
+        ref = rbq.distill_backward(x, t(idx, torch.int32), t(v, torch.float32), d, tail=tail)
+        st = torch.zeros(1, dtype=torch.int32, device=dev())
+        got = rbq.distill_backward(x, t(bad, torch.int32), t(v, torch.float32), d, tail=tail, status=st)
+        assert all(torch.equal(p, q) for p, q in zip(ref, got)) and torch.isfinite(got[0]).all()
+        assert int(st.item()) == rbq.RBQ_STATUS_BAD_TOKEN
+        assert torch.equal(ref[1], rbq.distill_forward(x, t(bad, torch.int32), t(v, torch.float32), tail=tail))
+
+
+@pytest.mark.parametrize("M,V", SIZES)
 def test_tokens_are_reported_where_no_log_probability_is_asked_for(M, V):
     """The C calls with logp NULL, rows without weight among them."""
     x = rows(M, V, M + V, torch.float16, masked=False)
