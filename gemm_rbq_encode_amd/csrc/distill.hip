@@ -80,16 +80,32 @@ __device__ __forceinline__ lg_row distill_sums(const typename T::bits *x, const 
     return lg_row_of(t);
 }
 
-// dx = e w of a slice.
-template <typename T, bool QUICK, int TH>
+// dx = e w of a slice; FAR: e up w.
+template <typename T, bool QUICK, bool FAR, int TH>
 __device__ __forceinline__ void distill_write(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
-                                              float m, float c, float w, void *held) {
+                                              float m, float c, float up, float w, void *held) {
     lg_walk<T, TH> walk(x, r, held);
     walk.down(dx, [&](float(&e)[LG_VEC], int) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < LG_VEC; ++i)
-            e[i] = __builtin_amdgcn_exp2f(lg_exponent<QUICK>(e[i], m, c)) * w;
+        for (int i = 0; i < LG_VEC; ++i) {
+            const float v = __builtin_amdgcn_exp2f(lg_exponent<QUICK>(e[i], m, c));
+            e[i] = (FAR ? v * up : v) * w;
+        }
     });
+}
+
+// A weight beyond fp32 -- the rest's share over a sum S of far entries alone -- goes in two
+// factors: up, the power of two that brings S to 1 .. 2, and what is left, which is of
+// the size of the gradient.  (A named token's e up may be infinite: it is written after.)
+template <typename T, bool QUICK, int TH>
+__device__ __forceinline__ void distill_scaled(const typename T::bits *x, typename T::bits *dx, const lg_range &r,
+                                               const lg_row &t, float c, double w, void *held) {
+    if (__builtin_fabs(w) < 0x1p127) {
+        distill_write<T, QUICK, false, TH>(x, dx, r, t.m, c, 1.0f, (float)w, held);
+    } else {
+        const int k = max(0, 127 - (int)(__builtin_bit_cast(uint32_t, t.S) >> 23));     // (S is normal)
+        distill_write<T, QUICK, true, TH>(x, dx, r, t.m, c, ldexpf(1.0f, k), (float)ldexp(w, -k), held);
+    }
 }
 
 // WHOLE: a row per workgroup; SUMS: the sums of a slice; REST: what follows from
@@ -279,6 +295,9 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
             t = distill_sums<T, KIND, false, TH>(x, r, sl, p.slots, a.c, map, part, held);
         }
     }
+    // (what is left of entries farther than fp32's exponents go is none: their e is 0 below)
+    if (KIND == LG_NAMED && t.S < 0x1p-126f)
+        t.S = 0.0f;
     const double S = KIND == LG_NAMED ? (double)t.S + (double)t.b : (double)t.S;
     if (tid < 64 && slice == 0 && p.loss != nullptr) {
         const float loss = distill_loss<KIND>(t, S, a.c, p.slots, sl);
@@ -298,9 +317,9 @@ __global__ __launch_bounds__(TH) void distill_kernel(lg_row_args a, lg_distill_a
         const double away = KIND == LG_NAMED && rest != 0.0 && t.S != 0.0f ? by * rest / (double)t.S : 0.0;
         // (every slot's logit has been read: dx may be x)
         if (MODE == DS_WHOLE && t.quick)
-            distill_write<T, true, TH>(x, dx, r, t.m, a.c, (float)(all - away), held);
+            distill_scaled<T, true, TH>(x, dx, r, t, a.c, all - away, held);
         else
-            distill_write<T, false, TH>(x, dx, r, t.m, a.c, (float)(all - away), held);
+            distill_scaled<T, false, TH>(x, dx, r, t, a.c, all - away, held);
         __syncthreads();    // then the named tokens, a thread a slot; a token named twice gets both in each
         for (int j = tid; j < p.slots; j += TH) {
             const int i = sl.index[j];
