@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     int in, int T, const uint16_t *__restrict__ X, int M, Y *__restrict__ y, float *__restrict__ parts, int tiles_m,
     int tiles_r, int slices) {
     constexpr int TM = 4, TN = 4, THREADS = 256, RT = Q4_ROWS, CT = Q4_TOKENS;
-    static_assert(RT == THREADS && RT == TM * 64 && CT == TN * 16);
+    static_assert(RT == THREADS && RT == TM * 64 && CT == TN * 16 && THREADS / 16 == 16);
     constexpr int PIECES = CT * 16 / THREADS;       // 16-byte pieces of X a thread stages
     __shared__ __align__(16) uint8_t lds[2][CT * 256];
     __shared__ __align__(16) uint16_t lscales[2][RT][Q4_AHEAD];
@@ -77,14 +77,22 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     const int t0 = __builtin_amdgcn_readfirstlane(T / slices * slice + min(slice, T % slices));
     const int t1 = t0 + __builtin_amdgcn_readfirstlane(T / slices + (slice < T % slices));
 
-    // Loads through buffer descriptors of the tile's rows and tokens: what lies
-    // past the last one reads as 0, and the parts of an address that all lanes
-    // share are scalar.
-    const uint32_t rows = (uint32_t)min((int64_t)RT, (int64_t)out - r0), toks = (uint32_t)min((int64_t)CT, (int64_t)M - m0);
-    const auto wbuf = q4_buffer(codes + r0 * (in / 2), rows * (uint32_t)(in / 2));
-    const auto xbuf = q4_buffer(X + m0 * in, toks * (uint32_t)in * 2u);
-    const uint32_t woff = (uint32_t)li * (uint32_t)(in / 2) + g * 16;
-    const uint32_t xoff = (uint32_t)(tid >> 4) * (uint32_t)in * 2u + (tid & 15) * 16;
+    // Loads through buffer descriptors of the tile's rows and tokens, so that the parts
+    // of an address that all lanes share are scalar.  Every load is inside the tile
+    // (q4_plan.h), with no help of the descriptors' ranges, which need not count the
+    // scalar part; only the 0 of tokens that do not count is a range's, of an offset that
+    // passes it by itself.
+    const int rows = (int)min((int64_t)RT, (int64_t)out - r0), toks = (int)min((int64_t)CT, (int64_t)M - m0);
+    const auto wbuf = q4_buffer(codes + r0 * (in / 2), (uint32_t)rows * (uint32_t)(in / 2));
+    const auto xbuf = q4_buffer(X + m0 * in, (uint32_t)toks * (uint32_t)in * 2u);
+    int rfirst[TM], mfirst[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+        rfirst[i] = q4_first(wr * 64 + i * 16, rows);
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+        mfirst[n] = q4_first(n * 16, toks);
+    const uint32_t woff = q4_lane_codes(rows, in, li, g), xoff = q4_lane_tokens(toks, in, tid >> 4, tid & 15);
     // (a thread's tokens are THREADS / 16 apart, a multiple of 16)
     const uint32_t xat = (uint32_t)((tid >> 4) * 256 + (q4_place(tid & 15, tid >> 4 & 15) * 16));
 
@@ -100,12 +108,12 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     q4_f16x8 a[TN][4], b[2][4];
     q4_f32x4 acc[TM][TN] = {}, p[2][TN] = {};
     auto request_w = [&](int t, int i) __attribute__((always_inline)) {
-        const uint32_t row = (uint32_t)(wr * 64 + i * 16);
-        wraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff, row * (uint32_t)(in / 2) + t * 64, 0));
+        const uint32_t at = (uint32_t)rfirst[i] * (uint32_t)(in / 2) + (uint32_t)q4_column(in, t) / 2;
+        wraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff, at, 0));
     };
     // Q4_AHEAD groups of the thread's row (past the row's end: anything, not used;
     // past the array's end none)
-    const int64_t srow = (r0 + min(tid, (int)rows - 1)) * T, send = (int64_t)out * T;
+    const int64_t srow = (r0 + q4_first(tid & ~15, rows) + min(tid & 15, rows - 1)) * T, send = (int64_t)out * T;
     auto stage_s = [&](int t, int buffer) __attribute__((always_inline)) {
         const int64_t at = srow + t;
         if (at + Q4_AHEAD <= send) {
@@ -128,10 +136,11 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
             zraw = lzeros[buffer][row][at];
     };
     auto request_x = [&](int t) __attribute__((always_inline)) {
-        const uint32_t at = t * 128 + (tid & 15) * 8 < in ? xoff : 0x80000000u;     // (past a row's end: 0)
+        const int column = q4_column(in, t);
+        const uint32_t at = column + (tid & 15) * 8 >= t * 128 ? xoff : Q4_BEYOND;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
-            xraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, (uint32_t)(i * (THREADS / 16)) * (uint32_t)in * 2u + t * 256, 0));
+            xraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, (uint32_t)mfirst[i] * (uint32_t)in * 2u + (uint32_t)column * 2u, 0));
     };
     auto stage_x = [&](int buffer) __attribute__((always_inline)) {
 #pragma unroll
@@ -216,24 +225,33 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     scale(TM - 1, before);
     const bool whole = slices == 1;
     float *part = parts + (int64_t)slice * M * out;
+    // (rows and tokens that stand twice are written by their own sixteen)
+    auto write = [&](auto full) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-    for (int n = 0; n < TN; ++n)
+        for (int n = 0; n < TN; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t m = m0 + n * 16 + 4 * g + k;
-            if (m >= M)
-                continue;
+            for (int k = 0; k < 4; ++k) {
+                const int m = (FULL ? n * 16 : mfirst[n]) + 4 * g + k;
+                if (!FULL && (m >= toks || m < n * 16))
+                    continue;
+                const int64_t at = (m0 + m) * out + r0;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int64_t r = r0 + wr * 64 + i * 16 + li;
-                if (r < out) {
-                    if (whole)
-                        y[m * out + r] = q4_to<Y>(acc[i][n][k]);
-                    else
-                        part[m * out + r] = acc[i][n][k];
+                for (int i = 0; i < TM; ++i) {
+                    const int r = (FULL ? wr * 64 + i * 16 : rfirst[i]) + li;
+                    if (FULL || (r < rows && r >= wr * 64 + i * 16)) {
+                        if (whole)
+                            y[at + r] = q4_to<Y>(acc[i][n][k]);
+                        else
+                            part[at + r] = acc[i][n][k];
+                    }
                 }
             }
-        }
+    };
+    if (rows == RT && toks == CT)
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 // Y = the slices' sums, in their order, eight loads on their way at a time.

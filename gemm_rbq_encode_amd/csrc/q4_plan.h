@@ -50,6 +50,29 @@ inline q4_few_plan plan_q4_few(int out, int in, int M) {
 // Tiles of the many-token kernel (gemm_q4.hip).
 constexpr int Q4_ROWS = 256, Q4_TOKENS = 64;
 
+// The loads of a tile are sixteen rows or tokens by a group of 128 columns, all inside
+// the tile whatever its size: sixteen that would end behind its last one are its last
+// sixteen, where there are fewer the last one is repeated (what stands twice is written
+// once), and a row's short last group is its last 128 columns, with the tokens of the
+// columns before that group 0.  Of rows shorter than 128 columns a lane's piece of codes
+// behind the end is the last one, with tokens 0.
+constexpr uint32_t Q4_BEYOND = 0x80000000u;      // an offset that reads as 0
+
+constexpr int q4_first(int at, int count) {      // first of the sixteen that stand for at .. at + 15
+    return std::max(0, std::min(at, count - 16));
+}
+constexpr int q4_column(int in, int t) {         // first column of what is loaded for group t
+    return std::min(t * 128, std::max(in - 128, 0));
+}
+// Bytes from the first of sixteen rows (tokens) and the first column on: of row li's 32
+// codes from column 32 g on, of token m's 8 columns from column 8 q on.
+constexpr uint32_t q4_lane_codes(int rows, int in, int li, int g) {
+    return (uint32_t)std::min(li, rows - 1) * (uint32_t)(in / 2) + (uint32_t)std::min(g * 16, in / 2 - 16);
+}
+constexpr uint32_t q4_lane_tokens(int toks, int in, int m, int q) {
+    return q * 8 < in ? (uint32_t)std::min(m, toks - 1) * (uint32_t)in * 2u + (uint32_t)q * 16u : Q4_BEYOND;
+}
+
 // Offsets inside a tile are 32-bit and the tiles are numbered in 31 bits.
 inline bool q4_tiled(int out, int in, int M) {
     return !q4_few(out, in, M) && in <= (1 << 23) && ((int64_t)out / Q4_ROWS + 1) * ((int64_t)M / Q4_TOKENS + 1) < (1 << 24);
