@@ -871,7 +871,8 @@ static rbq_status logits_check(const void *logits, uint32_t type, int32_t M, int
     return RBQ_OK;
 }
 
-// d_logits: the logits themselves, or apart from them.
+// d_logits: the logits themselves, or apart from them; with the same stride also between
+// their rows.
 static rbq_status logits_gradient_check(const void *logits, const void *d_logits, uint32_t type, int32_t M,
                                         int32_t vocab, int64_t row_stride, int64_t d_row_stride) {
     if (d_logits == nullptr || d_row_stride < vocab)
@@ -883,9 +884,11 @@ static rbq_status logits_gradient_check(const void *logits, const void *d_logits
     const uintptr_t b = logits_bytes(type), x0 = (uintptr_t)logits, d0 = (uintptr_t)d_logits;
     const uintptr_t x1 = x0 + ((uintptr_t)(M - 1) * (uintptr_t)row_stride + (uintptr_t)vocab) * b;
     const uintptr_t d1 = d0 + ((uintptr_t)(M - 1) * (uintptr_t)d_row_stride + (uintptr_t)vocab) * b;
-    if (x0 < d1 && d0 < x1 && !(x0 == d0 && row_stride == d_row_stride))
-        return RBQ_ERR_INVALID_ARG;
-    return RBQ_OK;
+    if (x0 >= d1 || d0 >= x1 || (x0 == d0 && row_stride == d_row_stride))
+        return RBQ_OK;
+    const uintptr_t step = (uintptr_t)row_stride * b, row = (uintptr_t)vocab * b;
+    const uintptr_t from = d0 >= x0 ? (d0 - x0) % step : step - 1 - (x0 - d0 - 1) % step;
+    return row_stride == d_row_stride && from >= row && from + row <= step ? RBQ_OK : RBQ_ERR_INVALID_ARG;
 }
 
 size_t rbq_token_logprobs_workspace_bytes(int32_t M, int32_t vocab, int32_t top) {

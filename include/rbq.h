@@ -862,7 +862,9 @@ rbq_status rbq_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8
  * ws_bytes 0) rows are not cut, which is slower and adds in another order.  Calls
  * that share one must be ordered on one stream.  Every call gives the same bits
  * in every run.  Outputs and the workspace may not overlap anything else, but
- * d_logits may be the logits themselves (the same address and stride).
+ * d_logits may be the logits themselves (the same address and stride), or, with the
+ * same stride, lie between their rows (columns of one wider array); with another
+ * stride its first entry to its last lie apart from theirs.
  * ------------------------------------------------------------------------- */
 #define RBQ_L_F16  0u
 #define RBQ_L_F32  1u
