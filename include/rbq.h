@@ -930,13 +930,15 @@ rbq_status rbq_token_logprobs_backward(const void *logits, uint32_t type, int32_
  *           twice counts with both.
  *   without RBQ_DISTILL_TAIL  p_j = e^t_j / sum_i e^t_i (t up to a constant of
  *           the row), loss = sum_j p_j (ln p_j - ln q_j), q the student's p of
- *           the token; a row without slots has loss and gradient 0
+ *           the token; a row without slots has loss and gradient 0, whatever it
+ *           holds
  *   with it p_j = e^t_j, and the rest r = max(0, 1 - sum p) is compared with the
  *           student's mass on all tokens not named:
  *           loss = sum_j p_j (ln p_j - ln q_j) + r (ln r - ln q_rest)
  *           r <= 2^-15, which the rounding of t leaves, is 0 where q_rest = 0
- * A class with p = 0 counts 0; where q = 0 < p the loss is +inf.  (q is 0 where
- * fp32 holds no e^x: 87 and more below the row's largest logit over T.)
+ * A class with p = 0 counts 0; where q = 0 < p the loss is +inf.  (q_rest is 0 where
+ * fp32 holds no e^x of the tokens not named: 87 and more below the row's largest logit
+ * over T.  ln q_j is formed from the token's logit, and finite however far that lies.)
  *   d_loss    device fp32 [M]: d_logits is the gradient of sum_m d_loss[m] loss[m]
  *             in the type of the logits (a factor T^2, where wanted, belongs
  *             into d_loss); a row with d_loss 0 gets 0, whatever it holds

@@ -59,3 +59,29 @@ def test_one_unnamed_token_is_left(V):
     args = [t(x, torch.float32), t(idx, torch.int32), t(v, torch.float32)]
     dx, loss = rbq.distill_backward(*args, t(d, torch.float32), tail=True)
     assert torch.isfinite(dx).all() and torch.isfinite(loss[t(near, torch.bool)]).all() and not torch.isnan(loss).any()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [3001, 30011, 60007])
+def test_named_tokens_far_below(V, tail):
+    """ln q of a token that the teacher names is finite where its e^x is not held."""
+    M = 4
+    rng = np.random.default_rng(V)
+    x = rng.normal(size=(M, V))
+    idx = np.stack([rng.permutation(V)[:5] for _ in range(M)]).astype(np.int32)
+    x[np.arange(M), idx[:, 1]] = [-80.0, -100.0, -1000.0, -30000.0]
+    v = np.full((M, 5), np.log(0.1), np.float32)
+    dx, loss = check_distill(t(x, torch.float32), idx, v, np.full(M, 2.0, np.float32), 1.0, tail)
+    assert torch.isfinite(dx).all() and torch.isfinite(loss).all()
+
+
+def test_rows_without_slots_are_not_looked_at():
+    """Without the tail nothing depends on their logits, NaN or not; with it their sums do."""
+    x = torch.zeros((3, 700), device=dev())
+    x[1, 3], x[2] = float("nan"), -INF
+    idx, v = torch.full((3, 2), -1, dtype=torch.int32, device=dev()), torch.zeros((3, 2), device=dev())
+    one = torch.ones(3, device=dev())
+    dx, loss = rbq.distill_backward(x, idx, v, one)
+    assert not dx.any() and not loss.any()
+    dx, loss = rbq.distill_backward(x, idx, v, one, tail=True)
+    assert torch.isnan(dx[1]).all() and torch.isnan(loss[1]) and loss[2] == INF and not dx[2].any()
