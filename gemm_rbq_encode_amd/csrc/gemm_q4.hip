@@ -39,8 +39,9 @@ __device__ __forceinline__ Y q4_to(float v) {
 // thread: loaded where they are used, 2 bytes from each of 16 rows, they took 39 of
 // 277 us (2048 tokens, 14336 x 4096).
 //
-// 2048 tokens of 14336 x 4096: 254 us, 0.95 PFLOP/s (a library's fp16 product of that
-// size: 211 us, 1.14).  8192 of 11008 x 4096: 747 us, 0.99.  Two workgroups a CU, at 41
+// 2048 tokens of 14336 x 4096: 240 to 250 us by the card, 0.96 to 1.0 PFLOP/s (a library's
+// fp16 product of that size: 211 us, 1.14).  8192 of 11008 x 4096: 717 to 740 us, 1.0 to
+// 1.03.  Two workgroups a CU, at 41
 // cycles a product and SIMD where the instruction takes 16: bound by issue, 3.7 vector
 // instructions beside a product (1 to scale its group's sum, 2.3 to unpack), of which
 // four alone bring 16 to 26 or 28.  Tried: 128 tokens a tile (unpacks half as often, but
@@ -84,7 +85,11 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     // passes it by itself.
     const int rows = (int)min((int64_t)RT, (int64_t)out - r0), toks = (int)min((int64_t)CT, (int64_t)M - m0);
     const auto wbuf = q4_buffer(codes + r0 * (in / 2), (uint32_t)rows * (uint32_t)(in / 2));
+    // (sixteen tokens that are none of the tile's are not read again: an empty range)
     const auto xbuf = q4_buffer(X + m0 * in, (uint32_t)toks * (uint32_t)in * 2u);
+    const auto none = q4_buffer(X + m0 * in, 0);
+    const decltype(q4_buffer(X, 0)) xbufs[PIECES] = {xbuf, toks > 16 ? xbuf : none, toks > 32 ? xbuf : none, toks > 48 ? xbuf : none};
+    static_assert(PIECES == 4);
     int rfirst[TM], mfirst[TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -113,19 +118,22 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
     };
     // Q4_AHEAD groups of the thread's row (past the row's end: anything, not used;
     // past the array's end none)
-    const int64_t srow = (r0 + q4_first(tid & ~15, rows) + min(tid & 15, rows - 1)) * T, send = (int64_t)out * T;
+    const uint16_t *const sfirst = scales + r0 * T;
+    const uint8_t *const zfirst = ZEROS ? zeros + r0 * T : nullptr;
+    const uint32_t srow = (uint32_t)(q4_first(tid & ~15, rows) + min(tid & 15, rows - 1)) * (uint32_t)T;
+    const uint32_t send = (uint32_t)min((int64_t)1 << 30, (out - r0) * T);
     auto stage_s = [&](int t, int buffer) __attribute__((always_inline)) {
-        const int64_t at = srow + t;
+        const uint32_t at = srow + (uint32_t)t;
         if (at + Q4_AHEAD <= send) {
-            *(uint4 *)lscales[buffer][tid] = __builtin_bit_cast(uint4, *(const q4_u32x4 *)(scales + at));
+            *(uint4 *)lscales[buffer][tid] = __builtin_bit_cast(uint4, *(const q4_u32x4 *)(sfirst + at));
             if (ZEROS)
-                *(uint2 *)lzeros[buffer][tid] = __builtin_bit_cast(uint2, *(const q4_u32x2 *)(zeros + at));
+                *(uint2 *)lzeros[buffer][tid] = __builtin_bit_cast(uint2, *(const q4_u32x2 *)(zfirst + at));
         } else {
             for (int e = 0; e < Q4_AHEAD; ++e)
                 if (at + e < send) {
-                    lscales[buffer][tid][e] = scales[at + e];
+                    lscales[buffer][tid][e] = sfirst[at + e];
                     if (ZEROS)
-                        lzeros[buffer][tid][e] = zeros[at + e];
+                        lzeros[buffer][tid][e] = zfirst[at + e];
                 }
         }
     };
@@ -140,7 +148,7 @@ __global__ __launch_bounds__(256, 2) void gemm_q4_tile_kernel(
         const uint32_t at = column + (tid & 15) * 8 >= t * 128 ? xoff : Q4_BEYOND;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
-            xraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, (uint32_t)mfirst[i] * (uint32_t)in * 2u + (uint32_t)column * 2u, 0));
+            xraw[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(xbufs[i], at, (uint32_t)mfirst[i] * (uint32_t)in * 2u + (uint32_t)column * 2u, 0));
     };
     auto stage_x = [&](int buffer) __attribute__((always_inline)) {
 #pragma unroll
