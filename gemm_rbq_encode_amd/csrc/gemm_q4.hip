@@ -41,12 +41,12 @@ __device__ __forceinline__ Y q4_to(float v) {
 //
 // 2048 tokens of 14336 x 4096: 240 to 250 us by the card, 0.96 to 1.0 PFLOP/s (a library's
 // fp16 product of that size: 211 us, 1.14).  8192 of 11008 x 4096: 717 to 740 us, 1.0 to
-// 1.03.  Two workgroups a CU, at 41
-// cycles a product and SIMD where the instruction takes 16: bound by issue, 3.7 vector
-// instructions beside a product (1 to scale its group's sum, 2.3 to unpack), of which
-// four alone bring 16 to 26 or 28.  Tried: 128 tokens a tile (unpacks half as often, but
-// one wave a SIMD and 141 moves between register files: 290 us), 512 rows (292 us), two
-// or four products before the other work (256, 278), no order given (255 to 262).
+// 1.03.  Two workgroups a CU, at 41 cycles a product and SIMD where the instruction takes
+// 16: bound by issue, 3.7 vector instructions beside a product (1 to scale its group's
+// sum, 2.3 to unpack), of which four alone bring 16 to 26 or 28.  Tried, beside 254 then:
+// 128 tokens a tile (unpacks half as often, but one wave a SIMD and 141 moves between
+// register files: 290 us), 512 rows (292 us), two or four products before the other work
+// (256, 278), no order given (255 to 262).
 constexpr int Q4_AHEAD = 8;
 
 typedef uint32_t q4_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
