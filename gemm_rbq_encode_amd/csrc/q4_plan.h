@@ -56,7 +56,7 @@ constexpr int Q4_ROWS = 256, Q4_TOKENS = 64;
 // once), and a row's short last group is its last 128 columns, with the tokens of the
 // columns before that group 0.  Of rows shorter than 128 columns a lane's piece of codes
 // behind the end is the last one, with tokens 0.
-constexpr uint32_t Q4_BEYOND = 0x80000000u;      // an offset that reads as 0
+constexpr uint32_t Q4_BEYOND = 0x80000000u;      // an offset that reads as 0: behind every range
 
 constexpr int q4_first(int at, int count) {      // first of the sixteen that stand for at .. at + 15
     return std::max(0, std::min(at, count - 16));

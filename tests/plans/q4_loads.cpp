@@ -38,6 +38,9 @@ int main() {
                 for (int t = 0; t < T; ++t) {
                     std::vector<int> met(128);
                     const int column = q4_column(in, t);
+                    // what reads as 0 passes the range, with or without the scalar part taken off it
+                    const uint32_t range = at < toks ? (uint32_t)toks * in * 2 : 0, scalar = at < toks ? (uint32_t)first * in * 2 + column * 2 : 0;
+                    tokens_out += Q4_BEYOND < range || Q4_BEYOND < range - scalar;
                     for (int q = 0; q < 16; ++q) {
                         const uint32_t lane = column + q * 8 >= t * 128 ? q4_lane_tokens(toks, in, m, q) : Q4_BEYOND;
                         if (lane == Q4_BEYOND)
